@@ -298,3 +298,212 @@ def rmsnorm_backward(dy, x, s, r, *, w=None, add=None, dx=None, dw=None, stream=
     a.dw = _ptr(dw)
     st = (stream or torch.cuda.current_stream()).cuda_stream
     N.check(lib.gemm_epi_rmsnorm_backward(ctypes.byref(a), ctypes.c_void_p(st)), lib)
+
+
+ROTARY_LAYOUTS = {"half": N.GEMM_EPI_ROTARY_HALF, "interleaved": N.GEMM_EPI_ROTARY_INTERLEAVED}
+ROTARY_SCALINGS = {"linear": N.GEMM_EPI_ROTARY_LINEAR, "ntk": N.GEMM_EPI_ROTARY_NTK,
+                   "by_parts": N.GEMM_EPI_ROTARY_BY_PARTS}
+HEAD_TYPES = {torch.bfloat16: N.GEMM_EPI_TYPE_BF16, torch.float32: N.GEMM_EPI_TYPE_F32}
+
+
+class Rotary:
+    """The frequencies of rotary positions (gemm_epi_rotary_steps), copied to
+    `device` once and kept for every call.
+
+    The first `rotary_dim` values of a head (all of them by default) are
+    rotated in pairs: (i, i + rotary_dim / 2) with layout "half", (2i, 2i + 1)
+    with "interleaved".  Pair i turns by base^(-2i / rotary_dim) radians per
+    position, or by freqs[i].  `scaling` stretches them for long contexts:
+    dict(kind="linear" | "ntk", factor=f) or dict(kind="by_parts", factor=f,
+    original_length=n, low=1, high=32), each with an optional amplitude the
+    rotated part is multiplied by (default 1).
+    """
+
+    def __init__(self, head_dim: int, rotary_dim: Optional[int] = None, base: float = 10000.0, layout: str = "half",
+                 scaling: Optional[dict] = None, freqs: Optional[Sequence[float]] = None, device="cuda"):
+        if layout not in ROTARY_LAYOUTS:
+            raise ValueError("unknown rotary layout %r" % (layout,))
+        self.head_dim = int(head_dim)
+        self.rotary_dim = self.head_dim if rotary_dim is None else int(rotary_dim)
+        if self.rotary_dim > self.head_dim:
+            raise ValueError("rotary_dim %d is above head_dim %d" % (self.rotary_dim, self.head_dim))
+        self.layout, self.layout_code = layout, ROTARY_LAYOUTS[layout]
+        f = N.gemm_epi_rotary_freq()
+        f.rotary_dim, f.base = self.rotary_dim, float(base)
+        opts = dict(scaling or {})
+        kind = opts.pop("kind", None)
+        if scaling is not None:
+            if kind not in ROTARY_SCALINGS:
+                raise ValueError("unknown rotary scaling %r" % (kind,))
+            f.scaling, f.factor = ROTARY_SCALINGS[kind], float(opts.pop("factor"))
+            if kind == "by_parts":
+                f.original_length = float(opts.pop("original_length"))
+                f.low, f.high = float(opts.pop("low", 1.0)), float(opts.pop("high", 32.0))
+        self.amplitude = float(opts.pop("amplitude", 1.0))
+        if opts:
+            raise ValueError("unknown options of rotary scaling %r: %s" % (kind, ", ".join(sorted(opts))))
+        given = None
+        if freqs is not None:
+            given = (ctypes.c_double * len(freqs))(*[float(x) for x in freqs])
+            if len(freqs) != self.rotary_dim // 2:
+                raise ValueError("%d frequencies for %d pairs" % (len(freqs), self.rotary_dim // 2))
+            f.freq = ctypes.cast(given, ctypes.POINTER(ctypes.c_double))
+        steps = (ctypes.c_uint64 * max(1, self.rotary_dim // 2))()
+        lib = N.load()
+        N.check(lib.gemm_epi_rotary_steps(ctypes.byref(f), steps), lib)
+        # uint64 bits in an int64 tensor: torch has no arithmetic on them here
+        self.steps = torch.frombuffer(steps, dtype=torch.int64).clone().to(device)
+
+
+def _heads(name: str, t: torch.Tensor, like: Optional[torch.Tensor], dst, rope: Rotary) -> None:
+    """Fills a gemm_epi_heads from a (batch, tokens, heads, head_dim) or
+    (tokens, heads, head_dim) tensor; `like`: the tensor whose shape, type and
+    device it must have."""
+    shape = t.shape
+    if len(shape) not in (3, 4) or shape[-1] != rope.head_dim:
+        raise ValueError("%s: expected (batch, tokens, heads, %d) or (tokens, heads, %d), got %s"
+                         % (name, rope.head_dim, rope.head_dim, tuple(shape)))
+    if t.dtype not in HEAD_TYPES:
+        raise TypeError("%s: expected a bf16 or fp32 tensor, got %s" % (name, t.dtype))
+    if like is not None and (shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError("%s: %s %s on %s does not match %s %s on %s"
+                         % (name, t.dtype, tuple(shape), t.device, like.dtype, tuple(like.shape), like.device))
+    st = t.stride()
+    if st[-1] != 1 and t.numel():
+        raise ValueError("%s: the values of a head must be contiguous" % name)
+    dst.data = t.data_ptr()
+    dst.stride_token, dst.stride_head = st[-3], st[-2]
+    dst.stride_batch = st[0] if len(st) == 4 else 0
+
+
+def _vector(name: str, t: Optional[torch.Tensor], rope: Rotary, device) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != torch.float32:
+        raise TypeError("%s: expected a f32 tensor, got %s" % (name, t.dtype))
+    if t.shape != (rope.head_dim,) or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s: expected %d contiguous values on %s" % (name, rope.head_dim, device))
+    return t.data_ptr()
+
+
+def _qk_args(q, k, rope: Rotary, positions, q_out, k_out, *, optional_out: bool = False):
+    """gemm_epi_qk_args of q and k (either may be None), checked; returns it
+    with the tensors' device."""
+    a = N.gemm_epi_qk_args()
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q and k are both None")
+    device = first.device
+    for name, t, o, src, dst in (("q", q, q_out, a.q, a.q_out), ("k", k, k_out, a.k, a.k_out)):
+        if t is None:
+            if o is not None:
+                raise ValueError("%s_out without %s" % (name, name))
+            continue
+        _heads(name, t, None, src, rope)
+        if o is not None:
+            _heads(name + "_out", o, t, dst, rope)
+        elif not optional_out:
+            raise ValueError("%s_out is missing (pass %s itself to work in place)" % (name, name))
+    if q is not None and k is not None and (q.shape[:-2] != k.shape[:-2] or q.dtype != k.dtype or q.device != k.device):
+        raise ValueError("q %s %s on %s and k %s %s on %s do not belong together"
+                         % (q.dtype, tuple(q.shape), q.device, k.dtype, tuple(k.shape), k.device))
+    shape = first.shape
+    a.batch, a.tokens = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
+    a.q_heads = 0 if q is None else q.shape[-2]
+    a.k_heads = 0 if k is None else k.shape[-2]
+    a.head_dim, a.rotary_dim, a.layout = rope.head_dim, rope.rotary_dim, rope.layout_code
+    a.type = HEAD_TYPES[first.dtype]
+    if rope.steps.device != device:
+        raise ValueError("the rotary steps are on %s, q and k on %s" % (rope.steps.device, device))
+    a.steps, a.amplitude = rope.steps.data_ptr(), rope.amplitude
+    if positions is not None:
+        a.positions, a.positions_64, a.position_stride = _positions(positions, a.batch, a.tokens, device)
+    return a, device
+
+
+def _positions(p: torch.Tensor, batch: int, tokens: int, device):
+    """(pointer, is 64-bit, batch stride) of a (tokens,) or (batch, tokens) tensor."""
+    if p.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions: expected an int32 or int64 tensor, got %s" % p.dtype)
+    if p.device != device:
+        raise ValueError("positions are on %s, q and k on %s" % (p.device, device))
+    if p.shape == (tokens,):
+        stride = 0
+    elif p.shape == (batch, tokens):
+        stride = p.stride(0) if batch > 1 else 0
+    else:
+        raise ValueError("positions: expected (%d,) or (%d, %d), got %s" % (tokens, batch, tokens, tuple(p.shape)))
+    if tokens > 1 and p.stride(-1) != 1:
+        raise ValueError("positions: the positions of a sequence must be contiguous")
+    return p.data_ptr(), int(p.dtype == torch.int64), stride
+
+
+def _launch(fn, a, device, stream) -> None:
+    """Calls a C entry point on the current (or given) stream of the tensors'
+    device."""
+    lib = N.load()
+    if device.type != "cuda":
+        raise ValueError("expected CUDA tensors, got %s" % device)
+    if device.index == torch.cuda.current_device():
+        s = (stream or torch.cuda.current_stream()).cuda_stream
+        N.check(fn(ctypes.byref(a), s), lib)
+    else:
+        with torch.cuda.device(device):
+            s = (stream or torch.cuda.current_stream()).cuda_stream
+            N.check(fn(ctypes.byref(a), s), lib)
+
+
+def rotary(q, k, rope: Rotary, positions=None, *, q_out=None, k_out=None, inverse: bool = False, stream=None) -> None:
+    """gemm_epi_rotary: q and k (either may be None) rotated by their tokens'
+    positions into q_out and k_out, which may be q and k themselves.
+
+    q: (batch, tokens, heads, head_dim) or (tokens, heads, head_dim), bf16 or
+    fp32, any strides over contiguous heads (a transposed view where heads are
+    outside tokens); k the same with its own number of heads.  positions: int32
+    or int64, (tokens,) or (batch, tokens); None counts every sequence from 0.
+    inverse=True applies the transpose: the backward pass, from the gradients
+    of q_out and k_out to those of q and k.  Asynchronous."""
+    a, device = _qk_args(q, k, rope, positions, q_out, k_out)
+    a.inverse = 1 if inverse else 0
+    _launch(N.load().gemm_epi_rotary, a, device, stream)
+
+
+def qk_norm_rotary(q, k, rope: Rotary, positions=None, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+                   q_out=None, k_out=None, stream=None) -> None:
+    """gemm_epi_qk_norm_rotary: each head of q and k divided by its root mean
+    square (plus eps), multiplied by the fp32 weight (None: 1) and rotated, in
+    one pass; arguments as for rotary().  Asynchronous."""
+    a, device = _qk_args(q, k, rope, positions, q_out, k_out)
+    a.eps = eps
+    a.q_weight, a.k_weight = _vector("q_weight", q_weight, rope, device), _vector("k_weight", k_weight, rope, device)
+    _launch(N.load().gemm_epi_qk_norm_rotary, a, device, stream)
+
+
+def qk_norm_rotary_workspace(head_dim: int) -> int:
+    """Bytes of workspace qk_norm_rotary_backward needs for dwq or dwk."""
+    return int(N.load().gemm_epi_qk_norm_rotary_workspace_size(head_dim))
+
+
+def qk_norm_rotary_backward(dyq, dyk, q, k, rope: Rotary, positions=None, *, q_weight=None, k_weight=None,
+                            eps: float = 1e-6, dq=None, dk=None, dwq=None, dwk=None, workspace=None,
+                            stream=None) -> None:
+    """gemm_epi_qk_norm_rotary_backward: from the gradients dyq and dyk of
+    qk_norm_rotary's outputs and its inputs q and k, the gradients of q and k
+    into dq and dk (which may be the memory of q or dyq, k or dyk) and those of
+    the weights, summed over batch, tokens and heads, into the fp32 dwq and dwk
+    (overwritten).  Each of the four may be None; dwq and dwk need a workspace
+    of qk_norm_rotary_workspace(head_dim) bytes.  Asynchronous."""
+    a, device = _qk_args(q, k, rope, positions, dq, dk, optional_out=True)
+    for name, dy, x, dst in (("dyq", dyq, q, a.dy_q), ("dyk", dyk, k, a.dy_k)):
+        if (dy is None) != (x is None):
+            raise ValueError("%s and its input must be given together" % name)
+        if dy is not None:
+            _heads(name, dy, x, dst, rope)
+    a.eps = eps
+    a.q_weight, a.k_weight = _vector("q_weight", q_weight, rope, device), _vector("k_weight", k_weight, rope, device)
+    a.dw_q, a.dw_k = _vector("dwq", dwq, rope, device), _vector("dwk", dwk, rope, device)
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace: expected a contiguous tensor on %s" % device)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch(N.load().gemm_epi_qk_norm_rotary_backward, a, device, stream)

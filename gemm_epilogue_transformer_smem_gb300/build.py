@@ -19,11 +19,11 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libgemm_epi.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-UNITS = ["gemm_epi.cu", "spec_forward.cu", "spec_aux.cu", "spec_fp8.cu", "spec_common.cu"]
+UNITS = ["gemm_epi.cu", "spec_forward.cu", "spec_aux.cu", "spec_fp8.cu", "spec_common.cu", "heads.cu"]
 
 
 def sources(csrc=CSRC):
-    files = [os.path.join(csrc, f) for f in sorted(os.listdir(csrc)) if f.endswith((".cu", ".cuh"))]
+    files = [os.path.join(csrc, f) for f in sorted(os.listdir(csrc)) if f.endswith((".cu", ".cuh", ".h"))]
     files.append(os.path.join(ROOT, "include", "gemm_epi.h"))
     return files
 

@@ -23,11 +23,12 @@
 #include <vector>
 
 #include "gemm_epi.h"
+#include "host.h"
 #include "programs.cuh"
 #include "rmsnorm_bwd.cuh"
 #include "unfused_kernel.cuh"
 
-namespace {
+namespace ge_host {
 
 thread_local std::string g_last_error;
 
@@ -44,6 +45,16 @@ gemm_epi_status fail(gemm_epi_status s, const char* fmt, ...) {
 gemm_epi_status cuda_fail(cudaError_t e, const char* what) {
   return fail(GEMM_EPI_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+
+void clear_error() { g_last_error.clear(); }
+
+}  // namespace ge_host
+
+namespace {
+
+using ge_host::cuda_fail;
+using ge_host::fail;
+using ge_host::g_last_error;
 
 constexpr size_t WS_HEADER = 256;  // status words; row counters follow
 constexpr int DEFAULT_GROUP_M = 16;
@@ -166,6 +177,17 @@ gemm_epi_status device_state(DeviceState** out, int* dev_out) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+gemm_epi_status ge_host::device_sms(int* sms) {
+  DeviceState* dev = nullptr;
+  const gemm_epi_status s = device_state(&dev, nullptr);
+  if (s == GEMM_EPI_OK) *sms = dev->sms;
+  return s;
+}
+
+namespace {
 
 // 3-D tiled map: x (contiguous), rows, batch.  `batch_bytes` == 0 means the
 // operand is shared across the batch (a batch extent of 1).

@@ -1,0 +1,292 @@
+// heads.cu -- host side of the entry points that act on the heads of q and k
+// (rotary positions, the head norm with the rotation, its backward), and
+// their kernels.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "heads.cuh"
+#include "host.h"
+
+namespace {
+
+using ge_host::cuda_fail;
+using ge_host::fail;
+
+// ---------------------------------------------------------------- frequencies
+
+constexpr double TWO_PI = 6.283185307179586476925286766559;
+
+// ---------------------------------------------------------------- kernels
+
+using HeadKernel = void (*)(ge::HeadParams);
+
+template <class T, int V, bool HALF>
+HeadKernel kernel_of(int mode) {
+  switch (mode) {
+    case ge::HEAD_ROTARY: return ge::heads_kernel<T, V, HALF, ge::HEAD_ROTARY>;
+    case ge::HEAD_NORM: return ge::heads_kernel<T, V, HALF, ge::HEAD_NORM>;
+    default: return ge::heads_kernel<T, V, HALF, ge::HEAD_NORM_BWD>;
+  }
+}
+
+template <class T>
+HeadKernel kernel_of(int mode, bool wide, bool half) {
+  if (wide) return half ? kernel_of<T, 8, true>(mode) : kernel_of<T, 8, false>(mode);
+  return half ? kernel_of<T, 2, true>(mode) : kernel_of<T, 2, false>(mode);
+}
+
+// Forward passes: warps to start per SM before heads of one token share a
+// warp (fewer warps than this leave SMs idle; more recompute the angles).
+constexpr int64_t HD_WARPS_PER_SM = 48;
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+struct Checked {
+  bool wide = true;  // 16-byte accesses serve every tensor
+  size_t size = 2;
+};
+
+gemm_epi_status check_tensor(const gemm_epi_heads& h, const char* name, Checked& c) {
+  if (!h.data) return fail(GEMM_EPI_ERR_INVALID_VALUE, "%s is NULL", name);
+  if (!aligned(h.data, c.size))
+    return fail(GEMM_EPI_ERR_MISALIGNED, "%s is not aligned to its element size", name);
+  const int64_t lim = int64_t(1) << 40;
+  for (int64_t st : {h.stride_batch, h.stride_token, h.stride_head}) {
+    if (st <= -lim || st >= lim) return fail(GEMM_EPI_ERR_INVALID_VALUE, "a stride of %s is out of range", name);
+    if (st * static_cast<int64_t>(c.size) % 16 != 0) c.wide = false;
+  }
+  if (!aligned(h.data, 16)) c.wide = false;
+  return GEMM_EPI_OK;
+}
+
+// Different elements of an output must not share memory: no dimension of more
+// than one step may advance by less than a head.
+gemm_epi_status check_output(const gemm_epi_qk_args& a, const gemm_epi_heads& h, int32_t heads, const char* name) {
+  const int64_t extent[3] = {a.batch, a.tokens, heads};
+  const int64_t stride[3] = {h.stride_batch, h.stride_token, h.stride_head};
+  for (int i = 0; i < 3; ++i)
+    if (extent[i] > 1 && stride[i] < a.head_dim && stride[i] > -a.head_dim)
+      return fail(GEMM_EPI_ERR_INVALID_VALUE, "%s: a stride below head_dim makes heads overlap", name);
+  return GEMM_EPI_OK;
+}
+
+bool same_place(const gemm_epi_heads& a, const gemm_epi_heads& b) {
+  return a.data == b.data && a.stride_batch == b.stride_batch && a.stride_token == b.stride_token &&
+         a.stride_head == b.stride_head;
+}
+
+// An output is written over an input element by element or not at all.
+gemm_epi_status check_in_place(const gemm_epi_heads& out, const gemm_epi_heads& in, const char* o, const char* i) {
+  if (out.data && out.data == in.data && !same_place(out, in))
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "%s starts where %s does but has other strides", o, i);
+  return GEMM_EPI_OK;
+}
+
+gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) {
+  ge_host::clear_error();
+  if (!a) return fail(GEMM_EPI_ERR_INVALID_VALUE, "args must not be NULL");
+  const int64_t LIM = 0x7FFFFFFF;
+  if (a->batch < 0 || a->tokens < 0 || a->batch > LIM || a->tokens > LIM || a->batch * a->tokens > LIM)
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "batch, tokens and their product must be in [0, 2^31)");
+  if (a->q_heads < 0 || a->k_heads < 0 || a->q_heads > 65535 || a->k_heads > 65535)
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "q_heads and k_heads must be in [0, 65535]");
+  if (a->head_dim < 2 || a->head_dim > ge::HD_MAX_DIM || a->head_dim % 2)
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "head_dim must be even, in [2, %d] (got %d)", ge::HD_MAX_DIM, a->head_dim);
+  if (a->rotary_dim < 2 || a->rotary_dim > a->head_dim || a->rotary_dim % 2)
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "rotary_dim must be even, in [2, head_dim] (got %d)", a->rotary_dim);
+  if (a->layout != GEMM_EPI_ROTARY_HALF && a->layout != GEMM_EPI_ROTARY_INTERLEAVED)
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "unknown rotary layout %d", a->layout);
+  if (a->layout == GEMM_EPI_ROTARY_HALF && a->rotary_dim % 4)
+    return fail(GEMM_EPI_ERR_UNSUPPORTED, "the half layout needs rotary_dim %% 4 == 0 (got %d)", a->rotary_dim);
+  if (a->type != GEMM_EPI_TYPE_BF16 && a->type != GEMM_EPI_TYPE_F32)
+    return fail(GEMM_EPI_ERR_UNSUPPORTED, "q and k must be BF16 or F32 (type %d)", a->type);
+  if (!std::isfinite(a->amplitude)) return fail(GEMM_EPI_ERR_INVALID_VALUE, "amplitude must be finite");
+  if (mode != ge::HEAD_ROTARY && (!(a->eps >= 0.0f) || !std::isfinite(a->eps)))
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "eps must be finite and >= 0");
+  const bool rows = a->batch > 0 && a->tokens > 0;
+  const bool bwd = mode == ge::HEAD_NORM_BWD;
+  const bool wants_dw = bwd && (a->dw_q || a->dw_k);
+
+  Checked c;
+  c.size = a->type == GEMM_EPI_TYPE_F32 ? 4 : 2;
+  gemm_epi_status s;
+  const gemm_epi_heads* in[2] = {&a->q, &a->k};
+  const gemm_epi_heads* dy[2] = {&a->dy_q, &a->dy_k};
+  const gemm_epi_heads* out[2] = {&a->q_out, &a->k_out};
+  const int32_t heads[2] = {a->q_heads, a->k_heads};
+  static const char* const names[2][3] = {{"q", "dy_q", "q_out"}, {"k", "dy_k", "k_out"}};
+  const float* w[2] = {a->q_weight, a->k_weight};
+  for (int i = 0; i < 2; ++i) {
+    if (w[i] && !aligned(w[i], 4)) return fail(GEMM_EPI_ERR_MISALIGNED, "%s_weight must be 4-byte aligned", names[i][0]);
+    if (!rows || heads[i] == 0) continue;
+    if ((s = check_tensor(*in[i], names[i][0], c))) return s;
+    if (bwd && (s = check_tensor(*dy[i], names[i][1], c))) return s;
+    // the backward pass may leave a gradient of q or k out
+    if ((!bwd || out[i]->data) &&
+        ((s = check_tensor(*out[i], names[i][2], c)) || (s = check_output(*a, *out[i], heads[i], names[i][2]))))
+      return s;
+    if ((s = check_in_place(*out[i], *in[i], names[i][2], names[i][0]))) return s;
+    if (bwd && (s = check_in_place(*out[i], *dy[i], names[i][2], names[i][1]))) return s;
+    for (int j = 0; j < 2; ++j)  // one tensor's rows must not be another's results
+      if (j != i && heads[j] > 0 && out[i]->data &&
+          (out[i]->data == in[j]->data || (bwd && out[i]->data == dy[j]->data) || out[i]->data == out[j]->data))
+        return fail(GEMM_EPI_ERR_INVALID_VALUE, "%s shares its memory with a tensor of %s", names[i][2], names[j][0]);
+  }
+  for (const float* d : {a->dw_q, a->dw_k})
+    if (bwd && d && !aligned(d, 4)) return fail(GEMM_EPI_ERR_MISALIGNED, "dw_q and dw_k must be 4-byte aligned");
+  if (wants_dw && a->dw_q == a->dw_k) return fail(GEMM_EPI_ERR_INVALID_VALUE, "dw_q and dw_k are the same buffer");
+  const bool work = rows && (a->q_heads > 0 || a->k_heads > 0) && (!bwd || wants_dw || a->q_out.data || a->k_out.data);
+  if (work) {
+    if (!a->steps) return fail(GEMM_EPI_ERR_INVALID_VALUE, "steps is NULL");
+    if (!aligned(a->steps, 8)) return fail(GEMM_EPI_ERR_MISALIGNED, "steps must be 8-byte aligned");
+    if (a->positions && !aligned(a->positions, a->positions_64 ? 8 : 4))
+      return fail(GEMM_EPI_ERR_MISALIGNED, "positions is not aligned to its element size");
+    if (a->positions && a->position_stride != 0 && a->position_stride < a->tokens)
+      return fail(GEMM_EPI_ERR_INVALID_VALUE, "position_stride must be 0 (shared by the batch) or at least tokens");
+  }
+  const size_t ws = gemm_epi_qk_norm_rotary_workspace_size(a->head_dim);
+  if (wants_dw && work && (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < ws))
+    return fail(GEMM_EPI_ERR_WORKSPACE, "workspace must be 16-byte aligned and hold %zu bytes (got %zu)", ws,
+                a->workspace ? a->workspace_bytes : static_cast<size_t>(0));
+  int sms = 0;
+  if ((s = ge_host::device_sms(&sms))) return s;
+  cudaError_t e;
+  if (!work) {
+    // no rows: the weights' gradients are zero
+    for (float* d : {a->dw_q, a->dw_k})
+      if (bwd && d && (e = cudaMemsetAsync(d, 0, sizeof(float) * a->head_dim, st)) != cudaSuccess)
+        return cuda_fail(e, "cudaMemsetAsync of dw");
+    return GEMM_EPI_OK;
+  }
+
+  const bool half = a->layout == GEMM_EPI_ROTARY_HALF;
+  const int pairs = a->rotary_dim / 2;
+  // 16-byte accesses need whole chunks of 8 values: in the head, and in each
+  // half of the rotated part.
+  const bool wide = c.wide && a->head_dim % 8 == 0 && (!half || pairs % 8 == 0);
+  const int V = wide ? 8 : 2, slots = 8 / V;
+
+  ge::HeadParams p;
+  std::memset(&p, 0, sizeof p);
+  p.tokens = static_cast<int32_t>(a->tokens);
+  p.rows = static_cast<int32_t>(a->batch * a->tokens);
+  p.dim = a->head_dim;
+  p.rot_pairs = pairs;
+  p.first_plain = (pairs + V - 1) / V;
+  p.num_pc = (a->head_dim / V + 1) / 2;
+  if (half) p.num_pc = p.first_plain + (a->head_dim / V - 2 * p.first_plain + 1) / 2;
+  // In place and without a norm, what does not rotate is already there.
+  bool in_place = mode == ge::HEAD_ROTARY;
+  for (int i = 0; i < 2; ++i) in_place = in_place && (heads[i] == 0 || same_place(*in[i], *out[i]));
+  if (in_place) p.num_pc = p.first_plain;
+  p.log_g = 0;
+  while ((slots << p.log_g) < p.num_pc) ++p.log_g;
+  const int per_iter = 32 >> p.log_g;
+  int total_iters = 0;
+  for (int i = 0; i < 2; ++i) {
+    ge::HeadPart& h = p.part[i];
+    h.heads = heads[i];
+    h.iters = (heads[i] + per_iter - 1) / per_iter;
+    total_iters += h.iters;
+    h.x = in[i]->data, h.x_b = in[i]->stride_batch, h.x_t = in[i]->stride_token, h.x_h = in[i]->stride_head;
+    h.dy = dy[i]->data, h.dy_b = dy[i]->stride_batch, h.dy_t = dy[i]->stride_token, h.dy_h = dy[i]->stride_head;
+    h.y = out[i]->data, h.y_b = out[i]->stride_batch, h.y_t = out[i]->stride_token, h.y_h = out[i]->stride_head;
+    h.w = w[i];
+  }
+  p.steps = a->steps;
+  p.positions = a->positions;
+  p.positions_64 = a->positions_64 ? 1 : 0;
+  p.pos_b = a->position_stride;
+  p.amplitude = a->amplitude;
+  p.sin_sign = (bwd || (mode == ge::HEAD_ROTARY && a->inverse)) ? -1.0f : 1.0f;
+  p.eps = a->eps;
+  p.inv_dim = 1.0f / static_cast<float>(a->head_dim);
+  p.partials = wants_dw ? static_cast<float*>(a->workspace) : nullptr;
+
+  // A warp takes a whole token while there are tokens enough for every SM,
+  // and fewer of its heads below that.
+  const int64_t warps = static_cast<int64_t>(sms) * (bwd ? ge::HD_BWD_BLOCKS * ge::HD_WARPS : HD_WARPS_PER_SM);
+  const int64_t fair = static_cast<int64_t>(p.rows) * total_iters / warps;
+  p.iters_per_unit = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(fair, total_iters)));
+  p.units_per_row = (total_iters + p.iters_per_unit - 1) / p.iters_per_unit;
+  const int64_t units = static_cast<int64_t>(p.rows) * p.units_per_row;
+  int64_t blocks = (units + ge::HD_WARPS - 1) / ge::HD_WARPS;
+  // The backward pass keeps its weight gradients in registers over a warp's
+  // tokens: one wave of blocks, each leaving one partial row.
+  if (bwd) blocks = std::min<int64_t>(blocks, std::min<int64_t>(ge::HD_MAX_PARTIALS, sms * ge::HD_BWD_BLOCKS));
+  const HeadKernel kernel = a->type == GEMM_EPI_TYPE_F32 ? kernel_of<float>(mode, wide, half)
+                                                         : kernel_of<uint16_t>(mode, wide, half);
+  kernel<<<static_cast<unsigned>(blocks), ge::HD_THREADS, 0, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "launch of the head kernel");
+  if (wants_dw) {
+    ge::head_weight_grad_kernel<<<static_cast<unsigned>((2 * a->head_dim + 31) / 32), dim3(32, 32), 0, st>>>(
+        p.partials, static_cast<int>(blocks), a->head_dim, a->dw_q, a->dw_k);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "launch of the weight gradient kernel");
+  }
+  return GEMM_EPI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_epi_status gemm_epi_rotary_steps(const gemm_epi_rotary_freq* f, uint64_t* steps) {
+  ge_host::clear_error();
+  if (!f || !steps) return fail(GEMM_EPI_ERR_INVALID_VALUE, "freq and steps must not be NULL");
+  if (f->rotary_dim < 2 || f->rotary_dim % 2 || f->rotary_dim > ge::HD_MAX_DIM)
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "rotary_dim must be even, in [2, %d] (got %d)", ge::HD_MAX_DIM,
+                f->rotary_dim);
+  if (!f->freq && (!(f->base > 0.0) || !std::isfinite(f->base)))
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "base must be finite and > 0");
+  if (f->scaling < GEMM_EPI_ROTARY_UNSCALED || f->scaling > GEMM_EPI_ROTARY_BY_PARTS)
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "unknown scaling %d", f->scaling);
+  if (f->scaling != GEMM_EPI_ROTARY_UNSCALED && (!(f->factor > 0.0) || !std::isfinite(f->factor)))
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "factor must be finite and > 0");
+  if (f->scaling == GEMM_EPI_ROTARY_NTK && (f->rotary_dim < 4 || f->freq))
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "NTK scaling changes the base: it needs rotary_dim >= 4 and no freq");
+  if (f->scaling == GEMM_EPI_ROTARY_BY_PARTS &&
+      (!(f->original_length > 0.0) || !std::isfinite(f->original_length) || !std::isfinite(f->low) ||
+       !std::isfinite(f->high) || !(f->low < f->high)))
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "BY_PARTS scaling needs original_length > 0 and low < high");
+  double base = f->base;
+  if (f->scaling == GEMM_EPI_ROTARY_NTK)
+    base *= std::pow(f->factor, f->rotary_dim / (f->rotary_dim - 2.0));
+  if (!f->freq && !std::isfinite(base)) return fail(GEMM_EPI_ERR_INVALID_VALUE, "the scaled base is not finite");
+  for (int i = 0; i < f->rotary_dim / 2; ++i) {
+    double w = f->freq ? f->freq[i] : std::pow(base, -2.0 * i / f->rotary_dim);
+    if (f->scaling == GEMM_EPI_ROTARY_LINEAR) w /= f->factor;
+    if (f->scaling == GEMM_EPI_ROTARY_BY_PARTS) {
+      const double turns = f->original_length * w / TWO_PI;
+      const double keep = std::min(1.0, std::max(0.0, (turns - f->low) / (f->high - f->low)));
+      w = w * keep + w / f->factor * (1.0 - keep);
+    }
+    if (!std::isfinite(w)) return fail(GEMM_EPI_ERR_INVALID_VALUE, "frequency %d is not finite", i);
+    double frac = w / TWO_PI;
+    frac -= std::floor(frac);  // [0, 1]
+    const double scaled = std::nearbyint(frac * 18446744073709551616.0);
+    steps[i] = scaled >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(scaled);
+  }
+  return GEMM_EPI_OK;
+}
+
+gemm_epi_status gemm_epi_rotary(const gemm_epi_qk_args* args, void* stream) {
+  return run_heads(args, ge::HEAD_ROTARY, static_cast<cudaStream_t>(stream));
+}
+
+gemm_epi_status gemm_epi_qk_norm_rotary(const gemm_epi_qk_args* args, void* stream) {
+  return run_heads(args, ge::HEAD_NORM, static_cast<cudaStream_t>(stream));
+}
+
+gemm_epi_status gemm_epi_qk_norm_rotary_backward(const gemm_epi_qk_args* args, void* stream) {
+  return run_heads(args, ge::HEAD_NORM_BWD, static_cast<cudaStream_t>(stream));
+}
+
+size_t gemm_epi_qk_norm_rotary_workspace_size(int32_t head_dim) {
+  if (head_dim < 2 || head_dim > ge::HD_MAX_DIM) return 0;
+  return static_cast<size_t>(ge::HD_MAX_PARTIALS) * 2 * static_cast<size_t>(head_dim) * sizeof(float);
+}
+
+}  // extern "C"

@@ -30,6 +30,15 @@ STATUS_NAMES = {
 GEMM_EPI_TYPE_BF16 = 0
 GEMM_EPI_TYPE_E4M3 = 1
 GEMM_EPI_TYPE_E5M2 = 2
+GEMM_EPI_TYPE_F32 = 3
+
+# gemm_epi_rotary_layout, gemm_epi_rotary_scaling
+GEMM_EPI_ROTARY_HALF = 0
+GEMM_EPI_ROTARY_INTERLEAVED = 1
+GEMM_EPI_ROTARY_UNSCALED = 0
+GEMM_EPI_ROTARY_LINEAR = 1
+GEMM_EPI_ROTARY_NTK = 2
+GEMM_EPI_ROTARY_BY_PARTS = 3
 
 # gemm_epi_b_layout
 GEMM_EPI_B_KN = 0
@@ -112,6 +121,38 @@ class gemm_epi_rmsnorm_bwd_args(ctypes.Structure):
     ]
 
 
+class gemm_epi_rotary_freq(ctypes.Structure):
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+        ("base", ctypes.c_double), ("factor", ctypes.c_double), ("original_length", ctypes.c_double),
+        ("low", ctypes.c_double), ("high", ctypes.c_double),
+        ("freq", ctypes.POINTER(ctypes.c_double)),
+    ]
+
+
+class gemm_epi_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64)]
+
+
+class gemm_epi_qk_args(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("tokens", ctypes.c_int64),
+        ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32), ("type", ctypes.c_int32),
+        ("q", gemm_epi_heads), ("k", gemm_epi_heads),
+        ("q_out", gemm_epi_heads), ("k_out", gemm_epi_heads),
+        ("dy_q", gemm_epi_heads), ("dy_k", gemm_epi_heads),
+        ("steps", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("position_stride", ctypes.c_int64), ("positions_64", ctypes.c_int32), ("inverse", ctypes.c_int32),
+        ("amplitude", ctypes.c_float), ("eps", ctypes.c_float),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        ("dw_q", ctypes.c_void_p), ("dw_k", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 gemm_epi_handle = ctypes.c_void_p
 
 # (name, restype, argtypes): every entry point declared in include/gemm_epi.h.
@@ -125,6 +166,12 @@ SIGNATURES = [
      [gemm_epi_handle, ctypes.POINTER(gemm_epi_args), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
     ("gemm_epi_run_no_alloc", ctypes.c_int, [gemm_epi_handle, ctypes.POINTER(gemm_epi_args), ctypes.c_void_p]),
     ("gemm_epi_rmsnorm_backward", ctypes.c_int, [ctypes.POINTER(gemm_epi_rmsnorm_bwd_args), ctypes.c_void_p]),
+    ("gemm_epi_rotary_steps", ctypes.c_int,
+     [ctypes.POINTER(gemm_epi_rotary_freq), ctypes.POINTER(ctypes.c_uint64)]),
+    ("gemm_epi_rotary", ctypes.c_int, [ctypes.POINTER(gemm_epi_qk_args), ctypes.c_void_p]),
+    ("gemm_epi_qk_norm_rotary", ctypes.c_int, [ctypes.POINTER(gemm_epi_qk_args), ctypes.c_void_p]),
+    ("gemm_epi_qk_norm_rotary_backward", ctypes.c_int, [ctypes.POINTER(gemm_epi_qk_args), ctypes.c_void_p]),
+    ("gemm_epi_qk_norm_rotary_workspace_size", ctypes.c_size_t, [ctypes.c_int32]),
     ("gemm_epi_query_status", ctypes.c_int, [gemm_epi_handle, ctypes.c_void_p, ctypes.c_void_p]),
     ("gemm_epi_status_string", ctypes.c_char_p, [ctypes.c_int]),
     ("gemm_epi_last_error", ctypes.c_char_p, []),

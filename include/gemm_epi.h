@@ -120,7 +120,8 @@ typedef enum gemm_epi_status {
 typedef enum gemm_epi_type {
     GEMM_EPI_TYPE_BF16 = 0,
     GEMM_EPI_TYPE_E4M3 = 1,   /* OCP FP8 E4M3FN */
-    GEMM_EPI_TYPE_E5M2 = 2    /* OCP FP8 E5M2 */
+    GEMM_EPI_TYPE_E5M2 = 2,   /* OCP FP8 E5M2 */
+    GEMM_EPI_TYPE_F32 = 3     /* the head operators' tensors only (gemm_epi_qk_args) */
 } gemm_epi_type;
 
 typedef enum gemm_epi_b_layout {
@@ -349,6 +350,103 @@ typedef struct gemm_epi_rmsnorm_bwd_args {
 /* Enqueues the second pass on `stream` (a cudaStream_t).  Asynchronous;
  * capture-safe; checks sizes, pointers and alignment first. */
 GEMM_EPI_API gemm_epi_status gemm_epi_rmsnorm_backward(const gemm_epi_rmsnorm_bwd_args *args, void *stream);
+
+/*
+ * Rotary positions and the norm of each head of q and k.
+ *
+ * A projection's output holds heads of head_dim values.  With x one head at
+ * position p, its first rotary_dim values in pairs, f_i the frequency of pair
+ * i (radians per position) and A an amplitude:
+ *   rotation  R(p): (a, b) -> A (a cos(p f_i) - b sin(p f_i),
+ *                               b cos(p f_i) + a sin(p f_i)) on each pair;
+ *             the other head_dim - rotary_dim values pass through.
+ *   norm      n(x) = x r w,  r = 1 / sqrt(mean(x^2) + eps) over the whole head.
+ * gemm_epi_rotary writes R(p) x; gemm_epi_qk_norm_rotary R(p) n(x), the norm
+ * kept in fp32 up to the one rounding of the result; and
+ * gemm_epi_qk_norm_rotary_backward, from the gradient dy of that result and
+ * the same x, with g = R(p)^T dy:
+ *   dx = r (g w - x r mean(g w x r)),   dw = sum over batch, tokens and heads
+ * of g x r.  The rotation alone has its transpose as backward pass:
+ * gemm_epi_rotary with `inverse`.
+ */
+typedef enum gemm_epi_rotary_layout {
+    GEMM_EPI_ROTARY_HALF = 0,        /* pair i: values i and i + rotary_dim / 2 (rotary_dim % 4 == 0) */
+    GEMM_EPI_ROTARY_INTERLEAVED = 1  /* pair i: values 2i and 2i + 1 */
+} gemm_epi_rotary_layout;
+
+/* Frequencies, f_i = base^(-2i / rotary_dim) scaled for contexts longer than
+ * the ones trained on. */
+typedef enum gemm_epi_rotary_scaling {
+    GEMM_EPI_ROTARY_UNSCALED = 0,
+    GEMM_EPI_ROTARY_LINEAR = 1,    /* f / factor */
+    GEMM_EPI_ROTARY_NTK = 2,       /* base * factor^(rotary_dim / (rotary_dim - 2)) */
+    GEMM_EPI_ROTARY_BY_PARTS = 3   /* f (k + (1 - k) / factor), k = clamp((t - low) / (high - low), 0, 1),
+                                      t = original_length f / 2 pi, the turns pair i makes over the
+                                      original length: fast pairs keep f, slow ones get f / factor */
+} gemm_epi_rotary_scaling;
+
+typedef struct gemm_epi_rotary_freq {
+    int32_t rotary_dim;     /* even, 2 .. 512 */
+    int32_t scaling;        /* gemm_epi_rotary_scaling */
+    double base;
+    double factor;          /* scaled kinds: > 0 */
+    double original_length, low, high;  /* BY_PARTS: original_length > 0, low < high */
+    const double *freq;     /* rotary_dim / 2 frequencies on the host in place of the powers
+                               of `base` (then scaled the same way; not with NTK), or NULL */
+} gemm_epi_rotary_freq;
+
+/* Pure host code: the rotary_dim / 2 steps the entry points below read, each
+ * the fraction of a turn pair i advances per position, times 2^64 (so the
+ * phase of any 64-bit position is exact: the low 64 bits of position * step).
+ * The caller copies them to device memory once. */
+GEMM_EPI_API gemm_epi_status gemm_epi_rotary_steps(const gemm_epi_rotary_freq *freq, uint64_t *steps);
+
+/* The heads of q or k: element (b, t, h, d) at data + b stride_batch +
+ * t stride_token + h stride_head + d, strides in elements, any order (tokens
+ * outside heads or inside, heads of a packed q|k|v projection).  Any strides
+ * and element-aligned pointers are taken; 16-byte aligned pointers and strides
+ * with head_dim % 8 == 0 (and rotary_dim % 16 == 0 in the half layout) move
+ * 16 bytes per access, the rest single elements. */
+typedef struct gemm_epi_heads {
+    void *data;
+    int64_t stride_batch, stride_token, stride_head;
+} gemm_epi_heads;
+
+typedef struct gemm_epi_qk_args {
+    int64_t batch, tokens;        /* batch * tokens < 2^31; 0 is allowed */
+    int32_t q_heads, k_heads;     /* 0: q or k is not given */
+    int32_t head_dim;             /* even, 2 .. 512 */
+    int32_t rotary_dim;           /* even, 2 .. head_dim */
+    int32_t layout;               /* gemm_epi_rotary_layout */
+    int32_t type;                 /* BF16 or F32: every tensor below */
+    gemm_epi_heads q, k;          /* x (not written unless an output is the same tensor) */
+    gemm_epi_heads q_out, k_out;  /* results; dx in the backward pass, where data NULL leaves one out.
+                                     Each may be its own x (or dy) -- same pointer and strides -- and
+                                     must not overlap any tensor otherwise */
+    gemm_epi_heads dy_q, dy_k;    /* backward pass: gradients of q_out and k_out */
+    const uint64_t *steps;        /* device, rotary_dim / 2 values of gemm_epi_rotary_steps */
+    const void *positions;        /* device int32 / int64, tokens per sequence; NULL: 0, 1, 2, ... */
+    int64_t position_stride;      /* elements between the sequences' positions; 0: shared */
+    int32_t positions_64;         /* 1: int64 positions */
+    int32_t inverse;              /* gemm_epi_rotary: 1 applies A R(p)^T (the backward pass) */
+    float amplitude;              /* A, usually 1 */
+    float eps;                    /* norm */
+    const float *q_weight, *k_weight;  /* norm: head_dim values, NULL: 1 */
+    float *dw_q, *dw_k;           /* backward pass: head_dim values each, overwritten; NULL leaves one out */
+    void *workspace;              /* backward pass with dw_q or dw_k: device, 16-byte aligned, not shared by */
+    size_t workspace_bytes;       /* calls that may run at once */
+} gemm_epi_qk_args;
+
+/* Each enqueues its kernels on `stream`: asynchronous, capture-safe, checks
+ * sizes, pointers and alignment first, allocates nothing.  The same call gives
+ * the same bits every time. */
+GEMM_EPI_API gemm_epi_status gemm_epi_rotary(const gemm_epi_qk_args *args, void *stream);
+GEMM_EPI_API gemm_epi_status gemm_epi_qk_norm_rotary(const gemm_epi_qk_args *args, void *stream);
+GEMM_EPI_API gemm_epi_status gemm_epi_qk_norm_rotary_backward(const gemm_epi_qk_args *args, void *stream);
+
+/* Bytes of workspace the backward pass needs for its weight gradients (0 for
+ * a head_dim out of range). */
+GEMM_EPI_API size_t gemm_epi_qk_norm_rotary_workspace_size(int32_t head_dim);
 
 /* Synchronises `stream`, then reads the status words the last run on that
  * workspace left: GEMM_EPI_OK or GEMM_EPI_ERR_TIMEOUT (the last-error string
