@@ -7,7 +7,8 @@ colon):
 
   alpha, bias, row_scale, residual, gelu_tanh, relu, silu, pair_swiglu[:g], pair_mul[:g],
   gelu_tanh_grad, amax, store_bf16, store_e4m3, row_rms[:eps],
-  row_rms_unrounded[:eps], col_sum, dswiglu[:g], col_scale, row_dot
+  row_rms_unrounded[:eps], col_sum, dswiglu[:g], col_scale, row_dot,
+  head_rms[:eps], rotary
 """
 from __future__ import annotations
 
@@ -39,6 +40,8 @@ PROGRAM_OPS = {
     "row_rms": N.GEMM_EPI_OP_ROW_RMS_RSQRT,
     "row_rms_unrounded": N.GEMM_EPI_OP_ROW_RMS_RSQRT,
     "col_sum": N.GEMM_EPI_OP_COL_SUM,
+    "head_rms": N.GEMM_EPI_OP_HEAD_RMS,
+    "rotary": N.GEMM_EPI_OP_ROTARY,
 }
 
 
@@ -52,7 +55,7 @@ def encode_program(program: Sequence[str]):
         i0, f0 = 0, 0.0
         if name in ("pair_swiglu", "pair_mul", "dswiglu"):
             i0 = int(arg) if arg else 1
-        elif name.startswith("row_rms"):
+        elif name.startswith("row_rms") or name == "head_rms":
             f0 = float(arg) if arg else 1e-6
             i0 = 1 if name == "row_rms_unrounded" else 0
         ops[i] = N.gemm_epi_op(code, i0, f0)
@@ -122,7 +125,12 @@ def out_cols(program: Sequence[str], N_: int) -> int:
 
 class Plan:
     """One validated GEMM + epilogue plan (gemm_epi_create).  Strides default
-    to tight row-major packing."""
+    to tight row-major packing.
+
+    Programs with head_rms or rotary (a q|k|v projection): columns
+    [0, head_cols) are the heads of q and k, `rotary` holds the frequencies,
+    head size and layout (head_dim alone is enough without the rotary op), and
+    run() takes the rows' positions."""
 
     def __init__(self, M: int, N_: int, K: int, program: Sequence[str], b_layout: str = "kn",
                  lda: Optional[int] = None, ldb: Optional[int] = None, ldc: Optional[int] = None,
@@ -130,7 +138,8 @@ class Plan:
                  batch: int = 1, batch_stride_a: Optional[int] = None,
                  batch_stride_b: Optional[int] = None, batch_stride_c: Optional[int] = None,
                  batch_stride_c8: Optional[int] = None, batch_stride_aux: Optional[int] = None,
-                 a_type: str = "bf16", b_type: str = "bf16"):
+                 a_type: str = "bf16", b_type: str = "bf16", rotary: Optional["Rotary"] = None,
+                 head_dim: Optional[int] = None, head_cols: int = 0):
         self.lib = N.load()
         self.program = list(program)
         self.M, self.N, self.K = M, N_, K
@@ -160,6 +169,15 @@ class Plan:
         self.batch = batch
         d.a_type, d.b_type = OPERAND_TYPES[a_type], OPERAND_TYPES[b_type]
         self.a_type, self.b_type = a_type, b_type
+        self.rotary = rotary
+        if rotary is not None:
+            if head_dim is not None and head_dim != rotary.head_dim:
+                raise ValueError("head_dim %d is not the rotary's %d" % (head_dim, rotary.head_dim))
+            head_dim = rotary.head_dim
+            d.rotary_dim, d.rotary_layout = rotary.rotary_dim, rotary.layout_code
+        elif "rotary" in self.program:
+            raise ValueError("a program with the rotary op needs rotary=")
+        d.head_dim, d.head_cols = head_dim or 0, head_cols
         self.desc = d
         h = N.gemm_epi_handle()
         N.check(self.lib.gemm_epi_create(ctypes.byref(h), ctypes.byref(d)), self.lib)
@@ -176,8 +194,23 @@ class Plan:
     def args(self, A, B, *, alpha=1.0, fp8_scale=1.0, bias=None, row_scale=None, residual=None,
              preact=None, C=None, C8=None, amax=None, row_out=None, col_out=None, workspace=None,
              timeout_ms=0, debug_flags=0, B2=None, a_scale_inv=None, b_scale_inv=None,
-             col_scale=None) -> N.gemm_epi_args:
+             col_scale=None, positions=None) -> N.gemm_epi_args:
         a = N.gemm_epi_args()
+        if self.rotary is not None:
+            if A is not None and self.rotary.steps.device != A.device:
+                raise ValueError("the rotary steps are on %s, A on %s" % (self.rotary.steps.device, A.device))
+            a.rotary_steps, a.rotary_amplitude = self.rotary.steps.data_ptr(), self.rotary.amplitude
+            if positions is not None:
+                if positions.dtype not in (torch.int32, torch.int64):
+                    raise TypeError("positions: expected an int32 or int64 tensor, got %s" % positions.dtype)
+                if not positions.is_contiguous() or positions.numel() != self.batch * self.M:
+                    raise ValueError("positions: expected %d contiguous values, got %s"
+                                     % (self.batch * self.M, tuple(positions.shape)))
+                if A is not None and positions.device != A.device:
+                    raise ValueError("positions are on %s, A on %s" % (positions.device, A.device))
+                a.positions, a.positions_64 = positions.data_ptr(), int(positions.dtype == torch.int64)
+        elif positions is not None:
+            raise ValueError("positions: the plan has no rotary")
         a.A, a.B, a.B2 = _ptr(A), _ptr(B), _ptr(B2)
         a.a_scale_inv, a.b_scale_inv = _ptr(a_scale_inv), _ptr(b_scale_inv)
         a.col_scale = _ptr(col_scale)

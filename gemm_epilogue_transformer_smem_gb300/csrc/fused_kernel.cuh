@@ -51,6 +51,7 @@
 
 #include "gemm_epi.h"
 #include "ptx.cuh"
+#include "rotary.cuh"
 
 namespace ge {
 
@@ -177,6 +178,14 @@ struct KernelParams {
   uint32_t* row_counter;  // workspace: one arrival counter per 128-row block
   uint64_t timeout_ns;
   uint32_t debug_flags;
+  // HEAD_RMS and ROTARY (programs with Prog::heads)
+  int32_t head_cols, head_chunks;  // columns of whole heads; 32-column chunks per head
+  int32_t head_rms_at, rotary_at;  // their indices in ops, or -1
+  int32_t rot_pairs, rot_half;     // rotated pairs per head; 1: pairs (i, i + rot_pairs)
+  float head_inv_dim, head_eps, rot_amplitude;
+  const uint64_t* rot_steps;
+  const void* positions;  // NULL: the row index
+  int32_t positions_64;
   EpiOpDev ops[GEMM_EPI_MAX_OPS];
 };
 
@@ -194,6 +203,14 @@ struct KernelParams {
 
 struct DynamicProgram {
   static constexpr bool is_static = false;
+  static constexpr bool heads = false;
+};
+
+// The interpreter for programs with HEAD_RMS or ROTARY: a kernel of its own,
+// so that what they keep in registers costs the other programs nothing.
+struct DynamicHeadProgram {
+  static constexpr bool is_static = false;
+  static constexpr bool heads = true;
 };
 
 template <int... Ops>
@@ -229,6 +246,12 @@ struct StaticProgram {
       if (code_of(i) == code) return true;
     return false;
   }
+  static constexpr int index_of(int code) {
+    for (int i = 0; i < n; ++i)
+      if (code_of(i) == code) return i;
+    return -1;
+  }
+  static constexpr bool heads = has(GEMM_EPI_OP_HEAD_RMS) || has(GEMM_EPI_OP_ROTARY);
 };
 
 template <int Begin, class F, int... Is>
@@ -258,10 +281,19 @@ template <class Prog>
 __host__ __device__ constexpr int prog_expand_g() {
   if constexpr (Prog::is_static) return Prog::expand_g(); else return 1;
 }
-// First op applied to output columns: after the pair or expanding op.
+// Index of an op of a static program, -1 if it has none.
+template <class Prog>
+__host__ __device__ constexpr int prog_index_of(int code) {
+  if constexpr (Prog::is_static) return Prog::index_of(code); else return -1;
+}
+// First op applied to output columns: after the pair, expanding or head ops.
 template <class Prog>
 __host__ __device__ constexpr int prog_post_begin() {
   if constexpr (Prog::is_static) {
+    if (Prog::heads) {
+      const int n = Prog::index_of(GEMM_EPI_OP_HEAD_RMS), r = Prog::index_of(GEMM_EPI_OP_ROTARY);
+      return (n > r ? n : r) + 1;
+    }
     return Prog::pair_at() >= 0 ? Prog::pair_at() + 1 : Prog::expand_at() >= 0 ? Prog::expand_at() + 1 : 0;
   } else {
     return 0;
@@ -679,6 +711,42 @@ __device__ __forceinline__ void dswiglu_expand(const float (&dh)[16], const floa
   }
 }
 
+// Rotates 32 pairs (a[j], b[j]), pair pair0 + j of the head, by `position`.
+__device__ __forceinline__ void rotate_halves(const KernelParams& p, int64_t position, int pair0, float (&a)[32],
+                                              float (&b)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    float c, s;
+    turn_cos_sin<true>(phase_turns(position, __ldg(p.rot_steps + pair0 + j)), c, s);
+    c *= p.rot_amplitude;
+    s *= p.rot_amplitude;
+    const float x = a[j], y = b[j];
+    a[j] = fmaf(x, c, -(y * s));
+    b[j] = fmaf(y, c, x * s);
+  }
+}
+
+// The same on the 16 pairs inside a 32-column chunk that starts at pair pair0
+// of the head: (2j, 2j + 1) or, HALF, (j, j + 16).  Pairs past the rotated
+// part stay.
+template <bool HALF>
+__device__ __forceinline__ void rotate_chunk(const KernelParams& p, int64_t position, int pair0, float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (pair0 + j < p.rot_pairs) {
+      float c, s;
+      turn_cos_sin<true>(phase_turns(position, __ldg(p.rot_steps + pair0 + j)), c, s);
+      c *= p.rot_amplitude;
+      s *= p.rot_amplitude;
+      float& a = v[HALF ? j : 2 * j];
+      float& b = v[HALF ? j + 16 : 2 * j + 1];
+      const float x = a, y = b;
+      a = fmaf(x, c, -(y * s));
+      b = fmaf(y, c, x * s);
+    }
+  }
+}
+
 // This thread's 32 auxiliary bf16 values of row m, columns col0.. (zeros
 // outside the tensor), straight from global memory.
 __device__ __forceinline__ void load_aux_row(uint4 (&w)[4], const KernelParams& p, const uint16_t* aux,
@@ -1044,7 +1112,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t e80 = sbase + L::OFF_E8 + ew * E8_BUFS * E8_BUF_BYTES;
     uint8_t* epi0_ptr = smem + L::OFF_EPI + ew * EPI_BUFS * EPI_BUF_BYTES;
     uint8_t* e80_ptr = smem + L::OFF_E8 + ew * E8_BUFS * E8_BUF_BYTES;
-    const int op_begin = paired ? pair_at + 1 : expand ? expand_at + 1 : 0;
+    // HEAD_RMS and ROTARY: ops [0, head_first) run on the accumulator, [mid, mid_end)
+    // between the two, the rest after them.
+    const int head_rms_at = kStatic ? prog_index_of<Prog>(GEMM_EPI_OP_HEAD_RMS) : Prog::heads ? p.head_rms_at : -1;
+    const int rotary_at = kStatic ? prog_index_of<Prog>(GEMM_EPI_OP_ROTARY) : Prog::heads ? p.rotary_at : -1;
+    const int op_begin = Prog::heads ? max(head_rms_at, rotary_at) + 1
+                                     : paired ? pair_at + 1 : expand ? expand_at + 1 : 0;
 
     float amax_f = 0.0f;  // max |y| so far; a NaN sticks (NaN wins, as in the integer maximum below)
     uint32_t gchunk = 0;                 // this warp's running chunk number
@@ -1086,9 +1159,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + buf * BLOCK_N;
       float row_ss = 0.0f;
 
-      for (int c = 0; c < chunks; ++c) {
-        const uint32_t g = gchunk + c;
+      // This row's position; the head in hand: its 1 / rms, and the second
+      // chunk of a rotated pair of chunks, until its turn.
+      int64_t position = m;
+      float head_r = 1.0f;
+      float held[Prog::heads ? 32 : 1];
+      if constexpr (Prog::heads) {
+        if (rotary_at >= 0 && p.positions != nullptr && row_ok)
+          position = p.positions_64 ? __ldg(static_cast<const long long*>(p.positions) + row_base + m)
+                                    : __ldg(static_cast<const int*>(p.positions) + row_base + m);
+      }
+
+      for (int ci = 0; ci < chunks; ++ci) {
+        const uint32_t g = gchunk + ci;
         const uint32_t eb = g % EPI_BUFS;
+        // Chunk of the tile: in order, but for the rotated part of a head in
+        // the half layout, whose chunks come in pairs (i, i + half).
+        int c = ci;
+        const int in_head = Prog::heads ? ci & (p.head_chunks - 1) : 0;
+        const int rot_half_chunks = Prog::heads && p.rot_half && rotary_at >= 0 ? p.rot_pairs >> 5 : 0;
+        const bool in_pair = Prog::heads && nacc0 + ci * CHUNK < p.head_cols && in_head < 2 * rot_half_chunks;
+        if (Prog::heads && in_pair) c = ci - in_head + (in_head >> 1) + (in_head & 1) * rot_half_chunks;
         const int col0 = n0 + c * CHUNK;  // first output column of the chunk
         float v[32];
 
@@ -1115,6 +1206,87 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             });
           } else {
             for (int i = 0; i < expand_at; ++i) apply_pointwise<16>(p.ops[i].code, dh, p, nacc0 + c * 16, p.N, rs_m);
+          }
+        } else if constexpr (Prog::heads) {
+          const int head_first = head_rms_at >= 0 ? head_rms_at : rotary_at;
+          // Accumulator chunk cc with the ops before HEAD_RMS (and ROTARY).
+          auto load_acc = [&](int cc, float (&u)[32]) {
+            if (flags & F_ZERO_ACC) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) u[j] = 0.0f;
+            } else {
+              uint32_t r[32];
+              ptx::tmem_ld32_sync(t_row + cc * 32, r);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) u[j] = __uint_as_float(r[j]);
+              if (flags & F_DEQ) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) u[j] *= deq;
+              }
+            }
+            if constexpr (kStatic) {
+              constexpr int n = prog_index_of<Prog>(GEMM_EPI_OP_HEAD_RMS), r = prog_index_of<Prog>(GEMM_EPI_OP_ROTARY);
+              static_for<0, (n >= 0 ? n : r)>([&](auto I) {
+                apply_pointwise<32>(std::integral_constant<int, Prog::code_of(decltype(I)::value)>{}, u, p,
+                                    nacc0 + cc * 32, p.N, rs_m);
+              });
+            } else {
+              for (int i = 0; i < head_first; ++i) apply_pointwise<32>(p.ops[i].code, u, p, nacc0 + cc * 32, p.N, rs_m);
+            }
+          };
+          // What follows it up to ROTARY: the head's 1 / rms (1 where there is
+          // no head) and the ops between the two.
+          auto scale_acc = [&](int cc, float (&u)[32]) {
+            if (head_rms_at >= 0) {
+              const float2 r2 = splat2(head_r);
+              for_pairs(u, [&](float2 y, int) { return __fmul2_rn(y, r2); });
+              if constexpr (kStatic) {
+                constexpr int n = prog_index_of<Prog>(GEMM_EPI_OP_HEAD_RMS),
+                              r = prog_index_of<Prog>(GEMM_EPI_OP_ROTARY);
+                static_for<(n >= 0 && r >= 0 ? n + 1 : 0), (n >= 0 && r >= 0 ? r : 0)>([&](auto I) {
+                  apply_pointwise<32>(std::integral_constant<int, Prog::code_of(decltype(I)::value)>{}, u, p,
+                                      nacc0 + cc * 32, p.N, rs_m);
+                });
+              } else {
+                for (int i = head_rms_at + 1; i < rotary_at; ++i)
+                  apply_pointwise<32>(p.ops[i].code, u, p, nacc0 + cc * 32, p.N, rs_m);
+              }
+            }
+          };
+          const bool head = nacc0 + ci * CHUNK < p.head_cols;  // the same for every chunk of a head
+          if (head_rms_at >= 0 && in_head == 0) {
+            // A row of the head is in this thread's TMEM lane, so its sum of
+            // squares is a first pass over the head's chunks.
+            head_r = 1.0f;
+            if (head) {
+              float2 ss = make_float2(0.0f, 0.0f);
+              for (int k = 0; k < p.head_chunks; ++k) {
+                load_acc(ci + k, v);
+                for_pairs(v, [&](float2 y, int) {
+                  ss = __ffma2_rn(y, y, ss);
+                  return y;
+                });
+              }
+              head_r = 1.0f / sqrtf(fmaf(ss.x + ss.y, p.head_inv_dim, p.head_eps));
+            }
+          }
+          if (in_pair && (in_head & 1)) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = held[j];
+          } else {
+            load_acc(c, v);
+            scale_acc(c, v);
+            if (rotary_at >= 0 && head) {
+              if (in_pair) {
+                load_acc(c + rot_half_chunks, held);
+                scale_acc(c + rot_half_chunks, held);
+                rotate_halves(p, position, (in_head >> 1) * 32, v, held);
+              } else if (p.rot_half) {
+                if (in_head == 0 && p.rot_pairs == 16) rotate_chunk<true>(p, position, 0, v);
+              } else {
+                rotate_chunk<false>(p, position, in_head * 16, v);
+              }
+            }
           }
         } else if (!paired) {
           if (flags & F_ZERO_ACC) {
@@ -1168,7 +1340,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // (Compiled programs without a pair or expanding op, whose output
         // chunk c sits in accumulator columns 32c..32c+31; the interpreter
         // keeps the shuffle form, which needs no extra registers.)
-        const bool tmem_col_sums = kStatic && (flags & F_COL) && !expand && !paired;
+        const bool tmem_col_sums = kStatic && (flags & F_COL) && !expand && !paired && !Prog::heads;
         auto release_accumulator = [&]() {
           ptx::tc_fence_before_sync();
           __syncwarp();
@@ -1179,7 +1351,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               ptx::mbar_arrive_cluster(ptx::mapa_shared(bar(BAR_TEMPTY + buf), 0));
           }
         };
-        if (c == chunks - 1 && !tmem_col_sums) release_accumulator();
+        if (ci == chunks - 1 && !tmem_col_sums) release_accumulator();
 
         // ---- auxiliary tile (residual / pre-activation), this thread's row
         float x[32];
@@ -1346,7 +1518,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         } else {
           for (int i = op_begin; i < p.n_ops; ++i) run_op(p.ops[i].code);
         }
-        if (c == chunks - 1 && tmem_col_sums) release_accumulator();
+        if (ci == chunks - 1 && tmem_col_sums) release_accumulator();
 
         // ---- TMA stores of this chunk's staged outputs
         if (flags & (F_STORE | F_E8)) {

@@ -84,7 +84,7 @@ struct SpecTable {
 };
 const SpecTable kSpecTables[] = {
     {ge::kSpecsForward, &ge::kNumSpecsForward}, {ge::kSpecsAux, &ge::kNumSpecsAux}, {ge::kSpecsFp8, &ge::kNumSpecsFp8},
-    {ge::kSpecsCommon, &ge::kNumSpecsCommon}};
+    {ge::kSpecsCommon, &ge::kNumSpecsCommon}, {ge::kSpecsHeads, &ge::kNumSpecsHeads}};
 constexpr int kNumSpecTables = sizeof(kSpecTables) / sizeof(kSpecTables[0]);
 
 // The interpreting kernels (any program); static ones come from the tables.
@@ -116,6 +116,9 @@ gemm_epi_status device_state(DeviceState** out, int* dev_out) {
       e = cudaFuncSetAttribute(kDynamic1, cudaFuncAttributeMaxDynamicSharedMemorySize, ge::Smem<1>::BYTES);
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kDynamic2, cudaFuncAttributeMaxDynamicSharedMemorySize, ge::Smem<2>::BYTES);
+      for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+        e = cudaFuncSetAttribute(ge::kDynamicHeads[i / 2][i % 2], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 i % 2 == 0 ? ge::Smem<1>::BYTES : ge::Smem<2>::BYTES);
       for (int c = 0; c < 2 && e == cudaSuccess; ++c)
         e = cudaFuncSetAttribute(ge::kDynamicFp8[c], cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  c == 0 ? ge::Smem<1>::BYTES : ge::Smem<2>::BYTES);
@@ -259,6 +262,9 @@ struct gemm_epi_plan {
   uint32_t flags = 0;
   bool uses_bias = false, uses_row_scale = false, uses_residual = false, uses_preact = false;
   bool uses_col_scale = false;
+  int head_rms_at = -1, rotary_at = -1;
+  float head_eps = 0.0f;
+  bool heads() const { return head_rms_at >= 0 || rotary_at >= 0; }
   float rms_eps = 0.0f;
   int rms_unrounded = 0;
   int64_t num_m_tiles = 0, num_n_tiles = 0;
@@ -295,7 +301,7 @@ gemm_epi_status validate(gemm_epi_plan& P) {
   int seen[32] = {0};  // indexed by op code
   for (int i = 0; i < d.n_ops; ++i) {
     const gemm_epi_op& op = d.ops[i];
-    if (op.code < GEMM_EPI_OP_SCALE_ALPHA || op.code > GEMM_EPI_OP_ROW_DOT)
+    if (op.code < GEMM_EPI_OP_SCALE_ALPHA || op.code > GEMM_EPI_OP_ROTARY)
       return fail(GEMM_EPI_ERR_INVALID_VALUE, "op %d: unknown code %d", i, op.code);
     if (is_output_op(op.code) && seen[op.code])
       return fail(GEMM_EPI_ERR_INVALID_VALUE, "op %d: output op %d appears twice", i, op.code);
@@ -350,6 +356,21 @@ gemm_epi_status validate(gemm_epi_plan& P) {
         P.pair_silu = op.code == GEMM_EPI_OP_PAIR_SWIGLU ? 1 : 0;
         break;
       }
+      case GEMM_EPI_OP_HEAD_RMS:
+      case GEMM_EPI_OP_ROTARY: {
+        if (seen[op.code] > 1) return fail(GEMM_EPI_ERR_INVALID_VALUE, "op %d: HEAD_RMS or ROTARY appears twice", i);
+        const bool norm = op.code == GEMM_EPI_OP_HEAD_RMS;
+        if (norm && P.rotary_at >= 0) return fail(GEMM_EPI_ERR_UNSUPPORTED, "HEAD_RMS after ROTARY");
+        for (int j = 0; j < i; ++j)
+          if (!is_pre_pair_op(d.ops[j].code) && j != P.head_rms_at)
+            return fail(GEMM_EPI_ERR_UNSUPPORTED, "op %d (code %d) before HEAD_RMS or ROTARY is not supported", j,
+                        d.ops[j].code);
+        if (norm && (!(op.f0 >= 0.0f) || !std::isfinite(op.f0)))
+          return fail(GEMM_EPI_ERR_INVALID_VALUE, "HEAD_RMS eps must be finite and >= 0");
+        (norm ? P.head_rms_at : P.rotary_at) = i;
+        if (norm) P.head_eps = op.f0;
+        break;
+      }
       case GEMM_EPI_OP_ROW_RMS_RSQRT:
         if (!(op.f0 >= 0.0f) || !std::isfinite(op.f0))
           return fail(GEMM_EPI_ERR_INVALID_VALUE, "ROW_RMS_RSQRT eps must be finite and >= 0");
@@ -372,6 +393,25 @@ gemm_epi_status validate(gemm_epi_plan& P) {
       case GEMM_EPI_OP_STORE_E4M3: P.flags |= ge::F_E8; break;
       case GEMM_EPI_OP_COL_SUM: P.flags |= ge::F_COL; break;
       default: break;
+    }
+  }
+  if (P.heads()) {
+    if (P.pair_at >= 0 || P.expand_at >= 0 || P.uses_residual || P.uses_preact || P.dual)
+      return fail(GEMM_EPI_ERR_UNSUPPORTED, "HEAD_RMS and ROTARY go with no pair op, DSWIGLU, GEMM_EPI_B_DUAL or "
+                                            "op that reads residual or preact");
+    if (d.head_dim != 32 && d.head_dim != 64 && d.head_dim != 128 && d.head_dim != 256)
+      return fail(GEMM_EPI_ERR_UNSUPPORTED, "head_dim %d: HEAD_RMS and ROTARY run on heads of 32, 64, 128 or 256 "
+                                            "columns (gemm_epi_qk_norm_rotary takes the others)", d.head_dim);
+    if (d.head_cols < 0 || d.head_cols > d.N || d.head_cols % d.head_dim)
+      return fail(GEMM_EPI_ERR_INVALID_VALUE, "head_cols must be a multiple of head_dim, at most N");
+    if (P.rotary_at >= 0) {
+      if (d.rotary_layout != GEMM_EPI_ROTARY_HALF && d.rotary_layout != GEMM_EPI_ROTARY_INTERLEAVED)
+        return fail(GEMM_EPI_ERR_INVALID_VALUE, "unknown rotary layout %d", d.rotary_layout);
+      if (d.rotary_dim < 2 || d.rotary_dim > d.head_dim || d.rotary_dim % 2)
+        return fail(GEMM_EPI_ERR_INVALID_VALUE, "rotary_dim must be even, in [2, head_dim] (got %d)", d.rotary_dim);
+      if (d.rotary_layout == GEMM_EPI_ROTARY_HALF && d.rotary_dim != 32 && d.rotary_dim % 64)
+        return fail(GEMM_EPI_ERR_UNSUPPORTED, "ROTARY in the half layout needs rotary_dim 32 or a multiple of 64 "
+                                              "(gemm_epi_rotary takes the others)");
     }
   }
   if (P.uses_residual && P.uses_preact)
@@ -487,6 +527,8 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
   L.cg = choose_cta_group(P, a, dev);
   if (P.spec && !(a.debug_flags & GEMM_EPI_DEBUG_FORCE_INTERPRETER))
     L.kernel = L.cg == 2 ? P.spec->kernel_2sm : P.spec->kernel_1sm;
+  else if (P.heads())
+    L.kernel = ge::kDynamicHeads[P.in8 ? 1 : 0][L.cg == 2 ? 1 : 0];
   else if (P.in8)
     L.kernel = ge::kDynamicFp8[L.cg == 2 ? 1 : 0];
   else
@@ -558,6 +600,20 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
   k.row_counter = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.workspace) + WS_HEADER);
   k.timeout_ns = static_cast<uint64_t>(a.timeout_ms ? a.timeout_ms : DEFAULT_TIMEOUT_MS) * 1000000ull;
   k.debug_flags = a.debug_flags;
+  k.head_rms_at = P.head_rms_at;
+  k.rotary_at = P.rotary_at;
+  if (P.heads()) {
+    k.head_cols = static_cast<int32_t>(d.head_cols);
+    k.head_chunks = d.head_dim / ge::CHUNK;
+    k.head_inv_dim = 1.0f / static_cast<float>(d.head_dim);
+    k.head_eps = P.head_eps;
+    k.rot_pairs = d.rotary_dim / 2;
+    k.rot_half = d.rotary_layout == GEMM_EPI_ROTARY_HALF ? 1 : 0;
+    k.rot_amplitude = a.rotary_amplitude;
+    k.rot_steps = a.rotary_steps;
+    k.positions = a.positions;
+    k.positions_64 = a.positions_64 ? 1 : 0;
+  }
   for (size_t i = 0; i < P.ops.size(); ++i) {
     k.ops[i].code = P.ops[i].code;
     k.ops[i].i0 = P.ops[i].i0;
@@ -634,6 +690,14 @@ gemm_epi_status check_args(const gemm_epi_plan& P, const gemm_epi_args& a) {
     if (P.uses_row_scale && (s = need(a.row_scale, "row_scale"))) return s;
     if (P.uses_residual && (s = need(a.residual, "residual"))) return s;
     if (P.uses_preact && (s = need(a.preact, "preact"))) return s;
+    if (P.rotary_at >= 0) {
+      if (!a.rotary_steps) return fail(GEMM_EPI_ERR_INVALID_VALUE, "rotary_steps is NULL but the program uses it");
+      if ((reinterpret_cast<uintptr_t>(a.rotary_steps) & 7u) ||
+          (reinterpret_cast<uintptr_t>(a.positions) & (a.positions_64 ? 7u : 3u)))
+        return fail(GEMM_EPI_ERR_MISALIGNED, "rotary_steps or positions is not aligned to its element size");
+      if (!std::isfinite(a.rotary_amplitude))
+        return fail(GEMM_EPI_ERR_INVALID_VALUE, "rotary_amplitude must be finite");
+    }
   }
   if ((P.flags & ge::F_AMAX) && (s = need(a.amax, "amax"))) return s;
   for (const float* sc : {a.a_scale_inv, a.b_scale_inv})
@@ -739,6 +803,9 @@ gemm_epi_status gemm_epi_run_unfused(gemm_epi_handle h, const gemm_epi_args* arg
   if (h->pair_at >= 0 && h->pair_g > 8)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "the separate pass handles pair groups up to 8");
   if (h->batch > 1) return fail(GEMM_EPI_ERR_UNSUPPORTED, "the separate pass runs single problems");
+  if (h->heads())
+    return fail(GEMM_EPI_ERR_UNSUPPORTED, "the separate pass has no HEAD_RMS or ROTARY: run the GEMM and "
+                                          "gemm_epi_qk_norm_rotary or gemm_epi_rotary");
   if (h->expand_at >= 0 && h->expand_g > 4)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "the separate pass handles DSWIGLU groups up to 4");
   DeviceState* dev = nullptr;

@@ -59,6 +59,13 @@ using ProgGeluGrad = StaticProgram<GEMM_EPI_OP_MUL_GELU_TANH_GRAD, GEMM_EPI_OP_S
 using ProgAlpha = StaticProgram<GEMM_EPI_OP_SCALE_ALPHA, GEMM_EPI_OP_STORE_BF16>;
 using ProgRowScale = StaticProgram<GEMM_EPI_OP_MUL_ROW_SCALE, GEMM_EPI_OP_STORE_BF16>;
 
+// Projections of queries and keys: each head's norm with its weights as a
+// column scale, rotary positions, bf16 store.
+using ProgRotary = StaticProgram<GEMM_EPI_OP_ROTARY, GEMM_EPI_OP_STORE_BF16>;
+using ProgBiasRotary = StaticProgram<GEMM_EPI_OP_ADD_BIAS_COL, GEMM_EPI_OP_ROTARY, GEMM_EPI_OP_STORE_BF16>;
+using ProgNormRotary = StaticProgram<GEMM_EPI_OP_HEAD_RMS, GEMM_EPI_OP_MUL_COL_SCALE, GEMM_EPI_OP_ROTARY,
+                                     GEMM_EPI_OP_STORE_BF16>;
+
 // One compiled program: its op list (code | pair group << 8), the operand
 // width it was compiled for, its kernels for the 1-SM and 2-SM main loops and
 // its separate-pass kernel for the unfused baseline (NULL if the pass does
@@ -98,6 +105,11 @@ extern const KernelSpec kSpecsFp8[];
 extern const int kNumSpecsFp8;
 extern const KernelSpec kSpecsCommon[];
 extern const int kNumSpecsCommon;
+extern const KernelSpec kSpecsHeads[];
+extern const int kNumSpecsHeads;
+// The interpreting kernels for programs with HEAD_RMS or ROTARY, for bf16 and
+// 8-bit operands (1-SM, 2-SM), from the same translation unit as kSpecsHeads.
+extern const void* const kDynamicHeads[2][2];
 // The interpreting kernels for 8-bit operands (1-SM, 2-SM), from the same
 // translation unit as kSpecsFp8.
 extern const void* const kDynamicFp8[2];

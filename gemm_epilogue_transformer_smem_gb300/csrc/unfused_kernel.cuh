@@ -347,10 +347,13 @@ __global__ void __launch_bounds__(UF_THREADS)
 }
 
 // The separate pass of a static program, or NULL where the pass does not
-// cover the program (pair groups above 8, DSWIGLU groups above 4).
+// cover the program (pair groups above 8, DSWIGLU groups above 4, HEAD_RMS
+// and ROTARY, which have passes of their own).
 template <class Prog>
 inline const void* unfused_kernel_for() {
   if constexpr (Prog::pair_at() >= 0 && Prog::pair_g() > 8) {
+    return nullptr;
+  } else if constexpr (Prog::heads) {
     return nullptr;
   } else if constexpr (Prog::expand_at() >= 0 && Prog::expand_g() > 4) {
     return nullptr;

@@ -64,6 +64,8 @@ GEMM_EPI_OP_PAIR_MUL = 15
 GEMM_EPI_OP_DSWIGLU = 16
 GEMM_EPI_OP_MUL_COL_SCALE = 17
 GEMM_EPI_OP_ROW_DOT = 18
+GEMM_EPI_OP_HEAD_RMS = 19
+GEMM_EPI_OP_ROTARY = 20
 
 GEMM_EPI_MAX_OPS = 16
 GEMM_EPI_DEBUG_SKIP_FIRST_LOAD = 1
@@ -90,6 +92,8 @@ class gemm_epi_desc(ctypes.Structure):
         ("batch_stride_c", ctypes.c_int64), ("batch_stride_c8", ctypes.c_int64),
         ("batch_stride_aux", ctypes.c_int64),
         ("a_type", ctypes.c_int32), ("b_type", ctypes.c_int32),
+        ("head_cols", ctypes.c_int64), ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32), ("rotary_layout", ctypes.c_int32),
     ]
 
 
@@ -106,6 +110,8 @@ class gemm_epi_args(ctypes.Structure):
         ("B2", ctypes.c_void_p),
         ("a_scale_inv", ctypes.c_void_p), ("b_scale_inv", ctypes.c_void_p),
         ("col_scale", ctypes.c_void_p),
+        ("rotary_steps", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("positions_64", ctypes.c_int32), ("rotary_amplitude", ctypes.c_float),
     ]
 
 

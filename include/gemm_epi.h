@@ -6,7 +6,8 @@
  * and, while each output tile is still on chip, runs a
  * short epilogue program on it: scaling, bias, row scale, residual add,
  * activations, a pairwise SwiGLU on interleaved gate/up columns, the GELU-tanh
- * derivative, AMAX, row RMS statistics, column sums, and bf16 / FP8-e4m3
+ * derivative, AMAX, row RMS statistics, column sums, the norm and rotary
+ * positions of a projection's heads, and bf16 / FP8-e4m3
  * stores.  Only the program's outputs reach global memory.
  *
  * Where the operations come from (page title, section):
@@ -180,11 +181,23 @@ typedef enum gemm_epi_op_code {
                                            op may read preact or residual.  Counts as the
                                            program's pair op.                               */
     GEMM_EPI_OP_MUL_COL_SCALE = 17,     /* y = y * col_scale[n]     (args.col_scale)        */
-    GEMM_EPI_OP_ROW_DOT = 18            /* row_out[m] = sum over n of y * residual[m, n]
+    GEMM_EPI_OP_ROW_DOT = 18,           /* row_out[m] = sum over n of y * residual[m, n]
                                            (args.residual): the row reduction of the
                                            RMSNorm backward, finished by
                                            gemm_epi_rmsnorm_backward.  Not with
                                            ROW_RMS_RSQRT (both write row_out).              */
+    GEMM_EPI_OP_HEAD_RMS = 19,          /* columns n < desc.head_cols, in heads of desc.head_dim:
+                                           y = y / sqrt(mean of y^2 over the head + f0), f0 = eps */
+    GEMM_EPI_OP_ROTARY = 20             /* the same columns: the first desc.rotary_dim values of
+                                           each head rotated in pairs by the row's position, as
+                                           gemm_epi_rotary does (args.rotary_steps, positions,
+                                           rotary_amplitude).  HEAD_RMS and ROTARY appear at most
+                                           once each, HEAD_RMS first; only SCALE_ALPHA,
+                                           ADD_BIAS_COL, MUL_COL_SCALE, MUL_ROW_SCALE and the
+                                           activations may come before either (after HEAD_RMS a
+                                           column scale holds the norm's weight of every column,
+                                           1 past head_cols).  Not with a pair op, DSWIGLU,
+                                           GEMM_EPI_B_DUAL or ops reading residual or preact.    */
 } gemm_epi_op_code;
 
 typedef struct gemm_epi_op {
@@ -214,6 +227,14 @@ typedef struct gemm_epi_desc {
     int64_t batch;
     int64_t batch_stride_a, batch_stride_b, batch_stride_c, batch_stride_c8, batch_stride_aux;
     int32_t a_type, b_type;   /* gemm_epi_type of A and of B (and B2); 0 = BF16 */
+    /* HEAD_RMS and ROTARY: a q|k|v projection's columns.  A head lies in one
+     * 256-column tile, and the two halves of a rotated part in whole 32-column
+     * chunks or in one; gemm_epi_rotary and gemm_epi_qk_norm_rotary take every
+     * other size from the stored projection. */
+    int64_t head_cols;        /* columns [0, head_cols) are heads (q and k); a multiple of head_dim, <= N */
+    int32_t head_dim;         /* 32, 64, 128 or 256 */
+    int32_t rotary_dim;       /* ROTARY: half layout 32 or a multiple of 64, interleaved even; <= head_dim */
+    int32_t rotary_layout;    /* gemm_epi_rotary_layout */
 } gemm_epi_desc;
 
 typedef struct gemm_epi_args {
@@ -244,6 +265,10 @@ typedef struct gemm_epi_args {
     const float *a_scale_inv;
     const float *b_scale_inv;
     const float *col_scale;   /* MUL_COL_SCALE: fp32, one value per column at its point of use */
+    const uint64_t *rotary_steps;  /* ROTARY: device, rotary_dim / 2 values of gemm_epi_rotary_steps */
+    const void *positions;    /* ROTARY: device int32 / int64, M values per batch; NULL: row m is at position m */
+    int32_t positions_64;     /* 1: int64 positions */
+    float rotary_amplitude;   /* ROTARY: factor of the rotated part, usually 1 */
 } gemm_epi_args;
 
 /* Test hook: the first CTA's producer skips the operand loads of the first

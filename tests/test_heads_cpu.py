@@ -226,3 +226,83 @@ def test_reference_gradients_against_differences(layout):
     # the inverse rotation is the rotation's transpose
     lhs, rhs = (ang.rotate(x) * dy).sum(), (x * ang.rotate(dy, inverse=True)).sum()
     assert abs(lhs - rhs).item() < 1e-12 * x.numel()
+
+
+def create(lib, program, N_=512, **kw):
+    ops = api.encode_program(list(program))
+    d = N.gemm_epi_desc(M=64, N=N_, K=64, lda=64, ldb=kw.pop("ldb", 64), ldc=2 * N_, ldc8=2 * N_, ld_aux=2 * N_,
+                        b_layout=kw.pop("b_layout", N.GEMM_EPI_B_NK), n_ops=len(program),
+                        ops=ctypes.cast(ops, ctypes.POINTER(N.gemm_epi_op)))
+    d.head_dim, d.head_cols, d.rotary_dim = 128, 384, 128
+    for k, v in kw.items():
+        setattr(d, k, v)
+    h = N.gemm_epi_handle()
+    s = lib.gemm_epi_create(ctypes.byref(h), ctypes.byref(d))
+    if s == N.GEMM_EPI_OK:
+        lib.gemm_epi_destroy(h)
+    return s
+
+
+NORM = ("head_rms:1e-5", "col_scale", "rotary", "store_bf16")
+
+
+@pytest.mark.parametrize("program,kw", [
+    (NORM, {}), (NORM, dict(head_cols=0)), (NORM, dict(head_cols=512)), (("rotary",), dict(rotary_dim=64)),
+    (("rotary", "store_bf16"), dict(rotary_dim=32)), (("rotary", "store_bf16"), dict(rotary_dim=2, rotary_layout=1)),
+    (("head_rms", "store_bf16"), dict(rotary_dim=0)), (("bias", "alpha", "gelu_tanh", "rotary", "store_bf16"), {}),
+    (("rotary", "amax", "store_bf16", "store_e4m3", "col_sum", "row_rms"), {}),
+])
+def test_create_accepts_head_programs(lib, program, kw):
+    assert create(lib, program, **kw) == N.GEMM_EPI_OK, lib.gemm_epi_last_error()
+
+
+@pytest.mark.parametrize("program,kw,status", [
+    (NORM, dict(head_dim=96, head_cols=96), UNS), (NORM, dict(head_dim=0), UNS), (NORM, dict(head_dim=512, head_cols=512), UNS),
+    (NORM, dict(head_cols=100), BAD), (NORM, dict(head_cols=640), BAD), (NORM, dict(head_cols=-128), BAD),
+    (NORM, dict(rotary_layout=2), BAD), (NORM, dict(rotary_dim=0), BAD), (NORM, dict(rotary_dim=130), BAD),
+    (NORM, dict(rotary_dim=63), BAD), (NORM, dict(rotary_dim=96), UNS), (NORM, dict(rotary_dim=48), UNS),
+    (("head_rms:-1", "store_bf16"), {}, BAD), (("head_rms:nan", "store_bf16"), {}, BAD),
+    (("head_rms", "head_rms", "store_bf16"), {}, BAD), (("rotary", "rotary", "store_bf16"), {}, BAD),
+    (("rotary", "head_rms", "store_bf16"), {}, UNS), (("store_bf16", "rotary"), {}, UNS),
+    (("residual", "rotary", "store_bf16"), {}, UNS), (("rotary", "residual", "store_bf16"), {}, UNS),
+    (("rotary", "gelu_tanh_grad", "store_bf16"), {}, UNS), (("rotary", "store_bf16", "row_dot"), {}, UNS),
+    (("pair_swiglu", "rotary", "store_bf16"), {}, UNS), (("rotary", "pair_swiglu", "store_bf16"), {}, UNS),
+    (("rotary", "dswiglu", "store_bf16"), {}, UNS), (("dswiglu", "rotary", "store_bf16"), {}, UNS),
+    (NORM, dict(b_layout=N.GEMM_EPI_B_NK | N.GEMM_EPI_B_DUAL), UNS),
+])
+def test_create_rejects_head_programs(lib, program, kw, status):
+    assert create(lib, program, **kw) == status, lib.gemm_epi_last_error()
+    assert lib.gemm_epi_last_error()
+
+
+def test_plan_checks_rotary_and_positions(lib):
+    rope = api.Rotary(64, device="cpu")
+    with pytest.raises(ValueError, match="needs rotary="):
+        api.Plan(64, 256, 64, ["rotary", "store_bf16"], head_dim=64, head_cols=128)
+    with pytest.raises(ValueError, match="not the rotary's"):
+        api.Plan(64, 256, 64, ["rotary", "store_bf16"], rotary=rope, head_dim=128, head_cols=128)
+    plan = api.Plan(64, 256, 64, ["rotary", "store_bf16"], rotary=rope, head_cols=128)
+    A, B = torch.zeros(64, 64, dtype=torch.bfloat16), torch.zeros(64, 256, dtype=torch.bfloat16)
+    C, ws = torch.zeros(64, 256, dtype=torch.bfloat16), torch.zeros(plan.workspace_bytes, dtype=torch.uint8)
+    pos = torch.zeros(64, dtype=torch.int32)
+    a = plan.args(A, B, C=C, workspace=ws, positions=pos)
+    assert a.positions == pos.data_ptr() and a.positions_64 == 0 and a.rotary_amplitude == 1.0
+    for bad, kind in ((pos.float(), TypeError), (pos[:32], ValueError), (torch.zeros(128, dtype=torch.int32)[::2], ValueError)):
+        with pytest.raises(kind, match="positions"):
+            plan.args(A, B, C=C, workspace=ws, positions=bad)
+    bare = api.Plan(64, 256, 64, ["store_bf16"])
+    with pytest.raises(ValueError, match="no rotary"):
+        bare.args(A, B, C=C, workspace=ws, positions=pos)
+    # everything given: stops only at the missing GPU; the separate pass has no such ops
+    with pytest.raises(N.GemmEpiError) as err:
+        plan.run(A, B, C=C, workspace=ws, positions=pos, stream=FakeStream())
+    assert err.value.status in (N.GEMM_EPI_ERR_CUDA, N.GEMM_EPI_ERR_ARCH), str(err.value)
+    with pytest.raises(N.GemmEpiError) as err:
+        plan.run_unfused(A, B, C=C, workspace=ws, positions=pos, scratch=torch.zeros_like(C), stream=FakeStream())
+    assert err.value.status == UNS
+    # the C ABI's own checks of the pointers
+    for field, value, status in (("rotary_steps", None, BAD), ("rotary_steps", rope.steps.data_ptr() + 4, MIS),
+                                 ("positions", pos.data_ptr() + 2, MIS), ("rotary_amplitude", float("inf"), BAD)):
+        a = plan.args(A, B, C=C, workspace=ws, positions=pos)
+        setattr(a, field, value)
+        assert lib.gemm_epi_run(plan.handle, ctypes.byref(a), None) == status, field
