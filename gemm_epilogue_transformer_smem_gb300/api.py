@@ -13,6 +13,7 @@ colon):
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -62,8 +63,17 @@ def encode_program(program: Sequence[str]):
     return ops
 
 
+# The current stream of a device as an integer, without the stream object that
+# torch.cuda.current_stream() builds (2.9 us of a small call's 7).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
+
+
+_KIND_DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 
 def _bytes_after(t: torch.Tensor) -> int:
@@ -184,6 +194,7 @@ class Plan:
         self.handle = h
         self.n_out = int(self.lib.gemm_epi_out_cols(h))
         self.workspace_bytes = int(self.lib.gemm_epi_workspace_size(h))
+        self._extents = self._operand_extents()
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -196,63 +207,70 @@ class Plan:
              timeout_ms=0, debug_flags=0, B2=None, a_scale_inv=None, b_scale_inv=None,
              col_scale=None, positions=None) -> N.gemm_epi_args:
         a = N.gemm_epi_args()
+        a.alpha, a.fp8_scale = alpha, fp8_scale
+        for name, t in (("A", A), ("B", B), ("B2", B2), ("bias", bias), ("row_scale", row_scale),
+                        ("residual", residual), ("preact", preact), ("C", C), ("C8", C8), ("amax", amax),
+                        ("row_out", row_out), ("col_out", col_out), ("a_scale_inv", a_scale_inv),
+                        ("b_scale_inv", b_scale_inv), ("col_scale", col_scale)):
+            if t is not None:
+                kind, elements, extent = self._extents[name]
+                # A contiguous tensor of the right type and size needs no look at its storage.
+                if (t.dtype is not _KIND_DTYPE.get(kind) or t.numel() < elements or not t.is_contiguous()):
+                    _expect(name, t, kind, *extent)
+                setattr(a, name, t.data_ptr())
+        if workspace is not None:
+            a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        if timeout_ms or debug_flags:
+            a.timeout_ms, a.debug_flags = int(timeout_ms), int(debug_flags)
         if self.rotary is not None:
-            if A is not None and self.rotary.steps.device != A.device:
+            index = self.rotary.index
+            if A is not None and index != A.get_device():
                 raise ValueError("the rotary steps are on %s, A on %s" % (self.rotary.steps.device, A.device))
-            a.rotary_steps, a.rotary_amplitude = self.rotary.steps.data_ptr(), self.rotary.amplitude
+            a.rotary_steps, a.rotary_amplitude = self.rotary.steps_ptr, self.rotary.amplitude
             if positions is not None:
-                if positions.dtype not in (torch.int32, torch.int64):
+                if positions.dtype is not torch.int32 and positions.dtype is not torch.int64:
                     raise TypeError("positions: expected an int32 or int64 tensor, got %s" % positions.dtype)
-                if not positions.is_contiguous() or positions.numel() != self.batch * self.M:
+                if positions.numel() != self.batch * self.M or not positions.is_contiguous():
                     raise ValueError("positions: expected %d contiguous values, got %s"
                                      % (self.batch * self.M, tuple(positions.shape)))
-                if A is not None and positions.device != A.device:
-                    raise ValueError("positions are on %s, A on %s" % (positions.device, A.device))
-                a.positions, a.positions_64 = positions.data_ptr(), int(positions.dtype == torch.int64)
+                if positions.get_device() != index:
+                    raise ValueError("positions are on %s, the rotary steps on %s"
+                                     % (positions.device, self.rotary.steps.device))
+                a.positions, a.positions_64 = positions.data_ptr(), 1 if positions.dtype is torch.int64 else 0
         elif positions is not None:
             raise ValueError("positions: the plan has no rotary")
-        a.A, a.B, a.B2 = _ptr(A), _ptr(B), _ptr(B2)
-        a.a_scale_inv, a.b_scale_inv = _ptr(a_scale_inv), _ptr(b_scale_inv)
-        a.col_scale = _ptr(col_scale)
-        a.alpha, a.fp8_scale = float(alpha), float(fp8_scale)
-        a.bias, a.row_scale = _ptr(bias), _ptr(row_scale)
-        a.residual, a.preact = _ptr(residual), _ptr(preact)
-        a.C, a.C8 = _ptr(C), _ptr(C8)
-        a.amax, a.row_out, a.col_out = _ptr(amax), _ptr(row_out), _ptr(col_out)
-        a.workspace = _ptr(workspace)
-        a.workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        a.timeout_ms, a.debug_flags = int(timeout_ms), int(debug_flags)
-        self._check(A, B, B2, bias, row_scale, residual, preact, C, C8, amax, row_out, col_out,
-                    a_scale_inv, b_scale_inv, col_scale)
         return a
 
-    def _check(self, A, B, B2, bias, row_scale, residual, preact, C, C8, amax, row_out, col_out,
-               a_scale_inv, b_scale_inv, col_scale):
+    def _operand_extents(self):
+        """What _expect() needs of each tensor, and the elements from its first
+        to its last: {name: (kind, elements, (rows, cols, ld, batch, batch_stride))}."""
         d, M, K, Bt = self.desc, self.M, self.K, self.batch
         op_kind = lambda t: "bf16" if t == "bf16" else "byte"  # noqa: E731
         b_cols = self.N // 2 if self.dual else self.N
         b_rows, b_inner = (K, b_cols) if self.b_layout == "kn" else (b_cols, K)
-        _expect("A", A, op_kind(self.a_type), M, K, d.lda, Bt, d.batch_stride_a)
-        _expect("B", B, op_kind(self.b_type), b_rows, b_inner, d.ldb, Bt, d.batch_stride_b)
-        _expect("B2", B2, op_kind(self.b_type), b_rows, b_inner, d.ldb, Bt, d.batch_stride_b)
-        _expect("C", C, "bf16", M, self.n_out, d.ldc, Bt, d.batch_stride_c)
-        _expect("C8", C8, "byte", M, self.n_out, d.ldc8, Bt, d.batch_stride_c8)
-        for name, t in (("residual", residual), ("preact", preact)):
-            _expect(name, t, "bf16", M, self.n_out, d.ld_aux, Bt, d.batch_stride_aux)
-        _expect("row_scale", row_scale, "f32", Bt * M)
-        _expect("row_out", row_out, "f32", Bt * M)
-        _expect("col_out", col_out, "f32", Bt * self.n_out)
-        for name, t in (("amax", amax), ("a_scale_inv", a_scale_inv), ("b_scale_inv", b_scale_inv)):
-            _expect(name, t, "f32", 1)
         widths = dict((op, w) for op, w in _width_at(self.program, self.N))
-        _expect("bias", bias, "f32", widths.get("bias", 1))
-        _expect("col_scale", col_scale, "f32", widths.get("col_scale", 1))
+        matrix = {"A": (op_kind(self.a_type), M, K, d.lda, Bt, d.batch_stride_a),
+                  "B": (op_kind(self.b_type), b_rows, b_inner, d.ldb, Bt, d.batch_stride_b),
+                  "B2": (op_kind(self.b_type), b_rows, b_inner, d.ldb, Bt, d.batch_stride_b),
+                  "C": ("bf16", M, self.n_out, d.ldc, Bt, d.batch_stride_c),
+                  "C8": ("byte", M, self.n_out, d.ldc8, Bt, d.batch_stride_c8),
+                  "residual": ("bf16", M, self.n_out, d.ld_aux, Bt, d.batch_stride_aux),
+                  "preact": ("bf16", M, self.n_out, d.ld_aux, Bt, d.batch_stride_aux),
+                  "row_scale": ("f32", Bt * M, 1, 1, 1, 0), "row_out": ("f32", Bt * M, 1, 1, 1, 0),
+                  "col_out": ("f32", Bt * self.n_out, 1, 1, 1, 0),
+                  "bias": ("f32", widths.get("bias", 1), 1, 1, 1, 0),
+                  "col_scale": ("f32", widths.get("col_scale", 1), 1, 1, 1, 0)}
+        for name in ("amax", "a_scale_inv", "b_scale_inv"):
+            matrix[name] = ("f32", 1, 1, 1, 1, 0)
+        return {name: (v[0], (v[4] - 1) * v[5] + (v[1] - 1) * v[3] + v[2], v[1:]) for name, v in matrix.items()}
 
     def run(self, *tensors, stream: Optional[torch.cuda.Stream] = None, **kw):
         """gemm_epi_run on the current (or given) CUDA stream; asynchronous."""
         a = self.args(*tensors, **kw)
-        s = (stream or torch.cuda.current_stream()).cuda_stream
-        N.check(self.lib.gemm_epi_run(self.handle, ctypes.byref(a), ctypes.c_void_p(s)), self.lib)
+        s = _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+        status = self.lib.gemm_epi_run(self.handle, ctypes.byref(a), s)
+        if status:
+            N.check(status, self.lib)
 
     def run_unfused(self, *tensors, scratch: torch.Tensor, stream=None, **kw):
         a = self.args(*tensors, **kw)
@@ -386,104 +404,143 @@ class Rotary:
         N.check(lib.gemm_epi_rotary_steps(ctypes.byref(f), steps), lib)
         # uint64 bits in an int64 tensor: torch has no arithmetic on them here
         self.steps = torch.frombuffer(steps, dtype=torch.int64).clone().to(device)
+        self.steps_ptr, self.index = self.steps.data_ptr(), self.steps.get_device()
 
 
-def _heads(name: str, t: torch.Tensor, like: Optional[torch.Tensor], dst, rope: Rotary) -> None:
-    """Fills a gemm_epi_heads from a (batch, tokens, heads, head_dim) or
-    (tokens, heads, head_dim) tensor; `like`: the tensor whose shape, type and
-    device it must have."""
-    shape = t.shape
-    if len(shape) not in (3, 4) or shape[-1] != rope.head_dim:
+# gemm_epi_qk_args, packed in one step: filling a ctypes structure field by
+# field took 2.4 us of a small call.
+_QK_ARGS = struct.Struct("@qqiiiiii24qQQqiiffQQQQQN")
+assert _QK_ARGS.size == ctypes.sizeof(N.gemm_epi_qk_args)
+_NO_HEADS = (0, 0, 0, 0)
+_head_entries: dict = {}
+
+
+def _head_entry(name: str):
+    """The entry point taking a gemm_epi_qk_args as packed bytes."""
+    fn = _head_entries.get(name)
+    if fn is None:
+        fn = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, ctypes.c_void_p)((name, N.load()))
+        _head_entries[name] = fn
+    return fn
+
+
+def _heads(name: str, t: torch.Tensor, rope: Rotary, dtype, index: int, shape=None):
+    """(pointer, batch, token and head strides) of a (batch, tokens, heads,
+    head_dim) or (tokens, heads, head_dim) tensor, checked; `shape`: the one it
+    must have."""
+    own = t.shape
+    if shape is not None:
+        if own != shape:
+            raise ValueError("%s: shape %s does not match %s" % (name, tuple(own), tuple(shape)))
+    elif len(own) not in (3, 4) or own[-1] != rope.head_dim:
         raise ValueError("%s: expected (batch, tokens, heads, %d) or (tokens, heads, %d), got %s"
-                         % (name, rope.head_dim, rope.head_dim, tuple(shape)))
-    if t.dtype not in HEAD_TYPES:
-        raise TypeError("%s: expected a bf16 or fp32 tensor, got %s" % (name, t.dtype))
-    if like is not None and (shape != like.shape or t.dtype != like.dtype or t.device != like.device):
-        raise ValueError("%s: %s %s on %s does not match %s %s on %s"
-                         % (name, t.dtype, tuple(shape), t.device, like.dtype, tuple(like.shape), like.device))
+                         % (name, rope.head_dim, rope.head_dim, tuple(own)))
+    if t.dtype is not dtype:
+        raise ValueError("%s: %s does not match %s" % (name, t.dtype, dtype))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, not with the other tensors" % (name, t.device))
     st = t.stride()
     if st[-1] != 1 and t.numel():
         raise ValueError("%s: the values of a head must be contiguous" % name)
-    dst.data = t.data_ptr()
-    dst.stride_token, dst.stride_head = st[-3], st[-2]
-    dst.stride_batch = st[0] if len(st) == 4 else 0
+    if len(st) == 4:
+        return t.data_ptr(), st[0], st[1], st[2]
+    return t.data_ptr(), 0, st[0], st[1]
 
 
-def _vector(name: str, t: Optional[torch.Tensor], rope: Rotary, device) -> Optional[int]:
+def _vector(name: str, t: Optional[torch.Tensor], rope: Rotary, index: int) -> int:
     if t is None:
-        return None
-    if t.dtype != torch.float32:
+        return 0
+    if t.dtype is not torch.float32:
         raise TypeError("%s: expected a f32 tensor, got %s" % (name, t.dtype))
-    if t.shape != (rope.head_dim,) or not t.is_contiguous() or t.device != device:
-        raise ValueError("%s: expected %d contiguous values on %s" % (name, rope.head_dim, device))
+    if t.shape != (rope.head_dim,) or not t.is_contiguous():
+        raise ValueError("%s: expected %d contiguous values, got %s" % (name, rope.head_dim, tuple(t.shape)))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, not with the other tensors" % (name, t.device))
     return t.data_ptr()
 
 
-def _qk_args(q, k, rope: Rotary, positions, q_out, k_out, *, optional_out: bool = False):
-    """gemm_epi_qk_args of q and k (either may be None), checked; returns it
-    with the tensors' device."""
-    a = N.gemm_epi_qk_args()
+def _head_call(entry: str, q, k, rope: Rotary, positions, q_out, k_out, dyq=None, dyk=None, *, backward=False,
+               inverse=False, eps=0.0, q_weight=None, k_weight=None, dwq=None, dwk=None, workspace=None,
+               stream=None) -> None:
+    """Checks the tensors of a gemm_epi_qk_args, packs it and calls `entry` on
+    the current (or given) stream of their device."""
     first = q if q is not None else k
     if first is None:
         raise ValueError("q and k are both None")
-    device = first.device
-    for name, t, o, src, dst in (("q", q, q_out, a.q, a.q_out), ("k", k, k_out, a.k, a.k_out)):
-        if t is None:
-            if o is not None:
-                raise ValueError("%s_out without %s" % (name, name))
-            continue
-        _heads(name, t, None, src, rope)
-        if o is not None:
-            _heads(name + "_out", o, t, dst, rope)
-        elif not optional_out:
-            raise ValueError("%s_out is missing (pass %s itself to work in place)" % (name, name))
-    if q is not None and k is not None and (q.shape[:-2] != k.shape[:-2] or q.dtype != k.dtype or q.device != k.device):
-        raise ValueError("q %s %s on %s and k %s %s on %s do not belong together"
-                         % (q.dtype, tuple(q.shape), q.device, k.dtype, tuple(k.shape), k.device))
-    shape = first.shape
-    a.batch, a.tokens = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
-    a.q_heads = 0 if q is None else q.shape[-2]
-    a.k_heads = 0 if k is None else k.shape[-2]
-    a.head_dim, a.rotary_dim, a.layout = rope.head_dim, rope.rotary_dim, rope.layout_code
-    a.type = HEAD_TYPES[first.dtype]
-    if rope.steps.device != device:
-        raise ValueError("the rotary steps are on %s, q and k on %s" % (rope.steps.device, device))
-    a.steps, a.amplitude = rope.steps.data_ptr(), rope.amplitude
+    dtype, index = first.dtype, first.get_device()
+    if dtype not in HEAD_TYPES:
+        raise TypeError("%s: expected a bf16 or fp32 tensor, got %s" % ("q" if q is not None else "k", dtype))
+    q_heads = k_heads = 0
+    tq = tqo = tdq = tk = tko = tdk = _NO_HEADS
+    if q is not None:
+        tq = _heads("q", q, rope, dtype, index)
+        shape = q.shape
+        q_heads = shape[-2]
+        if q_out is not None:
+            tqo = _heads("dq" if backward else "q_out", q_out, rope, dtype, index, shape)
+        if dyq is not None:
+            tdq = _heads("dyq", dyq, rope, dtype, index, shape)
+    if k is not None:
+        if q is not None and (q.shape[:-2] != k.shape[:-2] or k.dtype is not dtype):
+            raise ValueError("q %s %s and k %s %s do not belong together" % (dtype, tuple(q.shape), k.dtype, tuple(k.shape)))
+        tk = _heads("k", k, rope, dtype, index)
+        shape = k.shape
+        k_heads = shape[-2]
+        if k_out is not None:
+            tko = _heads("dk" if backward else "k_out", k_out, rope, dtype, index, shape)
+        if dyk is not None:
+            tdk = _heads("dyk", dyk, rope, dtype, index, shape)
+    if backward:
+        if (dyq is None) != (q is None) or (dyk is None) != (k is None):
+            raise ValueError("a gradient and its input (dyq and q, dyk and k) must be given together")
+    elif (q is not None and q_out is None) or (k is not None and k_out is None):
+        raise ValueError("%s_out is missing (pass %s itself to work in place)" % (("q",) * 2 if q is not None and q_out is None else ("k",) * 2))
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("%s_out without %s" % (("q",) * 2 if q is None else ("k",) * 2))
+    batch, tokens = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
+    if rope.index != index:
+        raise ValueError("the rotary steps are on %s, q and k on %s" % (rope.steps.device, first.device))
+    at = wide = pos_stride = 0
     if positions is not None:
-        a.positions, a.positions_64, a.position_stride = _positions(positions, a.batch, a.tokens, device)
-    return a, device
+        at, wide, pos_stride = _positions(positions, batch, tokens, index)
+    ws = ws_bytes = 0
+    if workspace is not None:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace: expected a contiguous tensor with the others")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    packed = _QK_ARGS.pack(
+        batch, tokens, q_heads, k_heads, rope.head_dim, rope.rotary_dim, rope.layout_code, HEAD_TYPES[dtype],
+        *tq, *tk, *tqo, *tko, *tdq, *tdk, rope.steps_ptr, at, pos_stride, wide, 1 if inverse else 0,
+        rope.amplitude, eps, _vector("q_weight", q_weight, rope, index), _vector("k_weight", k_weight, rope, index),
+        _vector("dwq", dwq, rope, index), _vector("dwk", dwk, rope, index), ws, ws_bytes)
+    if index < 0:
+        raise ValueError("expected CUDA tensors, got %s" % first.device)
+    if index == torch.cuda.current_device():
+        status = _head_entry(entry)(packed, _raw_stream(index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            status = _head_entry(entry)(packed, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if status:
+        N.check(status)
 
 
-def _positions(p: torch.Tensor, batch: int, tokens: int, device):
-    """(pointer, is 64-bit, batch stride) of a (tokens,) or (batch, tokens) tensor."""
-    if p.dtype not in (torch.int32, torch.int64):
+def _positions(p: torch.Tensor, batch: int, tokens: int, index: int):
+    """(pointer, 1 if 64-bit, batch stride) of a (tokens,) or (batch, tokens) tensor."""
+    if p.dtype is not torch.int32 and p.dtype is not torch.int64:
         raise TypeError("positions: expected an int32 or int64 tensor, got %s" % p.dtype)
-    if p.device != device:
-        raise ValueError("positions are on %s, q and k on %s" % (p.device, device))
-    if p.shape == (tokens,):
+    if p.get_device() != index:
+        raise ValueError("positions are on %s, not with the other tensors" % p.device)
+    shape = p.shape
+    st = p.stride()
+    if shape == (batch, tokens):
+        stride = st[0] if batch > 1 else 0
+    elif shape == (tokens,):
         stride = 0
-    elif p.shape == (batch, tokens):
-        stride = p.stride(0) if batch > 1 else 0
     else:
-        raise ValueError("positions: expected (%d,) or (%d, %d), got %s" % (tokens, batch, tokens, tuple(p.shape)))
-    if tokens > 1 and p.stride(-1) != 1:
+        raise ValueError("positions: expected (%d,) or (%d, %d), got %s" % (tokens, batch, tokens, tuple(shape)))
+    if tokens > 1 and st[-1] != 1:
         raise ValueError("positions: the positions of a sequence must be contiguous")
-    return p.data_ptr(), int(p.dtype == torch.int64), stride
-
-
-def _launch(fn, a, device, stream) -> None:
-    """Calls a C entry point on the current (or given) stream of the tensors'
-    device."""
-    lib = N.load()
-    if device.type != "cuda":
-        raise ValueError("expected CUDA tensors, got %s" % device)
-    if device.index == torch.cuda.current_device():
-        s = (stream or torch.cuda.current_stream()).cuda_stream
-        N.check(fn(ctypes.byref(a), s), lib)
-    else:
-        with torch.cuda.device(device):
-            s = (stream or torch.cuda.current_stream()).cuda_stream
-            N.check(fn(ctypes.byref(a), s), lib)
+    return p.data_ptr(), 1 if p.dtype is torch.int64 else 0, stride
 
 
 def rotary(q, k, rope: Rotary, positions=None, *, q_out=None, k_out=None, inverse: bool = False, stream=None) -> None:
@@ -496,9 +553,7 @@ def rotary(q, k, rope: Rotary, positions=None, *, q_out=None, k_out=None, invers
     or int64, (tokens,) or (batch, tokens); None counts every sequence from 0.
     inverse=True applies the transpose: the backward pass, from the gradients
     of q_out and k_out to those of q and k.  Asynchronous."""
-    a, device = _qk_args(q, k, rope, positions, q_out, k_out)
-    a.inverse = 1 if inverse else 0
-    _launch(N.load().gemm_epi_rotary, a, device, stream)
+    _head_call("gemm_epi_rotary", q, k, rope, positions, q_out, k_out, inverse=inverse, stream=stream)
 
 
 def qk_norm_rotary(q, k, rope: Rotary, positions=None, *, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -506,10 +561,8 @@ def qk_norm_rotary(q, k, rope: Rotary, positions=None, *, q_weight=None, k_weigh
     """gemm_epi_qk_norm_rotary: each head of q and k divided by its root mean
     square (plus eps), multiplied by the fp32 weight (None: 1) and rotated, in
     one pass; arguments as for rotary().  Asynchronous."""
-    a, device = _qk_args(q, k, rope, positions, q_out, k_out)
-    a.eps = eps
-    a.q_weight, a.k_weight = _vector("q_weight", q_weight, rope, device), _vector("k_weight", k_weight, rope, device)
-    _launch(N.load().gemm_epi_qk_norm_rotary, a, device, stream)
+    _head_call("gemm_epi_qk_norm_rotary", q, k, rope, positions, q_out, k_out, eps=eps, q_weight=q_weight,
+               k_weight=k_weight, stream=stream)
 
 
 def qk_norm_rotary_workspace(head_dim: int) -> int:
@@ -526,17 +579,5 @@ def qk_norm_rotary_backward(dyq, dyk, q, k, rope: Rotary, positions=None, *, q_w
     the weights, summed over batch, tokens and heads, into the fp32 dwq and dwk
     (overwritten).  Each of the four may be None; dwq and dwk need a workspace
     of qk_norm_rotary_workspace(head_dim) bytes.  Asynchronous."""
-    a, device = _qk_args(q, k, rope, positions, dq, dk, optional_out=True)
-    for name, dy, x, dst in (("dyq", dyq, q, a.dy_q), ("dyk", dyk, k, a.dy_k)):
-        if (dy is None) != (x is None):
-            raise ValueError("%s and its input must be given together" % name)
-        if dy is not None:
-            _heads(name, dy, x, dst, rope)
-    a.eps = eps
-    a.q_weight, a.k_weight = _vector("q_weight", q_weight, rope, device), _vector("k_weight", k_weight, rope, device)
-    a.dw_q, a.dw_k = _vector("dwq", dwq, rope, device), _vector("dwk", dwk, rope, device)
-    if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError("workspace: expected a contiguous tensor on %s" % device)
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _launch(N.load().gemm_epi_qk_norm_rotary_backward, a, device, stream)
+    _head_call("gemm_epi_qk_norm_rotary_backward", q, k, rope, positions, dq, dk, dyq, dyk, backward=True, eps=eps,
+               q_weight=q_weight, k_weight=k_weight, dwq=dwq, dwk=dwk, workspace=workspace, stream=stream)

@@ -717,7 +717,7 @@ __device__ __forceinline__ void rotate_halves(const KernelParams& p, int64_t pos
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
     float c, s;
-    turn_cos_sin<true>(phase_turns(position, __ldg(p.rot_steps + pair0 + j)), c, s);
+    turn_cos_sin<true>(phase_bits(position, __ldg(p.rot_steps + pair0 + j)), c, s);
     c *= p.rot_amplitude;
     s *= p.rot_amplitude;
     const float x = a[j], y = b[j];
@@ -735,7 +735,7 @@ __device__ __forceinline__ void rotate_chunk(const KernelParams& p, int64_t posi
   for (int j = 0; j < 16; ++j) {
     if (pair0 + j < p.rot_pairs) {
       float c, s;
-      turn_cos_sin<true>(phase_turns(position, __ldg(p.rot_steps + pair0 + j)), c, s);
+      turn_cos_sin<true>(phase_bits(position, __ldg(p.rot_steps + pair0 + j)), c, s);
       c *= p.rot_amplitude;
       s *= p.rot_amplitude;
       float& a = v[HALF ? j : 2 * j];

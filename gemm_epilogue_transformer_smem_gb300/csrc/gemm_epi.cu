@@ -183,10 +183,10 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 }  // namespace
 
-gemm_epi_status ge_host::device_sms(int* sms) {
-  DeviceState* dev = nullptr;
-  const gemm_epi_status s = device_state(&dev, nullptr);
-  if (s == GEMM_EPI_OK) *sms = dev->sms;
+gemm_epi_status ge_host::device_sms(int* dev, int* sms) {
+  DeviceState* state = nullptr;
+  const gemm_epi_status s = device_state(&state, dev);
+  if (s == GEMM_EPI_OK) *sms = state->sms;
   return s;
 }
 

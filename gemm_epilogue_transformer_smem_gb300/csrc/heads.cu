@@ -2,6 +2,7 @@
 // (rotary positions, the head norm with the rotation, its backward), and
 // their kernels.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -19,26 +20,50 @@ constexpr double TWO_PI = 6.283185307179586476925286766559;
 
 // ---------------------------------------------------------------- kernels
 
-using HeadKernel = void (*)(ge::HeadParams);
+// A kernel, its resident blocks per SM and its dynamic shared memory.
+struct HeadKernel {
+  void (*fn)(ge::HeadParams);
+  int blocks, smem;
+};
 
-template <class T, int V, bool HALF>
-HeadKernel kernel_of(int mode) {
+template <class T, bool HALF>
+HeadKernel kernel_of(int mode, bool wide) {
+  using Forward = ge::HeadRing<T, HALF, 1>;
+  using Backward = ge::HeadRing<T, HALF, 2>;
   switch (mode) {
-    case ge::HEAD_ROTARY: return ge::heads_kernel<T, V, HALF, ge::HEAD_ROTARY>;
-    case ge::HEAD_NORM: return ge::heads_kernel<T, V, HALF, ge::HEAD_NORM>;
-    default: return ge::heads_kernel<T, V, HALF, ge::HEAD_NORM_BWD>;
+    case ge::HEAD_ROTARY:
+      return wide ? HeadKernel{ge::heads_kernel<T, HALF, false>, ge::HD_ROTARY_BLOCKS, Forward::BYTES}
+                  : HeadKernel{ge::heads_any_kernel<T, HALF, false>, 2, 0};
+    case ge::HEAD_NORM:
+      return wide ? HeadKernel{ge::heads_kernel<T, HALF, true>, ge::HD_NORM_BLOCKS, Forward::BYTES}
+                  : HeadKernel{ge::heads_any_kernel<T, HALF, true>, 2, 0};
+    default:
+      return wide ? HeadKernel{ge::heads_backward_kernel<T, HALF>, ge::HD_BWD_BLOCKS, Backward::BYTES}
+                  : HeadKernel{ge::heads_backward_any_kernel<T, HALF>, ge::HD_BWD_BLOCKS, 0};
   }
 }
 
-template <class T>
-HeadKernel kernel_of(int mode, bool wide, bool half) {
-  if (wide) return half ? kernel_of<T, 8, true>(mode) : kernel_of<T, 8, false>(mode);
-  return half ? kernel_of<T, 2, true>(mode) : kernel_of<T, 2, false>(mode);
+HeadKernel kernel_of(int mode, bool wide, bool half, bool f32) {
+  if (f32) return half ? kernel_of<float, true>(mode, wide) : kernel_of<float, false>(mode, wide);
+  return half ? kernel_of<uint16_t, true>(mode, wide) : kernel_of<uint16_t, false>(mode, wide);
 }
 
-// Forward passes: warps to start per SM before heads of one token share a
-// warp (fewer warps than this leave SMs idle; more recompute the angles).
-constexpr int64_t HD_WARPS_PER_SM = 48;
+// The current device's SM count.  The first call on a device gives every
+// kernel its shared-memory limit.
+gemm_epi_status device_setup(int* sms) {
+  static std::atomic<bool> ready[128];
+  int dev = 0;
+  const gemm_epi_status s = ge_host::device_sms(&dev, sms);
+  if (s != GEMM_EPI_OK || ready[dev].load(std::memory_order_acquire)) return s;
+  for (int i = 0; i < 3 * 2 * 2; ++i) {
+    const HeadKernel k = kernel_of(i / 4, true, (i & 1) != 0, (i & 2) != 0);
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k.fn),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  }
+  ready[dev].store(true, std::memory_order_release);
+  return GEMM_EPI_OK;
+}
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
@@ -150,7 +175,7 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
     return fail(GEMM_EPI_ERR_WORKSPACE, "workspace must be 16-byte aligned and hold %zu bytes (got %zu)", ws,
                 a->workspace ? a->workspace_bytes : static_cast<size_t>(0));
   int sms = 0;
-  if ((s = ge_host::device_sms(&sms))) return s;
+  if ((s = device_setup(&sms))) return s;
   cudaError_t e;
   if (!work) {
     // no rows: the weights' gradients are zero
@@ -162,10 +187,11 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
 
   const bool half = a->layout == GEMM_EPI_ROTARY_HALF;
   const int pairs = a->rotary_dim / 2;
-  // 16-byte accesses need whole chunks of 8 values: in the head, and in each
-  // half of the rotated part.
-  const bool wide = c.wide && a->head_dim % 8 == 0 && (!half || pairs % 8 == 0);
-  const int V = wide ? 8 : 2, slots = 8 / V;
+  // 16-byte accesses need whole chunks of them: in the head, and in each half
+  // of the rotated part.
+  const int chunk = static_cast<int>(16 / c.size);
+  const bool wide = c.wide && a->head_dim % chunk == 0 && (!half || pairs % chunk == 0);
+  const int V = wide ? chunk : 2, slots = 8 / V;
 
   ge::HeadParams p;
   std::memset(&p, 0, sizeof p);
@@ -173,13 +199,13 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
   p.rows = static_cast<int32_t>(a->batch * a->tokens);
   p.dim = a->head_dim;
   p.rot_pairs = pairs;
-  p.first_plain = (pairs + V - 1) / V;
-  p.num_pc = (a->head_dim / V + 1) / 2;
-  if (half) p.num_pc = p.first_plain + (a->head_dim / V - 2 * p.first_plain + 1) / 2;
   // In place and without a norm, what does not rotate is already there.
   bool in_place = mode == ge::HEAD_ROTARY;
   for (int i = 0; i < 2; ++i) in_place = in_place && (heads[i] == 0 || same_place(*in[i], *out[i]));
-  if (in_place) p.num_pc = p.first_plain;
+  p.reach = in_place ? (a->rotary_dim + V - 1) / V * V : a->head_dim;
+  const int chunks = p.reach / V;  // reach is whole chunks: V divides head_dim
+  p.first_plain = half ? pairs / V : 0;
+  p.num_pc = p.first_plain + (chunks - 2 * p.first_plain + 1) / 2;
   p.log_g = 0;
   while ((slots << p.log_g) < p.num_pc) ++p.log_g;
   const int per_iter = 32 >> p.log_g;
@@ -204,25 +230,44 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
   p.inv_dim = 1.0f / static_cast<float>(a->head_dim);
   p.partials = wants_dw ? static_cast<float*>(a->workspace) : nullptr;
 
-  // A warp takes a whole token while there are tokens enough for every SM,
-  // and fewer of its heads below that.
-  const int64_t warps = static_cast<int64_t>(sms) * (bwd ? ge::HD_BWD_BLOCKS * ge::HD_WARPS : HD_WARPS_PER_SM);
-  const int64_t fair = static_cast<int64_t>(p.rows) * total_iters / warps;
-  p.iters_per_unit = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(fair, total_iters)));
-  p.units_per_row = (total_iters + p.iters_per_unit - 1) / p.iters_per_unit;
-  const int64_t units = static_cast<int64_t>(p.rows) * p.units_per_row;
-  int64_t blocks = (units + ge::HD_WARPS - 1) / ge::HD_WARPS;
-  // The backward pass keeps its weight gradients in registers over a warp's
-  // tokens: one wave of blocks, each leaving one partial row.
-  if (bwd) blocks = std::min<int64_t>(blocks, std::min<int64_t>(ge::HD_MAX_PARTIALS, sms * ge::HD_BWD_BLOCKS));
-  const HeadKernel kernel = a->type == GEMM_EPI_TYPE_F32 ? kernel_of<float>(mode, wide, half)
-                                                         : kernel_of<uint16_t>(mode, wide, half);
-  kernel<<<static_cast<unsigned>(blocks), ge::HD_THREADS, 0, st>>>(p);
+  const HeadKernel kernel = kernel_of(mode, wide, half, a->type == GEMM_EPI_TYPE_F32);
+  const int64_t resident = static_cast<int64_t>(sms) * kernel.blocks;
+  // One wave of blocks, and no more warps than iterations.
+  const int64_t row_iters[2] = {p.part[0].iters, p.part[1].iters};
+  auto share_out = [&](ge::HeadShare& h, int64_t per_row, int64_t most) {
+    const int64_t total = p.rows * per_row;
+    const int64_t blocks = std::min(most, (total + ge::HD_WARPS - 1) / ge::HD_WARPS);
+    const int64_t warps = std::max<int64_t>(1, blocks * ge::HD_WARPS);
+    const int64_t left = p.rows % warps * per_row;  // iterations past the whole rounds
+    h.warps = static_cast<int32_t>(warps);
+    h.per_row = static_cast<int32_t>(std::max<int64_t>(1, per_row));
+    h.rounds = blocks ? static_cast<int32_t>(p.rows / warps) : 0;
+    h.base = static_cast<int32_t>(left / warps);
+    h.rest = static_cast<int32_t>(left % warps);
+    return blocks;
+  };
+  int64_t blocks;
+  if (bwd) {
+    // shared between q and k by their work; a part none of whose results is
+    // wanted gets no block
+    const int64_t most = std::min<int64_t>(ge::HD_MAX_PARTIALS, resident);
+    const int64_t q_work = a->q_out.data || a->dw_q ? row_iters[0] : 0;
+    const int64_t k_work = a->k_out.data || a->dw_k ? row_iters[1] : 0;
+    int64_t q_most = q_work ? most : 0;
+    if (q_work && k_work)
+      q_most = std::min(most - 1, std::max<int64_t>(1, (most * q_work + (q_work + k_work) / 2) / (q_work + k_work)));
+    const int64_t q = share_out(p.share[0], q_work, q_most), k = share_out(p.share[1], k_work, most - q_most);
+    p.q_blocks = static_cast<int32_t>(q);
+    blocks = q + k;
+  } else {
+    blocks = share_out(p.share[0], total_iters, resident);
+  }
+  kernel.fn<<<static_cast<unsigned>(blocks), ge::HD_THREADS, static_cast<size_t>(kernel.smem), st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch of the head kernel");
   if (wants_dw) {
-    ge::head_weight_grad_kernel<<<static_cast<unsigned>((2 * a->head_dim + 31) / 32), dim3(32, 32), 0, st>>>(
-        p.partials, static_cast<int>(blocks), a->head_dim, a->dw_q, a->dw_k);
+    ge::head_weight_grad_kernel<<<dim3(static_cast<unsigned>((a->head_dim + 31) / 32), 2), dim3(32, 32), 0, st>>>(
+        p.partials, p.q_blocks, static_cast<int>(blocks), a->head_dim, a->dw_q, a->dw_k);
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "launch of the weight gradient kernel");
   }
@@ -286,7 +331,7 @@ gemm_epi_status gemm_epi_qk_norm_rotary_backward(const gemm_epi_qk_args* args, v
 
 size_t gemm_epi_qk_norm_rotary_workspace_size(int32_t head_dim) {
   if (head_dim < 2 || head_dim > ge::HD_MAX_DIM) return 0;
-  return static_cast<size_t>(ge::HD_MAX_PARTIALS) * 2 * static_cast<size_t>(head_dim) * sizeof(float);
+  return static_cast<size_t>(ge::HD_MAX_PARTIALS) * static_cast<size_t>(head_dim) * sizeof(float);
 }
 
 }  // extern "C"

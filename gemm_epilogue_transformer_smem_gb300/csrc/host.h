@@ -13,7 +13,8 @@ gemm_epi_status fail(gemm_epi_status s, const char* fmt, ...);
 gemm_epi_status cuda_fail(cudaError_t e, const char* what);
 void clear_error();
 
-// SM count of the current device; GEMM_EPI_ERR_ARCH unless it is sm_103.
-gemm_epi_status device_sms(int* sms);
+// The current device (0..127) and its SM count; GEMM_EPI_ERR_ARCH unless it
+// is sm_103.
+gemm_epi_status device_sms(int* dev, int* sms);
 
 }  // namespace ge_host

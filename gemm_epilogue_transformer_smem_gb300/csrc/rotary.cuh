@@ -13,24 +13,49 @@
 
 namespace ge {
 
-// Signed turns of phase `position * step`: the top 32 of its 64 bits.
-__device__ __forceinline__ float phase_turns(int64_t position, uint64_t step) {
-  const uint64_t phase = static_cast<uint64_t>(position) * step;
-  return static_cast<float>(static_cast<int32_t>(phase >> 32)) * 2.3283064365386963e-10f;  // 2^-32
+// Phase of `position`, its top 32 bits: a signed fraction of a turn times 2^32.
+__device__ __forceinline__ int32_t phase_bits(int64_t position, uint64_t step) {
+  return static_cast<int32_t>((static_cast<uint64_t>(position) * step) >> 32);
 }
 
-// cos and sin of `turns` in [-1/2, 1/2).  FAST: the special-function unit, off
-// by about 2^-21; a bf16 result keeps 8 bits, so its rounding hides that.
-// fp32 results take the accurate functions.
+// cos and sin of a phase by the special-function unit, off by about 2^-21: for
+// bf16 results, which keep 8 bits, so that their rounding hides it.
+__device__ __forceinline__ void phase_cos_sin_fast(int32_t phase, float& c, float& s) {
+  const float angle = static_cast<float>(phase) * 1.4629180792671596e-9f;  // 2 pi 2^-32
+  c = __cosf(angle);
+  s = __sinf(angle);
+}
+
+// The same to fp32's accuracy.  The phase splits exactly, in integers, into
+// the nearest quarter turn and a rest of at most an eighth of a turn either
+// side: x in [-pi/4, pi/4], where the Taylor series of sin to x^9 and of cos
+// to x^10 are within 2^-29 (their next terms are below 2e-9 and 2e-10).
+__device__ __forceinline__ void phase_cos_sin(int32_t phase, float& c, float& s) {
+  const uint32_t quarter = (static_cast<uint32_t>(phase) + 0x20000000u) >> 30;
+  const int32_t rest = static_cast<int32_t>(static_cast<uint32_t>(phase) - (quarter << 30));
+  const float x = static_cast<float>(rest) * 1.4629180792671596e-9f;
+  const float z = x * x;
+  float sp = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  sp = fmaf(z, sp, 1.0f / 120.0f);
+  sp = fmaf(z, sp, -1.0f / 6.0f);
+  const float sx = fmaf(x * z, sp, x);
+  float cp = fmaf(z, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  cp = fmaf(z, cp, -1.0f / 720.0f);
+  cp = fmaf(z, cp, 1.0f / 24.0f);
+  cp = fmaf(z, cp, -0.5f);
+  const float cx = fmaf(z, cp, 1.0f);
+  const float u = (quarter & 1u) ? sx : cx, v = (quarter & 1u) ? cx : sx;
+  // quarter turns 0..3: cos = cx, -sx, -cx, sx; sin = sx, cx, -sx, -cx
+  c = ((quarter + 1u) & 2u) ? -u : u;
+  s = (quarter & 2u) ? -v : v;
+}
+
 template <bool FAST>
-__device__ __forceinline__ void turn_cos_sin(float turns, float& c, float& s) {
-  if constexpr (FAST) {
-    const float angle = turns * 6.2831853071795865f;
-    c = __cosf(angle);
-    s = __sinf(angle);
-  } else {
-    sincospif(2.0f * turns, &s, &c);
-  }
+__device__ __forceinline__ void turn_cos_sin(int32_t phase, float& c, float& s) {
+  if constexpr (FAST)
+    phase_cos_sin_fast(phase, c, s);
+  else
+    phase_cos_sin(phase, c, s);
 }
 
 }  // namespace ge

@@ -429,9 +429,9 @@ GEMM_EPI_API gemm_epi_status gemm_epi_rotary_steps(const gemm_epi_rotary_freq *f
 /* The heads of q or k: element (b, t, h, d) at data + b stride_batch +
  * t stride_token + h stride_head + d, strides in elements, any order (tokens
  * outside heads or inside, heads of a packed q|k|v projection).  Any strides
- * and element-aligned pointers are taken; 16-byte aligned pointers and strides
- * with head_dim % 8 == 0 (and rotary_dim % 16 == 0 in the half layout) move
- * 16 bytes per access, the rest single elements. */
+ * and element-aligned pointers are taken; 16-byte aligned pointers and strides,
+ * with whole 16-byte groups in a head (and in half the rotated part, in the
+ * half layout), move 16 bytes per access, the rest single elements. */
 typedef struct gemm_epi_heads {
     void *data;
     int64_t stride_batch, stride_token, stride_head;
