@@ -150,6 +150,7 @@ struct KernelParams {
   int32_t dual;  // 1: accumulator columns alternate between B and B2 in 128-column blocks
   int32_t a_batched, b_batched;  // operand advances with the batch (else shared)
   int32_t row_blocks;            // row counters per batch
+  int32_t split, split_rows;     // SPLIT kernels: CTAs along K per tile, rows of a tile's partial sums
   const float* a_scale_inv;      // dequantisation factors (F_DEQ), NULL = 1
   const float* b_scale_inv;
   int64_t bs_c, bs_c8, bs_aux;   // batch strides for direct accesses (elements; bytes for C8)
@@ -840,7 +841,16 @@ __device__ __forceinline__ float tmem_column_sums(const float (&s)[32], bool row
 // IN8 = 1: 8-bit operands (tcgen05 kind::f8f6f4); a K block is still one
 // 128-byte swizzle row per operand, now 128 elements.  The operand width is a
 // compile-time choice: a kernel issues MMAs of one kind only.
-template <int CG, class Prog, int IN8 = 0>
+//
+// SPLIT = 1 (CG = 1): few rows make few tiles, so a cluster of p.split CTAs
+// shares one tile, each over its part of K, and the grid still covers the SMs
+// that read the weights.  The heads of the tile (p.head_chunks chunks each)
+// are dealt out to the CTAs: once every main loop of the cluster is done, each
+// CTA writes its partial sums of the others' heads into their shared memory
+// (the operand rings, idle by then), adds the ones it received to its own
+// accumulator in a fixed order and runs the program on its heads.  One tile
+// per cluster.
+template <int CG, class Prog, int IN8 = 0, int SPLIT = 0>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fused_gemm_epilogue_kernel(const __grid_constant__ CUtensorMap tm_a,
                                const __grid_constant__ CUtensorMap tm_b,
@@ -872,8 +882,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;  // CTA within the pair
-  const int group = blockIdx.x / CG;                             // tile-walker index
-  const int num_groups = gridDim.x / CG;
+  const int split = SPLIT ? p.split : CG;                        // CTAs per tile
+  const int group = blockIdx.x / split;                          // tile-walker index
+  const int num_groups = gridDim.x / split;
+  // K-blocks [kb0, kb0 + num_kb) are this CTA's.
+  const int krank = SPLIT ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+  const int kb0 = SPLIT ? static_cast<int>(static_cast<int64_t>(p.num_k_blocks) * krank / split) : 0;
+  const int num_kb = SPLIT ? static_cast<int>(static_cast<int64_t>(p.num_k_blocks) * (krank + 1) / split) - kb0
+                           : p.num_k_blocks;
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < STAGES; ++s) ptx::mbar_init(bar(BAR_FULL + s), 1);
@@ -912,7 +928,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (lane == 0 && p.num_k_blocks > 0) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-      const int num_steps = (p.num_k_blocks + KPS - 1) / KPS;  // stages per tile
+      const int num_steps = (num_kb + KPS - 1) / KPS;  // stages per tile
       for (int t = group; ok && t < p.num_tiles; t += num_groups) {
         int bt, mb, nb;
         tile_coords(p, t, bt, mb, nb);
@@ -946,7 +962,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // A slot past the last K-block (odd count) loads the last one
             // again, so that every stage carries the same bytes; its MMAs
             // are not issued.
-            const int kb = min(ks * KPS + h, p.num_k_blocks - 1);
+            const int kb = kb0 + min(ks * KPS + h, num_kb - 1);
             const uint32_t sa = sbase + L::OFF_A + stage * L::A_STAGE_BYTES + h * A_KB_BYTES;
             const uint32_t sb = sbase + L::OFF_B + stage * L::B_STAGE_BYTES + h * L::B_KB_BYTES;
             if (CG == 1) {
@@ -1002,7 +1018,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (lane == 0 && rank == 0) {  // the even CTA issues for the whole group
       uint32_t stage = 0, phase = 0;
       bool ok = true, any_mma = false;
-      const int num_steps = (p.num_k_blocks + KPS - 1) / KPS;
+      const int num_steps = (num_kb + KPS - 1) / KPS;
       int local = 0;
       for (int t = group; ok && t < p.num_tiles; t += num_groups, ++local) {
         const uint32_t buf = local & 1, use = local >> 1;
@@ -1031,7 +1047,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint64_t b_d0 =
               smem_desc_sw128(sbase + L::OFF_B + stage * L::B_STAGE_BYTES, p.b_kn ? B_MN_BOX_BYTES : 16u, 1024);
           const uint32_t b_k = p.b_kn ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
-          const int kb_left = p.num_k_blocks - ks * KPS;  // K blocks of the tile from this stage on
+          const int kb_left = num_kb - ks * KPS;  // K blocks of the tile from this stage on
           const uint32_t empty0 = bar(BAR_EMPTY + stage * KPS);
           if (!wait_bar<CG>(bar(BAR_FULL + stage), phase, abort_flag, p, W_MMA_FULL)) {
             ok = false;
@@ -1150,13 +1166,62 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
       // All lanes wait; the outcome is made warp-uniform so that no lane
       // leaves while the others enter a warp-synchronous step.
-      if (!__all_sync(0xffffffffu,
-                      wait_bar<CG>(bar(BAR_TFULL + buf), use & 1u, abort_flag, p, W_EPI_TMEM_FULL))) {
-        ok = false;
-        break;
-      }
+      ok = __all_sync(0xffffffffu, wait_bar<CG>(bar(BAR_TFULL + buf), use & 1u, abort_flag, p, W_EPI_TMEM_FULL));
+      if (!SPLIT && !ok) break;
       ptx::tc_fence_after_sync();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + buf * BLOCK_N;
+      if constexpr (SPLIT) {
+        // The cluster barriers are passed by every warp of every CTA, also
+        // after a wait that ran out (all waits before them are bounded).
+        const uint32_t piece = static_cast<uint32_t>(p.split_rows) * 16u;  // 4 columns of all rows
+        const uint32_t unit_bytes = static_cast<uint32_t>(p.head_chunks) * 8u * piece;
+        const int units = chunks / p.head_chunks, per_rank = (units + split - 1) / split;
+        const uint32_t row_at = sbase + static_cast<uint32_t>(quad * 32 + lane) * 16u;
+        __syncwarp();
+        ptx::cluster_sync();  // every operand ring of the cluster is idle
+        if (ok && slab_ok) {
+          for (int c = 0; c < chunks; ++c) {
+            const int u = c / p.head_chunks, owner = u % split;
+            if (owner == krank) continue;
+            uint32_t r[32];
+            ptx::tmem_ld32_sync(t_row + c * 32, r);
+            const int src = krank < owner ? krank : krank - 1;
+            const uint32_t at = ptx::mapa_shared(row_at, owner) + (src * per_rank + u / split) * unit_bytes +
+                                static_cast<uint32_t>(c - u * p.head_chunks) * 8u * piece;
+            if (row_ok) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                ptx::st_shared_cluster_v4(at + q * piece, __uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                          __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+            }
+          }
+        }
+        __syncwarp();
+        ptx::cluster_sync();  // every partial sum is in place
+        if (!ok) break;
+        if (slab_ok) {
+          for (int c = 0; c < chunks; ++c) {
+            const int u = c / p.head_chunks;
+            if (u % split != krank) continue;
+            uint32_t r[32];
+            ptx::tmem_ld32_sync(t_row + c * 32, r);
+            const uint8_t* got = smem + static_cast<uint32_t>(quad * 32 + lane) * 16u + (u / split) * unit_bytes +
+                                 static_cast<uint32_t>(c - u * p.head_chunks) * 8u * piece;
+            for (int src = 0; row_ok && src < split - 1; ++src) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const float4 v = *reinterpret_cast<const float4*>(got + src * per_rank * unit_bytes + q * piece);
+                r[4 * q] = __float_as_uint(__uint_as_float(r[4 * q]) + v.x);
+                r[4 * q + 1] = __float_as_uint(__uint_as_float(r[4 * q + 1]) + v.y);
+                r[4 * q + 2] = __float_as_uint(__uint_as_float(r[4 * q + 2]) + v.z);
+                r[4 * q + 3] = __float_as_uint(__uint_as_float(r[4 * q + 3]) + v.w);
+              }
+            }
+            __syncwarp();
+            ptx::tmem_st32_sync(t_row + c * 32, r);
+          }
+        }
+      }
       float row_ss = 0.0f;
 
       // This row's position; the head in hand: its 1 / rms, and the second
@@ -1170,8 +1235,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                     : __ldg(static_cast<const int*>(p.positions) + row_base + m);
       }
 
+      uint32_t done_chunks = 0;
       for (int ci = 0; ci < chunks; ++ci) {
-        const uint32_t g = gchunk + ci;
+        if constexpr (SPLIT) {  // another CTA of the cluster has this head
+          if (ci / p.head_chunks % split != krank) continue;
+        }
+        const uint32_t g = gchunk + done_chunks++;
         const uint32_t eb = g % EPI_BUFS;
         // Chunk of the tile: in order, but for the rotated part of a head in
         // the half layout, whose chunks come in pairs (i, i + half).
@@ -1342,6 +1411,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // keeps the shuffle form, which needs no extra registers.)
         const bool tmem_col_sums = kStatic && (flags & F_COL) && !expand && !paired && !Prog::heads;
         auto release_accumulator = [&]() {
+          if constexpr (SPLIT) return;  // one tile per CTA
           ptx::tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) {
@@ -1558,7 +1628,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t prev = 0;
         if (lane == 0) prev = atomicAdd(p.row_counter + static_cast<int64_t>(bt) * p.row_blocks + blk, 1u);
         prev = __shfl_sync(0xffffffffu, prev, 0);
-        if (prev == static_cast<uint32_t>(NUM_EPI_WARPS * p.num_n_tiles - 1)) {
+        if (prev == static_cast<uint32_t>(NUM_EPI_WARPS * p.num_n_tiles * (SPLIT ? split : 1) - 1)) {
           __threadfence();
           const float inv_n = 1.0f / static_cast<float>(p.n_out);
           for (int r = lane; r < BLOCK_M; r += 32) {
@@ -1585,6 +1655,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 
   __syncwarp();  // role branches reconverge before the warp-aligned barrier
+  if (SPLIT && warp < 2) {  // the epilogue's two cluster barriers
+    ptx::cluster_sync();
+    ptx::cluster_sync();
+  }
   ptx::tc_fence_before_sync();
   // Every role of the group has finished: any abort flag is set by now, and
   // the odd CTA's load counts are visible to the even CTA.

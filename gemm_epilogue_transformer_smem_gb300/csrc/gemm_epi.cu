@@ -65,10 +65,15 @@ constexpr int DEFAULT_GROUP_M = 16;
 constexpr double L2_KEEP_BYTES = 60e6;
 constexpr uint32_t DEFAULT_TIMEOUT_MS = 2000;
 
+constexpr int MAX_SPLIT = 8;         // CTAs of a cluster along K (the portable cluster size)
+constexpr int MIN_SPLIT_BLOCKS = 4;  // K-blocks of a CTA that are worth a cluster's exchange
+
 struct DeviceState {
   bool ready = false;
   int cc_major = 0, cc_minor = 0, sms = 0;
   int pair_clusters = 0;  // CTA pairs of the 2-SM kernel that fit on the GPU at once
+  // Clusters of n CTAs of the split-K kernels that fit on the GPU at once.
+  int split_clusters[MAX_SPLIT + 1] = {0};
   int rb_blocks[2] = {0, 0};  // resident blocks per SM of the RMSNorm backward pass (without, with add)
   void* no_alloc_scratch = nullptr;  // device address of g_no_alloc_scratch
 };
@@ -116,9 +121,9 @@ gemm_epi_status device_state(DeviceState** out, int* dev_out) {
       e = cudaFuncSetAttribute(kDynamic1, cudaFuncAttributeMaxDynamicSharedMemorySize, ge::Smem<1>::BYTES);
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kDynamic2, cudaFuncAttributeMaxDynamicSharedMemorySize, ge::Smem<2>::BYTES);
-      for (int i = 0; i < 4 && e == cudaSuccess; ++i)
-        e = cudaFuncSetAttribute(ge::kDynamicHeads[i / 2][i % 2], cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 i % 2 == 0 ? ge::Smem<1>::BYTES : ge::Smem<2>::BYTES);
+      for (int i = 0; i < 6 && e == cudaSuccess; ++i)
+        e = cudaFuncSetAttribute(ge::kDynamicHeads[i / 3][i % 3], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 i % 3 == 1 ? ge::Smem<2>::BYTES : ge::Smem<1>::BYTES);
       for (int c = 0; c < 2 && e == cudaSuccess; ++c)
         e = cudaFuncSetAttribute(ge::kDynamicFp8[c], cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  c == 0 ? ge::Smem<1>::BYTES : ge::Smem<2>::BYTES);
@@ -131,6 +136,9 @@ gemm_epi_status device_state(DeviceState** out, int* dev_out) {
           if (e == cudaSuccess)
             e = cudaFuncSetAttribute(tab[i].kernel_2sm, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      ge::Smem<2>::BYTES);
+          if (e == cudaSuccess && tab[i].kernel_split)
+            e = cudaFuncSetAttribute(tab[i].kernel_split, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     ge::Smem<1>::BYTES);
         }
       }
       if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
@@ -152,6 +160,17 @@ gemm_epi_status device_state(DeviceState** out, int* dev_out) {
       e = cudaOccupancyMaxActiveClusters(&clusters, kDynamic2, &cfg);
       if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
       d.pair_clusters = clusters;
+      cfg.dynamicSmemBytes = ge::Smem<1>::BYTES;
+      for (int n = 2; n <= MAX_SPLIT; ++n) {
+        attr.val.clusterDim.x = n;
+        cfg.gridDim = dim3(n * d.sms, 1, 1);
+        e = cudaOccupancyMaxActiveClusters(&clusters, ge::kDynamicHeads[0][2], &cfg);
+        if (e != cudaSuccess) {  // a cluster size this device does not take
+          cudaGetLastError();
+          clusters = 0;
+        }
+        d.split_clusters[n] = clusters;
+      }
       for (int add = 0; add < 2; ++add) {
         const void* k = add ? reinterpret_cast<const void*>(&ge::rmsnorm_bwd_kernel<true>)
                             : reinterpret_cast<const void*>(&ge::rmsnorm_bwd_kernel<false>);
@@ -506,6 +525,7 @@ struct Launch {
   ge::KernelParams kp;
   int grid;
   int cg;              // CTAs per tile: 1 (128 x 256) or 2 (a CTA pair, 256 x 256)
+  int split;           // CTAs along K of each 128 x 256 tile, 1 = one loop over all of K
   const void* kernel;  // static kernel of the plan's program, or the interpreting one
 };
 
@@ -518,17 +538,40 @@ int choose_cta_group(const gemm_epi_plan& P, const gemm_epi_args& a, const Devic
   return P.d.M > ge::BLOCK_M ? 2 : 1;
 }
 
+// CTAs along K of a program with HEAD_RMS or ROTARY: 1, or as many as leave
+// the 128 x 256 tiles' clusters resident at once, each CTA MIN_SPLIT_BLOCKS
+// K-blocks, and room in a CTA's operand ring for the partial sums it receives
+// (every other CTA's, of its share of the tile's heads).  So a projection of
+// few rows reads its weights through most SMs, where one CTA per tile left
+// 128 of 152 idle (64 x 4096 -> 6144 columns).
+int choose_split(const gemm_epi_plan& P, const gemm_epi_args& a, const DeviceState& dev) {
+  if (!P.heads() || (a.debug_flags & (GEMM_EPI_DEBUG_FORCE_1SM | GEMM_EPI_DEBUG_FORCE_2SM))) return 1;
+  const int k_step = P.in8 ? 2 * ge::BLOCK_K : ge::BLOCK_K;
+  const int64_t k_blocks = (P.d.K + k_step - 1) / k_step;
+  const int64_t tiles = P.num_m_tiles * P.num_n_tiles * P.batch;
+  const int64_t rows = std::min<int64_t>(ge::BLOCK_M, (P.d.M + 31) / 32 * 32);
+  const int64_t units = ge::BLOCK_N / P.d.head_dim;
+  for (int n = MAX_SPLIT; n >= 2; --n) {
+    const int64_t bytes = (n - 1) * ((units + n - 1) / n) * P.d.head_dim * rows * 4;
+    if (tiles <= dev.split_clusters[n] && k_blocks >= n * MIN_SPLIT_BLOCKS &&
+        bytes <= static_cast<int64_t>(ge::Smem<1>::OFF_EPI))
+      return n;
+  }
+  return 1;
+}
+
 // Fills the kernel parameters and tensor maps of one fused launch.  `c`/`ldc`
 // may differ from the plan's (the unfused baseline stores the bare
 // accumulator into its scratch buffer with a store-only program).
 gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const DeviceState& dev, Launch& L) {
   const gemm_epi_desc& d = P.d;
   std::memset(&L, 0, sizeof L);
-  L.cg = choose_cta_group(P, a, dev);
+  L.split = choose_split(P, a, dev);
+  L.cg = L.split > 1 ? 1 : choose_cta_group(P, a, dev);
   if (P.spec && !(a.debug_flags & GEMM_EPI_DEBUG_FORCE_INTERPRETER))
-    L.kernel = L.cg == 2 ? P.spec->kernel_2sm : P.spec->kernel_1sm;
+    L.kernel = L.split > 1 ? P.spec->kernel_split : L.cg == 2 ? P.spec->kernel_2sm : P.spec->kernel_1sm;
   else if (P.heads())
-    L.kernel = ge::kDynamicHeads[P.in8 ? 1 : 0][L.cg == 2 ? 1 : 0];
+    L.kernel = ge::kDynamicHeads[P.in8 ? 1 : 0][L.split > 1 ? 2 : L.cg == 2 ? 1 : 0];
   else if (P.in8)
     L.kernel = ge::kDynamicFp8[L.cg == 2 ? 1 : 0];
   else
@@ -619,7 +662,11 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
     k.ops[i].i0 = P.ops[i].i0;
     k.ops[i].f0 = P.ops[i].f0;
   }
-  if (L.cg == 2)
+  k.split = L.split;
+  k.split_rows = static_cast<int32_t>(std::min<int64_t>(ge::BLOCK_M, (d.M + 31) / 32 * 32));
+  if (L.split > 1)
+    L.grid = k.num_tiles * L.split;
+  else if (L.cg == 2)
     L.grid = 2 * static_cast<int>(std::min<int64_t>(k.num_tiles, dev.pair_clusters));
   else
     L.grid = static_cast<int>(std::min<int64_t>(k.num_tiles, dev.sms));
@@ -731,16 +778,14 @@ gemm_epi_status launch_fused(const Launch& L, cudaStream_t st) {
   cfg.stream = st;
   cudaLaunchAttribute attr;  // lives until the launch below
   std::memset(&attr, 0, sizeof attr);
-  if (L.cg == 2) {
+  cfg.dynamicSmemBytes = L.cg == 2 ? ge::Smem<2>::BYTES : ge::Smem<1>::BYTES;
+  if (L.cg == 2 || L.split > 1) {
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.x = L.cg == 2 ? 2 : L.split;
     attr.val.clusterDim.y = 1;
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cfg.dynamicSmemBytes = ge::Smem<2>::BYTES;
-  } else {
-    cfg.dynamicSmemBytes = ge::Smem<1>::BYTES;
   }
   void* params[] = {const_cast<CUtensorMap*>(&L.ta), const_cast<CUtensorMap*>(&L.tb),
                     const_cast<CUtensorMap*>(&L.tb2),

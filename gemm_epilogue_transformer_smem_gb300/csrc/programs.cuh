@@ -69,7 +69,8 @@ using ProgNormRotary = StaticProgram<GEMM_EPI_OP_HEAD_RMS, GEMM_EPI_OP_MUL_COL_S
 // One compiled program: its op list (code | pair group << 8), the operand
 // width it was compiled for, its kernels for the 1-SM and 2-SM main loops and
 // its separate-pass kernel for the unfused baseline (NULL if the pass does
-// not cover the program).
+// not cover the program), and, for programs with HEAD_RMS or ROTARY, the kernel
+// that splits K over a cluster.
 struct KernelSpec {
   const char* name;
   int n_ops;
@@ -78,7 +79,16 @@ struct KernelSpec {
   const void* kernel_1sm;
   const void* kernel_2sm;
   const void* kernel_unfused;
+  const void* kernel_split;
 };
+
+template <class Prog, int IN8>
+inline const void* split_kernel_for() {
+  if constexpr (Prog::heads)
+    return reinterpret_cast<const void*>(&fused_gemm_epilogue_kernel<1, Prog, IN8, 1>);
+  else
+    return nullptr;
+}
 
 template <class Prog, int IN8, int... Is>
 inline KernelSpec make_spec(const char* name, std::integer_sequence<int, Is...>) {
@@ -88,7 +98,8 @@ inline KernelSpec make_spec(const char* name, std::integer_sequence<int, Is...>)
                     IN8,
                     reinterpret_cast<const void*>(&fused_gemm_epilogue_kernel<1, Prog, IN8>),
                     reinterpret_cast<const void*>(&fused_gemm_epilogue_kernel<2, Prog, IN8>),
-                    unfused_kernel_for<Prog>()};
+                    unfused_kernel_for<Prog>(),
+                    split_kernel_for<Prog, IN8>()};
 }
 
 template <class Prog, int IN8 = 0>
@@ -108,8 +119,9 @@ extern const int kNumSpecsCommon;
 extern const KernelSpec kSpecsHeads[];
 extern const int kNumSpecsHeads;
 // The interpreting kernels for programs with HEAD_RMS or ROTARY, for bf16 and
-// 8-bit operands (1-SM, 2-SM), from the same translation unit as kSpecsHeads.
-extern const void* const kDynamicHeads[2][2];
+// 8-bit operands (1-SM, 2-SM, K split over a cluster), from the same
+// translation unit as kSpecsHeads.
+extern const void* const kDynamicHeads[2][3];
 // The interpreting kernels for 8-bit operands (1-SM, 2-SM), from the same
 // translation unit as kSpecsFp8.
 extern const void* const kDynamicFp8[2];

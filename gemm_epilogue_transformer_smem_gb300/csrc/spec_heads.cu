@@ -13,10 +13,12 @@ const KernelSpec kSpecsHeads[] = {
 };
 const int kNumSpecsHeads = sizeof(kSpecsHeads) / sizeof(kSpecsHeads[0]);
 
-const void* const kDynamicHeads[2][2] = {
+const void* const kDynamicHeads[2][3] = {
     {reinterpret_cast<const void*>(&fused_gemm_epilogue_kernel<1, DynamicHeadProgram>),
-     reinterpret_cast<const void*>(&fused_gemm_epilogue_kernel<2, DynamicHeadProgram>)},
+     reinterpret_cast<const void*>(&fused_gemm_epilogue_kernel<2, DynamicHeadProgram>),
+     split_kernel_for<DynamicHeadProgram, 0>()},
     {reinterpret_cast<const void*>(&fused_gemm_epilogue_kernel<1, DynamicHeadProgram, 1>),
-     reinterpret_cast<const void*>(&fused_gemm_epilogue_kernel<2, DynamicHeadProgram, 1>)}};
+     reinterpret_cast<const void*>(&fused_gemm_epilogue_kernel<2, DynamicHeadProgram, 1>),
+     split_kernel_for<DynamicHeadProgram, 1>()}};
 
 }  // namespace ge

@@ -312,3 +312,66 @@ def test_allocation_free_run():
     torch.cuda.synchronize()
     y, mag = p.want()
     R.check(p.out.C[..., :p.n], y, mag, torch.bfloat16, 2.0 ** -18)
+
+
+# Few rows and a long K: a cluster of CTAs shares each tile (K split, partial
+# sums exchanged).  m, k, hq, hk, d, rot, layout, batch, b_layout
+SPLIT_CASES = [
+    (1, 4096, 32, 8, 128, 128, "half", 1, "nk"),
+    (64, 2048, 32, 8, 128, 128, "half", 1, "nk"),
+    (128, 1032, 6, 2, 128, 64, "half", 1, "kn"),
+    (130, 2048, 5, 1, 64, 64, "interleaved", 1, "nk"),
+    (300, 1024, 2, 1, 256, 256, "half", 1, "kn"),
+    (33, 520, 7, 3, 32, 32, "half", 1, "nk"),
+    (96, 2056, 1, 0, 64, 64, "half", 1, "nk"),
+    (40, 1024, 2, 1, 128, 128, "half", 3, "nk"),
+]
+
+
+@pytest.mark.parametrize("case", SPLIT_CASES, ids=["%dx%d-h%d+%d-d%d-b%d-%s" % (c[0], c[1], c[2], c[3], c[4], c[7], c[8])
+                                                   for c in SPLIT_CASES])
+@pytest.mark.parametrize("program", [ROT, NORM, ("bias", "head_rms:1e-4", "col_scale", "rotary", "amax", "store_bf16",
+                                                 "store_e4m3", "row_rms", "col_sum")], ids=["rotary", "norm", "all"])
+def test_split_k(case, program):
+    m, k, hq, hk, d, rot, layout, batch, b_layout = case
+    p = Problem(program, m, k, hq, hk, d, rot, layout, batch=batch, b_layout=b_layout)
+    p.run()
+    p.check()
+    got = [t.clone() for t in (p.out.C, p.out.C8, p.out.amax) if t is not None]
+    sums = [t.clone() for t in (p.out.row_out, p.out.col_out) if t is not None]
+    # the sums are exact, so one loop over all of K gives the same bits; the
+    # row and column statistics add in another order
+    p.run(VARIANTS["1sm"])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, [t for t in (p.out.C, p.out.C8, p.out.amax) if t is not None]))
+    for a, b in zip(sums, [t for t in (p.out.row_out, p.out.col_out) if t is not None]):
+        torch.testing.assert_close(a, b, rtol=1e-5, atol=1e-4)
+
+
+def test_split_k_fp8_operands():
+    p = Problem(NORM, 48, 2048, 6, 2, 128, 128, "half", in_type="e4m3")
+    p.run()
+    p.check()
+
+
+def test_split_k_repeats_bit_for_bit():
+    """Values whose sums round: the partial sums are added in a fixed order."""
+    p = Problem(NORM, 64, 4096, 32, 8, 128, 128, "half")
+    p.A = torch.randn(64, 4096, device=DEV).bfloat16()
+    got = []
+    for _ in range(5):
+        p.run()
+        got.append(p.out.C.clone())
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[0], x) for x in got[1:])
+
+
+def test_split_k_wait_that_runs_out_is_reported():
+    """A first load left out: the first CTA's MMA warp waits in vain, every
+    CTA of its cluster still passes the cluster barriers, and the status says
+    so; the next run is clean."""
+    p = Problem(NORM, 64, 2048, 6, 2, 128, 128, "half")
+    p.run(native.GEMM_EPI_DEBUG_SKIP_FIRST_LOAD, timeout_ms=20)
+    assert p.plan.query_status(p.out.workspace) == native.GEMM_EPI_ERR_TIMEOUT
+    p.run()
+    p.check()
