@@ -180,7 +180,8 @@ struct KernelParams {
   uint64_t timeout_ns;
   uint32_t debug_flags;
   // HEAD_RMS and ROTARY (programs with Prog::heads)
-  int32_t head_cols, head_chunks;  // columns of whole heads; 32-column chunks per head
+  int32_t head_cols;                     // columns of whole heads
+  int32_t head_chunks, log_head_chunks;  // 32-column chunks per head
   int32_t head_rms_at, rotary_at;  // their indices in ops, or -1
   int32_t rot_pairs, rot_half;     // rotated pairs per head; 1: pairs (i, i + rot_pairs)
   float head_inv_dim, head_eps, rot_amplitude;
@@ -286,6 +287,12 @@ __host__ __device__ constexpr int prog_expand_g() {
 template <class Prog>
 __host__ __device__ constexpr int prog_index_of(int code) {
   if constexpr (Prog::is_static) return Prog::index_of(code); else return -1;
+}
+// Programs with heads whose column vectors go through shared memory: compiled,
+// without the e4m3 store whose buffers these are.
+template <class Prog>
+__host__ __device__ constexpr bool prog_stages_columns() {
+  if constexpr (Prog::is_static) return Prog::heads && !Prog::has(GEMM_EPI_OP_STORE_E4M3); else return false;
 }
 // First op applied to output columns: after the pair, expanding or head ops.
 template <class Prog>
@@ -712,41 +719,61 @@ __device__ __forceinline__ void dswiglu_expand(const float (&dh)[16], const floa
   }
 }
 
-// Rotates 32 pairs (a[j], b[j]), pair pair0 + j of the head, by `position`.
-__device__ __forceinline__ void rotate_halves(const KernelParams& p, int64_t position, int pair0, float (&a)[32],
-                                              float (&b)[32]) {
-#pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    float c, s;
-    turn_cos_sin<true>(phase_bits(position, __ldg(p.rot_steps + pair0 + j)), c, s);
-    c *= p.rot_amplitude;
-    s *= p.rot_amplitude;
-    const float x = a[j], y = b[j];
-    a[j] = fmaf(x, c, -(y * s));
-    b[j] = fmaf(y, c, x * s);
-  }
-}
+// cos and sin of a row's position for up to 32 pairs of a head, two pairs to a
+// float2.
+struct RowAngles {
+  float2 c[16], s[16];
 
-// The same on the 16 pairs inside a 32-column chunk that starts at pair pair0
-// of the head: (2j, 2j + 1) or, HALF, (j, j + 16).  Pairs past the rotated
-// part stay.
-template <bool HALF>
-__device__ __forceinline__ void rotate_chunk(const KernelParams& p, int64_t position, int pair0, float (&v)[32]) {
+  // Pairs pair0 .. pair0 + NP - 1; WHOLE: all of them rotate, else those past
+  // the rotated part stay as they are.  Every step is read before the first is
+  // used: one latency, not one for each.
+  template <int NP, bool WHOLE>
+  __device__ __forceinline__ void set(const KernelParams& p, int64_t position, int pair0) {
+    uint64_t st[NP];
+    if constexpr (WHOLE) {
+      const ulonglong2* src = reinterpret_cast<const ulonglong2*>(p.rot_steps + pair0);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if (pair0 + j < p.rot_pairs) {
-      float c, s;
-      turn_cos_sin<true>(phase_bits(position, __ldg(p.rot_steps + pair0 + j)), c, s);
-      c *= p.rot_amplitude;
-      s *= p.rot_amplitude;
-      float& a = v[HALF ? j : 2 * j];
-      float& b = v[HALF ? j + 16 : 2 * j + 1];
-      const float x = a, y = b;
-      a = fmaf(x, c, -(y * s));
-      b = fmaf(y, c, x * s);
+      for (int i = 0; i < NP / 2; ++i) {
+        const ulonglong2 q = __ldg(src + i);
+        st[2 * i] = q.x;
+        st[2 * i + 1] = q.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) st[i] = __ldg(p.rot_steps + min(pair0 + i, p.rot_pairs - 1));
+    }
+#pragma unroll
+    for (int i = 0; i < NP / 2; ++i) {
+      turn_cos_sin<true>(phase_bits(position, st[2 * i]), c[i].x, s[i].x);
+      turn_cos_sin<true>(phase_bits(position, st[2 * i + 1]), c[i].y, s[i].y);
+    }
+    if (p.rot_amplitude != 1.0f) {
+      const float2 amp = splat2(p.rot_amplitude);
+#pragma unroll
+      for (int i = 0; i < NP / 2; ++i) {
+        c[i] = __fmul2_rn(c[i], amp);
+        s[i] = __fmul2_rn(s[i], amp);
+      }
+    }
+    if constexpr (!WHOLE) {
+#pragma unroll
+      for (int i = 0; i < NP / 2; ++i) {
+        if (pair0 + 2 * i >= p.rot_pairs) c[i].x = 1.0f, s[i].x = 0.0f;
+        if (pair0 + 2 * i + 1 >= p.rot_pairs) c[i].y = 1.0f, s[i].y = 0.0f;
+      }
     }
   }
-}
+  // Pairs 2i and 2i + 1: (a, b) -> (a c - b s, b c + a s).
+  __device__ __forceinline__ void rotate(int i, float& a0, float& a1, float& b0, float& b1) const {
+    const float2 a = make_float2(a0, a1), b = make_float2(b0, b1);
+    const float2 bs = __fmul2_rn(b, s[i]);
+    const float2 nb = __ffma2_rn(a, s[i], __fmul2_rn(b, c[i]));
+    a0 = fmaf(a.x, c[i].x, -bs.x);
+    a1 = fmaf(a.y, c[i].y, -bs.y);
+    b0 = nb.x;
+    b1 = nb.y;
+  }
+};
 
 // This thread's 32 auxiliary bf16 values of row m, columns col0.. (zeros
 // outside the tensor), straight from global memory.
@@ -844,12 +871,12 @@ __device__ __forceinline__ float tmem_column_sums(const float (&s)[32], bool row
 //
 // SPLIT = 1 (CG = 1): few rows make few tiles, so a cluster of p.split CTAs
 // shares one tile, each over its part of K, and the grid still covers the SMs
-// that read the weights.  The heads of the tile (p.head_chunks chunks each)
-// are dealt out to the CTAs: once every main loop of the cluster is done, each
-// CTA writes its partial sums of the others' heads into their shared memory
-// (the operand rings, idle by then), adds the ones it received to its own
-// accumulator in a fixed order and runs the program on its heads.  One tile
-// per cluster.
+// that read the weights.  The tile's heads (p.head_chunks chunks each), by
+// slabs of 32 rows, are dealt out to the CTAs: once every main loop of the
+// cluster is done, each CTA writes its partial sums of the others' pieces into
+// their shared memory (the operand rings, idle by then), adds the ones it
+// received to its own accumulator in a fixed order and runs the program on its
+// pieces.  One tile per cluster.
 template <int CG, class Prog, int IN8 = 0, int SPLIT = 0>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fused_gemm_epilogue_kernel(const __grid_constant__ CUtensorMap tm_a,
@@ -1128,6 +1155,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t e80 = sbase + L::OFF_E8 + ew * E8_BUFS * E8_BUF_BYTES;
     uint8_t* epi0_ptr = smem + L::OFF_EPI + ew * EPI_BUFS * EPI_BUF_BYTES;
     uint8_t* e80_ptr = smem + L::OFF_E8 + ew * E8_BUFS * E8_BUF_BYTES;
+    constexpr bool kStaged = prog_stages_columns<Prog>();
+    float* staged_cols = reinterpret_cast<float*>(e80_ptr);  // column scales, then biases, of the tile
     // HEAD_RMS and ROTARY: ops [0, head_first) run on the accumulator, [mid, mid_end)
     // between the two, the rest after them.
     const int head_rms_at = kStatic ? prog_index_of<Prog>(GEMM_EPI_OP_HEAD_RMS) : Prog::heads ? p.head_rms_at : -1;
@@ -1164,91 +1193,153 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint4 xa[4];
       if (flags & F_AUX) load_aux_row(xa, p, aux_b, m, row_ok, n0);
 
+      // With heads, while the main loop runs: the row's position, the angles of
+      // the first chunks, and the tile's column vectors, which compiled
+      // programs read from the warp's e4m3 staging buffers (they have no e4m3
+      // store); a first read of any of these from L2 between two chunks would
+      // cost as much as a chunk.
+      int64_t position = m;
+      RowAngles angles;
+      int angles_of = -1;
+      if constexpr (Prog::heads) {
+        if (rotary_at >= 0 && p.positions != nullptr && row_ok)
+          position = p.positions_64 ? __ldg(static_cast<const long long*>(p.positions) + row_base + m)
+                                    : __ldg(static_cast<const int*>(p.positions) + row_base + m);
+        if constexpr (kStaged) {
+          auto stage = [&](const float* src, float none, float* dst) {
+            const int col = nacc0 + lane * 8;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = none;
+            if (col + 8 <= p.N) {
+              const float4 a = __ldg(reinterpret_cast<const float4*>(src + col));
+              const float4 b = __ldg(reinterpret_cast<const float4*>(src + col) + 1);
+              v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (col + j < p.N) v[j] = __ldg(src + col + j);
+            }
+            float4* d = reinterpret_cast<float4*>(dst + lane * 8);
+            d[0] = make_float4(v[0], v[1], v[2], v[3]);
+            d[1] = make_float4(v[4], v[5], v[6], v[7]);
+          };
+          __syncwarp();  // the previous tile's reads
+          if (Prog::has(GEMM_EPI_OP_MUL_COL_SCALE)) stage(p.col_scale, 1.0f, staged_cols);
+          if (Prog::has(GEMM_EPI_OP_ADD_BIAS_COL)) stage(p.bias, 0.0f, staged_cols + BLOCK_N);
+          __syncwarp();
+          if (rotary_at >= 0 && nacc0 < p.head_cols) {
+            if (p.rot_half && p.rot_pairs >= 32)
+              angles.template set<32, true>(p, position, 0);
+            else
+              angles.template set<16, false>(p, position, 0);
+            angles_of = 0;
+          }
+        }
+      }
+
       // All lanes wait; the outcome is made warp-uniform so that no lane
       // leaves while the others enter a warp-synchronous step.
       ok = __all_sync(0xffffffffu, wait_bar<CG>(bar(BAR_TFULL + buf), use & 1u, abort_flag, p, W_EPI_TMEM_FULL));
       if (!SPLIT && !ok) break;
       ptx::tc_fence_after_sync();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + buf * BLOCK_N;
+      uint32_t own_units = 0;  // SPLIT: the tile's heads whose rows of this warp are this CTA's
       if constexpr (SPLIT) {
         // The cluster barriers are passed by every warp of every CTA, also
         // after a wait that ran out (all waits before them are bounded).
-        const uint32_t piece = static_cast<uint32_t>(p.split_rows) * 16u;  // 4 columns of all rows
-        const uint32_t unit_bytes = static_cast<uint32_t>(p.head_chunks) * 8u * piece;
-        const int units = chunks / p.head_chunks, per_rank = (units + split - 1) / split;
-        const uint32_t row_at = sbase + static_cast<uint32_t>(quad * 32 + lane) * 16u;
+        // Piece i = head * slabs + this warp's 32-row slab is CTA (i % split)'s, its
+        // (i / split)-th; a row's 4 columns are 16 bytes, neighbouring lanes
+        // neighbouring rows.
+        const uint32_t piece_bytes = static_cast<uint32_t>(p.head_chunks) * 8u * 512u;
+        const int slabs = p.split_rows >> 5, units = 8 >> p.log_head_chunks;
+        const uint32_t slots = static_cast<uint32_t>((units * slabs + split - 1) / split);
         __syncwarp();
         ptx::cluster_sync();  // every operand ring of the cluster is idle
         if (ok && slab_ok) {
-          for (int c = 0; c < chunks; ++c) {
-            const int u = c / p.head_chunks, owner = u % split;
-            if (owner == krank) continue;
-            uint32_t r[32];
-            ptx::tmem_ld32_sync(t_row + c * 32, r);
-            const int src = krank < owner ? krank : krank - 1;
-            const uint32_t at = ptx::mapa_shared(row_at, owner) + (src * per_rank + u / split) * unit_bytes +
-                                static_cast<uint32_t>(c - u * p.head_chunks) * 8u * piece;
-            if (row_ok) {
+          for (int u = 0; u < units; ++u) {
+            const int i = u * slabs + quad, nth = i / split, owner = i - nth * split;
+            if (owner == krank) {
+              own_units |= 1u << u;
+              continue;
+            }
+            const uint32_t src = krank < owner ? krank : krank - 1;
+            uint32_t at = ptx::mapa_shared(sbase + lane * 16u, owner) + (src * slots + nth) * piece_bytes;
+            for (int k = 0; k < p.head_chunks; ++k, at += 8u * 512u) {
+              uint32_t r[32];
+              ptx::tmem_ld32_sync(t_row + ((u << p.log_head_chunks) + k) * 32, r);
+              if (row_ok) {
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                ptx::st_shared_cluster_v4(at + q * piece, __uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                          __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+                for (int q = 0; q < 8; ++q)
+                  ptx::st_shared_cluster_v4(at + q * 512u, __uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                            __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+              }
+              __syncwarp();
             }
           }
         }
-        __syncwarp();
         ptx::cluster_sync();  // every partial sum is in place
         if (!ok) break;
-        if (slab_ok) {
-          for (int c = 0; c < chunks; ++c) {
-            const int u = c / p.head_chunks;
-            if (u % split != krank) continue;
+        for (int u = 0; u < units; ++u) {
+          if (!((own_units >> u) & 1u)) continue;
+          const uint8_t* got = smem + lane * 16u + (u * slabs + quad) / split * piece_bytes;
+          for (int k = 0; k < p.head_chunks; ++k, got += 8u * 512u) {
+            const uint32_t at = t_row + ((u << p.log_head_chunks) + k) * 32;
             uint32_t r[32];
-            ptx::tmem_ld32_sync(t_row + c * 32, r);
-            const uint8_t* got = smem + static_cast<uint32_t>(quad * 32 + lane) * 16u + (u / split) * unit_bytes +
-                                 static_cast<uint32_t>(c - u * p.head_chunks) * 8u * piece;
-            for (int src = 0; row_ok && src < split - 1; ++src) {
+            ptx::tmem_ld32_sync(at, r);
+            if (row_ok) {
+              for (int src = 0; src < split - 1; ++src) {
+                float4 v[8];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const float4 v = *reinterpret_cast<const float4*>(got + src * per_rank * unit_bytes + q * piece);
-                r[4 * q] = __float_as_uint(__uint_as_float(r[4 * q]) + v.x);
-                r[4 * q + 1] = __float_as_uint(__uint_as_float(r[4 * q + 1]) + v.y);
-                r[4 * q + 2] = __float_as_uint(__uint_as_float(r[4 * q + 2]) + v.z);
-                r[4 * q + 3] = __float_as_uint(__uint_as_float(r[4 * q + 3]) + v.w);
+                for (int q = 0; q < 8; ++q)
+                  v[q] = *reinterpret_cast<const float4*>(got + src * slots * piece_bytes + q * 512u);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                  r[4 * q] = __float_as_uint(__uint_as_float(r[4 * q]) + v[q].x);
+                  r[4 * q + 1] = __float_as_uint(__uint_as_float(r[4 * q + 1]) + v[q].y);
+                  r[4 * q + 2] = __float_as_uint(__uint_as_float(r[4 * q + 2]) + v[q].z);
+                  r[4 * q + 3] = __float_as_uint(__uint_as_float(r[4 * q + 3]) + v[q].w);
+                }
               }
             }
             __syncwarp();
-            ptx::tmem_st32_sync(t_row + c * 32, r);
+            ptx::tmem_st32_sync(at, r);
           }
         }
       }
       float row_ss = 0.0f;
 
-      // This row's position; the head in hand: its 1 / rms, and the second
-      // chunk of a rotated pair of chunks, until its turn.
-      int64_t position = m;
-      float head_r = 1.0f;
+      // HEAD_RMS and ROTARY: the tile's heads in lockstep, so that a row's
+      // angles are worked out once for all of them.  1 / rms of each head; the
+      // second chunk of a rotated pair of chunks, until its turn.
+      float head_r[Prog::heads ? 8 : 1];
       float held[Prog::heads ? 32 : 1];
-      if constexpr (Prog::heads) {
-        if (rotary_at >= 0 && p.positions != nullptr && row_ok)
-          position = p.positions_64 ? __ldg(static_cast<const long long*>(p.positions) + row_base + m)
-                                    : __ldg(static_cast<const int*>(p.positions) + row_base + m);
-      }
 
       uint32_t done_chunks = 0;
       for (int ci = 0; ci < chunks; ++ci) {
-        if constexpr (SPLIT) {  // another CTA of the cluster has this head
-          if (ci / p.head_chunks % split != krank) continue;
+        // Chunk of the tile: in order, or with heads chunk `in_head` of head
+        // `unit`: first the rotated part in the half layout, whose chunks come
+        // in pairs (i, i + half), head by head, then the other chunks.
+        int c = ci, unit = 0, in_head = 0;
+        bool in_pair = false, second = false;
+        const int rot_half_chunks = Prog::heads && p.rot_half && rotary_at >= 0 ? p.rot_pairs >> 5 : 0;
+        if constexpr (Prog::heads) {
+          const int log_units = 3 - p.log_head_chunks, units = 1 << log_units;
+          in_pair = ci < 2 * rot_half_chunks * units;
+          if (in_pair) {
+            unit = (ci >> 1) & (units - 1);
+            second = (ci & 1) != 0;
+            in_head = (ci >> (1 + log_units)) + (second ? rot_half_chunks : 0);
+          } else {
+            const int k = ci - 2 * rot_half_chunks * units;
+            unit = k & (units - 1);
+            in_head = 2 * rot_half_chunks + (k >> log_units);
+          }
+          c = (unit << p.log_head_chunks) + in_head;
+          if (SPLIT && !((own_units >> unit) & 1u)) continue;  // another CTA of the cluster has it
         }
         const uint32_t g = gchunk + done_chunks++;
         const uint32_t eb = g % EPI_BUFS;
-        // Chunk of the tile: in order, but for the rotated part of a head in
-        // the half layout, whose chunks come in pairs (i, i + half).
-        int c = ci;
-        const int in_head = Prog::heads ? ci & (p.head_chunks - 1) : 0;
-        const int rot_half_chunks = Prog::heads && p.rot_half && rotary_at >= 0 ? p.rot_pairs >> 5 : 0;
-        const bool in_pair = Prog::heads && nacc0 + ci * CHUNK < p.head_cols && in_head < 2 * rot_half_chunks;
-        if (Prog::heads && in_pair) c = ci - in_head + (in_head >> 1) + (in_head & 1) * rot_half_chunks;
         const int col0 = n0 + c * CHUNK;  // first output column of the chunk
         float v[32];
 
@@ -1278,6 +1369,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         } else if constexpr (Prog::heads) {
           const int head_first = head_rms_at >= 0 ? head_rms_at : rotary_at;
+          // An op on accumulator chunk cc, its column vector staged or not.
+          auto column_op = [&](auto code, int cc, float (&u)[32]) {
+            if constexpr (kStaged && code == GEMM_EPI_OP_MUL_COL_SCALE) {
+              const float4* c4 = reinterpret_cast<const float4*>(staged_cols) + cc * 8;
+              for_pairs(u, [&](float2 y, int i) {
+                const float4 c = c4[i / 2];
+                return __fmul2_rn(y, (i & 1) ? make_float2(c.z, c.w) : make_float2(c.x, c.y));
+              });
+            } else if constexpr (kStaged && code == GEMM_EPI_OP_ADD_BIAS_COL) {
+              const float4* b4 = reinterpret_cast<const float4*>(staged_cols + BLOCK_N) + cc * 8;
+              for_pairs(u, [&](float2 y, int i) {
+                const float4 c = b4[i / 2];
+                return __fadd2_rn(y, (i & 1) ? make_float2(c.z, c.w) : make_float2(c.x, c.y));
+              });
+            } else {
+              apply_pointwise<32>(code, u, p, nacc0 + cc * 32, p.N, rs_m);
+            }
+          };
           // Accumulator chunk cc with the ops before HEAD_RMS (and ROTARY).
           auto load_acc = [&](int cc, float (&u)[32]) {
             if (flags & F_ZERO_ACC) {
@@ -1296,8 +1405,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if constexpr (kStatic) {
               constexpr int n = prog_index_of<Prog>(GEMM_EPI_OP_HEAD_RMS), r = prog_index_of<Prog>(GEMM_EPI_OP_ROTARY);
               static_for<0, (n >= 0 ? n : r)>([&](auto I) {
-                apply_pointwise<32>(std::integral_constant<int, Prog::code_of(decltype(I)::value)>{}, u, p,
-                                    nacc0 + cc * 32, p.N, rs_m);
+                column_op(std::integral_constant<int, Prog::code_of(decltype(I)::value)>{}, cc, u);
               });
             } else {
               for (int i = 0; i < head_first; ++i) apply_pointwise<32>(p.ops[i].code, u, p, nacc0 + cc * 32, p.N, rs_m);
@@ -1305,16 +1413,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           };
           // What follows it up to ROTARY: the head's 1 / rms (1 where there is
           // no head) and the ops between the two.
+          const bool head = nacc0 + (unit << p.log_head_chunks) * CHUNK < p.head_cols;
+          float hr = 1.0f;
           auto scale_acc = [&](int cc, float (&u)[32]) {
             if (head_rms_at >= 0) {
-              const float2 r2 = splat2(head_r);
+              const float2 r2 = splat2(hr);
               for_pairs(u, [&](float2 y, int) { return __fmul2_rn(y, r2); });
               if constexpr (kStatic) {
                 constexpr int n = prog_index_of<Prog>(GEMM_EPI_OP_HEAD_RMS),
                               r = prog_index_of<Prog>(GEMM_EPI_OP_ROTARY);
                 static_for<(n >= 0 && r >= 0 ? n + 1 : 0), (n >= 0 && r >= 0 ? r : 0)>([&](auto I) {
-                  apply_pointwise<32>(std::integral_constant<int, Prog::code_of(decltype(I)::value)>{}, u, p,
-                                      nacc0 + cc * 32, p.N, rs_m);
+                  column_op(std::integral_constant<int, Prog::code_of(decltype(I)::value)>{}, cc, u);
                 });
               } else {
                 for (int i = head_rms_at + 1; i < rotary_at; ++i)
@@ -1322,38 +1431,66 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               }
             }
           };
-          const bool head = nacc0 + ci * CHUNK < p.head_cols;  // the same for every chunk of a head
-          if (head_rms_at >= 0 && in_head == 0) {
-            // A row of the head is in this thread's TMEM lane, so its sum of
-            // squares is a first pass over the head's chunks.
-            head_r = 1.0f;
-            if (head) {
+          if (head_rms_at >= 0) {
+            if (in_head == 0 && head) {
+              // A row of the head is in this thread's TMEM lane, so its sum of
+              // squares is a first pass over the head's chunks.
               float2 ss = make_float2(0.0f, 0.0f);
               for (int k = 0; k < p.head_chunks; ++k) {
-                load_acc(ci + k, v);
+                load_acc(c + k, v);
                 for_pairs(v, [&](float2 y, int) {
                   ss = __ffma2_rn(y, y, ss);
                   return y;
                 });
               }
-              head_r = 1.0f / sqrtf(fmaf(ss.x + ss.y, p.head_inv_dim, p.head_eps));
+              const float r = rsqrtf(fmaf(ss.x + ss.y, p.head_inv_dim, p.head_eps));
+#pragma unroll
+              for (int k = 0; k < 8; ++k) head_r[k] = k == unit ? r : head_r[k];
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) hr = head && k == unit ? head_r[k] : hr;
           }
-          if (in_pair && (in_head & 1)) {
+          if (in_pair && second) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = held[j];
           } else {
             load_acc(c, v);
             scale_acc(c, v);
+            if (in_pair) {
+              load_acc(c + rot_half_chunks, held);
+              scale_acc(c + rot_half_chunks, held);
+            }
             if (rotary_at >= 0 && head) {
+              // The first head of a chunk works its angles out for the others;
+              // the interpreter, whose registers they would not fit in, for
+              // eight pairs at a time as it turns them.
+              constexpr int KEPT = kStatic ? 32 : 8;
               if (in_pair) {
-                load_acc(c + rot_half_chunks, held);
-                scale_acc(c + rot_half_chunks, held);
-                rotate_halves(p, position, (in_head >> 1) * 32, v, held);
-              } else if (p.rot_half) {
-                if (in_head == 0 && p.rot_pairs == 16) rotate_chunk<true>(p, position, 0, v);
-              } else {
-                rotate_chunk<false>(p, position, in_head * 16, v);
+#pragma unroll
+                for (int i = 0; i < 16; i += KEPT / 2) {
+                  if (!kStatic || angles_of != in_head) angles.template set<KEPT, true>(p, position, in_head * 32 + 2 * i);
+#pragma unroll
+                  for (int j = 0; j < KEPT / 2; ++j)
+                    angles.rotate(j, v[2 * (i + j)], v[2 * (i + j) + 1], held[2 * (i + j)], held[2 * (i + j) + 1]);
+                }
+                angles_of = in_head;
+              } else if (p.rot_half ? in_head == 0 && p.rot_pairs == 16 : in_head * 16 < p.rot_pairs) {
+                // pairs within the chunk: (j, j + 16) or (2j, 2j + 1)
+                constexpr int KEPT16 = kStatic ? 16 : 8;
+#pragma unroll
+                for (int i = 0; i < 8; i += KEPT16 / 2) {
+                  if (!kStatic || angles_of != in_head)
+                    angles.template set<KEPT16, false>(p, position, in_head * 16 + 2 * i);
+#pragma unroll
+                  for (int j = 0; j < KEPT16 / 2; ++j) {
+                    const int k = i + j;
+                    if (p.rot_half)
+                      angles.rotate(j, v[2 * k], v[2 * k + 1], v[16 + 2 * k], v[17 + 2 * k]);
+                    else
+                      angles.rotate(j, v[4 * k], v[4 * k + 2], v[4 * k + 1], v[4 * k + 3]);
+                  }
+                }
+                angles_of = in_head;
               }
             }
           }

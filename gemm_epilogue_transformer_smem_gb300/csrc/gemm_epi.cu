@@ -541,7 +541,7 @@ int choose_cta_group(const gemm_epi_plan& P, const gemm_epi_args& a, const Devic
 // CTAs along K of a program with HEAD_RMS or ROTARY: 1, or as many as leave
 // the 128 x 256 tiles' clusters resident at once, each CTA MIN_SPLIT_BLOCKS
 // K-blocks, and room in a CTA's operand ring for the partial sums it receives
-// (every other CTA's, of its share of the tile's heads).  So a projection of
+// (every other CTA's, of its pieces).  So a projection of
 // few rows reads its weights through most SMs, where one CTA per tile left
 // 128 of 152 idle (64 x 4096 -> 6144 columns).
 int choose_split(const gemm_epi_plan& P, const gemm_epi_args& a, const DeviceState& dev) {
@@ -549,10 +549,10 @@ int choose_split(const gemm_epi_plan& P, const gemm_epi_args& a, const DeviceSta
   const int k_step = P.in8 ? 2 * ge::BLOCK_K : ge::BLOCK_K;
   const int64_t k_blocks = (P.d.K + k_step - 1) / k_step;
   const int64_t tiles = P.num_m_tiles * P.num_n_tiles * P.batch;
-  const int64_t rows = std::min<int64_t>(ge::BLOCK_M, (P.d.M + 31) / 32 * 32);
-  const int64_t units = ge::BLOCK_N / P.d.head_dim;
+  const int64_t slabs = std::min<int64_t>(ge::BLOCK_M, P.d.M + 31) / 32;
+  const int64_t pieces = ge::BLOCK_N / P.d.head_dim * slabs;  // heads of a tile by slabs of 32 rows
   for (int n = MAX_SPLIT; n >= 2; --n) {
-    const int64_t bytes = (n - 1) * ((units + n - 1) / n) * P.d.head_dim * rows * 4;
+    const int64_t bytes = (n - 1) * ((pieces + n - 1) / n) * P.d.head_dim * 32 * 4;
     if (tiles <= dev.split_clusters[n] && k_blocks >= n * MIN_SPLIT_BLOCKS &&
         bytes <= static_cast<int64_t>(ge::Smem<1>::OFF_EPI))
       return n;
@@ -648,6 +648,7 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
   if (P.heads()) {
     k.head_cols = static_cast<int32_t>(d.head_cols);
     k.head_chunks = d.head_dim / ge::CHUNK;
+    while ((1 << k.log_head_chunks) < k.head_chunks) ++k.log_head_chunks;
     k.head_inv_dim = 1.0f / static_cast<float>(d.head_dim);
     k.head_eps = P.head_eps;
     k.rot_pairs = d.rotary_dim / 2;
@@ -739,9 +740,9 @@ gemm_epi_status check_args(const gemm_epi_plan& P, const gemm_epi_args& a) {
     if (P.uses_preact && (s = need(a.preact, "preact"))) return s;
     if (P.rotary_at >= 0) {
       if (!a.rotary_steps) return fail(GEMM_EPI_ERR_INVALID_VALUE, "rotary_steps is NULL but the program uses it");
-      if ((reinterpret_cast<uintptr_t>(a.rotary_steps) & 7u) ||
+      if (!aligned16(a.rotary_steps) ||
           (reinterpret_cast<uintptr_t>(a.positions) & (a.positions_64 ? 7u : 3u)))
-        return fail(GEMM_EPI_ERR_MISALIGNED, "rotary_steps or positions is not aligned to its element size");
+        return fail(GEMM_EPI_ERR_MISALIGNED, "rotary_steps is not 16-byte aligned or positions not to its element size");
       if (!std::isfinite(a.rotary_amplitude))
         return fail(GEMM_EPI_ERR_INVALID_VALUE, "rotary_amplitude must be finite");
     }

@@ -18,10 +18,15 @@ __device__ __forceinline__ int32_t phase_bits(int64_t position, uint64_t step) {
   return static_cast<int32_t>((static_cast<uint64_t>(position) * step) >> 32);
 }
 
-// cos and sin of a phase by the special-function unit, off by about 2^-21: for
-// bf16 results, which keep 8 bits, so that their rounding hides it.
+// cos and sin of a phase by the special-function unit: for bf16 results, which
+// keep 8 bits.  The unit is off by about 2^-21 on [-pi, pi], and the phase's
+// top 23 bits, placed in the mantissa of a float in [2, 4) (an int-to-float
+// conversion would take the same unit as sin and cos), by 2 pi 2^-24: 2^-20
+// together.
 __device__ __forceinline__ void phase_cos_sin_fast(int32_t phase, float& c, float& s) {
-  const float angle = static_cast<float>(phase) * 1.4629180792671596e-9f;  // 2 pi 2^-32
+  const uint32_t top = (static_cast<uint32_t>(phase) ^ 0x80000000u) >> 9;  // half a turn on, unsigned
+  const float half_turns = __uint_as_float(0x40000000u | top) - 3.0f;      // [-1, 1)
+  const float angle = half_turns * 3.14159265358979f;
   c = __cosf(angle);
   s = __sinf(angle);
 }

@@ -265,7 +265,8 @@ typedef struct gemm_epi_args {
     const float *a_scale_inv;
     const float *b_scale_inv;
     const float *col_scale;   /* MUL_COL_SCALE: fp32, one value per column at its point of use */
-    const uint64_t *rotary_steps;  /* ROTARY: device, rotary_dim / 2 values of gemm_epi_rotary_steps */
+    const uint64_t *rotary_steps;  /* ROTARY: device, rotary_dim / 2 values of gemm_epi_rotary_steps,
+                                      16-byte aligned */
     const void *positions;    /* ROTARY: device int32 / int64, M values per batch; NULL: row m is at position m */
     int32_t positions_64;     /* 1: int64 positions */
     float rotary_amplitude;   /* ROTARY: factor of the rotated part, usually 1 */

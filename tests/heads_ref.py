@@ -6,7 +6,7 @@ bf16 and 2^-24 for fp32.  Before that:
   - cos and sin: the angle is off by at most half an ulp of half a turn
     (2 pi 2^-26) plus the rounding of its product with 2 pi; the
     special-function unit (bf16) by 2^-20.9, the accurate functions (fp32) by
-    two ulp.  Together below 2^-20, which multiplies |a| + |b| of the pair.
+    two ulp.  Together at most 2^-20, which multiplies |a| + |b| of the pair.
   - r: a sum of at most 512 squares, 16 values in a lane and 5 shuffles, 21
     additions deep: below 2^-19 of r, and the same for mean(g w x r) of the
     sum of its magnitudes; the products around them add a few 2^-24.
