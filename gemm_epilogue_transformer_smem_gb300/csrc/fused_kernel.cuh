@@ -863,6 +863,13 @@ __device__ __forceinline__ float tmem_column_sums(const float (&s)[32], bool row
   return p[0];
 }
 
+// Clears the workspace of a program with heads: its kernel is launched as a
+// dependent of this one, so that its setup does not wait for a memset.
+static __global__ void clear_workspace_kernel(uint4* ws, int n) {
+  ptx::launch_dependents();
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) ws[i] = make_uint4(0, 0, 0, 0);
+}
+
 // ------------------------------------------------------------------ kernel
 
 // IN8 = 1: 8-bit operands (tcgen05 kind::f8f6f4); a K block is still one
@@ -942,6 +949,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     ptx::tma_prefetch_desc(&tm_a);
     ptx::tma_prefetch_desc(&tm_b);
   }
+  // The launch before this one clears the workspace (the kernel's setup so far
+  // ran beside it); what ran before that is complete.
+  if (Prog::heads) ptx::wait_dependencies();
   ptx::tc_fence_before_sync();
   if (CG == 2)
     ptx::cluster_sync();  // the peer's barriers are initialised before anyone signals them

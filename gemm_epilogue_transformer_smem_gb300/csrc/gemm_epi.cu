@@ -762,31 +762,43 @@ gemm_epi_status check_args(const gemm_epi_plan& P, const gemm_epi_args& a) {
 // Zeroes what the kernels accumulate into: status words and row counters,
 // amax, row sums, column sums.
 gemm_epi_status clear_outputs(const gemm_epi_plan& P, const gemm_epi_args& a, cudaStream_t st) {
-  cudaError_t e = cudaMemsetAsync(a.workspace, 0, P.ws_bytes, st);
+  cudaError_t e = cudaSuccess;
+  if (!P.heads()) e = cudaMemsetAsync(a.workspace, 0, P.ws_bytes, st);
   if (e == cudaSuccess && (P.flags & ge::F_AMAX)) e = cudaMemsetAsync(a.amax, 0, sizeof(float), st);
   if (e == cudaSuccess && (P.flags & ge::F_ROW) && P.d.M > 0)
     e = cudaMemsetAsync(a.row_out, 0, sizeof(float) * P.d.M * P.batch, st);
   if (e == cudaSuccess && (P.flags & ge::F_COL) && P.n_out > 0)
     e = cudaMemsetAsync(a.col_out, 0, sizeof(float) * P.n_out * P.batch, st);
+  if (e == cudaSuccess && P.heads()) {
+    const int n = static_cast<int>(P.ws_bytes / 16), threads = std::min(n, 256);
+    ge::clear_workspace_kernel<<<std::min(64, (n + threads - 1) / threads), threads, 0, st>>>(
+        static_cast<uint4*>(a.workspace), n);
+    e = cudaGetLastError();
+  }
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "cudaMemsetAsync");
 }
 
-gemm_epi_status launch_fused(const Launch& L, cudaStream_t st) {
+gemm_epi_status launch_fused(const Launch& L, cudaStream_t st, bool dependent) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3(L.grid, 1, 1);
   cfg.blockDim = dim3(ge::NUM_THREADS, 1, 1);
   cfg.stream = st;
-  cudaLaunchAttribute attr;  // lives until the launch below
-  std::memset(&attr, 0, sizeof attr);
+  cudaLaunchAttribute attrs[2];  // live until the launch below
+  std::memset(attrs, 0, sizeof attrs);
+  cfg.attrs = attrs;
   cfg.dynamicSmemBytes = L.cg == 2 ? ge::Smem<2>::BYTES : ge::Smem<1>::BYTES;
   if (L.cg == 2 || L.split > 1) {
+    cudaLaunchAttribute& attr = attrs[cfg.numAttrs++];
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = L.cg == 2 ? 2 : L.split;
     attr.val.clusterDim.y = 1;
     attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+  }
+  if (dependent) {
+    cudaLaunchAttribute& attr = attrs[cfg.numAttrs++];
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
   }
   void* params[] = {const_cast<CUtensorMap*>(&L.ta), const_cast<CUtensorMap*>(&L.tb),
                     const_cast<CUtensorMap*>(&L.tb2),
@@ -839,7 +851,7 @@ gemm_epi_status gemm_epi_run(gemm_epi_handle h, const gemm_epi_args* args, void*
   if (h->d.M == 0 || h->n_out == 0) return GEMM_EPI_OK;
   Launch L;
   if ((s = prepare(*h, *args, *dev, L))) return s;
-  return launch_fused(L, st);
+  return launch_fused(L, st, h->heads());
 }
 
 gemm_epi_status gemm_epi_run_unfused(gemm_epi_handle h, const gemm_epi_args* args, void* scratch,
@@ -881,7 +893,7 @@ gemm_epi_status gemm_epi_run_unfused(gemm_epi_handle h, const gemm_epi_args* arg
   ba.C = scratch;
   Launch L;
   if ((s = prepare(bare, ba, *dev, L))) return s;
-  if ((s = launch_fused(L, st))) return s;
+  if ((s = launch_fused(L, st, false))) return s;
 
   // 2) the epilogue as a separate memory-bound pass over scratch.
   ge::UnfusedParams u;
@@ -984,7 +996,7 @@ gemm_epi_status gemm_epi_run_no_alloc(gemm_epi_handle h, const gemm_epi_args* ar
   if (h->d.M == 0 || h->n_out == 0) return GEMM_EPI_OK;
   Launch L;
   if ((s = prepare(*h, a, *dev, L))) return s;
-  return launch_fused(L, st);
+  return launch_fused(L, st, h->heads());
 }
 
 gemm_epi_status gemm_epi_rmsnorm_backward(const gemm_epi_rmsnorm_bwd_args* a, void* stream) {
