@@ -150,7 +150,9 @@ struct KernelParams {
   int32_t dual;  // 1: accumulator columns alternate between B and B2 in 128-column blocks
   int32_t a_batched, b_batched;  // operand advances with the batch (else shared)
   int32_t row_blocks;            // row counters per batch
-  int32_t split, split_rows;     // SPLIT kernels: CTAs along K per tile, rows of a tile's partial sums
+  // SPLIT kernels: CTAs along K per tile; rows of the A box (32, 64 or 128)
+  // and how often it is repeated to fill 128 rows.
+  int32_t split, split_rows, split_reps;
   const float* a_scale_inv;      // dequantisation factors (F_DEQ), NULL = 1
   const float* b_scale_inv;
   int64_t bs_c, bs_c8, bs_aux;   // batch strides for direct accesses (elements; bytes for C8)
@@ -883,7 +885,9 @@ static __global__ void clear_workspace_kernel(uint4* ws, int n) {
 // cluster is done, each CTA writes its partial sums of the others' pieces into
 // their shared memory (the operand rings, idle by then), adds the ones it
 // received to its own accumulator in a fixed order and runs the program on its
-// pieces.  One tile per cluster.
+// pieces.  Up to 64 rows are loaded twice or four times over, so that the warps
+// whose TMEM lanes would hold none share the chunks of a piece.  One tile per
+// cluster.
 template <int CG, class Prog, int IN8 = 0, int SPLIT = 0>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fused_gemm_epilogue_kernel(const __grid_constant__ CUtensorMap tm_a,
@@ -1004,6 +1008,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint32_t sb = sbase + L::OFF_B + stage * L::B_STAGE_BYTES + h * L::B_KB_BYTES;
             if (CG == 1) {
               ptx::tma_load_3d(sa, &tm_a, fb, kb * K_STEP, a_row, za);
+              if constexpr (SPLIT) {  // the same rows again
+                for (int r = 1; r < p.split_reps; ++r)
+                  ptx::tma_load_3d(sa + r * p.split_rows * 128, &tm_a, fb, kb * K_STEP, a_row, za);
+              }
               if (p.b_kn && p.b_blk) {
                 // with B2, blocks 0-1 come from B and 2-3 from B2
                 ptx::tma_load_4d(sb, &tm_b, fb, 0, kb * BLOCK_K, b_col / 64, zb);
@@ -1189,9 +1197,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint8_t* c8_b = p.c8 ? p.c8 + bt * p.bs_c8 : nullptr;
       float* col_b = p.col_out ? p.col_out + static_cast<int64_t>(bt) * p.n_out : nullptr;
       const int blk = mb * CG + static_cast<int>(rank);  // this CTA's 128-row block
-      const int m = blk * BLOCK_M + quad * 32 + lane;
+      // This warp's 32 rows; SPLIT: with repeated rows, its share of their chunks.
+      const int slabs = SPLIT ? p.split_rows >> 5 : 4;
+      const int slab = SPLIT ? quad & (slabs - 1) : quad, part = SPLIT ? quad / slabs : 0;
+      const int slab_row0 = blk * BLOCK_M + slab * 32;
+      const int m = slab_row0 + lane;
       const bool row_ok = m < p.M;
-      const int slab_row0 = blk * BLOCK_M + quad * 32;
       const bool slab_ok = slab_row0 < p.M;
       const int n0 = nb * tile_out_cols;       // first output column of the tile
       const int nacc0 = nb * BLOCK_N;          // first accumulator column
@@ -1202,6 +1213,55 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // one chunk ahead of their use (each thread reads its own row).
       uint4 xa[4];
       if (flags & F_AUX) load_aux_row(xa, p, aux_b, m, row_ok, n0);
+
+      // With heads, chunk ci of the walk through a tile: chunk `in_head` of head
+      // `unit`; first the rotated part in the half layout, whose chunks come in
+      // pairs (i, i + half), head by head, then the other chunks.  All heads of
+      // a tile in lockstep: a row's angles are worked out once for them.
+      struct HeadChunk {
+        int c, unit, in_head;
+        bool in_pair, second;
+      };
+      const int rot_half_chunks = Prog::heads && p.rot_half && rotary_at >= 0 ? p.rot_pairs >> 5 : 0;
+      auto head_chunk = [&](int ci) {
+        const int log_units = 3 - p.log_head_chunks, units = 1 << log_units;
+        HeadChunk h;
+        h.in_pair = ci < 2 * rot_half_chunks * units;
+        h.second = false;
+        if (h.in_pair) {
+          h.unit = (ci >> 1) & (units - 1);
+          h.second = (ci & 1) != 0;
+          h.in_head = (ci >> (1 + log_units)) + (h.second ? rot_half_chunks : 0);
+        } else {
+          const int k = ci - 2 * rot_half_chunks * units;
+          h.unit = k & (units - 1);
+          h.in_head = 2 * rot_half_chunks + (k >> log_units);
+        }
+        h.c = (h.unit << p.log_head_chunks) + h.in_head;
+        return h;
+      };
+      // SPLIT: piece i = head * slabs + slab is CTA (i % split)'s, its (i / split)-th
+      // (4 bits a head in `owners` and `slots_of`).  Bits of `shared`: the
+      // tile's chunks that are this warp's among those holding its rows; of
+      // `mine`: those of them whose piece is this CTA's.
+      uint32_t owners = 0, slots_of = 0, shared = 0, mine = 0;
+      int first_angles = 0;  // the first chunk that rotates
+      if constexpr (SPLIT) {
+        for (int u = 0; u < 8 >> p.log_head_chunks; ++u) {
+          const int i = u * slabs + slab, nth = i / split;
+          owners |= static_cast<uint32_t>(i - nth * split) << (4 * u);
+          slots_of |= static_cast<uint32_t>(nth) << (4 * u);
+        }
+        for (int ci = chunks - 1; ci >= 0; --ci) {
+          const HeadChunk h = head_chunk(ci);
+          const int share = h.unit + h.in_head - (h.second ? rot_half_chunks : 0);
+          if ((share & (p.split_reps - 1)) != part || !slab_ok) continue;
+          shared |= 1u << h.c;
+          if (((owners >> (4 * h.unit)) & 15u) != static_cast<uint32_t>(krank)) continue;
+          mine |= 1u << h.c;
+          if (!h.second) first_angles = h.in_head;
+        }
+      }
 
       // With heads, while the main loop runs: the row's position, the angles of
       // the first chunks, and the tile's column vectors, which compiled
@@ -1238,12 +1298,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (Prog::has(GEMM_EPI_OP_MUL_COL_SCALE)) stage(p.col_scale, 1.0f, staged_cols);
           if (Prog::has(GEMM_EPI_OP_ADD_BIAS_COL)) stage(p.bias, 0.0f, staged_cols + BLOCK_N);
           __syncwarp();
-          if (rotary_at >= 0 && nacc0 < p.head_cols) {
-            if (p.rot_half && p.rot_pairs >= 32)
-              angles.template set<32, true>(p, position, 0);
-            else
-              angles.template set<16, false>(p, position, 0);
-            angles_of = 0;
+          if (rotary_at >= 0 && nacc0 < p.head_cols && (!SPLIT || mine != 0)) {
+            if (first_angles < rot_half_chunks) {
+              angles.template set<32, true>(p, position, first_angles * 32);
+              angles_of = first_angles;
+            } else if (rot_half_chunks == 0 && first_angles * 16 < p.rot_pairs) {
+              angles.template set<16, false>(p, position, first_angles * 16);
+              angles_of = first_angles;
+            }
           }
         }
       }
@@ -1254,100 +1316,142 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!SPLIT && !ok) break;
       ptx::tc_fence_after_sync();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + buf * BLOCK_N;
-      uint32_t own_units = 0;  // SPLIT: the tile's heads whose rows of this warp are this CTA's
+
+      // With heads: an op on accumulator chunk cc, its column vector staged or
+      // not, and the ops before HEAD_RMS (and ROTARY).
+      auto column_op = [&](auto code, int cc, float (&u)[32]) {
+        if constexpr (kStaged && code == GEMM_EPI_OP_MUL_COL_SCALE) {
+          const float4* c4 = reinterpret_cast<const float4*>(staged_cols) + cc * 8;
+          for_pairs(u, [&](float2 y, int i) {
+            const float4 c = c4[i / 2];
+            return __fmul2_rn(y, (i & 1) ? make_float2(c.z, c.w) : make_float2(c.x, c.y));
+          });
+        } else if constexpr (kStaged && code == GEMM_EPI_OP_ADD_BIAS_COL) {
+          const float4* b4 = reinterpret_cast<const float4*>(staged_cols + BLOCK_N) + cc * 8;
+          for_pairs(u, [&](float2 y, int i) {
+            const float4 c = b4[i / 2];
+            return __fadd2_rn(y, (i & 1) ? make_float2(c.z, c.w) : make_float2(c.x, c.y));
+          });
+        } else {
+          apply_pointwise<32>(code, u, p, nacc0 + cc * 32, p.N, rs_m);
+        }
+      };
+      auto first_ops = [&](int cc, float (&u)[32]) {
+        if (flags & F_DEQ) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) u[j] *= deq;
+        }
+        if constexpr (kStatic) {
+          constexpr int n = prog_index_of<Prog>(GEMM_EPI_OP_HEAD_RMS), r = prog_index_of<Prog>(GEMM_EPI_OP_ROTARY);
+          static_for<0, (n >= 0 ? n : r)>([&](auto I) {
+            column_op(std::integral_constant<int, Prog::code_of(decltype(I)::value)>{}, cc, u);
+          });
+        } else {
+          const int head_first = head_rms_at >= 0 ? head_rms_at : rotary_at;
+          for (int i = 0; i < head_first; ++i) apply_pointwise<32>(p.ops[i].code, u, p, nacc0 + cc * 32, p.N, rs_m);
+        }
+      };
+      // The sum of squares of one chunk; a head's is the sum of its chunks', in
+      // order, so that it has the same bits however the chunks are shared out.
+      auto chunk_squares = [&](float (&u)[32]) {
+        float2 ss = make_float2(0.0f, 0.0f);
+        for_pairs(u, [&](float2 y, int) {
+          ss = __ffma2_rn(y, y, ss);
+          return y;
+        });
+        return ss.x + ss.y;
+      };
+      float head_r[Prog::heads ? 8 : 1];  // 1 / rms of each head of the tile (this row)
+
       if constexpr (SPLIT) {
         // The cluster barriers are passed by every warp of every CTA, also
-        // after a wait that ran out (all waits before them are bounded).
-        // Piece i = head * slabs + this warp's 32-row slab is CTA (i % split)'s, its
-        // (i / split)-th; a row's 4 columns are 16 bytes, neighbouring lanes
-        // neighbouring rows.
+        // after a wait that ran out (all waits before them are bounded).  A
+        // row's 4 columns are 16 bytes, neighbouring lanes neighbouring rows.
         const uint32_t piece_bytes = static_cast<uint32_t>(p.head_chunks) * 8u * 512u;
-        const int slabs = p.split_rows >> 5, units = 8 >> p.log_head_chunks;
+        const int units = 8 >> p.log_head_chunks;
         const uint32_t slots = static_cast<uint32_t>((units * slabs + split - 1) / split);
         __syncwarp();
         ptx::cluster_sync();  // every operand ring of the cluster is idle
-        if (ok && slab_ok) {
-          for (int u = 0; u < units; ++u) {
-            const int i = u * slabs + quad, nth = i / split, owner = i - nth * split;
-            if (owner == krank) {
-              own_units |= 1u << u;
-              continue;
-            }
-            const uint32_t src = krank < owner ? krank : krank - 1;
-            uint32_t at = ptx::mapa_shared(sbase + lane * 16u, owner) + (src * slots + nth) * piece_bytes;
-            for (int k = 0; k < p.head_chunks; ++k, at += 8u * 512u) {
-              uint32_t r[32];
-              ptx::tmem_ld32_sync(t_row + ((u << p.log_head_chunks) + k) * 32, r);
-              if (row_ok) {
+        if (ok) {
+          for (int c = 0; c < chunks; ++c) {
+            if (!((shared >> c) & 1u) || ((mine >> c) & 1u)) continue;
+            const int u = c >> p.log_head_chunks;
+            const uint32_t owner = (owners >> (4 * u)) & 15u, nth = (slots_of >> (4 * u)) & 15u;
+            const uint32_t src = static_cast<uint32_t>(krank) < owner ? krank : krank - 1;
+            const uint32_t at = ptx::mapa_shared(sbase + lane * 16u, owner) + (src * slots + nth) * piece_bytes +
+                                static_cast<uint32_t>(c & (p.head_chunks - 1)) * 4096u;
+            uint32_t r[32];
+            ptx::tmem_ld32_sync(t_row + c * 32, r);
+            if (row_ok) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  ptx::st_shared_cluster_v4(at + q * 512u, __uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                            __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
-              }
-              __syncwarp();
+              for (int q = 0; q < 8; ++q)
+                ptx::st_shared_cluster_v4(at + q * 512u, __uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                          __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
             }
+            __syncwarp();
           }
         }
         ptx::cluster_sync();  // every partial sum is in place
-        if (!ok) break;
-        for (int u = 0; u < units; ++u) {
-          if (!((own_units >> u) & 1u)) continue;
-          const uint8_t* got = smem + lane * 16u + (u * slabs + quad) / split * piece_bytes;
-          for (int k = 0; k < p.head_chunks; ++k, got += 8u * 512u) {
-            const uint32_t at = t_row + ((u << p.log_head_chunks) + k) * 32;
+        // Sums of squares [slab][chunk][row], above the pieces: with repeated
+        // rows each of a row's warps has some of its chunks.
+        float* squares = reinterpret_cast<float*>(smem + L::OFF_EPI - 4096u) + slab * 256 + lane;
+        if (ok) {
+          for (int c = 0; c < chunks; ++c) {
+            if (!((mine >> c) & 1u)) continue;
+            const int u = c >> p.log_head_chunks;
+            const uint8_t* got = smem + lane * 16u + ((slots_of >> (4 * u)) & 15u) * piece_bytes +
+                                 static_cast<uint32_t>(c & (p.head_chunks - 1)) * 4096u;
             uint32_t r[32];
-            ptx::tmem_ld32_sync(at, r);
-            if (row_ok) {
-              for (int src = 0; src < split - 1; ++src) {
-                float4 v[8];
+            ptx::tmem_ld32_sync(t_row + c * 32, r);
+            float y[32];
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  v[q] = *reinterpret_cast<const float4*>(got + src * slots * piece_bytes + q * 512u);
+            for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(r[j]);
+            for (int src = 0; src < split - 1; ++src) {
+              float4 v[8];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                  r[4 * q] = __float_as_uint(__uint_as_float(r[4 * q]) + v[q].x);
-                  r[4 * q + 1] = __float_as_uint(__uint_as_float(r[4 * q + 1]) + v[q].y);
-                  r[4 * q + 2] = __float_as_uint(__uint_as_float(r[4 * q + 2]) + v[q].z);
-                  r[4 * q + 3] = __float_as_uint(__uint_as_float(r[4 * q + 3]) + v[q].w);
-                }
-              }
+              for (int q = 0; q < 8; ++q)
+                v[q] = *reinterpret_cast<const float4*>(got + src * slots * piece_bytes + q * 512u);
+              for_pairs(y, [&](float2 a, int i) {
+                const float4 w = v[i / 2];
+                return __fadd2_rn(a, (i & 1) ? make_float2(w.z, w.w) : make_float2(w.x, w.y));
+              });
             }
-            __syncwarp();
-            ptx::tmem_st32_sync(at, r);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(y[j]);
+            ptx::tmem_st32_sync(t_row + c * 32, r);
+            if (head_rms_at >= 0) {
+              first_ops(c, y);
+              squares[c * 32] = chunk_squares(y);
+            }
           }
         }
+        if (head_rms_at >= 0) {
+          if (p.split_reps > 1)
+            ptx::named_barrier_sync(1, 32 * NUM_EPI_WARPS);
+          else
+            __syncwarp();
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            float ss = 0.0f;
+            if (u < units)
+              for (int k = 0; k < p.head_chunks; ++k) ss += squares[((u << p.log_head_chunks) + k) * 32];
+            head_r[u] = rsqrtf(fmaf(ss, p.head_inv_dim, p.head_eps));
+          }
+        }
+        if (!ok) break;
       }
       float row_ss = 0.0f;
 
-      // HEAD_RMS and ROTARY: the tile's heads in lockstep, so that a row's
-      // angles are worked out once for all of them.  1 / rms of each head; the
-      // second chunk of a rotated pair of chunks, until its turn.
-      float head_r[Prog::heads ? 8 : 1];
+      // The second chunk of a rotated pair of chunks, until its turn.
       float held[Prog::heads ? 32 : 1];
 
       uint32_t done_chunks = 0;
       for (int ci = 0; ci < chunks; ++ci) {
-        // Chunk of the tile: in order, or with heads chunk `in_head` of head
-        // `unit`: first the rotated part in the half layout, whose chunks come
-        // in pairs (i, i + half), head by head, then the other chunks.
-        int c = ci, unit = 0, in_head = 0;
-        bool in_pair = false, second = false;
-        const int rot_half_chunks = Prog::heads && p.rot_half && rotary_at >= 0 ? p.rot_pairs >> 5 : 0;
-        if constexpr (Prog::heads) {
-          const int log_units = 3 - p.log_head_chunks, units = 1 << log_units;
-          in_pair = ci < 2 * rot_half_chunks * units;
-          if (in_pair) {
-            unit = (ci >> 1) & (units - 1);
-            second = (ci & 1) != 0;
-            in_head = (ci >> (1 + log_units)) + (second ? rot_half_chunks : 0);
-          } else {
-            const int k = ci - 2 * rot_half_chunks * units;
-            unit = k & (units - 1);
-            in_head = 2 * rot_half_chunks + (k >> log_units);
-          }
-          c = (unit << p.log_head_chunks) + in_head;
-          if (SPLIT && !((own_units >> unit) & 1u)) continue;  // another CTA of the cluster has it
-        }
+        HeadChunk h = {ci, 0, 0, false, false};
+        if constexpr (Prog::heads) h = head_chunk(ci);
+        const int c = h.c, unit = h.unit, in_head = h.in_head;
+        const bool in_pair = h.in_pair, second = h.second;
+        if (SPLIT && !((mine >> c) & 1u)) continue;  // another CTA's, or another warp's
         const uint32_t g = gchunk + done_chunks++;
         const uint32_t eb = g % EPI_BUFS;
         const int col0 = n0 + c * CHUNK;  // first output column of the chunk
@@ -1378,25 +1482,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int i = 0; i < expand_at; ++i) apply_pointwise<16>(p.ops[i].code, dh, p, nacc0 + c * 16, p.N, rs_m);
           }
         } else if constexpr (Prog::heads) {
-          const int head_first = head_rms_at >= 0 ? head_rms_at : rotary_at;
-          // An op on accumulator chunk cc, its column vector staged or not.
-          auto column_op = [&](auto code, int cc, float (&u)[32]) {
-            if constexpr (kStaged && code == GEMM_EPI_OP_MUL_COL_SCALE) {
-              const float4* c4 = reinterpret_cast<const float4*>(staged_cols) + cc * 8;
-              for_pairs(u, [&](float2 y, int i) {
-                const float4 c = c4[i / 2];
-                return __fmul2_rn(y, (i & 1) ? make_float2(c.z, c.w) : make_float2(c.x, c.y));
-              });
-            } else if constexpr (kStaged && code == GEMM_EPI_OP_ADD_BIAS_COL) {
-              const float4* b4 = reinterpret_cast<const float4*>(staged_cols + BLOCK_N) + cc * 8;
-              for_pairs(u, [&](float2 y, int i) {
-                const float4 c = b4[i / 2];
-                return __fadd2_rn(y, (i & 1) ? make_float2(c.z, c.w) : make_float2(c.x, c.y));
-              });
-            } else {
-              apply_pointwise<32>(code, u, p, nacc0 + cc * 32, p.N, rs_m);
-            }
-          };
           // Accumulator chunk cc with the ops before HEAD_RMS (and ROTARY).
           auto load_acc = [&](int cc, float (&u)[32]) {
             if (flags & F_ZERO_ACC) {
@@ -1407,19 +1492,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               ptx::tmem_ld32_sync(t_row + cc * 32, r);
 #pragma unroll
               for (int j = 0; j < 32; ++j) u[j] = __uint_as_float(r[j]);
-              if (flags & F_DEQ) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) u[j] *= deq;
-              }
             }
-            if constexpr (kStatic) {
-              constexpr int n = prog_index_of<Prog>(GEMM_EPI_OP_HEAD_RMS), r = prog_index_of<Prog>(GEMM_EPI_OP_ROTARY);
-              static_for<0, (n >= 0 ? n : r)>([&](auto I) {
-                column_op(std::integral_constant<int, Prog::code_of(decltype(I)::value)>{}, cc, u);
-              });
-            } else {
-              for (int i = 0; i < head_first; ++i) apply_pointwise<32>(p.ops[i].code, u, p, nacc0 + cc * 32, p.N, rs_m);
-            }
+            first_ops(cc, u);
           };
           // What follows it up to ROTARY: the head's 1 / rms (1 where there is
           // no head) and the ops between the two.
@@ -1442,18 +1516,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           };
           if (head_rms_at >= 0) {
-            if (in_head == 0 && head) {
+            if (!SPLIT && in_head == 0 && head) {
               // A row of the head is in this thread's TMEM lane, so its sum of
               // squares is a first pass over the head's chunks.
-              float2 ss = make_float2(0.0f, 0.0f);
+              float ss = 0.0f;
               for (int k = 0; k < p.head_chunks; ++k) {
                 load_acc(c + k, v);
-                for_pairs(v, [&](float2 y, int) {
-                  ss = __ffma2_rn(y, y, ss);
-                  return y;
-                });
+                ss += chunk_squares(v);
               }
-              const float r = rsqrtf(fmaf(ss.x + ss.y, p.head_inv_dim, p.head_eps));
+              const float r = rsqrtf(fmaf(ss, p.head_inv_dim, p.head_eps));
 #pragma unroll
               for (int k = 0; k < 8; ++k) head_r[k] = k == unit ? r : head_r[k];
             }

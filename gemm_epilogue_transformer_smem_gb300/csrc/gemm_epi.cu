@@ -538,6 +538,9 @@ int choose_cta_group(const gemm_epi_plan& P, const gemm_epi_args& a, const Devic
   return P.d.M > ge::BLOCK_M ? 2 : 1;
 }
 
+// Rows of a split tile's A box: what M fills, repeated up to 128.
+int64_t split_rows(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : ge::BLOCK_M; }
+
 // CTAs along K of a program with HEAD_RMS or ROTARY: 1, or as many as leave
 // the 128 x 256 tiles' clusters resident at once, each CTA MIN_SPLIT_BLOCKS
 // K-blocks, and room in a CTA's operand ring for the partial sums it receives
@@ -549,12 +552,12 @@ int choose_split(const gemm_epi_plan& P, const gemm_epi_args& a, const DeviceSta
   const int k_step = P.in8 ? 2 * ge::BLOCK_K : ge::BLOCK_K;
   const int64_t k_blocks = (P.d.K + k_step - 1) / k_step;
   const int64_t tiles = P.num_m_tiles * P.num_n_tiles * P.batch;
-  const int64_t slabs = std::min<int64_t>(ge::BLOCK_M, P.d.M + 31) / 32;
+  const int64_t slabs = split_rows(P.d.M) / 32;
   const int64_t pieces = ge::BLOCK_N / P.d.head_dim * slabs;  // heads of a tile by slabs of 32 rows
   for (int n = MAX_SPLIT; n >= 2; --n) {
     const int64_t bytes = (n - 1) * ((pieces + n - 1) / n) * P.d.head_dim * 32 * 4;
     if (tiles <= dev.split_clusters[n] && k_blocks >= n * MIN_SPLIT_BLOCKS &&
-        bytes <= static_cast<int64_t>(ge::Smem<1>::OFF_EPI))
+        bytes + 4096 <= static_cast<int64_t>(ge::Smem<1>::OFF_EPI))  // and the sums of repeated rows
       return n;
   }
   return 1;
@@ -664,7 +667,8 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
     k.ops[i].f0 = P.ops[i].f0;
   }
   k.split = L.split;
-  k.split_rows = static_cast<int32_t>(std::min<int64_t>(ge::BLOCK_M, (d.M + 31) / 32 * 32));
+  k.split_rows = static_cast<int32_t>(split_rows(d.M));
+  k.split_reps = ge::BLOCK_M / k.split_rows;
   if (L.split > 1)
     L.grid = k.num_tiles * L.split;
   else if (L.cg == 2)
@@ -676,7 +680,8 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
   if (d.K > 0) {
     const CUtensorMapDataType op_dt = P.in8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int64_t esz = P.in8 ? 1 : 2;  // bytes per operand element
-    s = make_map(&L.ta, op_dt, a.A, d.K, d.M, d.lda * esz, k_step, ge::BLOCK_M, CU_TENSOR_MAP_SWIZZLE_128B,
+    s = make_map(&L.ta, op_dt, a.A, d.K, d.M, d.lda * esz, k_step, L.split > 1 ? k.split_rows : ge::BLOCK_M,
+                 CU_TENSOR_MAP_SWIZZLE_128B,
                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "A", P.batch, k.a_batched ? d.batch_stride_a * esz : 0);
     if (s) return s;
     // Each B operand: N (or N/2 with B2) columns; K-major boxes hold the

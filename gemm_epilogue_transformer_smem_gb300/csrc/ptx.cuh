@@ -60,6 +60,11 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
+// Barrier `id` (1..15) among `threads` threads of the CTA, whole warps.
+__device__ __forceinline__ void named_barrier_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // ------------------------------------------------------------------ dependent launches
 
 // Lets the next kernel of the stream, launched as a dependent one, start.
