@@ -1245,6 +1245,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // tile's chunks that are this warp's among those holding its rows; of
       // `mine`: those of them whose piece is this CTA's.
       uint32_t owners = 0, slots_of = 0, shared = 0, mine = 0;
+      uint32_t walk = 0;  // the steps ci of `mine`, 4 bits each
+      int steps = chunks;
       int first_angles = 0;  // the first chunk that rotates
       if constexpr (SPLIT) {
         for (int u = 0; u < 8 >> p.log_head_chunks; ++u) {
@@ -1252,6 +1254,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           owners |= static_cast<uint32_t>(i - nth * split) << (4 * u);
           slots_of |= static_cast<uint32_t>(nth) << (4 * u);
         }
+        steps = 0;
         for (int ci = chunks - 1; ci >= 0; --ci) {
           const HeadChunk h = head_chunk(ci);
           const int share = h.unit + h.in_head - (h.second ? rot_half_chunks : 0);
@@ -1259,6 +1262,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           shared |= 1u << h.c;
           if (((owners >> (4 * h.unit)) & 15u) != static_cast<uint32_t>(krank)) continue;
           mine |= 1u << h.c;
+          walk = walk << 4 | static_cast<uint32_t>(ci);
+          ++steps;
           if (!h.second) first_angles = h.in_head;
         }
       }
@@ -1406,6 +1411,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             float y[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(r[j]);
+#pragma unroll 2
             for (int src = 0; src < split - 1; ++src) {
               float4 v[8];
 #pragma unroll
@@ -1430,12 +1436,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ptx::named_barrier_sync(1, 32 * NUM_EPI_WARPS);
           else
             __syncwarp();
+          float q[8];  // chunks of other CTAs' heads hold anything
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            float ss = 0.0f;
-            if (u < units)
-              for (int k = 0; k < p.head_chunks; ++k) ss += squares[((u << p.log_head_chunks) + k) * 32];
-            head_r[u] = rsqrtf(fmaf(ss, p.head_inv_dim, p.head_eps));
+          for (int c = 0; c < 8; ++c) q[c] = squares[c * 32];
+          auto set = [&](int u, float ss) { head_r[u] = rsqrtf(fmaf(ss, p.head_inv_dim, p.head_eps)); };
+          if (p.log_head_chunks == 0) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) set(u, q[u]);
+          } else if (p.log_head_chunks == 1) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) set(u, q[2 * u] + q[2 * u + 1]);
+          } else if (p.log_head_chunks == 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) set(u, ((q[4 * u] + q[4 * u + 1]) + q[4 * u + 2]) + q[4 * u + 3]);
+          } else {
+            set(0, ((((((q[0] + q[1]) + q[2]) + q[3]) + q[4]) + q[5]) + q[6]) + q[7]);
           }
         }
         if (!ok) break;
@@ -1445,14 +1460,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // The second chunk of a rotated pair of chunks, until its turn.
       float held[Prog::heads ? 32 : 1];
 
-      uint32_t done_chunks = 0;
-      for (int ci = 0; ci < chunks; ++ci) {
+      for (int ci = 0; ci < steps; ++ci) {
         HeadChunk h = {ci, 0, 0, false, false};
-        if constexpr (Prog::heads) h = head_chunk(ci);
+        if constexpr (Prog::heads) h = head_chunk(SPLIT ? static_cast<int>(walk >> (4 * ci)) & 15 : ci);
         const int c = h.c, unit = h.unit, in_head = h.in_head;
         const bool in_pair = h.in_pair, second = h.second;
-        if (SPLIT && !((mine >> c) & 1u)) continue;  // another CTA's, or another warp's
-        const uint32_t g = gchunk + done_chunks++;
+        const uint32_t g = gchunk + ci;
         const uint32_t eb = g % EPI_BUFS;
         const int col0 = n0 + c * CHUNK;  // first output column of the chunk
         float v[32];
@@ -1639,7 +1652,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               ptx::mbar_arrive_cluster(ptx::mapa_shared(bar(BAR_TEMPTY + buf), 0));
           }
         };
-        if (ci == chunks - 1 && !tmem_col_sums) release_accumulator();
+        if (ci == steps - 1 && !tmem_col_sums) release_accumulator();
 
         // ---- auxiliary tile (residual / pre-activation), this thread's row
         float x[32];
@@ -1806,7 +1819,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         } else {
           for (int i = op_begin; i < p.n_ops; ++i) run_op(p.ops[i].code);
         }
-        if (ci == chunks - 1 && tmem_col_sums) release_accumulator();
+        if (ci == steps - 1 && tmem_col_sums) release_accumulator();
 
         // ---- TMA stores of this chunk's staged outputs
         if (flags & (F_STORE | F_E8)) {
