@@ -208,13 +208,9 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
   p.num_pc = p.first_plain + (chunks - 2 * p.first_plain + 1) / 2;
   p.log_g = 0;
   while ((slots << p.log_g) < p.num_pc) ++p.log_g;
-  const int per_iter = 32 >> p.log_g;
-  int total_iters = 0;
   for (int i = 0; i < 2; ++i) {
     ge::HeadPart& h = p.part[i];
     h.heads = heads[i];
-    h.iters = (heads[i] + per_iter - 1) / per_iter;
-    total_iters += h.iters;
     h.x = in[i]->data, h.x_b = in[i]->stride_batch, h.x_t = in[i]->stride_token, h.x_h = in[i]->stride_head;
     h.dy = dy[i]->data, h.dy_b = dy[i]->stride_batch, h.dy_t = dy[i]->stride_token, h.dy_h = dy[i]->stride_head;
     h.y = out[i]->data, h.y_b = out[i]->stride_batch, h.y_t = out[i]->stride_token, h.y_h = out[i]->stride_head;
@@ -233,15 +229,15 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
   const HeadKernel kernel = kernel_of(mode, wide, half, a->type == GEMM_EPI_TYPE_F32);
   const int64_t resident = static_cast<int64_t>(sms) * kernel.blocks;
   // One wave of blocks, and no more warps than iterations.
-  const int64_t row_iters[2] = {p.part[0].iters, p.part[1].iters};
+  const int64_t sets = (p.rows + (32 >> p.log_g) - 1) / (32 >> p.log_g);  // of tokens, one to each lane group
   auto share_out = [&](ge::HeadShare& h, int64_t per_row, int64_t most) {
-    const int64_t total = p.rows * per_row;
+    const int64_t total = sets * per_row;
     const int64_t blocks = std::min(most, (total + ge::HD_WARPS - 1) / ge::HD_WARPS);
     const int64_t warps = std::max<int64_t>(1, blocks * ge::HD_WARPS);
-    const int64_t left = p.rows % warps * per_row;  // iterations past the whole rounds
+    const int64_t left = sets % warps * per_row;  // iterations past the whole rounds
     h.warps = static_cast<int32_t>(warps);
     h.per_row = static_cast<int32_t>(std::max<int64_t>(1, per_row));
-    h.rounds = blocks ? static_cast<int32_t>(p.rows / warps) : 0;
+    h.rounds = blocks ? static_cast<int32_t>(sets / warps) : 0;
     h.base = static_cast<int32_t>(left / warps);
     h.rest = static_cast<int32_t>(left % warps);
     return blocks;
@@ -251,8 +247,8 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
     // shared between q and k by their work; a part none of whose results is
     // wanted gets no block
     const int64_t most = std::min<int64_t>(ge::HD_MAX_PARTIALS, resident);
-    const int64_t q_work = a->q_out.data || a->dw_q ? row_iters[0] : 0;
-    const int64_t k_work = a->k_out.data || a->dw_k ? row_iters[1] : 0;
+    const int64_t q_work = a->q_out.data || a->dw_q ? heads[0] : 0;
+    const int64_t k_work = a->k_out.data || a->dw_k ? heads[1] : 0;
     int64_t q_most = q_work ? most : 0;
     if (q_work && k_work)
       q_most = std::min(most - 1, std::max<int64_t>(1, (most * q_work + (q_work + k_work) / 2) / (q_work + k_work)));
@@ -260,7 +256,7 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
     p.q_blocks = static_cast<int32_t>(q);
     blocks = q + k;
   } else {
-    blocks = share_out(p.share[0], total_iters, resident);
+    blocks = share_out(p.share[0], heads[0] + heads[1], resident);
   }
   kernel.fn<<<static_cast<unsigned>(blocks), ge::HD_THREADS, static_cast<size_t>(kernel.smem), st>>>(p);
   e = cudaGetLastError();

@@ -18,9 +18,10 @@
 // that an access of a warp covers whole sectors.  Values are kept as arrays
 // of first and of second halves of pairs whatever the layout, so the rotation
 // needs no exchange between lanes and runs on packed fp32 pairs.  G = 2^g
-// lanes hold a head and reduce its sums with g shuffles; a warp works on 32 / G
-// heads of one token at a time and computes that token's angles once for all
-// of them.
+// lanes hold a head and reduce its sums with g shuffles; each of a warp's 32 / G
+// groups of lanes takes a token of its own and walks through that token's
+// heads, so that few heads leave no lane idle and the groups work out their
+// angles at once.
 #pragma once
 
 #include <stdint.h>
@@ -57,12 +58,12 @@ struct HeadPart {
   int64_t y_b, y_t, y_h;
   const float* w;  // NULL: 1
   int32_t heads;
-  int32_t iters;  // ceil(heads / (32 / G))
 };
 
-// How tokens of per_row iterations are shared out to `warps` warps: `rounds`
-// whole tokens each, warp by warp, and the iterations of the tokens left over
-// in order, `base` to each warp and one more to each of the first `rest`.
+// How sets of tokens (one to each lane group of a warp) of per_row iterations
+// (heads) are shared out to `warps` warps: `rounds` whole sets each, warp by
+// warp, and the iterations of the sets left over in order, `base` to each warp
+// and one more to each of the first `rest`.
 struct HeadShare {
   int32_t warps, per_row, rounds, base, rest;
 };
@@ -341,10 +342,15 @@ __device__ __forceinline__ int64_t head_position(const HeadParams& p, int b, int
                         : __ldg(static_cast<const int*>(p.positions) + at);
 }
 
-// Row `row` of the batch: its sequence and token.
+// The token of lane group `group` in set `set` of tokens: its sequence, its
+// place there, and whether there is one.
 struct HeadRow {
   uint32_t b, t;
-  __device__ __forceinline__ HeadRow(const HeadParams& p, uint32_t row) {
+  bool ok;
+  __device__ __forceinline__ HeadRow(const HeadParams& p, uint32_t set, int group) {
+    const uint32_t at = (set << (5 - p.log_g)) + group, rows = static_cast<uint32_t>(p.rows);
+    ok = at < rows;
+    const uint32_t row = ok ? at : rows - 1;
     b = p.rows == p.tokens ? 0u : row / static_cast<uint32_t>(p.tokens);
     t = row - b * static_cast<uint32_t>(p.tokens);
   }
@@ -368,7 +374,7 @@ __device__ __forceinline__ void head_forward(HeadPairs& v, const HeadPairs& w, c
 }
 
 // One head backward: v = x, g = dy in; v = dx out, dw added to where `ok` (a
-// lane group past the last head adds nothing).
+// lane group without a token adds nothing).
 __device__ __forceinline__ void head_backward(HeadPairs& v, HeadPairs& g, const HeadPairs& w, HeadPairs& dw,
                                               const HeadAngles& ang, const HeadParams& p, bool ok) {
   const float r = head_rms(v, p);
@@ -426,10 +432,9 @@ __device__ __forceinline__ void store_partial(const Lane& l, HeadPairs& dw, cons
   }
 }
 
-// A warp's share, token by token: iterations [it, end) of token `row`.  All
+// A warp's share, set by set of tokens: iterations [it, end) of set `row`.  All
 // warps get the same number of iterations, give or take one, so they end
-// together whatever the number of tokens (with whole tokens alone, 8192 of
-// them on 3648 warps take three rounds for two and a quarter).
+// together whatever the number of tokens.
 struct HeadSpan {
   uint32_t row;
   int it, end, rounds, left;
@@ -452,7 +457,7 @@ struct HeadSpan {
     left -= end - it;
   }
   __device__ __forceinline__ bool any() const { return it < end; }
-  // To the next token of the share, once this one's iterations are done.
+  // To the next set of the share, once this one's iterations are done.
   __device__ __forceinline__ void next(const HeadShare& s, int warp) {
     if (rounds > 1) {
       --rounds;
@@ -470,18 +475,16 @@ struct HeadSpan {
   }
 };
 
-// A run of iterations over one tensor of one token: where this lane's head
-// starts, how far the next iteration's is, and how many heads are left from
-// this lane group's on (none: the group is past the last head).
+// This lane group's token in one tensor, from head `head` on: one head further
+// each iteration.
 template <class T>
 struct HeadRun {
   T* at;
   int64_t step;
 
-  __device__ __forceinline__ void set(const void* base, int64_t sb, int64_t st, int64_t sh, const HeadRow& r, int head,
-                                      int per_iter) {
+  __device__ __forceinline__ void set(const void* base, int64_t sb, int64_t st, int64_t sh, const HeadRow& r, int head) {
     at = static_cast<T*>(const_cast<void*>(base)) + r.b * sb + r.t * st + head * sh;
-    step = per_iter * sh;
+    step = sh;
   }
 };
 
@@ -545,8 +548,7 @@ __global__ void __launch_bounds__(HD_THREADS, NORM ? HD_NORM_BLOCKS : HD_ROTARY_
   __shared__ __align__(16) float weights[2][NORM ? HD_MAX_DIM : 4];
   const int lane = threadIdx.x & 31, warp = blockIdx.x * HD_WARPS + (threadIdx.x >> 5);
   const int group = lane >> p.log_g, in_group = lane & ((1 << p.log_g) - 1);
-  const int per_iter = 32 >> p.log_g;
-  const int q_iters = p.part[0].iters;
+  const int q_heads = p.part[0].heads;
   const HeadShare& share = p.share[0];
   Lane l;
   l.place(p, in_group);
@@ -556,22 +558,22 @@ __global__ void __launch_bounds__(HD_THREADS, NORM ? HD_NORM_BLOCKS : HD_ROTARY_
 
   HeadSpan ahead(share, warp);  // what is fetched next: `n` iterations of run `src`
   HeadRun<T> src;
-  int n = 0, heads_ahead = 0;
+  int n = 0;
+  bool copies = false;
   auto open = [&]() {
-    const int k = ahead.it >= q_iters;
+    const int k = ahead.it >= q_heads;
     const HeadPart& h = p.part[k];
-    const int first = (ahead.it - (k ? q_iters : 0)) * per_iter + group;
-    src.set(h.x, h.x_b, h.x_t, h.x_h, HeadRow(p, ahead.row), first, per_iter);
-    heads_ahead = h.heads - first;
-    const int to = k ? ahead.end : min(ahead.end, q_iters);
+    const HeadRow r(p, ahead.row, group);
+    src.set(h.x, h.x_b, h.x_t, h.x_h, r, ahead.it - (k ? q_heads : 0));
+    copies = r.ok;
+    const int to = k ? ahead.end : min(ahead.end, q_heads);
     n = to - ahead.it;
     ahead.it = to;
   };
   auto fetch = [&](uint32_t at) {
     if (n > 0) {
-      if (heads_ahead > 0) Ring::fetch(ring + at, 0, l, src.at);
+      if (copies) Ring::fetch(ring + at, 0, l, src.at);
       src.at += src.step;
-      heads_ahead -= per_iter;
       if (--n == 0) {
         if (!ahead.any()) ahead.next(share, warp);
         if (ahead.any()) open();
@@ -596,18 +598,16 @@ __global__ void __launch_bounds__(HD_THREADS, NORM ? HD_NORM_BLOCKS : HD_ROTARY_
   uint32_t at = 0;
 #pragma unroll 1
   for (HeadSpan now(share, warp); now.any(); now.next(share, warp)) {
-    const HeadRow r(p, now.row);
+    const HeadRow r(p, now.row, group);
     HeadAngles ang;
     ang.set(p, l, in_group, head_position(p, r.b, r.t));
 #pragma unroll 1
     while (now.any()) {
-      const int k = now.it >= q_iters;
+      const int k = now.it >= q_heads;
       const HeadPart& h = p.part[k];
-      const int first = (now.it - (k ? q_iters : 0)) * per_iter + group;
-      const int to = k ? now.end : min(now.end, q_iters);
+      const int to = k ? now.end : min(now.end, q_heads);
       HeadRun<T> dst;
-      dst.set(h.y, h.y_b, h.y_t, h.y_h, r, first, per_iter);
-      int heads = h.heads - first;
+      dst.set(h.y, h.y_b, h.y_t, h.y_h, r, now.it - (k ? q_heads : 0));
       HeadPairs w;
       if constexpr (NORM) l.weights_shared(weights[k], w);
 #pragma unroll 1
@@ -616,9 +616,8 @@ __global__ void __launch_bounds__(HD_THREADS, NORM ? HD_NORM_BLOCKS : HD_ROTARY_
         HeadPairs v;
         Ring::read(mine + at, 0, v);
         head_forward<NORM>(v, w, ang, p);
-        if (heads > 0) l.store(dst.at, v);
+        if (r.ok) l.store(dst.at, v);
         dst.at += dst.step;
-        heads -= per_iter;
         fetch(at);  // the slot's values are in registers
         at = Ring::next(at);
       }
@@ -638,7 +637,6 @@ __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS) heads_backward_kern
   const int k = static_cast<int>(blockIdx.x) >= p.q_blocks;
   const int lane = threadIdx.x & 31, warp = (blockIdx.x - (k ? p.q_blocks : 0)) * HD_WARPS + (threadIdx.x >> 5);
   const int group = lane >> p.log_g, in_group = lane & ((1 << p.log_g) - 1);
-  const int per_iter = 32 >> p.log_g;
   const HeadPart& h = p.part[k];
   const HeadShare& share = p.share[k];
   Lane l;
@@ -649,24 +647,23 @@ __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS) heads_backward_kern
 
   HeadSpan ahead(share, warp);  // what is fetched next: `n` iterations of runs `x` and `dy`
   HeadRun<T> x, dy;
-  int n = 0, heads_ahead = 0;
+  int n = 0;
+  bool copies = false;
   auto open = [&]() {
-    const HeadRow r(p, ahead.row);
-    const int first = ahead.it * per_iter + group;
-    x.set(h.x, h.x_b, h.x_t, h.x_h, r, first, per_iter);
-    dy.set(h.dy, h.dy_b, h.dy_t, h.dy_h, r, first, per_iter);
-    heads_ahead = h.heads - first;
+    const HeadRow r(p, ahead.row, group);
+    x.set(h.x, h.x_b, h.x_t, h.x_h, r, ahead.it);
+    dy.set(h.dy, h.dy_b, h.dy_t, h.dy_h, r, ahead.it);
+    copies = r.ok;
     n = ahead.end - ahead.it;
   };
   auto fetch = [&](uint32_t at) {
     if (n > 0) {
-      if (heads_ahead > 0) {
+      if (copies) {
         Ring::fetch(ring + at, 0, l, x.at);
         Ring::fetch(ring + at, 1, l, dy.at);
       }
       x.at += x.step;
       dy.at += dy.step;
-      heads_ahead -= per_iter;
       if (--n == 0) {
         ahead.next(share, warp);
         if (ahead.any()) open();
@@ -688,23 +685,20 @@ __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS) heads_backward_kern
   uint32_t at = 0;
 #pragma unroll 1
   for (HeadSpan now(share, warp); now.any(); now.next(share, warp)) {
-    const HeadRow r(p, now.row);
+    const HeadRow r(p, now.row, group);
     HeadAngles ang;
     ang.set(p, l, in_group, head_position(p, r.b, r.t));
-    const int first = now.it * per_iter + group;
     HeadRun<T> dx;
-    dx.set(h.y, h.y_b, h.y_t, h.y_h, r, first, per_iter);
-    int heads = h.heads - first;
+    dx.set(h.y, h.y_b, h.y_t, h.y_h, r, now.it);
 #pragma unroll 1
     for (; now.it < now.end; ++now.it) {
       ptx::cp_async_wait<Ring::DEPTH - 1>();
       HeadPairs v, g;
       Ring::read(mine + at, 0, v);
       Ring::read(mine + at, 1, g);
-      head_backward(v, g, w, dw, ang, p, heads > 0);
-      if (heads > 0 && h.y != nullptr) l.store(dx.at, v);
+      head_backward(v, g, w, dw, ang, p, r.ok);
+      if (r.ok && h.y != nullptr) l.store(dx.at, v);
       dx.at += dx.step;
-      heads -= per_iter;
       fetch(at);
       at = Ring::next(at);
     }
@@ -723,38 +717,35 @@ __global__ void __launch_bounds__(HD_THREADS, 2) heads_any_kernel(const __grid_c
   using Lane = HeadLane<T, 2, HALF>;
   const int lane = threadIdx.x & 31, warp = blockIdx.x * HD_WARPS + (threadIdx.x >> 5);
   const int group = lane >> p.log_g, in_group = lane & ((1 << p.log_g) - 1);
-  const int per_iter = 32 >> p.log_g;
-  const int q_iters = p.part[0].iters;
+  const int q_heads = p.part[0].heads;
   Lane l;
   l.place(p, in_group);
 #pragma unroll 1
   for (HeadSpan now(p.share[0], warp); now.any(); now.next(p.share[0], warp)) {
-    const HeadRow r(p, now.row);
+    const HeadRow r(p, now.row, group);
     HeadAngles ang;
     ang.set(p, l, in_group, head_position(p, r.b, r.t));
 #pragma unroll 1
     while (now.any()) {
-      const int k = now.it >= q_iters;
+      const int k = now.it >= q_heads;
       const HeadPart& h = p.part[k];
-      const int first = (now.it - (k ? q_iters : 0)) * per_iter + group;
-      const int to = k ? now.end : min(now.end, q_iters);
+      const int first = now.it - (k ? q_heads : 0);
+      const int to = k ? now.end : min(now.end, q_heads);
       HeadRun<T> x, y;
-      x.set(h.x, h.x_b, h.x_t, h.x_h, r, first, per_iter);
-      y.set(h.y, h.y_b, h.y_t, h.y_h, r, first, per_iter);
-      int heads = h.heads - first;
+      x.set(h.x, h.x_b, h.x_t, h.x_h, r, first);
+      y.set(h.y, h.y_b, h.y_t, h.y_h, r, first);
       HeadPairs w;
       if constexpr (NORM) l.weights(h.w, w);
 #pragma unroll 1
       for (; now.it < to; ++now.it) {
         typename Lane::Raw raw;
-        l.load(raw, x.at, heads > 0);
+        l.load(raw, x.at, r.ok);
         HeadPairs v;
         Lane::unpack(raw, v);
         head_forward<NORM>(v, w, ang, p);
-        if (heads > 0) l.store(y.at, v);
+        if (r.ok) l.store(y.at, v);
         x.at += x.step;
         y.at += y.step;
-        heads -= per_iter;
       }
     }
   }
@@ -767,7 +758,6 @@ __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS)
   const int k = static_cast<int>(blockIdx.x) >= p.q_blocks;
   const int lane = threadIdx.x & 31, warp = (blockIdx.x - (k ? p.q_blocks : 0)) * HD_WARPS + (threadIdx.x >> 5);
   const int group = lane >> p.log_g, in_group = lane & ((1 << p.log_g) - 1);
-  const int per_iter = 32 >> p.log_g;
   const HeadPart& h = p.part[k];
   Lane l;
   l.place(p, in_group);
@@ -777,29 +767,26 @@ __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS)
   for (int i = 0; i < 4; ++i) dw.a[i] = dw.b[i] = both(0.0f);
 #pragma unroll 1
   for (HeadSpan now(p.share[k], warp); now.any(); now.next(p.share[k], warp)) {
-    const HeadRow r(p, now.row);
+    const HeadRow r(p, now.row, group);
     HeadAngles ang;
     ang.set(p, l, in_group, head_position(p, r.b, r.t));
-    const int first = now.it * per_iter + group;
     HeadRun<T> x, dy, dx;
-    x.set(h.x, h.x_b, h.x_t, h.x_h, r, first, per_iter);
-    dy.set(h.dy, h.dy_b, h.dy_t, h.dy_h, r, first, per_iter);
-    dx.set(h.y, h.y_b, h.y_t, h.y_h, r, first, per_iter);
-    int heads = h.heads - first;
+    x.set(h.x, h.x_b, h.x_t, h.x_h, r, now.it);
+    dy.set(h.dy, h.dy_b, h.dy_t, h.dy_h, r, now.it);
+    dx.set(h.y, h.y_b, h.y_t, h.y_h, r, now.it);
 #pragma unroll 1
     for (; now.it < now.end; ++now.it) {
       typename Lane::Raw rx, rg;
-      l.load(rx, x.at, heads > 0);
-      l.load(rg, dy.at, heads > 0);
+      l.load(rx, x.at, r.ok);
+      l.load(rg, dy.at, r.ok);
       HeadPairs v, g;
       Lane::unpack(rx, v);
       Lane::unpack(rg, g);
-      head_backward(v, g, w, dw, ang, p, heads > 0);
-      if (heads > 0 && h.y != nullptr) l.store(dx.at, v);
+      head_backward(v, g, w, dw, ang, p, r.ok);
+      if (r.ok && h.y != nullptr) l.store(dx.at, v);
       x.at += x.step;
       dy.at += dy.step;
       dx.at += dx.step;
-      heads -= per_iter;
     }
   }
   if (p.partials != nullptr) store_partial<Lane, 2>(l, dw, p, group, threadIdx.x >> 5);
