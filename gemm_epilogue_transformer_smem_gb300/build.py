@@ -20,7 +20,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libgemm_epi.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 UNITS = ["gemm_epi.cu", "spec_forward.cu", "spec_aux.cu", "spec_fp8.cu", "spec_common.cu", "spec_heads.cu",
-         "heads.cu"]
+         "spec_rotary.cu", "spec_head_norm.cu", "heads.cu"]
 
 
 def sources(csrc=CSRC):

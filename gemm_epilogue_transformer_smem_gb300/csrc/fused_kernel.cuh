@@ -185,6 +185,7 @@ struct KernelParams {
   int32_t head_cols;                     // columns of whole heads
   int32_t head_chunks, log_head_chunks;  // 32-column chunks per head
   int32_t head_rms_at, rotary_at;  // their indices in ops, or -1
+  int32_t uses_bias, uses_col_scale;
   int32_t rot_pairs, rot_half;     // rotated pairs per head; 1: pairs (i, i + rot_pairs)
   float head_inv_dim, head_eps, rot_amplitude;
   const uint64_t* rot_steps;
@@ -290,11 +291,11 @@ template <class Prog>
 __host__ __device__ constexpr int prog_index_of(int code) {
   if constexpr (Prog::is_static) return Prog::index_of(code); else return -1;
 }
-// Programs with heads whose column vectors go through shared memory: compiled,
-// without the e4m3 store whose buffers these are.
+// Programs with heads bring their column vectors into shared memory, unless
+// they have the e4m3 store whose buffers these are.
 template <class Prog>
 __host__ __device__ constexpr bool prog_stages_columns() {
-  if constexpr (Prog::is_static) return Prog::heads && !Prog::has(GEMM_EPI_OP_STORE_E4M3); else return false;
+  if constexpr (Prog::is_static) return Prog::heads && !Prog::has(GEMM_EPI_OP_STORE_E4M3); else return Prog::heads;
 }
 // First op applied to output columns: after the pair, expanding or head ops.
 template <class Prog>
@@ -1155,16 +1156,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int quad = warp & 3;  // TMEM lane quadrant this warp may read
     constexpr bool kStatic = Prog::is_static;
     const int pair_at = kStatic ? prog_pair_at<Prog>() : p.pair_at;
-    const bool paired = pair_at >= 0;
+    const bool paired = !Prog::heads && pair_at >= 0;
     const bool pair_g128 = paired && (kStatic ? prog_pair_g<Prog>() == 128 : p.pair_g == 128);
     // DSWIGLU expands: each 32-column output chunk comes from 16 accumulator
     // columns, so a tile has 2 * BLOCK_N output columns.
     const int expand_at = kStatic ? prog_expand_at<Prog>() : p.expand_at;
-    const bool expand = expand_at >= 0;
+    const bool expand = !Prog::heads && expand_at >= 0;
     const int chunks = paired ? BLOCK_N / 64 : expand ? 2 * BLOCK_N / CHUNK : BLOCK_N / CHUNK;
     const int tile_out_cols = paired ? BLOCK_N / 2 : expand ? 2 * BLOCK_N : BLOCK_N;
     // A static program fixes every flag but the K == 0 one at compile time.
-    const uint32_t flags = kStatic ? (p.flags & (F_ZERO_ACC | F_DEQ)) | static_flags<Prog>() : p.flags;
+    // Programs with heads read no auxiliary tensor.
+    const uint32_t flags = kStatic ? (p.flags & (F_ZERO_ACC | F_DEQ)) | static_flags<Prog>()
+                                   : Prog::heads ? p.flags & ~static_cast<uint32_t>(F_AUX) : p.flags;
     // Product of the dequantisation factors, in fp32 (1 without F_DEQ).
     const float deq = (flags & F_DEQ) ? (p.a_scale_inv ? __ldg(p.a_scale_inv) : 1.0f) *
                                             (p.b_scale_inv ? __ldg(p.b_scale_inv) : 1.0f)
@@ -1174,6 +1177,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint8_t* epi0_ptr = smem + L::OFF_EPI + ew * EPI_BUFS * EPI_BUF_BYTES;
     uint8_t* e80_ptr = smem + L::OFF_E8 + ew * E8_BUFS * E8_BUF_BYTES;
     constexpr bool kStaged = prog_stages_columns<Prog>();
+    const bool staged = kStaged && !(flags & F_E8);
     float* staged_cols = reinterpret_cast<float*>(e80_ptr);  // column scales, then biases, of the tile
     // HEAD_RMS and ROTARY: ops [0, head_first) run on the accumulator, [mid, mid_end)
     // between the two, the rest after them.
@@ -1269,10 +1273,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
 
       // With heads, while the main loop runs: the row's position, the angles of
-      // the first chunks, and the tile's column vectors, which compiled
-      // programs read from the warp's e4m3 staging buffers (they have no e4m3
-      // store); a first read of any of these from L2 between two chunks would
-      // cost as much as a chunk.
+      // the first chunks, and the tile's column vectors, which programs without
+      // an e4m3 store read from the warp's staging buffers for it; a first read
+      // of any of these from L2 between two chunks would cost as much as a
+      // chunk.
       int64_t position = m;
       RowAngles angles;
       int angles_of = -1;
@@ -1299,11 +1303,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             d[0] = make_float4(v[0], v[1], v[2], v[3]);
             d[1] = make_float4(v[4], v[5], v[6], v[7]);
           };
-          __syncwarp();  // the previous tile's reads
-          if (Prog::has(GEMM_EPI_OP_MUL_COL_SCALE)) stage(p.col_scale, 1.0f, staged_cols);
-          if (Prog::has(GEMM_EPI_OP_ADD_BIAS_COL)) stage(p.bias, 0.0f, staged_cols + BLOCK_N);
-          __syncwarp();
-          if (rotary_at >= 0 && nacc0 < p.head_cols && (!SPLIT || mine != 0)) {
+          if (staged) {
+            __syncwarp();  // the previous tile's reads
+            if (p.uses_col_scale) stage(p.col_scale, 1.0f, staged_cols);
+            if (p.uses_bias) stage(p.bias, 0.0f, staged_cols + BLOCK_N);
+            __syncwarp();
+          }
+          if (kStatic && rotary_at >= 0 && nacc0 < p.head_cols && (!SPLIT || mine != 0)) {
             if (first_angles < rot_half_chunks) {
               angles.template set<32, true>(p, position, first_angles * 32);
               angles_of = first_angles;
@@ -1325,13 +1331,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // With heads: an op on accumulator chunk cc, its column vector staged or
       // not, and the ops before HEAD_RMS (and ROTARY).
       auto column_op = [&](auto code, int cc, float (&u)[32]) {
-        if constexpr (kStaged && code == GEMM_EPI_OP_MUL_COL_SCALE) {
+        if (staged && static_cast<int>(code) == GEMM_EPI_OP_MUL_COL_SCALE) {
           const float4* c4 = reinterpret_cast<const float4*>(staged_cols) + cc * 8;
           for_pairs(u, [&](float2 y, int i) {
             const float4 c = c4[i / 2];
             return __fmul2_rn(y, (i & 1) ? make_float2(c.z, c.w) : make_float2(c.x, c.y));
           });
-        } else if constexpr (kStaged && code == GEMM_EPI_OP_ADD_BIAS_COL) {
+        } else if (staged && static_cast<int>(code) == GEMM_EPI_OP_ADD_BIAS_COL) {
           const float4* b4 = reinterpret_cast<const float4*>(staged_cols + BLOCK_N) + cc * 8;
           for_pairs(u, [&](float2 y, int i) {
             const float4 c = b4[i / 2];
@@ -1353,7 +1359,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           });
         } else {
           const int head_first = head_rms_at >= 0 ? head_rms_at : rotary_at;
-          for (int i = 0; i < head_first; ++i) apply_pointwise<32>(p.ops[i].code, u, p, nacc0 + cc * 32, p.N, rs_m);
+          for (int i = 0; i < head_first; ++i) column_op(p.ops[i].code, cc, u);
         }
       };
       // The sum of squares of one chunk; a head's is the sum of its chunks', in
@@ -1523,8 +1529,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                   column_op(std::integral_constant<int, Prog::code_of(decltype(I)::value)>{}, cc, u);
                 });
               } else {
-                for (int i = head_rms_at + 1; i < rotary_at; ++i)
-                  apply_pointwise<32>(p.ops[i].code, u, p, nacc0 + cc * 32, p.N, rs_m);
+                for (int i = head_rms_at + 1; i < rotary_at; ++i) column_op(p.ops[i].code, cc, u);
               }
             }
           };

@@ -66,7 +66,12 @@ constexpr double L2_KEEP_BYTES = 60e6;
 constexpr uint32_t DEFAULT_TIMEOUT_MS = 2000;
 
 constexpr int MAX_SPLIT = 8;         // CTAs of a cluster along K (the portable cluster size)
-constexpr int MIN_SPLIT_BLOCKS = 4;  // K-blocks of a CTA that are worth a cluster's exchange
+// K-blocks of a CTA that are worth a cluster's exchange: 273 x 488 -> 2304 (8
+// K-blocks) takes 16.4 us on clusters of 2, 17.8 on 4; 1106 x 248 -> 960 13.5 us
+// unsplit, 15.5 and 18.0 on 2 and 4.  Up to 64 rows gain from the second CTA
+// whatever its share, since the epilogue is split too: 3 x 128 -> 3584 (2
+// K-blocks) 12.7 us unsplit, 9.6 on 2; but 55 x 528 -> 1536 12.5 us on 2, 14.4 on 8.
+constexpr int MIN_SPLIT_BLOCKS = 4;
 
 struct DeviceState {
   bool ready = false;
@@ -89,7 +94,8 @@ struct SpecTable {
 };
 const SpecTable kSpecTables[] = {
     {ge::kSpecsForward, &ge::kNumSpecsForward}, {ge::kSpecsAux, &ge::kNumSpecsAux}, {ge::kSpecsFp8, &ge::kNumSpecsFp8},
-    {ge::kSpecsCommon, &ge::kNumSpecsCommon}, {ge::kSpecsHeads, &ge::kNumSpecsHeads}};
+    {ge::kSpecsCommon, &ge::kNumSpecsCommon}, {ge::kSpecsRotary, &ge::kNumSpecsRotary},
+    {ge::kSpecsHeadNorm, &ge::kNumSpecsHeadNorm}};
 constexpr int kNumSpecTables = sizeof(kSpecTables) / sizeof(kSpecTables[0]);
 
 // The interpreting kernels (any program); static ones come from the tables.
@@ -556,7 +562,8 @@ int choose_split(const gemm_epi_plan& P, const gemm_epi_args& a, const DeviceSta
   const int64_t pieces = ge::BLOCK_N / P.d.head_dim * slabs;  // heads of a tile by slabs of 32 rows
   for (int n = MAX_SPLIT; n >= 2; --n) {
     const int64_t bytes = (n - 1) * ((pieces + n - 1) / n) * P.d.head_dim * 32 * 4;
-    if (tiles <= dev.split_clusters[n] && k_blocks >= n * MIN_SPLIT_BLOCKS &&
+    const int64_t least = n == 2 && P.d.M <= 64 ? 1 : MIN_SPLIT_BLOCKS;
+    if (tiles <= dev.split_clusters[n] && k_blocks >= n * least &&
         bytes + 4096 <= static_cast<int64_t>(ge::Smem<1>::OFF_EPI))  // and the sums of repeated rows
       return n;
   }
@@ -649,6 +656,8 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
   k.head_rms_at = P.head_rms_at;
   k.rotary_at = P.rotary_at;
   if (P.heads()) {
+    k.uses_bias = P.uses_bias ? 1 : 0;
+    k.uses_col_scale = P.uses_col_scale ? 1 : 0;
     k.head_cols = static_cast<int32_t>(d.head_cols);
     k.head_chunks = d.head_dim / ge::CHUNK;
     while ((1 << k.log_head_chunks) < k.head_chunks) ++k.log_head_chunks;

@@ -262,9 +262,20 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch of the head kernel");
   if (wants_dw) {
-    ge::head_weight_grad_kernel<<<dim3(static_cast<unsigned>((a->head_dim + 31) / 32), 2), dim3(32, 32), 0, st>>>(
-        p.partials, p.q_blocks, static_cast<int>(blocks), a->head_dim, a->dw_q, a->dw_k);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>((a->head_dim + 31) / 32), 2);
+    cfg.blockDim = dim3(32, 32);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    std::memset(&attr, 0, sizeof attr);
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, ge::head_weight_grad_kernel, static_cast<const float*>(p.partials),
+                           static_cast<int>(p.q_blocks), static_cast<int>(blocks), static_cast<int>(a->head_dim),
+                           a->dw_q, a->dw_k);
     if (e != cudaSuccess) return cuda_fail(e, "launch of the weight gradient kernel");
   }
   return GEMM_EPI_OK;

@@ -634,6 +634,7 @@ __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS) heads_backward_kern
   using Ring = HeadRing<T, HALF, 2>;
   using Lane = typename Ring::Lane;
   extern __shared__ uint4 head_ring[];  // [DEPTH][SLOT][HD_THREADS]
+  ptx::launch_dependents();
   const int k = static_cast<int>(blockIdx.x) >= p.q_blocks;
   const int lane = threadIdx.x & 31, warp = (blockIdx.x - (k ? p.q_blocks : 0)) * HD_WARPS + (threadIdx.x >> 5);
   const int group = lane >> p.log_g, in_group = lane & ((1 << p.log_g) - 1);
@@ -755,6 +756,7 @@ template <class T, bool HALF>
 __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS)
     heads_backward_any_kernel(const __grid_constant__ HeadParams p) {
   using Lane = HeadLane<T, 2, HALF>;
+  ptx::launch_dependents();
   const int k = static_cast<int>(blockIdx.x) >= p.q_blocks;
   const int lane = threadIdx.x & 31, warp = (blockIdx.x - (k ? p.q_blocks : 0)) * HD_WARPS + (threadIdx.x >> 5);
   const int group = lane >> p.log_g, in_group = lane & ((1 << p.log_g) - 1);
@@ -794,11 +796,12 @@ __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS)
 
 // dw[d] = sum over the blocks' partial rows, q's before q_blocks and k's after
 // it, in a fixed order (the result does not depend on which block finished
-// first).  Block: 32 columns x 32 row groups; grid y 0: q, 1: k.  A gradient
+// first).  Launched as a dependent of the backward kernel.  Block: 32 columns x 32 row groups; grid y 0: q, 1: k.  A gradient
 // that is NULL is not wanted.
 __global__ void __launch_bounds__(1024) head_weight_grad_kernel(const float* partials, int q_blocks, int blocks,
                                                                 int dim, float* dw_q, float* dw_k) {
   __shared__ float part[32][33];
+  ptx::wait_dependencies();  // launched beside the backward kernel's end
   const int col = blockIdx.x * 32 + threadIdx.x;
   float* dst = blockIdx.y == 0 ? dw_q : dw_k;
   if (dst == nullptr) return;

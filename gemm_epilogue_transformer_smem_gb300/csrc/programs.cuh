@@ -65,6 +65,12 @@ using ProgRotary = StaticProgram<GEMM_EPI_OP_ROTARY, GEMM_EPI_OP_STORE_BF16>;
 using ProgBiasRotary = StaticProgram<GEMM_EPI_OP_ADD_BIAS_COL, GEMM_EPI_OP_ROTARY, GEMM_EPI_OP_STORE_BF16>;
 using ProgNormRotary = StaticProgram<GEMM_EPI_OP_HEAD_RMS, GEMM_EPI_OP_MUL_COL_SCALE, GEMM_EPI_OP_ROTARY,
                                      GEMM_EPI_OP_STORE_BF16>;
+using ProgBiasNormRotary = StaticProgram<GEMM_EPI_OP_ADD_BIAS_COL, GEMM_EPI_OP_HEAD_RMS, GEMM_EPI_OP_MUL_COL_SCALE,
+                                         GEMM_EPI_OP_ROTARY, GEMM_EPI_OP_STORE_BF16>;
+// The same behind an RMSNorm whose S the previous layer's epilogue gave.
+using ProgRmsRotary = StaticProgram<GEMM_EPI_OP_MUL_ROW_SCALE, GEMM_EPI_OP_ROTARY, GEMM_EPI_OP_STORE_BF16>;
+using ProgRmsNormRotary = StaticProgram<GEMM_EPI_OP_MUL_ROW_SCALE, GEMM_EPI_OP_HEAD_RMS, GEMM_EPI_OP_MUL_COL_SCALE,
+                                        GEMM_EPI_OP_ROTARY, GEMM_EPI_OP_STORE_BF16>;
 
 // One compiled program: its op list (code | pair group << 8), the operand
 // width it was compiled for, its kernels for the 1-SM and 2-SM main loops and
@@ -116,11 +122,12 @@ extern const KernelSpec kSpecsFp8[];
 extern const int kNumSpecsFp8;
 extern const KernelSpec kSpecsCommon[];
 extern const int kNumSpecsCommon;
-extern const KernelSpec kSpecsHeads[];
-extern const int kNumSpecsHeads;
+extern const KernelSpec kSpecsRotary[];
+extern const int kNumSpecsRotary;
+extern const KernelSpec kSpecsHeadNorm[];
+extern const int kNumSpecsHeadNorm;
 // The interpreting kernels for programs with HEAD_RMS or ROTARY, for bf16 and
-// 8-bit operands (1-SM, 2-SM, K split over a cluster), from the same
-// translation unit as kSpecsHeads.
+// 8-bit operands (1-SM, 2-SM, K split over a cluster).
 extern const void* const kDynamicHeads[2][3];
 // The interpreting kernels for 8-bit operands (1-SM, 2-SM), from the same
 // translation unit as kSpecsFp8.

@@ -1,17 +1,9 @@
-// spec_heads.cu -- kernels of the programs with HEAD_RMS or ROTARY (the norm
-// and rotary positions of a projection's heads): the interpreting kernels and
-// static forms of the common programs (compiled apart from the others to keep
-// builds parallel).
+// spec_heads.cu -- the interpreting kernels of the programs with HEAD_RMS or
+// ROTARY (the norm and rotary positions of a projection's heads), compiled
+// apart from the others to keep builds parallel.
 #include "programs.cuh"
 
 namespace ge {
-
-const KernelSpec kSpecsHeads[] = {
-    make_spec<ProgRotary>("rotary"),
-    make_spec<ProgBiasRotary>("bias_rotary"),
-    make_spec<ProgNormRotary>("head_norm_rotary"),
-};
-const int kNumSpecsHeads = sizeof(kSpecsHeads) / sizeof(kSpecsHeads[0]);
 
 const void* const kDynamicHeads[2][3] = {
     {reinterpret_cast<const void*>(&fused_gemm_epilogue_kernel<1, DynamicHeadProgram>),
