@@ -207,7 +207,7 @@ class Plan:
              timeout_ms=0, debug_flags=0, B2=None, a_scale_inv=None, b_scale_inv=None,
              col_scale=None, positions=None) -> N.gemm_epi_args:
         a = N.gemm_epi_args()
-        a.alpha, a.fp8_scale = alpha, fp8_scale
+        a.alpha, a.fp8_scale = float(alpha), float(fp8_scale)
         for name, t in (("A", A), ("B", B), ("B2", B2), ("bias", bias), ("row_scale", row_scale),
                         ("residual", residual), ("preact", preact), ("C", C), ("C8", C8), ("amax", amax),
                         ("row_out", row_out), ("col_out", col_out), ("a_scale_inv", a_scale_inv),

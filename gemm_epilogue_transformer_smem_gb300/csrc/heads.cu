@@ -72,14 +72,18 @@ struct Checked {
   size_t size = 2;
 };
 
-gemm_epi_status check_tensor(const gemm_epi_heads& h, const char* name, Checked& c) {
+gemm_epi_status check_tensor(const gemm_epi_qk_args& a, const gemm_epi_heads& h, int32_t heads, const char* name,
+                             Checked& c) {
   if (!h.data) return fail(GEMM_EPI_ERR_INVALID_VALUE, "%s is NULL", name);
   if (!aligned(h.data, c.size))
     return fail(GEMM_EPI_ERR_MISALIGNED, "%s is not aligned to its element size", name);
   const int64_t lim = int64_t(1) << 40;
-  for (int64_t st : {h.stride_batch, h.stride_token, h.stride_head}) {
-    if (st <= -lim || st >= lim) return fail(GEMM_EPI_ERR_INVALID_VALUE, "a stride of %s is out of range", name);
-    if (st * static_cast<int64_t>(c.size) % 16 != 0) c.wide = false;
+  const int64_t extent[3] = {a.batch, a.tokens, heads};
+  const int64_t stride[3] = {h.stride_batch, h.stride_token, h.stride_head};
+  for (int i = 0; i < 3; ++i) {
+    if (stride[i] <= -lim || stride[i] >= lim)
+      return fail(GEMM_EPI_ERR_INVALID_VALUE, "a stride of %s is out of range", name);
+    if (extent[i] > 1 && stride[i] * static_cast<int64_t>(c.size) % 16 != 0) c.wide = false;
   }
   if (!aligned(h.data, 16)) c.wide = false;
   return GEMM_EPI_OK;
@@ -145,11 +149,11 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
   for (int i = 0; i < 2; ++i) {
     if (w[i] && !aligned(w[i], 4)) return fail(GEMM_EPI_ERR_MISALIGNED, "%s_weight must be 4-byte aligned", names[i][0]);
     if (!rows || heads[i] == 0) continue;
-    if ((s = check_tensor(*in[i], names[i][0], c))) return s;
-    if (bwd && (s = check_tensor(*dy[i], names[i][1], c))) return s;
+    if ((s = check_tensor(*a, *in[i], heads[i], names[i][0], c))) return s;
+    if (bwd && (s = check_tensor(*a, *dy[i], heads[i], names[i][1], c))) return s;
     // the backward pass may leave a gradient of q or k out
     if ((!bwd || out[i]->data) &&
-        ((s = check_tensor(*out[i], names[i][2], c)) || (s = check_output(*a, *out[i], heads[i], names[i][2]))))
+        ((s = check_tensor(*a, *out[i], heads[i], names[i][2], c)) || (s = check_output(*a, *out[i], heads[i], names[i][2]))))
       return s;
     if ((s = check_in_place(*out[i], *in[i], names[i][2], names[i][0]))) return s;
     if (bwd && (s = check_in_place(*out[i], *dy[i], names[i][2], names[i][1]))) return s;

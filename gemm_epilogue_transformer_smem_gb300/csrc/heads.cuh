@@ -36,10 +36,16 @@ constexpr int HD_WARPS = 8;
 constexpr int HD_THREADS = 32 * HD_WARPS;
 constexpr int HD_MAX_DIM = 512;  // 16 values per lane x 32 lanes
 // Resident blocks per SM that the register budget allows, and iterations a
-// warp keeps in flight.  Measured on one GB300 at 16384 tokens of 32 + 8 heads
-// of 128 (bf16): norm 54.7 us with 2 blocks, 64.7 with 3 (80 registers, which
-// spill); rotary (65536 tokens) 209.9 us with 3 blocks, 219 with 4; norm 54.7
-// us at depth 3, 56.1 at 4; backward 94.9 us at depth 2, 100 at 3, 102 at 4.
+// warp keeps in flight.  Measured on one GB300 with 32 + 8 heads of 128 (bf16):
+//   norm, 16384 tokens (336 MB): 55.9 us = 6.0 TB/s, 0.88 of the measured copy;
+//     64.3 us with 3 blocks (80 registers, which spill), 59.4 at depth 2, 62.1 at 4
+//   rotary, 65536 tokens (1.34 GB): 210.6 us = 6.4 TB/s, 0.94; 8192 tokens 29.1
+//     us = 0.85; with 4 blocks 212.9 and 30.3, with 2 208.4 and 30.4
+//   backward, 16384 tokens (503 MB): 85.5 us = 5.9 TB/s, 0.87; 104.6 us at
+//     depth 1, 88.6 at 3, 93.9 at 4
+// The norm and the backward pass issue about two instructions in three cycles
+// beside their loads; the registers that hold a norm's weights, angles and one
+// head's values set how many warps share an SM.
 constexpr int HD_ROTARY_BLOCKS = 3, HD_NORM_BLOCKS = 2, HD_BWD_BLOCKS = 2;
 constexpr int HD_FWD_DEPTH = 3, HD_BWD_DEPTH = 2;
 // Partial dw rows of the backward pass: one per block, added up by

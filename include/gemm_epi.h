@@ -34,6 +34,10 @@
  *    pairwise transforms, accumulation) finished on the on-chip output tile,
  *    covering forward and backward work: "CODA: ... GEMM-Epilogue"
  *    (lehuy.net), "How CODA works".
+ *  - rotary positions (Su et al., "RoFormer") and their frequencies scaled for
+ *    long contexts (Peng et al., "YaRN": linear, base change, by parts); an RMS
+ *    norm of every query and key head before them.  The pages have no
+ *    counterpart: these complete the q|k|v projection whose GEMM they cover.
  *  - create once (validate + plan), then execute with a pack of pointers and
  *    a caller-owned workspace: cuDNN Graph API tutorial, five-step build
  *    paragraph; launches are safe to capture in a CUDA graph (same page, CUDA
@@ -44,7 +48,8 @@
  *    and owns (the workspace included).  The library owns only the host-side
  *    plan behind a gemm_epi_handle.
  *  - gemm_epi_run allocates nothing and never synchronises: it enqueues
- *    cudaMemsetAsync calls (reduction outputs and the workspace) and one
+ *    cudaMemsetAsync calls (reduction outputs and the workspace; programs with
+ *    HEAD_RMS or ROTARY clear the workspace with a kernel) and one
  *    kernel launch on `stream` (a cudaStream_t; NULL = legacy default stream).
  *  - Reduction outputs (amax, row_out, col_out) are OVERWRITTEN by each run,
  *    never accumulated across calls.

@@ -375,3 +375,29 @@ def test_split_k_wait_that_runs_out_is_reported():
     assert p.plan.query_status(p.out.workspace) == native.GEMM_EPI_ERR_TIMEOUT
     p.run()
     p.check()
+
+
+@pytest.mark.parametrize("m", [40, 300])
+def test_dequantisation_factors(m):
+    """Powers of two, so the accumulator stays exact: the head's norm is taken
+    after them (split over K at 40 rows, one loop at 300)."""
+    p = Problem(("head_rms:1e-2", "col_scale", "rotary", "store_bf16"), m, 2048, 3, 1, 128, 128, "half", in_type="e4m3")
+    p.run(a_scale_inv=torch.tensor([0.5], device=DEV), b_scale_inv=torch.tensor([0.0625], device=DEV))
+    p.A64, want_b = p.A64 * 0.5, p.B64 * 0.0625
+    p.B64 = want_b
+    p.check()
+
+
+def test_interpreted_and_compiled_programs_give_the_same_bits():
+    """The interpreter works its angles out eight pairs at a time and stages
+    its column vectors alike: every rounding is the same."""
+    for program in (ROT, NORM, ("bias", "rotary", "store_bf16"), ("row_scale", "rotary", "store_bf16"),
+                    ("bias",) + NORM, ("row_scale",) + NORM):
+        for m in (48, 200):
+            p = Problem(program, m, 1024, 5, 2, 64, 64, "interleaved")
+            p.run()
+            got = p.out.C.clone()
+            p.run(VARIANTS["interp"])
+            torch.cuda.synchronize()
+            assert torch.equal(got, p.out.C), program
+            p.check()

@@ -413,3 +413,31 @@ def test_refuses_host_tensors():
         api.rotary(x, None, rope, q_out=x)
     with pytest.raises(ValueError, match="steps are on"):
         api.rotary(x.cuda(), None, rope, q_out=x.cuda())
+
+
+def test_strides_of_single_steps_do_not_matter():
+    """One sequence of one token: the strides of those dimensions are never
+    used, whatever they are."""
+    d, rope = 64, api.Rotary(64, device=DEV)
+    x = normal(gen(15), 1, 1, 3, d)
+    odd = x.as_strided((1, 1, 3, d), (7, 5, d, 1))
+    want, got = torch.empty_like(x), torch.empty_like(x)
+    api.rotary(x, None, rope, q_out=want)
+    api.rotary(odd, None, rope, q_out=got.as_strided((1, 1, 3, d), (1, 3, d, 1)))
+    torch.cuda.synchronize()
+    assert torch.equal(want, got)
+
+
+def test_few_tokens_share_and_many_tokens_fill_the_grid_alike():
+    """A token's result does not depend on how many tokens go with it."""
+    d, rope = 96, api.Rotary(96, device=DEV)
+    x = normal(gen(16), 5000, 7, d)
+    pos = torch.arange(5000, device=DEV, dtype=torch.int32) * 3
+    w = 1.0 + 0.1 * normal(gen(17), d, dtype=F32)
+    full = torch.empty_like(x)
+    api.qk_norm_rotary(x, None, rope, pos, q_weight=w, q_out=full)
+    for a, b in ((0, 1), (17, 20), (4000, 4999), (4999, 5000)):
+        part = torch.empty(b - a, 7, d, dtype=BF, device=DEV)
+        api.qk_norm_rotary(x[a:b], None, rope, pos[a:b], q_weight=w, q_out=part)
+        torch.cuda.synchronize()
+        assert torch.equal(part, full[a:b])
