@@ -405,6 +405,7 @@ class Rotary:
         # uint64 bits in an int64 tensor: torch has no arithmetic on them here
         self.steps = torch.frombuffer(steps, dtype=torch.int64).clone().to(device)
         self.steps_ptr, self.index = self.steps.data_ptr(), self.steps.get_device()
+        self.vector_shape = (self.head_dim,)
 
 
 # gemm_epi_qk_args, packed in one step: filling a ctypes structure field by
@@ -424,114 +425,125 @@ def _head_entry(name: str):
     return fn
 
 
-def _heads(name: str, t: torch.Tensor, rope: Rotary, dtype, index: int, shape=None):
-    """(pointer, batch, token and head strides) of a (batch, tokens, heads,
-    head_dim) or (tokens, heads, head_dim) tensor, checked; `shape`: the one it
-    must have."""
-    own = t.shape
-    if shape is not None:
-        if own != shape:
-            raise ValueError("%s: shape %s does not match %s" % (name, tuple(own), tuple(shape)))
-    elif len(own) not in (3, 4) or own[-1] != rope.head_dim:
-        raise ValueError("%s: expected (batch, tokens, heads, %d) or (tokens, heads, %d), got %s"
-                         % (name, rope.head_dim, rope.head_dim, tuple(own)))
-    if t.dtype is not dtype:
-        raise ValueError("%s: %s does not match %s" % (name, t.dtype, dtype))
+def _heads(name: str, t: torch.Tensor, shape, dtype, index: int):
+    """(pointer, batch, token and head strides) of a tensor of q's or k's
+    shape, type and device, checked."""
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError("%s: %s %s does not match %s %s" % (name, t.dtype, tuple(t.shape), dtype, tuple(shape)))
     if t.get_device() != index:
         raise ValueError("%s is on %s, not with the other tensors" % (name, t.device))
     st = t.stride()
-    if st[-1] != 1 and t.numel():
-        raise ValueError("%s: the values of a head must be contiguous" % name)
     if len(st) == 4:
-        return t.data_ptr(), st[0], st[1], st[2]
-    return t.data_ptr(), 0, st[0], st[1]
+        sb, ss, sh, sd = st
+    else:
+        sb, (ss, sh, sd) = 0, st
+    if sd != 1 and t.numel():
+        raise ValueError("%s: the values of a head must be contiguous" % name)
+    return t.data_ptr(), sb, ss, sh
 
 
-def _vector(name: str, t: Optional[torch.Tensor], rope: Rotary, index: int) -> int:
-    if t is None:
-        return 0
+def _head_shape(name: str, t: torch.Tensor, rope: Rotary):
+    shape = t.shape
+    if len(shape) not in (3, 4) or shape[-1] != rope.head_dim:
+        raise ValueError("%s: expected (batch, tokens, heads, %d) or (tokens, heads, %d), got %s"
+                         % (name, rope.head_dim, rope.head_dim, tuple(shape)))
+    return shape
+
+
+def _vector(name: str, t: torch.Tensor, rope: Rotary, index: int) -> int:
     if t.dtype is not torch.float32:
         raise TypeError("%s: expected a f32 tensor, got %s" % (name, t.dtype))
-    if t.shape != (rope.head_dim,) or not t.is_contiguous():
+    if t.shape != rope.vector_shape or not t.is_contiguous():
         raise ValueError("%s: expected %d contiguous values, got %s" % (name, rope.head_dim, tuple(t.shape)))
     if t.get_device() != index:
         raise ValueError("%s is on %s, not with the other tensors" % (name, t.device))
     return t.data_ptr()
 
 
-def _head_call(entry: str, q, k, rope: Rotary, positions, q_out, k_out, dyq=None, dyk=None, *, backward=False,
-               inverse=False, eps=0.0, q_weight=None, k_weight=None, dwq=None, dwk=None, workspace=None,
-               stream=None) -> None:
+def _head_call(entry: str, q, k, rope: Rotary, positions, q_out, k_out, stream, inverse=0, eps=0.0, q_weight=None,
+               k_weight=None, backward=False, dyq=None, dyk=None, dwq=None, dwk=None, workspace=None) -> None:
     """Checks the tensors of a gemm_epi_qk_args, packs it and calls `entry` on
     the current (or given) stream of their device."""
     first = q if q is not None else k
     if first is None:
         raise ValueError("q and k are both None")
     dtype, index = first.dtype, first.get_device()
-    if dtype not in HEAD_TYPES:
+    type_code = HEAD_TYPES.get(dtype)
+    if type_code is None:
         raise TypeError("%s: expected a bf16 or fp32 tensor, got %s" % ("q" if q is not None else "k", dtype))
     q_heads = k_heads = 0
     tq = tqo = tdq = tk = tko = tdk = _NO_HEADS
+    shape = None
     if q is not None:
-        tq = _heads("q", q, rope, dtype, index)
-        shape = q.shape
+        shape = _head_shape("q", q, rope)
         q_heads = shape[-2]
+        tq = _heads("q", q, shape, dtype, index)
         if q_out is not None:
-            tqo = _heads("dq" if backward else "q_out", q_out, rope, dtype, index, shape)
-        if dyq is not None:
-            tdq = _heads("dyq", dyq, rope, dtype, index, shape)
+            tqo = _heads("dq" if backward else "q_out", q_out, shape, dtype, index)
+        elif not backward:
+            raise ValueError("q_out is missing (pass q itself to work in place)")
+        if backward and dyq is not None:
+            tdq = _heads("dyq", dyq, shape, dtype, index)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
     if k is not None:
-        if q is not None and (q.shape[:-2] != k.shape[:-2] or k.dtype is not dtype):
-            raise ValueError("q %s %s and k %s %s do not belong together" % (dtype, tuple(q.shape), k.dtype, tuple(k.shape)))
-        tk = _heads("k", k, rope, dtype, index)
-        shape = k.shape
+        k_shape = _head_shape("k", k, rope)
+        if shape is not None and (k_shape[:-2] != shape[:-2] or k.dtype is not dtype):
+            raise ValueError("q %s %s and k %s %s do not belong together" % (dtype, tuple(shape), k.dtype, tuple(k_shape)))
+        shape = k_shape
         k_heads = shape[-2]
+        tk = _heads("k", k, shape, dtype, index)
         if k_out is not None:
-            tko = _heads("dk" if backward else "k_out", k_out, rope, dtype, index, shape)
-        if dyk is not None:
-            tdk = _heads("dyk", dyk, rope, dtype, index, shape)
-    if backward:
-        if (dyq is None) != (q is None) or (dyk is None) != (k is None):
-            raise ValueError("a gradient and its input (dyq and q, dyk and k) must be given together")
-    elif (q is not None and q_out is None) or (k is not None and k_out is None):
-        raise ValueError("%s_out is missing (pass %s itself to work in place)" % (("q",) * 2 if q is not None and q_out is None else ("k",) * 2))
-    if (q is None and q_out is not None) or (k is None and k_out is not None):
-        raise ValueError("%s_out without %s" % (("q",) * 2 if q is None else ("k",) * 2))
+            tko = _heads("dk" if backward else "k_out", k_out, shape, dtype, index)
+        elif not backward:
+            raise ValueError("k_out is missing (pass k itself to work in place)")
+        if backward and dyk is not None:
+            tdk = _heads("dyk", dyk, shape, dtype, index)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if backward and ((dyq is None) != (q is None) or (dyk is None) != (k is None)):
+        raise ValueError("a gradient and its input (dyq and q, dyk and k) must be given together")
     batch, tokens = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
     if rope.index != index:
         raise ValueError("the rotary steps are on %s, q and k on %s" % (rope.steps.device, first.device))
-    at = wide = pos_stride = 0
+    at = wide = pos_stride = ws = ws_bytes = wq = wk = dq_at = dk_at = 0
     if positions is not None:
         at, wide, pos_stride = _positions(positions, batch, tokens, index)
-    ws = ws_bytes = 0
-    if workspace is not None:
-        if workspace.get_device() != index or not workspace.is_contiguous():
-            raise ValueError("workspace: expected a contiguous tensor with the others")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    packed = _QK_ARGS.pack(
-        batch, tokens, q_heads, k_heads, rope.head_dim, rope.rotary_dim, rope.layout_code, HEAD_TYPES[dtype],
-        *tq, *tk, *tqo, *tko, *tdq, *tdk, rope.steps_ptr, at, pos_stride, wide, 1 if inverse else 0,
-        rope.amplitude, eps, _vector("q_weight", q_weight, rope, index), _vector("k_weight", k_weight, rope, index),
-        _vector("dwq", dwq, rope, index), _vector("dwk", dwk, rope, index), ws, ws_bytes)
+    if q_weight is not None:
+        wq = _vector("q_weight", q_weight, rope, index)
+    if k_weight is not None:
+        wk = _vector("k_weight", k_weight, rope, index)
+    if backward:
+        if dwq is not None:
+            dq_at = _vector("dwq", dwq, rope, index)
+        if dwk is not None:
+            dk_at = _vector("dwk", dwk, rope, index)
+        if workspace is not None:
+            if workspace.get_device() != index or not workspace.is_contiguous():
+                raise ValueError("workspace: expected a contiguous tensor with the others")
+            ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    packed = _QK_ARGS.pack(batch, tokens, q_heads, k_heads, rope.head_dim, rope.rotary_dim, rope.layout_code, type_code,
+                           *tq, *tk, *tqo, *tko, *tdq, *tdk, rope.steps_ptr, at, pos_stride, wide, inverse,
+                           rope.amplitude, eps, wq, wk, dq_at, dk_at, ws, ws_bytes)
     if index < 0:
         raise ValueError("expected CUDA tensors, got %s" % first.device)
+    fn = _head_entries.get(entry) or _head_entry(entry)
     if index == torch.cuda.current_device():
-        status = _head_entry(entry)(packed, _raw_stream(index) if stream is None else stream.cuda_stream)
+        status = fn(packed, _raw_stream(index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(index):
-            status = _head_entry(entry)(packed, _raw_stream(index) if stream is None else stream.cuda_stream)
+            status = fn(packed, _raw_stream(index) if stream is None else stream.cuda_stream)
     if status:
         N.check(status)
 
 
 def _positions(p: torch.Tensor, batch: int, tokens: int, index: int):
     """(pointer, 1 if 64-bit, batch stride) of a (tokens,) or (batch, tokens) tensor."""
-    if p.dtype is not torch.int32 and p.dtype is not torch.int64:
-        raise TypeError("positions: expected an int32 or int64 tensor, got %s" % p.dtype)
+    dtype, shape, st = p.dtype, p.shape, p.stride()
+    if dtype is not torch.int32 and dtype is not torch.int64:
+        raise TypeError("positions: expected an int32 or int64 tensor, got %s" % dtype)
     if p.get_device() != index:
         raise ValueError("positions are on %s, not with the other tensors" % p.device)
-    shape = p.shape
-    st = p.stride()
     if shape == (batch, tokens):
         stride = st[0] if batch > 1 else 0
     elif shape == (tokens,):
@@ -540,7 +552,7 @@ def _positions(p: torch.Tensor, batch: int, tokens: int, index: int):
         raise ValueError("positions: expected (%d,) or (%d, %d), got %s" % (tokens, batch, tokens, tuple(shape)))
     if tokens > 1 and st[-1] != 1:
         raise ValueError("positions: the positions of a sequence must be contiguous")
-    return p.data_ptr(), 1 if p.dtype is torch.int64 else 0, stride
+    return p.data_ptr(), 1 if dtype is torch.int64 else 0, stride
 
 
 def rotary(q, k, rope: Rotary, positions=None, *, q_out=None, k_out=None, inverse: bool = False, stream=None) -> None:
@@ -553,7 +565,7 @@ def rotary(q, k, rope: Rotary, positions=None, *, q_out=None, k_out=None, invers
     or int64, (tokens,) or (batch, tokens); None counts every sequence from 0.
     inverse=True applies the transpose: the backward pass, from the gradients
     of q_out and k_out to those of q and k.  Asynchronous."""
-    _head_call("gemm_epi_rotary", q, k, rope, positions, q_out, k_out, inverse=inverse, stream=stream)
+    _head_call("gemm_epi_rotary", q, k, rope, positions, q_out, k_out, stream, 1 if inverse else 0)
 
 
 def qk_norm_rotary(q, k, rope: Rotary, positions=None, *, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -561,8 +573,7 @@ def qk_norm_rotary(q, k, rope: Rotary, positions=None, *, q_weight=None, k_weigh
     """gemm_epi_qk_norm_rotary: each head of q and k divided by its root mean
     square (plus eps), multiplied by the fp32 weight (None: 1) and rotated, in
     one pass; arguments as for rotary().  Asynchronous."""
-    _head_call("gemm_epi_qk_norm_rotary", q, k, rope, positions, q_out, k_out, eps=eps, q_weight=q_weight,
-               k_weight=k_weight, stream=stream)
+    _head_call("gemm_epi_qk_norm_rotary", q, k, rope, positions, q_out, k_out, stream, 0, eps, q_weight, k_weight)
 
 
 def qk_norm_rotary_workspace(head_dim: int) -> int:
@@ -579,5 +590,5 @@ def qk_norm_rotary_backward(dyq, dyk, q, k, rope: Rotary, positions=None, *, q_w
     the weights, summed over batch, tokens and heads, into the fp32 dwq and dwk
     (overwritten).  Each of the four may be None; dwq and dwk need a workspace
     of qk_norm_rotary_workspace(head_dim) bytes.  Asynchronous."""
-    _head_call("gemm_epi_qk_norm_rotary_backward", q, k, rope, positions, dq, dk, dyq, dyk, backward=True, eps=eps,
-               q_weight=q_weight, k_weight=k_weight, dwq=dwq, dwk=dwk, workspace=workspace, stream=stream)
+    _head_call("gemm_epi_qk_norm_rotary_backward", q, k, rope, positions, dq, dk, stream, 0, eps, q_weight, k_weight,
+               True, dyq, dyk, dwq, dwk, workspace)
