@@ -223,10 +223,11 @@ class Plan:
         if timeout_ms or debug_flags:
             a.timeout_ms, a.debug_flags = int(timeout_ms), int(debug_flags)
         if self.rotary is not None:
-            index = self.rotary.index
+            steps = self.rotary.steps
+            index = steps.get_device()
             if A is not None and index != A.get_device():
-                raise ValueError("the rotary steps are on %s, A on %s" % (self.rotary.steps.device, A.device))
-            a.rotary_steps, a.rotary_amplitude = self.rotary.steps_ptr, self.rotary.amplitude
+                raise ValueError("the rotary steps are on %s, A on %s" % (steps.device, A.device))
+            a.rotary_steps, a.rotary_amplitude = steps.data_ptr(), self.rotary.amplitude
             if positions is not None:
                 if positions.dtype is not torch.int32 and positions.dtype is not torch.int64:
                     raise TypeError("positions: expected an int32 or int64 tensor, got %s" % positions.dtype)
@@ -235,7 +236,7 @@ class Plan:
                                      % (self.batch * self.M, tuple(positions.shape)))
                 if positions.get_device() != index:
                     raise ValueError("positions are on %s, the rotary steps on %s"
-                                     % (positions.device, self.rotary.steps.device))
+                                     % (positions.device, steps.device))
                 a.positions, a.positions_64 = positions.data_ptr(), 1 if positions.dtype is torch.int64 else 0
         elif positions is not None:
             raise ValueError("positions: the plan has no rotary")
@@ -404,7 +405,6 @@ class Rotary:
         N.check(lib.gemm_epi_rotary_steps(ctypes.byref(f), steps), lib)
         # uint64 bits in an int64 tensor: torch has no arithmetic on them here
         self.steps = torch.frombuffer(steps, dtype=torch.int64).clone().to(device)
-        self.steps_ptr, self.index = self.steps.data_ptr(), self.steps.get_device()
         self.vector_shape = (self.head_dim,)
 
 
@@ -504,8 +504,9 @@ def _head_call(entry: str, q, k, rope: Rotary, positions, q_out, k_out, stream, 
     if backward and ((dyq is None) != (q is None) or (dyk is None) != (k is None)):
         raise ValueError("a gradient and its input (dyq and q, dyk and k) must be given together")
     batch, tokens = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
-    if rope.index != index:
-        raise ValueError("the rotary steps are on %s, q and k on %s" % (rope.steps.device, first.device))
+    steps = rope.steps
+    if steps.get_device() != index:
+        raise ValueError("the rotary steps are on %s, q and k on %s" % (steps.device, first.device))
     at = wide = pos_stride = ws = ws_bytes = wq = wk = dq_at = dk_at = 0
     if positions is not None:
         at, wide, pos_stride = _positions(positions, batch, tokens, index)
@@ -523,7 +524,7 @@ def _head_call(entry: str, q, k, rope: Rotary, positions, q_out, k_out, stream, 
                 raise ValueError("workspace: expected a contiguous tensor with the others")
             ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     packed = _QK_ARGS.pack(batch, tokens, q_heads, k_heads, rope.head_dim, rope.rotary_dim, rope.layout_code, type_code,
-                           *tq, *tk, *tqo, *tko, *tdq, *tdk, rope.steps_ptr, at, pos_stride, wide, inverse,
+                           *tq, *tk, *tqo, *tko, *tdq, *tdk, steps.data_ptr(), at, pos_stride, wide, inverse,
                            rope.amplitude, eps, wq, wk, dq_at, dk_at, ws, ws_bytes)
     if index < 0:
         raise ValueError("expected CUDA tensors, got %s" % first.device)

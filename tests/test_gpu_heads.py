@@ -441,3 +441,62 @@ def test_few_tokens_share_and_many_tokens_fill_the_grid_alike():
         api.qk_norm_rotary(x[a:b], None, rope, pos[a:b], q_weight=w, q_out=part)
         torch.cuda.synchronize()
         assert torch.equal(part, full[a:b])
+
+
+FIRST_CALL_IN_A_CAPTURE = """
+import torch
+from gemm_epilogue_transformer_smem_gb300 import api
+d = 64
+q, dy = (torch.randn(1, 50, 4, d, device="cuda").bfloat16() for _ in range(2))
+rope, ws = api.Rotary(d), torch.empty(api.qk_norm_rotary_workspace(d), dtype=torch.uint8, device="cuda")
+y, y2, dq = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+dw = torch.empty(d, device="cuda")
+plan = api.Plan(48, 256, 512, ["head_rms", "rotary", "store_bf16"], b_layout="nk", rotary=rope, head_cols=128)
+x, w = torch.randn(48, 512, device="cuda").bfloat16(), torch.randn(256, 512, device="cuda").bfloat16()
+out = api.allocate_outputs(plan, "cuda")
+
+def step():
+    api.rotary(q, None, rope, q_out=y)
+    api.qk_norm_rotary(q, None, rope, q_out=y2)
+    api.qk_norm_rotary_backward(dy, None, q, None, rope, dq=dq, dwq=dw, workspace=ws)
+    plan.run(x, w, C=out.C, workspace=out.workspace)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (y, y2, dq, dw, out.C)]
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (y, y2, dq, dw, out.C)))
+print("ok")
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    """Nothing a first call sets up is in the way of a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_A_CAPTURE], cwd=root, capture_output=True, text=True,
+                       timeout=300, env=dict(os.environ, PYTHONPATH=root))
+    assert r.returncode == 0 and "ok" in r.stdout, r.stderr[-2000:]
+
+
+def test_frequencies_follow_their_tensor():
+    """A copy of the frequencies, or ones put in their place, are the ones used."""
+    import copy
+    d = 64
+    x = normal(gen(18), 1, 20, 2, d)
+    rope, other = api.Rotary(d, device=DEV), api.Rotary(d, base=500.0, device=DEV)
+    want, got = torch.empty_like(x), torch.empty_like(x)
+    api.rotary(x, None, other, q_out=want)
+    twin = copy.deepcopy(rope)
+    del rope
+    twin.steps = other.steps.clone()
+    api.rotary(x, None, twin, q_out=got)
+    torch.cuda.synchronize()
+    assert torch.equal(want, got)
