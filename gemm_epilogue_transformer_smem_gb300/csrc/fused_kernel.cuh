@@ -1222,14 +1222,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // `unit`; first the rotated part in the half layout, whose chunks come in
       // pairs (i, i + half), head by head, then the other chunks.  All heads of
       // a tile in lockstep: a row's angles are worked out once for them.
-      struct HeadChunk {
+      struct HeadStep {
         int c, unit, in_head;
         bool in_pair, second;
       };
       const int rot_half_chunks = Prog::heads && p.rot_half && rotary_at >= 0 ? p.rot_pairs >> 5 : 0;
-      auto head_chunk = [&](int ci) {
+      auto head_step = [&](int ci) {
         const int log_units = 3 - p.log_head_chunks, units = 1 << log_units;
-        HeadChunk h;
+        HeadStep h;
         h.in_pair = ci < 2 * rot_half_chunks * units;
         h.second = false;
         if (h.in_pair) {
@@ -1260,7 +1260,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         steps = 0;
         for (int ci = chunks - 1; ci >= 0; --ci) {
-          const HeadChunk h = head_chunk(ci);
+          const HeadStep h = head_step(ci);
           const int share = h.unit + h.in_head - (h.second ? rot_half_chunks : 0);
           if ((share & (p.split_reps - 1)) != part || !slab_ok) continue;
           shared |= 1u << h.c;
@@ -1467,8 +1467,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       float held[Prog::heads ? 32 : 1];
 
       for (int ci = 0; ci < steps; ++ci) {
-        HeadChunk h = {ci, 0, 0, false, false};
-        if constexpr (Prog::heads) h = head_chunk(SPLIT ? static_cast<int>(walk >> (4 * ci)) & 15 : ci);
+        HeadStep h = {ci, 0, 0, false, false};
+        if constexpr (Prog::heads) h = head_step(SPLIT ? static_cast<int>(walk >> (4 * ci)) & 15 : ci);
         const int c = h.c, unit = h.unit, in_head = h.in_head;
         const bool in_pair = h.in_pair, second = h.second;
         const uint32_t g = gchunk + ci;
