@@ -165,7 +165,10 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
   for (const float* d : {a->dw_q, a->dw_k})
     if (bwd && d && !aligned(d, 4)) return fail(GEMM_EPI_ERR_MISALIGNED, "dw_q and dw_k must be 4-byte aligned");
   if (wants_dw && a->dw_q == a->dw_k) return fail(GEMM_EPI_ERR_INVALID_VALUE, "dw_q and dw_k are the same buffer");
-  const bool work = rows && (a->q_heads > 0 || a->k_heads > 0) && (!bwd || wants_dw || a->q_out.data || a->k_out.data);
+  // The heads that a pass over the rows is for: backward, those a wanted result comes from.
+  const int64_t q_work = !bwd || a->q_out.data || a->dw_q ? heads[0] : 0;
+  const int64_t k_work = !bwd || a->k_out.data || a->dw_k ? heads[1] : 0;
+  const bool work = rows && q_work + k_work > 0;
   if (work) {
     if (!a->steps) return fail(GEMM_EPI_ERR_INVALID_VALUE, "steps is NULL");
     if (!aligned(a->steps, 8)) return fail(GEMM_EPI_ERR_MISALIGNED, "steps must be 8-byte aligned");
@@ -182,7 +185,7 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
   if ((s = device_setup(&sms))) return s;
   cudaError_t e;
   if (!work) {
-    // no rows: the weights' gradients are zero
+    // nothing to sum: the weights' gradients are zero
     for (float* d : {a->dw_q, a->dw_k})
       if (bwd && d && (e = cudaMemsetAsync(d, 0, sizeof(float) * a->head_dim, st)) != cudaSuccess)
         return cuda_fail(e, "cudaMemsetAsync of dw");
@@ -251,8 +254,6 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
     // shared between q and k by their work; a part none of whose results is
     // wanted gets no block
     const int64_t most = std::min<int64_t>(ge::HD_MAX_PARTIALS, resident);
-    const int64_t q_work = a->q_out.data || a->dw_q ? heads[0] : 0;
-    const int64_t k_work = a->k_out.data || a->dw_k ? heads[1] : 0;
     int64_t q_most = q_work ? most : 0;
     if (q_work && k_work)
       q_most = std::min(most - 1, std::max<int64_t>(1, (most * q_work + (q_work + k_work) / 2) / (q_work + k_work)));
@@ -260,7 +261,7 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
     p.q_blocks = static_cast<int32_t>(q);
     blocks = q + k;
   } else {
-    blocks = share_out(p.share[0], heads[0] + heads[1], resident);
+    blocks = share_out(p.share[0], q_work + k_work, resident);
   }
   kernel.fn<<<static_cast<unsigned>(blocks), ge::HD_THREADS, static_cast<size_t>(kernel.smem), st>>>(p);
   e = cudaGetLastError();

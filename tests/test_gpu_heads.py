@@ -261,6 +261,28 @@ def test_no_rows():
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_weight_gradient_of_no_heads(dtype):
+    """The gradient of a weight that no head used is zero, also where nothing
+    else is asked for."""
+    d, rope = 64, api.Rotary(64, device=DEV)
+    x = torch.randn(2, 3, 4, d, device=DEV).to(dtype)
+    dy = torch.randn(2, 3, 4, d, device=DEV).to(dtype)
+    none = torch.empty(2, 3, 0, d, dtype=dtype, device=DEV)
+    ws = torch.empty(api.qk_norm_rotary_workspace(d), dtype=torch.uint8, device=DEV)
+    dwq, dwk, dwq2 = (torch.full((d,), 7.0, device=DEV) for _ in range(3))
+    api.qk_norm_rotary_backward(none, dy, none, x, rope, dwq=dwq, workspace=ws)
+    api.qk_norm_rotary_backward(dy, None, x, None, rope, dwk=dwk)
+    dk = torch.empty_like(x)
+    api.qk_norm_rotary_backward(none, dy, none, x, rope, dk=dk, dwq=dwq2, workspace=ws)
+    want = torch.empty_like(x)
+    api.qk_norm_rotary_backward(dy, None, x, None, rope, dq=want)
+    torch.cuda.synchronize()
+    for dw in (dwq, dwk, dwq2):
+        assert bool((dw == 0).all())
+    assert torch.equal(dk, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_positions_far_negative_and_shared(dtype):
     """Phases are exact for any 64-bit position; int32 and int64 agree; one row
     of positions serves a batch."""
