@@ -727,13 +727,14 @@ __device__ __forceinline__ void dswiglu_expand(const float (&dh)[16], const floa
 struct RowAngles {
   float2 c[16], s[16];
 
-  // Pairs pair0 .. pair0 + NP - 1; WHOLE: all of them rotate, else those past
-  // the rotated part stay as they are.  Every step is read before the first is
-  // used: one latency, not one for each.
+  // Pairs pair0 .. pair0 + NP - 1 (pair0 even); WHOLE: all of them rotate, else
+  // those past the rotated part stay as they are.  Every step is read before
+  // the first is used: one latency, not one for each.
   template <int NP, bool WHOLE>
   __device__ __forceinline__ void set(const KernelParams& p, int64_t position, int pair0) {
     uint64_t st[NP];
-    if constexpr (WHOLE) {
+    const bool whole = WHOLE || pair0 + NP <= p.rot_pairs;
+    if (whole) {
       const ulonglong2* src = reinterpret_cast<const ulonglong2*>(p.rot_steps + pair0);
 #pragma unroll
       for (int i = 0; i < NP / 2; ++i) {
@@ -758,7 +759,7 @@ struct RowAngles {
         s[i] = __fmul2_rn(s[i], amp);
       }
     }
-    if constexpr (!WHOLE) {
+    if (!whole) {
 #pragma unroll
       for (int i = 0; i < NP / 2; ++i) {
         if (pair0 + 2 * i >= p.rot_pairs) c[i].x = 1.0f, s[i].x = 0.0f;
@@ -775,6 +776,15 @@ struct RowAngles {
     a1 = fmaf(a.y, c[i].y, -bs.y);
     b0 = nb.x;
     b1 = nb.y;
+  }
+  // The same on neighbours in registers, one pair at a time: packed operands
+  // would have to be put together first.
+  __device__ __forceinline__ void rotate_interleaved(int i, float& a0, float& b0, float& a1, float& b1) const {
+    const float x = a0, y = a1;
+    a0 = fmaf(x, c[i].x, -__fmul_rn(b0, s[i].x));
+    b0 = fmaf(x, s[i].x, __fmul_rn(b0, c[i].x));
+    a1 = fmaf(y, c[i].y, -__fmul_rn(b1, s[i].y));
+    b1 = fmaf(y, s[i].y, __fmul_rn(b1, c[i].y));
   }
 };
 
@@ -1362,15 +1372,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int i = 0; i < head_first; ++i) column_op(p.ops[i].code, cc, u);
         }
       };
-      // The sum of squares of one chunk; a head's is the sum of its chunks', in
-      // order, so that it has the same bits however the chunks are shared out.
+      // The sum of squares of one chunk (four chains: a single one is 16 dependent
+      // steps); a head's is the sum of its chunks', in order, so that it has the
+      // same bits however the chunks are shared out.
       auto chunk_squares = [&](float (&u)[32]) {
-        float2 ss = make_float2(0.0f, 0.0f);
-        for_pairs(u, [&](float2 y, int) {
-          ss = __ffma2_rn(y, y, ss);
+        float2 ss[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ss[i] = make_float2(0.0f, 0.0f);
+        for_pairs(u, [&](float2 y, int i) {
+          ss[i % 4] = __ffma2_rn(y, y, ss[i % 4]);
           return y;
         });
-        return ss.x + ss.y;
+        const float2 t = __fadd2_rn(__fadd2_rn(ss[0], ss[1]), __fadd2_rn(ss[2], ss[3]));
+        return t.x + t.y;
       };
       float head_r[Prog::heads ? 8 : 1];  // 1 / rms of each head of the tile (this row)
 
@@ -1466,6 +1480,64 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // The second chunk of a rotated pair of chunks, until its turn.
       float held[Prog::heads ? 32 : 1];
 
+      // With heads: accumulator chunk cc, and two at once: one wait for both in
+      // the compiled programs, which have the registers.
+      auto load_acc = [&](int cc, float (&u)[32]) {
+        if (flags & F_ZERO_ACC) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) u[j] = 0.0f;
+        } else {
+          uint32_t r[32];
+          ptx::tmem_ld32_sync(t_row + cc * 32, r);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) u[j] = __uint_as_float(r[j]);
+        }
+      };
+      auto load_two = [&](int c0, int c1, float (&u)[32], float (&w)[32]) {
+        if (!kStatic || (flags & F_ZERO_ACC)) {
+          load_acc(c0, u);
+          load_acc(c1, w);
+        } else {
+          uint32_t r[64];
+          ptx::tmem_ld64_sync(t_row + c0 * 32, t_row + c1 * 32, r);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            u[j] = __uint_as_float(r[j]);
+            w[j] = __uint_as_float(r[32 + j]);
+          }
+        }
+      };
+      if constexpr (Prog::heads && !SPLIT) {
+        // A row of a head is in this thread's TMEM lane, so its sum of squares
+        // is a first pass over the head's chunks.
+        if (head_rms_at >= 0) {
+          const int units = 8 >> p.log_head_chunks;
+          for (int unit = 0; unit < units; ++unit) {
+            const int c = unit << p.log_head_chunks;
+            if (nacc0 + c * CHUNK >= p.head_cols) break;
+            float ss = 0.0f, u[32];
+            if (!kStatic || p.head_chunks == 1) {
+              for (int k = 0; k < p.head_chunks; ++k) {
+                load_acc(c + k, u);
+                first_ops(c + k, u);
+                ss += chunk_squares(u);
+              }
+            } else {
+              for (int k = 0; k < p.head_chunks; k += 2) {
+                load_two(c + k, c + k + 1, u, held);
+                first_ops(c + k, u);
+                first_ops(c + k + 1, held);
+                ss += chunk_squares(u);
+                ss += chunk_squares(held);
+              }
+            }
+            const float r = rsqrtf(fmaf(ss, p.head_inv_dim, p.head_eps));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) head_r[k] = k == unit ? r : head_r[k];
+          }
+        }
+      }
+
       for (int ci = 0; ci < steps; ++ci) {
         HeadStep h = {ci, 0, 0, false, false};
         if constexpr (Prog::heads) h = head_step(SPLIT ? static_cast<int>(walk >> (4 * ci)) & 15 : ci);
@@ -1501,19 +1573,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int i = 0; i < expand_at; ++i) apply_pointwise<16>(p.ops[i].code, dh, p, nacc0 + c * 16, p.N, rs_m);
           }
         } else if constexpr (Prog::heads) {
-          // Accumulator chunk cc with the ops before HEAD_RMS (and ROTARY).
-          auto load_acc = [&](int cc, float (&u)[32]) {
-            if (flags & F_ZERO_ACC) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) u[j] = 0.0f;
-            } else {
-              uint32_t r[32];
-              ptx::tmem_ld32_sync(t_row + cc * 32, r);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) u[j] = __uint_as_float(r[j]);
-            }
-            first_ops(cc, u);
-          };
           // What follows it up to ROTARY: the head's 1 / rms (1 where there is
           // no head) and the ops between the two.
           const bool head = nacc0 + (unit << p.log_head_chunks) * CHUNK < p.head_cols;
@@ -1534,18 +1593,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           };
           if (head_rms_at >= 0) {
-            if (!SPLIT && in_head == 0 && head) {
-              // A row of the head is in this thread's TMEM lane, so its sum of
-              // squares is a first pass over the head's chunks.
-              float ss = 0.0f;
-              for (int k = 0; k < p.head_chunks; ++k) {
-                load_acc(c + k, v);
-                ss += chunk_squares(v);
-              }
-              const float r = rsqrtf(fmaf(ss, p.head_inv_dim, p.head_eps));
-#pragma unroll
-              for (int k = 0; k < 8; ++k) head_r[k] = k == unit ? r : head_r[k];
-            }
 #pragma unroll
             for (int k = 0; k < 8; ++k) hr = head && k == unit ? head_r[k] : hr;
           }
@@ -1553,12 +1600,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = held[j];
           } else {
-            load_acc(c, v);
-            scale_acc(c, v);
             if (in_pair) {
-              load_acc(c + rot_half_chunks, held);
+              load_two(c, c + rot_half_chunks, v, held);
+              first_ops(c + rot_half_chunks, held);
               scale_acc(c + rot_half_chunks, held);
+            } else {
+              load_acc(c, v);
             }
+            first_ops(c, v);
+            scale_acc(c, v);
             if (rotary_at >= 0 && head) {
               // The first head of a chunk works its angles out for the others;
               // the interpreter, whose registers they would not fit in, for
@@ -1580,13 +1630,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 for (int i = 0; i < 8; i += KEPT16 / 2) {
                   if (!kStatic || angles_of != in_head)
                     angles.template set<KEPT16, false>(p, position, in_head * 16 + 2 * i);
+                  if (p.rot_half) {
 #pragma unroll
-                  for (int j = 0; j < KEPT16 / 2; ++j) {
-                    const int k = i + j;
-                    if (p.rot_half)
+                    for (int j = 0, k = i; j < KEPT16 / 2; ++j, ++k)
                       angles.rotate(j, v[2 * k], v[2 * k + 1], v[16 + 2 * k], v[17 + 2 * k]);
-                    else
-                      angles.rotate(j, v[4 * k], v[4 * k + 2], v[4 * k + 1], v[4 * k + 3]);
+                  } else {
+#pragma unroll
+                    for (int j = 0, k = i; j < KEPT16 / 2; ++j, ++k)
+                      angles.rotate_interleaved(j, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                   }
                 }
                 angles_of = in_head;
