@@ -1254,18 +1254,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         h.c = (h.unit << p.log_head_chunks) + h.in_head;
         return h;
       };
-      // SPLIT: piece i = head * slabs + slab is CTA (i % split)'s, its (i / split)-th
-      // (4 bits a head in `owners` and `slots_of`).  Bits of `shared`: the
-      // tile's chunks that are this warp's among those holding its rows; of
-      // `mine`: those of them whose piece is this CTA's.
+      // SPLIT: piece i = head * slabs + slab is the (i / split)-th of a CTA: CTA i % split
+      // at first, one further each time that would give a CTA the same slabs
+      // again, whose warps would do all its work while others idle (64 x 512 ->
+      // 6144 on clusters of 2).  4 bits a head in `owners` and `slots_of`.  Bits
+      // of `shared`: the tile's chunks that are this warp's among those holding
+      // its rows; of `mine`: those of them whose piece is this CTA's.
       uint32_t owners = 0, slots_of = 0, shared = 0, mine = 0;
       uint32_t walk = 0;  // the steps ci of `mine`, 4 bits each
       int steps = chunks;
       int first_angles = 0;  // the first chunk that rotates
       if constexpr (SPLIT) {
+        const int turns = slabs / min(slabs, split & -split);  // rounds of pieces until CTA and slab meet again
         for (int u = 0; u < 8 >> p.log_head_chunks; ++u) {
           const int i = u * slabs + slab, nth = i / split;
-          owners |= static_cast<uint32_t>(i - nth * split) << (4 * u);
+          owners |= static_cast<uint32_t>((i + nth / turns) % split) << (4 * u);
           slots_of |= static_cast<uint32_t>(nth) << (4 * u);
         }
         steps = 0;

@@ -66,12 +66,22 @@ constexpr double L2_KEEP_BYTES = 60e6;
 constexpr uint32_t DEFAULT_TIMEOUT_MS = 2000;
 
 constexpr int MAX_SPLIT = 8;         // CTAs of a cluster along K (the portable cluster size)
-// K-blocks of a CTA that are worth a cluster's exchange: 273 x 488 -> 2304 (8
-// K-blocks) takes 16.4 us on clusters of 2, 17.8 on 4; 1106 x 248 -> 960 13.5 us
-// unsplit, 15.5 and 18.0 on 2 and 4.  Up to 64 rows gain from the second CTA
-// whatever its share, since the epilogue is split too: 3 x 128 -> 3584 (2
-// K-blocks) 12.7 us unsplit, 9.6 on 2; but 55 x 528 -> 1536 12.5 us on 2, 14.4 on 8.
-constexpr int MIN_SPLIT_BLOCKS = 4;
+// What sharing a tile over n CTAs costs, in K-blocks of one CTA's main loop:
+// fixed + each * n, fitted to 412 problems of 3 to 1003 rows, K 64 to 4096 and
+// heads of 32 to 256, each timed on every n (one GB300; the n chosen takes 0.5 to
+// 1.5 % more than the best n of its problem on average).  Up to 32 and 64 rows
+// the exchange pays early, since a row's four or two copies share the epilogue
+// out as well: 3 x 128 -> 1536 (2 K-blocks) 10.7 us unsplit, 8.4 on 2 CTAs; 64 x
+// 512 -> 6144 11.3 unsplit, 9.8 on 3; 64 x 4096 -> 6144 35.3 unsplit, 18.6 on 5.
+// Above that 1003 x 512 -> 1152 is level (13.0 and 12.7 on 2) and 1003 x 2048
+// 19.4, 16.0 on 3.  There a tile that is one head has one piece for each 32 rows,
+// so that its epilogue takes as long as before on any n: 100 x 1024 -> 1280 with
+// heads of 256 15.1 unsplit, 17.2 on 2, 17.5 on 4; x 4096 29.0, 20.3 on 5.
+struct SplitCost {
+  double fixed, each;
+};
+constexpr SplitCost SPLIT_COST_32_ROWS = {-4.0, 0.5}, SPLIT_COST_64_ROWS = {0.0, 1.0}, SPLIT_COST = {2.0, 1.0},
+                    SPLIT_COST_ONE_HEAD = {10.0, 1.0};
 
 struct DeviceState {
   bool ready = false;
@@ -547,27 +557,36 @@ int choose_cta_group(const gemm_epi_plan& P, const gemm_epi_args& a, const Devic
 // Rows of a split tile's A box: what M fills, repeated up to 128.
 int64_t split_rows(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : ge::BLOCK_M; }
 
-// CTAs along K of a program with HEAD_RMS or ROTARY: 1, or as many as leave
-// the 128 x 256 tiles' clusters resident at once, each CTA MIN_SPLIT_BLOCKS
-// K-blocks, and room in a CTA's operand ring for the partial sums it receives
-// (every other CTA's, of its pieces).  So a projection of
-// few rows reads its weights through most SMs, where one CTA per tile left
-// 128 of 152 idle (64 x 4096 -> 6144 columns).
+// CTAs along K of a program with HEAD_RMS or ROTARY: the cheapest n (above) of
+// those that leave the 128 x 256 tiles' clusters resident at once, each CTA a
+// K-block, and room in a CTA's operand ring for the partial sums it receives
+// (every other CTA's, of its pieces).  So a projection of few rows reads its
+// weights through most SMs, where one CTA per tile left 128 of 152 idle (64 x
+// 4096 -> 6144 columns).
 int choose_split(const gemm_epi_plan& P, const gemm_epi_args& a, const DeviceState& dev) {
   if (!P.heads() || (a.debug_flags & (GEMM_EPI_DEBUG_FORCE_1SM | GEMM_EPI_DEBUG_FORCE_2SM))) return 1;
   const int k_step = P.in8 ? 2 * ge::BLOCK_K : ge::BLOCK_K;
   const int64_t k_blocks = (P.d.K + k_step - 1) / k_step;
   const int64_t tiles = P.num_m_tiles * P.num_n_tiles * P.batch;
-  const int64_t slabs = split_rows(P.d.M) / 32;
-  const int64_t pieces = ge::BLOCK_N / P.d.head_dim * slabs;  // heads of a tile by slabs of 32 rows
-  for (int n = MAX_SPLIT; n >= 2; --n) {
+  const int64_t rows = split_rows(P.d.M);
+  const int64_t pieces = ge::BLOCK_N / P.d.head_dim * (rows / 32);  // heads of a tile by slabs of 32 rows
+  const SplitCost cost = rows == 32   ? SPLIT_COST_32_ROWS
+                         : rows == 64 ? SPLIT_COST_64_ROWS
+                                      : P.d.head_dim == ge::BLOCK_N ? SPLIT_COST_ONE_HEAD : SPLIT_COST;
+  int best = 1;
+  double least = static_cast<double>(k_blocks);
+  for (int n = 2; n <= MAX_SPLIT; ++n) {
     const int64_t bytes = (n - 1) * ((pieces + n - 1) / n) * P.d.head_dim * 32 * 4;
-    const int64_t least = n == 2 && P.d.M <= 64 ? 1 : MIN_SPLIT_BLOCKS;
-    if (tiles <= dev.split_clusters[n] && k_blocks >= n * least &&
-        bytes + 4096 <= static_cast<int64_t>(ge::Smem<1>::OFF_EPI))  // and the sums of repeated rows
-      return n;
+    if (tiles > dev.split_clusters[n] || k_blocks < n ||
+        bytes + 4096 > static_cast<int64_t>(ge::Smem<1>::OFF_EPI))  // with the sums of repeated rows
+      continue;
+    const double c = static_cast<double>((k_blocks + n - 1) / n) + cost.fixed + cost.each * n;
+    if (c < least) {
+      least = c;
+      best = n;
+    }
   }
-  return 1;
+  return best;
 }
 
 // Fills the kernel parameters and tensor maps of one fused launch.  `c`/`ldc`
