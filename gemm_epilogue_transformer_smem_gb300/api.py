@@ -67,6 +67,8 @@ def encode_program(program: Sequence[str]):
 # torch.cuda.current_stream() builds (2.9 us of a small call's 7).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+# The current device, where a CUDA tensor is at hand: CUDA is initialised.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -442,12 +444,21 @@ def _heads(name: str, t: torch.Tensor, shape, dtype, index: int):
     return t.data_ptr(), sb, ss, sh
 
 
-def _head_shape(name: str, t: torch.Tensor, rope: Rotary):
-    shape = t.shape
-    if len(shape) not in (3, 4) or shape[-1] != rope.head_dim:
+def _head_input(name: str, t: torch.Tensor, shape, head_dim: int):
+    """batch, tokens, heads and (pointer, batch, token and head strides) of q or k."""
+    batch = dim = 1
+    if len(shape) == 4:
+        batch, tokens, heads, dim = shape
+        sb, ss, sh, sd = t.stride()
+    elif len(shape) == 3:
+        tokens, heads, dim = shape
+        sb, (ss, sh, sd) = 0, t.stride()
+    if dim != head_dim:
         raise ValueError("%s: expected (batch, tokens, heads, %d) or (tokens, heads, %d), got %s"
-                         % (name, rope.head_dim, rope.head_dim, tuple(shape)))
-    return shape
+                         % (name, head_dim, head_dim, tuple(shape)))
+    if sd != 1 and t.numel():
+        raise ValueError("%s: the values of a head must be contiguous" % name)
+    return batch, tokens, heads, (t.data_ptr(), sb, ss, sh)
 
 
 def _vector(name: str, t: torch.Tensor, rope: Rotary, index: int) -> int:
@@ -467,17 +478,14 @@ def _head_call(entry: str, q, k, rope: Rotary, positions, q_out, k_out, stream, 
     first = q if q is not None else k
     if first is None:
         raise ValueError("q and k are both None")
-    dtype, index = first.dtype, first.get_device()
+    shape, dtype, index, head_dim = first.shape, first.dtype, first.get_device(), rope.head_dim
     type_code = HEAD_TYPES.get(dtype)
     if type_code is None:
         raise TypeError("%s: expected a bf16 or fp32 tensor, got %s" % ("q" if q is not None else "k", dtype))
     q_heads = k_heads = 0
     tq = tqo = tdq = tk = tko = tdk = _NO_HEADS
-    shape = None
     if q is not None:
-        shape = _head_shape("q", q, rope)
-        q_heads = shape[-2]
-        tq = _heads("q", q, shape, dtype, index)
+        batch, tokens, q_heads, tq = _head_input("q", q, shape, head_dim)
         if q_out is not None:
             tqo = _heads("dq" if backward else "q_out", q_out, shape, dtype, index)
         elif not backward:
@@ -487,23 +495,24 @@ def _head_call(entry: str, q, k, rope: Rotary, positions, q_out, k_out, stream, 
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k is not None:
-        k_shape = _head_shape("k", k, rope)
-        if shape is not None and (k_shape[:-2] != shape[:-2] or k.dtype is not dtype):
+        k_shape = k.shape
+        k_batch, k_tokens, k_heads, tk = _head_input("k", k, k_shape, head_dim)
+        if q is None:
+            batch, tokens = k_batch, k_tokens
+        elif k_batch != batch or k_tokens != tokens or len(k_shape) != len(shape) or k.dtype is not dtype:
             raise ValueError("q %s %s and k %s %s do not belong together" % (dtype, tuple(shape), k.dtype, tuple(k_shape)))
-        shape = k_shape
-        k_heads = shape[-2]
-        tk = _heads("k", k, shape, dtype, index)
+        elif k.get_device() != index:
+            raise ValueError("k is on %s, not with the other tensors" % k.device)
         if k_out is not None:
-            tko = _heads("dk" if backward else "k_out", k_out, shape, dtype, index)
+            tko = _heads("dk" if backward else "k_out", k_out, k_shape, dtype, index)
         elif not backward:
             raise ValueError("k_out is missing (pass k itself to work in place)")
         if backward and dyk is not None:
-            tdk = _heads("dyk", dyk, shape, dtype, index)
+            tdk = _heads("dyk", dyk, k_shape, dtype, index)
     elif k_out is not None:
         raise ValueError("k_out without k")
     if backward and ((dyq is None) != (q is None) or (dyk is None) != (k is None)):
         raise ValueError("a gradient and its input (dyq and q, dyk and k) must be given together")
-    batch, tokens = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
     steps = rope.steps
     if steps.get_device() != index:
         raise ValueError("the rotary steps are on %s, q and k on %s" % (steps.device, first.device))
@@ -523,13 +532,13 @@ def _head_call(entry: str, q, k, rope: Rotary, positions, q_out, k_out, stream, 
             if workspace.get_device() != index or not workspace.is_contiguous():
                 raise ValueError("workspace: expected a contiguous tensor with the others")
             ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    packed = _QK_ARGS.pack(batch, tokens, q_heads, k_heads, rope.head_dim, rope.rotary_dim, rope.layout_code, type_code,
+    packed = _QK_ARGS.pack(batch, tokens, q_heads, k_heads, head_dim, rope.rotary_dim, rope.layout_code, type_code,
                            *tq, *tk, *tqo, *tko, *tdq, *tdk, steps.data_ptr(), at, pos_stride, wide, inverse,
                            rope.amplitude, eps, wq, wk, dq_at, dk_at, ws, ws_bytes)
     if index < 0:
         raise ValueError("expected CUDA tensors, got %s" % first.device)
     fn = _head_entries.get(entry) or _head_entry(entry)
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(packed, _raw_stream(index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(index):
