@@ -38,6 +38,17 @@
 // tile's main loop.  Tiles are walked persistently (grid = number of SMs) in
 // groups of `group_m` M-tiles so that neighbouring CTAs share A and B in L2.
 //
+// Programs with HEAD_RMS or ROTARY (y = R(position) (x r w) on heads of 32 to
+// 256 columns, r = 1/sqrt(mean x^2 + eps)): a row of a head is in one thread's
+// TMEM lane, so its sum of squares is a first pass over the head's chunks and
+// both halves of every pair are at hand.  With few rows a cluster shares each
+// tile over K (SPLIT) and its CTAs share the epilogue out.  On one GB300, us in
+// a graph: 64 x 4096 -> 6144 18.3 (weights alone 7.4 at the measured copy rate),
+// 35 with one CTA to a tile; 8192 x 4096 -> 6144 226 to 243 under the power cap,
+// the bare GEMM 220 to 236; 8192 x 1024 89 and 66: there the epilogue bounds it,
+// four warps of about 350 instructions a chunk at one in five cycles, a third
+// of them angles (16 cycles of the special-function unit a pair and warp).
+//
 // Every mbarrier wait is bounded: when one runs out the CTA records a status
 // in the workspace, raises a shared abort flag that every other wait checks,
 // waits (bounded) for its copies and MMAs in flight -- the operand loads of
@@ -1189,8 +1200,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr bool kStaged = prog_stages_columns<Prog>();
     const bool staged = kStaged && !(flags & F_E8);
     float* staged_cols = reinterpret_cast<float*>(e80_ptr);  // column scales, then biases, of the tile
-    // HEAD_RMS and ROTARY: ops [0, head_first) run on the accumulator, [mid, mid_end)
-    // between the two, the rest after them.
+    // HEAD_RMS and ROTARY: the ops before the first of them run on accumulator
+    // chunks, those between the two on the normalised ones, the rest after them.
     const int head_rms_at = kStatic ? prog_index_of<Prog>(GEMM_EPI_OP_HEAD_RMS) : Prog::heads ? p.head_rms_at : -1;
     const int rotary_at = kStatic ? prog_index_of<Prog>(GEMM_EPI_OP_ROTARY) : Prog::heads ? p.rotary_at : -1;
     const int op_begin = Prog::heads ? max(head_rms_at, rotary_at) + 1
