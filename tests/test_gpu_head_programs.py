@@ -348,6 +348,25 @@ def test_split_k(case, program):
         torch.testing.assert_close(a, b, rtol=1e-5, atol=1e-4)
 
 
+# Growing K: from one CTA to a tile up to eight, so that the heads' pieces are
+# dealt out to every number of CTAs for 32, 64 and 128 rows of a slab.
+GROWING_K = [(40, k, 8, 2, 64) for k in (72, 136, 392, 640, 2000, 2504, 3000, 4096)] + \
+            [(300, k, 5, 2, 128) for k in (264, 776, 1400, 2104, 3000, 4096)] + \
+            [(20, k, 3, 1, 32) for k in (136, 200, 1032, 2056, 3400, 4096)] + \
+            [(129, k, 2, 1, 256) for k in (1032, 1800, 3000, 4096)]
+
+
+@pytest.mark.parametrize("m,k,hq,hk,d", GROWING_K)
+def test_split_k_over_any_number_of_ctas(m, k, hq, hk, d):
+    p = Problem(NORM, m, k, hq, hk, d, d, "half")
+    p.run()
+    p.check()
+    got = p.out.C.clone()
+    p.run(VARIANTS["1sm"])
+    torch.cuda.synchronize()
+    assert torch.equal(got, p.out.C)
+
+
 def test_split_k_fp8_operands():
     p = Problem(NORM, 48, 2048, 6, 2, 128, 128, "half", in_type="e4m3")
     p.run()
