@@ -599,6 +599,7 @@ def qk_norm_rotary_backward(dyq, dyk, q, k, rope: Rotary, positions=None, *, q_w
     into dq and dk (which may be the memory of q or dyq, k or dyk) and those of
     the weights, summed over batch, tokens and heads, into the fp32 dwq and dwk
     (overwritten).  Each of the four may be None; dwq and dwk need a workspace
-    of qk_norm_rotary_workspace(head_dim) bytes.  Asynchronous."""
+    of qk_norm_rotary_workspace(head_dim) bytes that no call running at the same
+    time (another stream's, another graph's) shares.  Asynchronous."""
     _head_call("gemm_epi_qk_norm_rotary_backward", q, k, rope, positions, dq, dk, stream, 0, eps, q_weight, k_weight,
                True, dyq, dyk, dwq, dwk, workspace)
