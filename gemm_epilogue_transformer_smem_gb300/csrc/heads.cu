@@ -26,26 +26,32 @@ struct HeadKernel {
   int blocks, smem;
 };
 
-template <class T, bool HALF>
+template <class T, bool HALF, bool PART>
 HeadKernel kernel_of(int mode, bool wide) {
   using Forward = ge::HeadRing<T, HALF, 1>;
   using Backward = ge::HeadRing<T, HALF, 2>;
   switch (mode) {
     case ge::HEAD_ROTARY:
-      return wide ? HeadKernel{ge::heads_kernel<T, HALF, false>, ge::HD_ROTARY_BLOCKS, Forward::BYTES}
-                  : HeadKernel{ge::heads_any_kernel<T, HALF, false>, 2, 0};
+      return wide ? HeadKernel{ge::heads_kernel<T, HALF, false, PART>, ge::HD_ROTARY_BLOCKS, Forward::BYTES}
+                  : HeadKernel{ge::heads_any_kernel<T, HALF, false, PART>, 2, 0};
     case ge::HEAD_NORM:
-      return wide ? HeadKernel{ge::heads_kernel<T, HALF, true>, ge::HD_NORM_BLOCKS, Forward::BYTES}
-                  : HeadKernel{ge::heads_any_kernel<T, HALF, true>, 2, 0};
+      return wide ? HeadKernel{ge::heads_kernel<T, HALF, true, PART>, ge::HD_NORM_BLOCKS, Forward::BYTES}
+                  : HeadKernel{ge::heads_any_kernel<T, HALF, true, PART>, 2, 0};
     default:
-      return wide ? HeadKernel{ge::heads_backward_kernel<T, HALF>, ge::HD_BWD_BLOCKS, Backward::BYTES}
-                  : HeadKernel{ge::heads_backward_any_kernel<T, HALF>, ge::HD_BWD_BLOCKS, 0};
+      return wide ? HeadKernel{ge::heads_backward_kernel<T, HALF, PART>, ge::HD_BWD_BLOCKS, Backward::BYTES}
+                  : HeadKernel{ge::heads_backward_any_kernel<T, HALF, PART>, ge::HD_BWD_BLOCKS, 0};
   }
 }
 
-HeadKernel kernel_of(int mode, bool wide, bool half, bool f32) {
-  if (f32) return half ? kernel_of<float, true>(mode, wide) : kernel_of<float, false>(mode, wide);
-  return half ? kernel_of<uint16_t, true>(mode, wide) : kernel_of<uint16_t, false>(mode, wide);
+template <class T>
+HeadKernel kernel_of(int mode, bool wide, bool half, bool part) {
+  if (half) return part ? kernel_of<T, true, true>(mode, wide) : kernel_of<T, true, false>(mode, wide);
+  return part ? kernel_of<T, false, true>(mode, wide) : kernel_of<T, false, false>(mode, wide);
+}
+
+// part: some of the values worked on do not rotate.
+HeadKernel kernel_of(int mode, bool wide, bool half, bool part, bool f32) {
+  return f32 ? kernel_of<float>(mode, wide, half, part) : kernel_of<uint16_t>(mode, wide, half, part);
 }
 
 // The current device's SM count.  The first call on a device gives every
@@ -55,8 +61,8 @@ gemm_epi_status device_setup(int* sms) {
   int dev = 0;
   const gemm_epi_status s = ge_host::device_sms(&dev, sms);
   if (s != GEMM_EPI_OK || ready[dev].load(std::memory_order_acquire)) return s;
-  for (int i = 0; i < 3 * 2 * 2; ++i) {
-    const HeadKernel k = kernel_of(i / 4, true, (i & 1) != 0, (i & 2) != 0);
+  for (int i = 0; i < 3 * 2 * 2 * 2; ++i) {
+    const HeadKernel k = kernel_of(i / 8, true, (i & 1) != 0, (i & 2) != 0, (i & 4) != 0);
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k.fn),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
@@ -233,7 +239,7 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
   p.inv_dim = 1.0f / static_cast<float>(a->head_dim);
   p.partials = wants_dw ? static_cast<float*>(a->workspace) : nullptr;
 
-  const HeadKernel kernel = kernel_of(mode, wide, half, a->type == GEMM_EPI_TYPE_F32);
+  const HeadKernel kernel = kernel_of(mode, wide, half, a->rotary_dim < p.reach, a->type == GEMM_EPI_TYPE_F32);
   const int64_t resident = static_cast<int64_t>(sms) * kernel.blocks;
   // One wave of blocks, and no more warps than iterations.
   const int64_t sets = (p.rows + (32 >> p.log_g) - 1) / (32 >> p.log_g);  // of tokens, one to each lane group

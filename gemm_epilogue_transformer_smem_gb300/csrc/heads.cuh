@@ -167,12 +167,16 @@ struct HeadPairs {
 };
 
 // Where a lane's values lie in a head: S slots of two chunks of V values.
-template <class T, int V, bool HALF>
+template <class T, int VALUES, bool HALF>
 struct HeadLane {
+  using Type = T;
+  static constexpr int V = VALUES;
+  static constexpr bool HALVES = HALF;
   using Chunk = HeadChunk<T, V>;
   static constexpr int S = 8 / V;
   int off0[S], off1[S];    // element offsets of the two chunks
   bool in0[S], in1[S];     // inside the head
+  uint32_t turning;        // bit k: the lane's pair k (k % V of slot k / V) rotates
 
   // The raw chunks of one head.
   struct Raw {
@@ -191,6 +195,10 @@ struct HeadLane {
       off0[i] = in0[i] ? a : 0;
       off1[i] = in1[i] ? b : 0;
     }
+    turning = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      turning |= static_cast<uint32_t>(pair_of(p, lane_in_group, k / V, k % V) < p.rot_pairs) << k;
   }
   // Index of the head's rotated pair in place j of slot i; past the rotated
   // pairs where there is none.
@@ -285,21 +293,25 @@ struct HeadLane {
   }
 };
 
-// The rotation of a lane's 8 pairs at one position.
+// The rotation of a lane's 8 pairs at one position.  PART: some values of a head
+// do not rotate.  Their pairs keep them untouched: c = 1 and s = 0 would let an
+// infinity or NaN of one value make its partner NaN.  Kernels of their own, as
+// the test costs them up to 3 % (32 + 8 heads of 128, half of each rotated:
+// rotary 29.1 -> 29.6 us, norm 55.8 in both, backward 84.5 -> 86.8).
+template <class Lane, bool PART>
 struct HeadAngles {
   float2 c[4], s[4];  // cos and sin, times the amplitude
+  uint32_t turning;   // PART: bit k: pair k rotates
 
-  // 1 and 0 where nothing rotates.
-  template <class T, int V, bool HALF>
-  __device__ __forceinline__ void set(const HeadParams& p, const HeadLane<T, V, HALF>& l, int lane_in_group,
-                                      int64_t position) {
+  __device__ __forceinline__ void set(const HeadParams& p, const Lane& l, int lane_in_group, int64_t position) {
     const float as = p.amplitude * p.sin_sign;
+    turning = l.turning;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int pair = l.pair_of(p, lane_in_group, k / V, k % V);
+      const int pair = l.pair_of(p, lane_in_group, k / Lane::V, k % Lane::V);
       float cc = 1.0f, ss = 0.0f;
       if (pair < p.rot_pairs) {
-        turn_cos_sin<sizeof(T) == 2>(phase_bits(position, __ldg(p.steps + pair)), cc, ss);
+        turn_cos_sin<sizeof(typename Lane::Type) == 2>(phase_bits(position, __ldg(p.steps + pair)), cc, ss);
         cc *= p.amplitude;
         ss *= as;
       }
@@ -310,15 +322,26 @@ struct HeadAngles {
     }
   }
 
-  // (a, b) -> (a c - b s, b c + a s)
+  // (a, b) -> (a c - b s, b c + a s).
   __device__ __forceinline__ void rotate(HeadPairs& x) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 a = x.a[i], b = x.b[i];
-      const float2 bs = __fmul2_rn(b, s[i]);
-      x.a[i] = make_float2(fmaf(a.x, c[i].x, -bs.x), fmaf(a.y, c[i].y, -bs.y));
-      x.b[i] = __ffma2_rn(a, s[i], __fmul2_rn(b, c[i]));
+      if constexpr (!PART) {
+        turn(i, x.a[i], x.b[i]);
+      } else if constexpr (Lane::HALVES) {  // a slot's pairs rotate all or none
+        if ((turning >> (2 * i / Lane::V * Lane::V)) & 1u) turn(i, x.a[i], x.b[i]);
+      } else {
+        float2 a = x.a[i], b = x.b[i];
+        turn(i, a, b);
+        if ((turning >> (2 * i)) & 1u) x.a[i].x = a.x, x.b[i].x = b.x;
+        if ((turning >> (2 * i + 1)) & 1u) x.a[i].y = a.y, x.b[i].y = b.y;
+      }
     }
+  }
+  __device__ __forceinline__ void turn(int i, float2& a, float2& b) const {
+    const float2 x = a, bs = __fmul2_rn(b, s[i]);
+    a = make_float2(fmaf(x.x, c[i].x, -bs.x), fmaf(x.y, c[i].y, -bs.y));
+    b = __ffma2_rn(x, s[i], __fmul2_rn(b, c[i]));
   }
 };
 
@@ -365,8 +388,8 @@ struct HeadRow {
 // ---------------------------------------------------------------- arithmetic
 
 // One head forward: norm (r, w) and rotation.
-template <bool NORM>
-__device__ __forceinline__ void head_forward(HeadPairs& v, const HeadPairs& w, const HeadAngles& ang,
+template <bool NORM, class Angles>
+__device__ __forceinline__ void head_forward(HeadPairs& v, const HeadPairs& w, const Angles& ang,
                                              const HeadParams& p) {
   if constexpr (NORM) {
     const float2 r = both(head_rms(v, p));
@@ -381,8 +404,9 @@ __device__ __forceinline__ void head_forward(HeadPairs& v, const HeadPairs& w, c
 
 // One head backward: v = x, g = dy in; v = dx out, dw added to where `ok` (a
 // lane group without a token adds nothing).
+template <class Angles>
 __device__ __forceinline__ void head_backward(HeadPairs& v, HeadPairs& g, const HeadPairs& w, HeadPairs& dw,
-                                              const HeadAngles& ang, const HeadParams& p, bool ok) {
+                                              const Angles& ang, const HeadParams& p, bool ok) {
   const float r = head_rms(v, p);
   ang.rotate(g);  // sin_sign = -1: the transpose
 #pragma unroll
@@ -545,7 +569,7 @@ struct HeadRing {
   static __device__ __forceinline__ uint32_t next(uint32_t at) { return at + SLOT_BYTES == BYTES ? 0u : at + SLOT_BYTES; }
 };
 
-template <class T, bool HALF, bool NORM>
+template <class T, bool HALF, bool NORM, bool PART>
 __global__ void __launch_bounds__(HD_THREADS, NORM ? HD_NORM_BLOCKS : HD_ROTARY_BLOCKS)
     heads_kernel(const __grid_constant__ HeadParams p) {
   using Ring = HeadRing<T, HALF, 1>;
@@ -605,7 +629,7 @@ __global__ void __launch_bounds__(HD_THREADS, NORM ? HD_NORM_BLOCKS : HD_ROTARY_
 #pragma unroll 1
   for (HeadSpan now(share, warp); now.any(); now.next(share, warp)) {
     const HeadRow r(p, now.row, group);
-    HeadAngles ang;
+    HeadAngles<Lane, PART> ang;
     ang.set(p, l, in_group, head_position(p, r.b, r.t));
 #pragma unroll 1
     while (now.any()) {
@@ -635,7 +659,7 @@ __global__ void __launch_bounds__(HD_THREADS, NORM ? HD_NORM_BLOCKS : HD_ROTARY_
 // Backward pass of the norm and rotation.  A block works on q or on k, so that
 // its warps keep one weight gradient in registers over all of their share;
 // each block leaves one partial row.
-template <class T, bool HALF>
+template <class T, bool HALF, bool PART>
 __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS) heads_backward_kernel(const __grid_constant__ HeadParams p) {
   using Ring = HeadRing<T, HALF, 2>;
   using Lane = typename Ring::Lane;
@@ -693,7 +717,7 @@ __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS) heads_backward_kern
 #pragma unroll 1
   for (HeadSpan now(share, warp); now.any(); now.next(share, warp)) {
     const HeadRow r(p, now.row, group);
-    HeadAngles ang;
+    HeadAngles<Lane, PART> ang;
     ang.set(p, l, in_group, head_position(p, r.b, r.t));
     HeadRun<T> dx;
     dx.set(h.y, h.y_b, h.y_t, h.y_h, r, now.it);
@@ -719,7 +743,7 @@ __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS) heads_backward_kern
 // The same passes with single-element accesses, for sizes, strides and
 // addresses that 16-byte ones do not serve.
 
-template <class T, bool HALF, bool NORM>
+template <class T, bool HALF, bool NORM, bool PART>
 __global__ void __launch_bounds__(HD_THREADS, 2) heads_any_kernel(const __grid_constant__ HeadParams p) {
   using Lane = HeadLane<T, 2, HALF>;
   const int lane = threadIdx.x & 31, warp = blockIdx.x * HD_WARPS + (threadIdx.x >> 5);
@@ -730,7 +754,7 @@ __global__ void __launch_bounds__(HD_THREADS, 2) heads_any_kernel(const __grid_c
 #pragma unroll 1
   for (HeadSpan now(p.share[0], warp); now.any(); now.next(p.share[0], warp)) {
     const HeadRow r(p, now.row, group);
-    HeadAngles ang;
+    HeadAngles<Lane, PART> ang;
     ang.set(p, l, in_group, head_position(p, r.b, r.t));
 #pragma unroll 1
     while (now.any()) {
@@ -758,7 +782,7 @@ __global__ void __launch_bounds__(HD_THREADS, 2) heads_any_kernel(const __grid_c
   }
 }
 
-template <class T, bool HALF>
+template <class T, bool HALF, bool PART>
 __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS)
     heads_backward_any_kernel(const __grid_constant__ HeadParams p) {
   using Lane = HeadLane<T, 2, HALF>;
@@ -776,7 +800,7 @@ __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS)
 #pragma unroll 1
   for (HeadSpan now(p.share[k], warp); now.any(); now.next(p.share[k], warp)) {
     const HeadRow r(p, now.row, group);
-    HeadAngles ang;
+    HeadAngles<Lane, PART> ang;
     ang.set(p, l, in_group, head_position(p, r.b, r.t));
     HeadRun<T> x, dy, dx;
     x.set(h.x, h.x_b, h.x_t, h.x_h, r, now.it);
