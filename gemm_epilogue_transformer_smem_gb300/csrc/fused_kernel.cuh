@@ -739,7 +739,7 @@ struct RowAngles {
   float2 c[16], s[16];
 
   // Pairs pair0 .. pair0 + NP - 1 (pair0 even); WHOLE: all of them rotate, else
-  // those past the rotated part stay as they are.  Every step is read before
+  // those past the rotated part get the angle 0.  Every step is read before
   // the first is used: one latency, not one for each.
   template <int NP, bool WHOLE>
   __device__ __forceinline__ void set(const KernelParams& p, int64_t position, int pair0) {
@@ -1649,9 +1649,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     for (int j = 0, k = i; j < KEPT16 / 2; ++j, ++k)
                       angles.rotate(j, v[2 * k], v[2 * k + 1], v[16 + 2 * k], v[17 + 2 * k]);
                   } else {
+                    // Pairs past the rotated part keep their values: their cos = 1 and
+                    // sin = 0 would spread an infinity or NaN to the partner.
+                    const int left = p.rot_pairs - in_head * 16;
 #pragma unroll
-                    for (int j = 0, k = i; j < KEPT16 / 2; ++j, ++k)
-                      angles.rotate_interleaved(j, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    for (int j = 0, k = i; j < KEPT16 / 2; ++j, ++k) {
+                      float a0 = v[4 * k], b0 = v[4 * k + 1], a1 = v[4 * k + 2], b1 = v[4 * k + 3];
+                      angles.rotate_interleaved(j, a0, b0, a1, b1);
+                      if (2 * k < left) v[4 * k] = a0, v[4 * k + 1] = b0;
+                      if (2 * k + 1 < left) v[4 * k + 2] = a1, v[4 * k + 3] = b1;
+                    }
                   }
                 }
                 angles_of = in_head;
