@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 #include "heads.cuh"
@@ -95,14 +96,24 @@ gemm_epi_status check_tensor(const gemm_epi_qk_args& a, const gemm_epi_heads& h,
   return GEMM_EPI_OK;
 }
 
-// Different elements of an output must not share memory: no dimension of more
-// than one step may advance by less than a head.
+// Different elements of an output must not share memory: taken by stride, each
+// dimension of more than one step advances by at least what the smaller ones
+// span (strides and extents are below 2^40 and 2^31: saturating, a span past
+// 2^62 is followed by no larger stride).
 gemm_epi_status check_output(const gemm_epi_qk_args& a, const gemm_epi_heads& h, int32_t heads, const char* name) {
-  const int64_t extent[3] = {a.batch, a.tokens, heads};
-  const int64_t stride[3] = {h.stride_batch, h.stride_token, h.stride_head};
-  for (int i = 0; i < 3; ++i)
-    if (extent[i] > 1 && stride[i] < a.head_dim && stride[i] > -a.head_dim)
-      return fail(GEMM_EPI_ERR_INVALID_VALUE, "%s: a stride below head_dim makes heads overlap", name);
+  struct Dim {
+    int64_t stride, extent;
+  } dims[3] = {{std::abs(h.stride_batch), a.batch}, {std::abs(h.stride_token), a.tokens}, {std::abs(h.stride_head), heads}};
+  std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  const int64_t MOST = int64_t(1) << 62;
+  int64_t span = a.head_dim;
+  for (const Dim& d : dims) {
+    if (d.extent <= 1) continue;
+    if (d.stride < span)
+      return fail(GEMM_EPI_ERR_INVALID_VALUE, "%s: a stride of %lld where the dimensions inside it span %lld makes heads "
+                  "overlap", name, static_cast<long long>(d.stride), static_cast<long long>(span));
+    span = d.stride > (MOST - span) / (d.extent - 1) ? MOST : span + d.stride * (d.extent - 1);
+  }
   return GEMM_EPI_OK;
 }
 
