@@ -117,14 +117,16 @@ gemm_epi_status check_output(const gemm_epi_qk_args& a, const gemm_epi_heads& h,
   return GEMM_EPI_OK;
 }
 
-bool same_place(const gemm_epi_heads& a, const gemm_epi_heads& b) {
-  return a.data == b.data && a.stride_batch == b.stride_batch && a.stride_token == b.stride_token &&
-         a.stride_head == b.stride_head;
+// The same elements: strides of dimensions of one step do not matter.
+bool same_place(const gemm_epi_qk_args& args, int32_t heads, const gemm_epi_heads& a, const gemm_epi_heads& b) {
+  return a.data == b.data && (args.batch <= 1 || a.stride_batch == b.stride_batch) &&
+         (args.tokens <= 1 || a.stride_token == b.stride_token) && (heads <= 1 || a.stride_head == b.stride_head);
 }
 
 // An output is written over an input element by element or not at all.
-gemm_epi_status check_in_place(const gemm_epi_heads& out, const gemm_epi_heads& in, const char* o, const char* i) {
-  if (out.data && out.data == in.data && !same_place(out, in))
+gemm_epi_status check_in_place(const gemm_epi_qk_args& args, int32_t heads, const gemm_epi_heads& out,
+                               const gemm_epi_heads& in, const char* o, const char* i) {
+  if (out.data && out.data == in.data && !same_place(args, heads, out, in))
     return fail(GEMM_EPI_ERR_INVALID_VALUE, "%s starts where %s does but has other strides", o, i);
   return GEMM_EPI_OK;
 }
@@ -172,8 +174,8 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
     if ((!bwd || out[i]->data) &&
         ((s = check_tensor(*a, *out[i], heads[i], names[i][2], c)) || (s = check_output(*a, *out[i], heads[i], names[i][2]))))
       return s;
-    if ((s = check_in_place(*out[i], *in[i], names[i][2], names[i][0]))) return s;
-    if (bwd && (s = check_in_place(*out[i], *dy[i], names[i][2], names[i][1]))) return s;
+    if ((s = check_in_place(*a, heads[i], *out[i], *in[i], names[i][2], names[i][0]))) return s;
+    if (bwd && (s = check_in_place(*a, heads[i], *out[i], *dy[i], names[i][2], names[i][1]))) return s;
     for (int j = 0; j < 2; ++j)  // one tensor's rows must not be another's results
       if (j != i && heads[j] > 0 && out[i]->data &&
           (out[i]->data == in[j]->data || (bwd && out[i]->data == dy[j]->data) || out[i]->data == out[j]->data))
@@ -225,7 +227,7 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
   p.rot_pairs = pairs;
   // In place and without a norm, what does not rotate is already there.
   bool in_place = mode == ge::HEAD_ROTARY;
-  for (int i = 0; i < 2; ++i) in_place = in_place && (heads[i] == 0 || same_place(*in[i], *out[i]));
+  for (int i = 0; i < 2; ++i) in_place = in_place && (heads[i] == 0 || same_place(*a, heads[i], *in[i], *out[i]));
   p.reach = in_place ? (a->rotary_dim + V - 1) / V * V : a->head_dim;
   const int chunks = p.reach / V;  // reach is whole chunks: V divides head_dim
   p.first_plain = half ? pairs / V : 0;

@@ -452,10 +452,11 @@ typedef struct gemm_epi_qk_args {
     int32_t type;                 /* BF16 or F32: every tensor below */
     gemm_epi_heads q, k;          /* x (not written unless an output is the same tensor) */
     gemm_epi_heads q_out, k_out;  /* results; dx in the backward pass, where data NULL leaves one out.
-                                     Each may be its own x (or dy) -- same pointer and strides -- and
-                                     must not overlap any tensor otherwise.  Taken by size, each
-                                     stride of more than one step is at least what the smaller
-                                     dimensions span (INVALID_VALUE else) */
+                                     Each may be its own x (or dy) -- same pointer, and same strides
+                                     where there is more than one step -- and must not overlap any
+                                     tensor otherwise.  Taken by size, each stride of more than one
+                                     step is at least what the smaller dimensions span (else
+                                     INVALID_VALUE) */
     gemm_epi_heads dy_q, dy_k;    /* backward pass: gradients of q_out and k_out */
     const uint64_t *steps;        /* device, rotary_dim / 2 values of gemm_epi_rotary_steps */
     const void *positions;        /* device int32 / int64, tokens per sequence; NULL: 0, 1, 2, ... */

@@ -73,3 +73,21 @@ def test_outputs_whose_heads_overlap(lib, entry):
         strides(a.q_out, st)
         assert getattr(lib, entry)(ctypes.byref(a), None) in REFUSED, (b, t, h, st)
         assert b"overlap" in lib.gemm_epi_last_error()
+
+
+@pytest.mark.parametrize("entry", ENTRIES)
+def test_in_place_views_that_differ_in_single_steps(lib, entry):
+    """The same memory through two views: the stride of a dimension of one step
+    does not matter, another one does."""
+    for batch, tokens, heads in ((4, 1, 3), (1, 5, 3), (4, 5, 1), (1, 1, 1)):
+        for name in ("stride_batch", "stride_token", "stride_head"):
+            a = args(batch, tokens, heads)
+            a.q_out.data = a.q.data
+            setattr(a.q_out, name, getattr(a.q, name) * 2)
+            single = {"stride_batch": batch, "stride_token": tokens, "stride_head": heads}[name] == 1
+            got = getattr(lib, entry)(ctypes.byref(a), None)
+            assert got in (TAKEN if single else REFUSED), (batch, tokens, heads, name, lib.gemm_epi_last_error())
+            a.q_out.data = a.dy_q.data  # over the gradient: any other memory to the forward pass
+            got = getattr(lib, entry)(ctypes.byref(a), None)
+            if entry.endswith("backward") or single:
+                assert got in (TAKEN if single else REFUSED), (batch, tokens, heads, name, lib.gemm_epi_last_error())
