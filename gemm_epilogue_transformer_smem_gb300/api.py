@@ -225,7 +225,7 @@ class Plan:
         if timeout_ms or debug_flags:
             a.timeout_ms, a.debug_flags = int(timeout_ms), int(debug_flags)
         if self.rotary is not None:
-            steps = self.rotary.steps
+            steps = self.rotary._steps
             index = steps.get_device()
             if A is not None and index != A.get_device():
                 raise ValueError("the rotary steps are on %s, A on %s" % (steps.device, A.device))
@@ -409,6 +409,20 @@ class Rotary:
         self.steps = torch.frombuffer(steps, dtype=torch.int64).clone().to(device)
         self.vector_shape = (self.head_dim,)
 
+    @property
+    def steps(self) -> torch.Tensor:
+        """The device's rotary_dim / 2 steps (gemm_epi_rotary_steps), as int64;
+        others of that type and size may be put in their place."""
+        return self._steps
+
+    @steps.setter
+    def steps(self, t: torch.Tensor) -> None:
+        # checked here, once, so that no call has to: the kernels read this many
+        if t.dtype is not torch.int64 or t.shape != (self.rotary_dim // 2,) or not t.is_contiguous():
+            raise ValueError("steps: expected %d contiguous int64 values, got %s %s"
+                             % (self.rotary_dim // 2, t.dtype, tuple(t.shape)))
+        self._steps = t
+
 
 # gemm_epi_qk_args, packed in one step: filling a ctypes structure field by
 # field took 2.4 us of a small call.
@@ -513,7 +527,7 @@ def _head_call(entry: str, q, k, rope: Rotary, positions, q_out, k_out, stream, 
         raise ValueError("k_out without k")
     if backward and ((dyq is None) != (q is None) or (dyk is None) != (k is None)):
         raise ValueError("a gradient and its input (dyq and q, dyk and k) must be given together")
-    steps = rope.steps
+    steps = rope._steps
     if steps.get_device() != index:
         raise ValueError("the rotary steps are on %s, q and k on %s" % (steps.device, first.device))
     at = wide = pos_stride = ws = ws_bytes = wq = wk = dq_at = dk_at = 0
