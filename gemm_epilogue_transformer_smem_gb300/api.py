@@ -178,7 +178,7 @@ class Plan:
         d.batch_stride_c = M * d.ldc if batch_stride_c is None else batch_stride_c
         d.batch_stride_c8 = M * d.ldc8 if batch_stride_c8 is None else batch_stride_c8
         d.batch_stride_aux = M * d.ld_aux if batch_stride_aux is None else batch_stride_aux
-        self.batch = batch
+        self.batch = max(1, batch)  # 0 is a single problem too
         d.a_type, d.b_type = OPERAND_TYPES[a_type], OPERAND_TYPES[b_type]
         self.a_type, self.b_type = a_type, b_type
         self.rotary = rotary

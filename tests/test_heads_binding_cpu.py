@@ -27,3 +27,21 @@ def test_steps_put_in_place_are_checked(lib):
         with pytest.raises(ValueError, match="16 contiguous int64"):
             rope.steps = bad
     assert torch.equal(rope.steps, other.steps)
+
+
+def test_a_batch_of_zero_is_one_problem_to_the_checks_too(lib):
+    """The C ABI runs M rows for batch 0; the binding asked for no positions and
+    let operands of any size through."""
+    rope = api.Rotary(64, device="cpu")
+    plan = api.Plan(64, 256, 64, ["rotary", "store_bf16"], batch=0, rotary=rope, head_cols=128)
+    A, B, C = (torch.zeros(64, n, dtype=BF) for n in (64, 256, 256))
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8)
+    pos = torch.zeros(64, dtype=torch.int32)
+    assert plan.args(A, B, C=C, workspace=ws, positions=pos).positions == pos.data_ptr()
+    with pytest.raises(ValueError, match="positions: expected 64"):
+        plan.args(A, B, C=C, workspace=ws, positions=pos[:0])
+    with pytest.raises(ValueError, match="A: 8192 bytes"):
+        plan.args(A[:32].clone(), B, C=C, workspace=ws, positions=pos)
+    with pytest.raises(ValueError, match="C: 32768 bytes"):
+        plan.args(A, B, C=torch.zeros(64, 128, dtype=BF), workspace=ws, positions=pos)
+    assert api.allocate_outputs(plan, "cpu").C.shape == (64, 256)
