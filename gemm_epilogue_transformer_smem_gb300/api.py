@@ -71,6 +71,19 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+def _call_on(t: Optional[torch.Tensor], stream: Optional[torch.cuda.Stream], call):
+    """call(stream) with the given stream, or the current one of t's device, as
+    an integer, and that device current: the library launches on the current
+    device, which cannot read another one's memory."""
+    index = -1 if t is None else t.get_device()
+    if index < 0:  # host memory: the library says what is wrong
+        return call(_raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream)
+    if index == _current_device():
+        return call(_raw_stream(index) if stream is None else stream.cuda_stream)
+    with torch.cuda.device(index):
+        return call(_raw_stream(index) if stream is None else stream.cuda_stream)
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -229,6 +242,8 @@ class Plan:
             index = steps.get_device()
             if A is not None and index != A.get_device():
                 raise ValueError("the rotary steps are on %s, A on %s" % (steps.device, A.device))
+            if workspace is not None and index != workspace.get_device():
+                raise ValueError("the rotary steps are on %s, the workspace on %s" % (steps.device, workspace.device))
             a.rotary_steps, a.rotary_amplitude = steps.data_ptr(), self.rotary.amplitude
             if positions is not None:
                 if positions.dtype is not torch.int32 and positions.dtype is not torch.int64:
@@ -268,24 +283,21 @@ class Plan:
         return {name: (v[0], (v[4] - 1) * v[5] + (v[1] - 1) * v[3] + v[2], v[1:]) for name, v in matrix.items()}
 
     def run(self, *tensors, stream: Optional[torch.cuda.Stream] = None, **kw):
-        """gemm_epi_run on the current (or given) CUDA stream; asynchronous."""
+        """gemm_epi_run on the current (or given) stream of the workspace's device; asynchronous."""
         a = self.args(*tensors, **kw)
-        s = _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
-        status = self.lib.gemm_epi_run(self.handle, ctypes.byref(a), s)
+        status = _call_on(kw.get("workspace"), stream, lambda s: self.lib.gemm_epi_run(self.handle, ctypes.byref(a), s))
         if status:
             N.check(status, self.lib)
 
     def run_unfused(self, *tensors, scratch: torch.Tensor, stream=None, **kw):
         a = self.args(*tensors, **kw)
         _expect("scratch", scratch, "bf16", self.M, self.N, scratch.stride(0))
-        s = (stream or torch.cuda.current_stream()).cuda_stream
-        N.check(self.lib.gemm_epi_run_unfused(self.handle, ctypes.byref(a), ctypes.c_void_p(scratch.data_ptr()),
-                                              scratch.stride(0), ctypes.c_void_p(s)), self.lib)
+        N.check(_call_on(scratch, stream, lambda s: self.lib.gemm_epi_run_unfused(
+            self.handle, ctypes.byref(a), ctypes.c_void_p(scratch.data_ptr()), scratch.stride(0), s)), self.lib)
 
     def query_status(self, workspace: torch.Tensor, stream=None) -> int:
-        s = (stream or torch.cuda.current_stream()).cuda_stream
-        return int(self.lib.gemm_epi_query_status(self.handle, ctypes.c_void_p(workspace.data_ptr()),
-                                                  ctypes.c_void_p(s)))
+        return int(_call_on(workspace, stream, lambda s: self.lib.gemm_epi_query_status(
+            self.handle, ctypes.c_void_p(workspace.data_ptr()), s)))
 
 
 @dataclass
@@ -350,8 +362,7 @@ def rmsnorm_backward(dy, x, s, r, *, w=None, add=None, dx=None, dw=None, stream=
     a.w, a.s, a.r = _ptr(w), _ptr(s), _ptr(r)
     a.dx, a.ld_dx = _ptr(dx), (dx.stride(0) if dx is not None else 0)
     a.dw = _ptr(dw)
-    st = (stream or torch.cuda.current_stream()).cuda_stream
-    N.check(lib.gemm_epi_rmsnorm_backward(ctypes.byref(a), ctypes.c_void_p(st)), lib)
+    N.check(_call_on(dy, stream, lambda st: lib.gemm_epi_rmsnorm_backward(ctypes.byref(a), st)), lib)
 
 
 ROTARY_LAYOUTS = {"half": N.GEMM_EPI_ROTARY_HALF, "interleaved": N.GEMM_EPI_ROTARY_INTERLEAVED}
@@ -555,8 +566,7 @@ def _head_call(entry: str, q, k, rope: Rotary, positions, q_out, k_out, stream, 
     if index == _current_device():
         status = fn(packed, _raw_stream(index) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(index):
-            status = fn(packed, _raw_stream(index) if stream is None else stream.cuda_stream)
+        status = _call_on(first, stream, lambda s: fn(packed, s))
     if status:
         N.check(status)
 
