@@ -554,6 +554,9 @@ int choose_cta_group(const gemm_epi_plan& P, const gemm_epi_args& a, const Devic
   return P.d.M > ge::BLOCK_M ? 2 : 1;
 }
 
+// n of GEMM_EPI_DEBUG_FORCE_SPLIT(n), 0 without it.
+int forced_split(uint32_t debug_flags) { return static_cast<int>(debug_flags >> 8 & 15u); }
+
 // Rows of a split tile's A box: what M fills, repeated up to 128.
 int64_t split_rows(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : ge::BLOCK_M; }
 
@@ -562,9 +565,15 @@ int64_t split_rows(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : ge::BLOCK_M
 // K-block, and room in a CTA's operand ring for the partial sums it receives
 // (every other CTA's, of its pieces).  So a projection of few rows reads its
 // weights through most SMs, where one CTA per tile left 128 of 152 idle (64 x
-// 4096 -> 6144 columns).
-int choose_split(const gemm_epi_plan& P, const gemm_epi_args& a, const DeviceState& dev) {
-  if (!P.heads() || (a.debug_flags & (GEMM_EPI_DEBUG_FORCE_1SM | GEMM_EPI_DEBUG_FORCE_2SM))) return 1;
+// 4096 -> 6144 columns).  A forced n has to be one of those.
+gemm_epi_status choose_split(const gemm_epi_plan& P, const gemm_epi_args& a, const DeviceState& dev, int* split) {
+  *split = 1;
+  const int forced = forced_split(a.debug_flags);
+  if (!P.heads() || (a.debug_flags & (GEMM_EPI_DEBUG_FORCE_1SM | GEMM_EPI_DEBUG_FORCE_2SM))) {
+    if (forced) return fail(GEMM_EPI_ERR_UNSUPPORTED, "K is shared by a cluster in programs with HEAD_RMS or ROTARY, on "
+                                                      "neither forced main loop");
+    return GEMM_EPI_OK;
+  }
   const int k_step = P.in8 ? 2 * ge::BLOCK_K : ge::BLOCK_K;
   const int64_t k_blocks = (P.d.K + k_step - 1) / k_step;
   const int64_t tiles = P.num_m_tiles * P.num_n_tiles * P.batch;
@@ -573,20 +582,28 @@ int choose_split(const gemm_epi_plan& P, const gemm_epi_args& a, const DeviceSta
   const SplitCost cost = rows == 32   ? SPLIT_COST_32_ROWS
                          : rows == 64 ? SPLIT_COST_64_ROWS
                                       : P.d.head_dim == ge::BLOCK_N ? SPLIT_COST_ONE_HEAD : SPLIT_COST;
-  int best = 1;
+  auto fits = [&](int n) {
+    const int64_t bytes = (n - 1) * ((pieces + n - 1) / n) * P.d.head_dim * 32 * 4;
+    return tiles <= dev.split_clusters[n] && k_blocks >= n &&
+           bytes + 4096 <= static_cast<int64_t>(ge::Smem<1>::OFF_EPI);  // with the sums of repeated rows
+  };
+  if (forced) {
+    if (!fits(forced))
+      return fail(GEMM_EPI_ERR_UNSUPPORTED, "%lld tiles of %lld K-blocks do not fit on clusters of %d CTAs",
+                  static_cast<long long>(tiles), static_cast<long long>(k_blocks), forced);
+    *split = forced;
+    return GEMM_EPI_OK;
+  }
   double least = static_cast<double>(k_blocks);
   for (int n = 2; n <= MAX_SPLIT; ++n) {
-    const int64_t bytes = (n - 1) * ((pieces + n - 1) / n) * P.d.head_dim * 32 * 4;
-    if (tiles > dev.split_clusters[n] || k_blocks < n ||
-        bytes + 4096 > static_cast<int64_t>(ge::Smem<1>::OFF_EPI))  // with the sums of repeated rows
-      continue;
+    if (!fits(n)) continue;
     const double c = static_cast<double>((k_blocks + n - 1) / n) + cost.fixed + cost.each * n;
     if (c < least) {
       least = c;
-      best = n;
+      *split = n;
     }
   }
-  return best;
+  return GEMM_EPI_OK;
 }
 
 // Fills the kernel parameters and tensor maps of one fused launch.  `c`/`ldc`
@@ -595,7 +612,8 @@ int choose_split(const gemm_epi_plan& P, const gemm_epi_args& a, const DeviceSta
 gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const DeviceState& dev, Launch& L) {
   const gemm_epi_desc& d = P.d;
   std::memset(&L, 0, sizeof L);
-  L.split = choose_split(P, a, dev);
+  gemm_epi_status s = choose_split(P, a, dev, &L.split);
+  if (s) return s;
   L.cg = L.split > 1 ? 1 : choose_cta_group(P, a, dev);
   if (P.spec && !(a.debug_flags & GEMM_EPI_DEBUG_FORCE_INTERPRETER))
     L.kernel = L.split > 1 ? P.spec->kernel_split : L.cg == 2 ? P.spec->kernel_2sm : P.spec->kernel_1sm;
@@ -704,7 +722,6 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
   else
     L.grid = static_cast<int>(std::min<int64_t>(k.num_tiles, dev.sms));
 
-  gemm_epi_status s;
   if (d.K > 0) {
     const CUtensorMapDataType op_dt = P.in8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int64_t esz = P.in8 ? 1 : 2;  // bytes per operand element
@@ -786,6 +803,9 @@ gemm_epi_status check_args(const gemm_epi_plan& P, const gemm_epi_args& a) {
       return fail(GEMM_EPI_ERR_MISALIGNED, "a_scale_inv / b_scale_inv must be 4-byte aligned");
   if ((P.flags & ge::F_ROW) && d.M > 0 && (s = need(a.row_out, "row_out"))) return s;
   if ((P.flags & ge::F_COL) && P.n_out > 0 && (s = need(a.col_out, "col_out"))) return s;
+  const int split = forced_split(a.debug_flags);
+  if (split == 1 || split > MAX_SPLIT)
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "GEMM_EPI_DEBUG_FORCE_SPLIT takes 2 to %d CTAs (got %d)", MAX_SPLIT, split);
   if (!a.workspace || !aligned16(a.workspace) || a.workspace_bytes < P.ws_bytes)
     return fail(GEMM_EPI_ERR_WORKSPACE, "workspace must be 16-byte aligned and hold %zu bytes (got %zu)",
                 P.ws_bytes, a.workspace ? a.workspace_bytes : static_cast<size_t>(0));

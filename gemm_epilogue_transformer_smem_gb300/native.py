@@ -68,12 +68,16 @@ GEMM_EPI_OP_HEAD_RMS = 19
 GEMM_EPI_OP_ROTARY = 20
 
 GEMM_EPI_MAX_OPS = 16
+GEMM_EPI_NO_ALLOC_SCRATCH_BYTES = 65536
 GEMM_EPI_DEBUG_SKIP_FIRST_LOAD = 1
 GEMM_EPI_DEBUG_FORCE_1SM = 2
 GEMM_EPI_DEBUG_FORCE_2SM = 4
 GEMM_EPI_DEBUG_FORCE_INTERPRETER = 8
 GEMM_EPI_DEBUG_SKIP_SECOND_LOAD = 16
-GEMM_EPI_NO_ALLOC_SCRATCH_BYTES = 65536
+
+
+def GEMM_EPI_DEBUG_FORCE_SPLIT(n: int) -> int:
+    return n << 8
 
 
 class gemm_epi_op(ctypes.Structure):

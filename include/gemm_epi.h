@@ -296,6 +296,12 @@ typedef struct gemm_epi_args {
 /* Test hook: run the op-interpreting kernel even when the program has a
  * compiled (static) kernel, so both forms can be checked on one program. */
 #define GEMM_EPI_DEBUG_FORCE_INTERPRETER 8u
+/* Test hook: share each tile of a program with HEAD_RMS or ROTARY over K by n
+ * CTAs (2 to 8), however many the library would choose.  UNSUPPORTED where n
+ * does not fit: other programs, fewer K-blocks than CTAs, more tiles than
+ * clusters of n are resident at once, no room for the partial sums, or with
+ * either of the forced main loops. */
+#define GEMM_EPI_DEBUG_FORCE_SPLIT(n) ((uint32_t)(n) << 8)
 
 typedef struct gemm_epi_plan *gemm_epi_handle;
 

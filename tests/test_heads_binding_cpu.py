@@ -105,3 +105,17 @@ def test_plans_run_on_the_device_of_their_tensors(lib, monkeypatch):
     heads = api.Plan(64, 256, 64, ["rotary", "store_bf16"], rotary=rope, head_cols=128)
     with pytest.raises(ValueError, match="the workspace on cuda:1"):
         heads.args(None, None, C=C, workspace=ws)
+
+
+def test_a_forced_split_is_two_to_eight(lib):
+    plan = api.Plan(64, 256, 1024, ["rotary", "store_bf16"], rotary=api.Rotary(64, device="cpu"), head_cols=128)
+    A, B, C = torch.zeros(64, 1024, dtype=BF), torch.zeros(1024, 256, dtype=BF), torch.zeros(64, 256, dtype=BF)
+    ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8)
+
+    class Stream:
+        cuda_stream = 0
+
+    for n in (1, 9, 15):
+        with pytest.raises(N.GemmEpiError, match="2 to 8") as err:
+            plan.run(A, B, C=C, workspace=ws, stream=Stream(), debug_flags=N.GEMM_EPI_DEBUG_FORCE_SPLIT(n))
+        assert err.value.status == N.GEMM_EPI_ERR_INVALID_VALUE
