@@ -255,7 +255,8 @@ gemm_epi_status run_heads(const gemm_epi_qk_args* a, int mode, cudaStream_t st) 
   const HeadKernel kernel = kernel_of(mode, wide, half, a->rotary_dim < p.reach, a->type == GEMM_EPI_TYPE_F32);
   const int64_t resident = static_cast<int64_t>(sms) * kernel.blocks;
   // One wave of blocks, and no more warps than iterations.
-  const int64_t sets = (p.rows + (32 >> p.log_g) - 1) / (32 >> p.log_g);  // of tokens, one to each lane group
+  const int64_t groups = 32 >> p.log_g;                   // lane groups of a warp, a token to each
+  const int64_t sets = (p.rows + groups - 1) / groups;    // of tokens (64-bit: rows may be 2^31 - 1)
   auto share_out = [&](ge::HeadShare& h, int64_t per_row, int64_t most) {
     const int64_t total = sets * per_row;
     const int64_t blocks = std::min(most, (total + ge::HD_WARPS - 1) / ge::HD_WARPS);
