@@ -45,7 +45,7 @@
 // tile over K (SPLIT) and its CTAs share the epilogue out.  On one GB300, us in
 // a graph: 64 x 4096 -> 6144 18.3 (weights alone 7.4 at the measured copy rate),
 // 35 with one CTA to a tile; 8192 x 4096 -> 6144 226 to 243 under the power cap,
-// the bare GEMM 220 to 236; 8192 x 1024 89 and 66: there the epilogue bounds it,
+// the bare GEMM 220 to 236; 8192 x 1024 90 and 66: there the epilogue bounds it,
 // four warps of about 350 instructions a chunk at one in five cycles, a third
 // of them angles (16 cycles of the special-function unit a pair and warp).
 //
@@ -734,7 +734,8 @@ __device__ __forceinline__ void dswiglu_expand(const float (&dh)[16], const floa
 }
 
 // cos and sin of a row's position for up to 32 pairs of a head, two pairs to a
-// float2.
+// float2: to 2^-20, for bf16 and e4m3 results.  AMAX, column sums and unrounded
+// row statistics of rotated values are fp32 with that error in them.
 struct RowAngles {
   float2 c[16], s[16];
 

@@ -37,15 +37,17 @@ constexpr int HD_THREADS = 32 * HD_WARPS;
 constexpr int HD_MAX_DIM = 512;  // 16 values per lane x 32 lanes
 // Resident blocks per SM that the register budget allows, and iterations a
 // warp keeps in flight.  Measured on one GB300 with 32 + 8 heads of 128 (bf16):
-//   norm, 16384 tokens (336 MB): 55.9 us = 6.0 TB/s, 0.88 of the measured copy;
-//     64.3 us with 3 blocks (80 registers, which spill), 59.4 at depth 2, 62.1 at 4
-//   rotary, 65536 tokens (1.34 GB): 210.6 us = 6.4 TB/s, 0.94; 8192 tokens 29.1
-//     us = 0.85; with 4 blocks 212.9 and 30.3, with 2 208.4 and 30.4
+//   norm, 16384 tokens (336 MB): 56.4 us = 6.0 TB/s, 0.88 of the measured copy;
+//     64.3 us with 3 blocks (80 registers, which spill), 59.4 at depth 2, 62.1 at 4;
+//     fp32, 8192 tokens (336 MB) 60.2 us, 0.82
+//   rotary, 65536 tokens (1.34 GB): 209.3 us = 6.4 TB/s, 0.94; 8192 tokens 28.8
+//     us = 0.86; with 4 blocks 212.9 and 30.3, with 2 208.4 and 30.4
 //   backward, 16384 tokens (503 MB): 85.5 us = 5.9 TB/s, 0.87; 104.6 us at
 //     depth 1, 88.6 at 3, 93.9 at 4
-// The norm and the backward pass issue about two instructions in three cycles
-// beside their loads; the registers that hold a norm's weights, angles and one
-// head's values set how many warps share an SM.
+// The norm and the backward pass use 0.42 and 0.43 of the issue slots: beside
+// HBM it is latency that is left, of each head's sums over its lanes, hidden by
+// the 16 warps of an SM that the registers (a norm's weights, angles and one
+// head's values) allow.
 constexpr int HD_ROTARY_BLOCKS = 3, HD_NORM_BLOCKS = 2, HD_BWD_BLOCKS = 2;
 constexpr int HD_FWD_DEPTH = 3, HD_BWD_DEPTH = 2;
 // Partial dw rows of the backward pass: one per block, added up by
@@ -403,7 +405,10 @@ __device__ __forceinline__ void head_forward(HeadPairs& v, const HeadPairs& w, c
 }
 
 // One head backward: v = x, g = dy in; v = dx out, dw added to where `ok` (a
-// lane group without a token adds nothing).
+// lane group without a token adds nothing).  A lane adds its share's terms one
+// after the other in fp32, 67 of them with 32 + 8 heads of 128 and 16384 tokens;
+// then lane groups, warps and blocks are added up.  The error grows with the
+// length of a share; fp64 sums would take 16 registers more.
 template <class Angles>
 __device__ __forceinline__ void head_backward(HeadPairs& v, HeadPairs& g, const HeadPairs& w, HeadPairs& dw,
                                               const Angles& ang, const HeadParams& p, bool ok) {
@@ -741,7 +746,9 @@ __global__ void __launch_bounds__(HD_THREADS, HD_BWD_BLOCKS) heads_backward_kern
 // ---------------------------------------------------------------- any alignment
 //
 // The same passes with single-element accesses, for sizes, strides and
-// addresses that 16-byte ones do not serve.
+// addresses that 16-byte ones do not serve.  bf16, 8192 tokens of 32 + 8 heads
+// of 96 with 24 values rotated in the half layout: rotary 63.9 us (0.29 of the
+// measured copy), norm 69.9, backward 138.5 (0.20).
 
 template <class T, bool HALF, bool NORM, bool PART>
 __global__ void __launch_bounds__(HD_THREADS, 2) heads_any_kernel(const __grid_constant__ HeadParams p) {

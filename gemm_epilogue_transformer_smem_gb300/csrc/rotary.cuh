@@ -3,9 +3,13 @@
 // A pair i turns by freq[i] radians per position.  An angle only matters
 // modulo one turn, so a frequency is kept as the 64-bit fraction of a turn it
 // advances per position, step = freq / (2 pi) * 2^64 mod 2^64, and the phase
-// of a position is the low 64 bits of position * step: exact for every 64-bit
-// position (negative ones too), where an fp32 product position * freq is off
-// by up to half an ulp of the angle -- 0.03 radians at position 1e6.  The
+// of a position is the low 64 bits of position * step.  That product is exact
+// for every 64-bit position (negative ones too), where an fp32 product
+// position * freq is off by up to half an ulp of the angle -- 0.03 radians at
+// position 1e6.  The step is not: freq and freq / (2 pi) are doubles, so that for
+// frequencies up to 1 it is off by up to 2^-55 of a turn and the phase of a
+// position by that many times the position: 2^-32 of a turn, the last bit used,
+// at position 2^23; 2^-24, what bf16 results keep, at 2^31; 2^-15 at 2^40.  The
 // phase's top 32 bits are read as a signed fraction of a turn in [-1/2, 1/2).
 #pragma once
 

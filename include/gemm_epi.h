@@ -201,8 +201,10 @@ typedef enum gemm_epi_op_code {
                                            ADD_BIAS_COL, MUL_COL_SCALE, MUL_ROW_SCALE and the
                                            activations may come before either (after HEAD_RMS a
                                            column scale holds the norm's weight of every column,
-                                           1 past head_cols).  Not with a pair op, DSWIGLU,
-                                           GEMM_EPI_B_DUAL or ops reading residual or preact.    */
+                                           1 past head_cols).  cos and sin are within 2^-20, also
+                                           for fp32 outputs (AMAX, COL_SUM).  Not with a pair op,
+                                           DSWIGLU, GEMM_EPI_B_DUAL or ops reading residual or
+                                           preact.                                               */
 } gemm_epi_op_code;
 
 typedef struct gemm_epi_op {
@@ -434,16 +436,19 @@ typedef struct gemm_epi_rotary_freq {
 
 /* Pure host code: the rotary_dim / 2 steps the entry points below read, each
  * the fraction of a turn pair i advances per position, times 2^64 (so the
- * phase of any 64-bit position is exact: the low 64 bits of position * step).
+ * phase of a position is the low 64 bits of position * step, exact for any 64-bit
+ * position but for the step's own rounding: up to 2^-55 of a turn per position
+ * for frequencies up to 1, 2^-24 of a turn at position 2^31).
  * The caller copies them to device memory once. */
 GEMM_EPI_API gemm_epi_status gemm_epi_rotary_steps(const gemm_epi_rotary_freq *freq, uint64_t *steps);
 
 /* The heads of q or k: element (b, t, h, d) at data + b stride_batch +
  * t stride_token + h stride_head + d, strides in elements, any order (tokens
  * outside heads or inside, heads of a packed q|k|v projection).  Any strides
- * and element-aligned pointers are taken; 16-byte aligned pointers and strides,
- * with whole 16-byte groups in a head (and in half the rotated part, in the
- * half layout), move 16 bytes per access, the rest single elements. */
+ * and element-aligned pointers are taken.  A call moves 16 bytes per access if
+ * every one of its tensors has 16-byte aligned pointers and strides and a head
+ * (and half the rotated part, in the half layout) is whole 16-byte groups;
+ * else it moves single elements, at about a third of the speed. */
 typedef struct gemm_epi_heads {
     void *data;
     int64_t stride_batch, stride_token, stride_head;
