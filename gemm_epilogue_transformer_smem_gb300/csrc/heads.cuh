@@ -44,10 +44,10 @@ constexpr int HD_MAX_DIM = 512;  // 16 values per lane x 32 lanes
 //     us = 0.86; with 4 blocks 212.9 and 30.3, with 2 208.4 and 30.4
 //   backward, 16384 tokens (503 MB): 85.5 us = 5.9 TB/s, 0.87; 104.6 us at
 //     depth 1, 88.6 at 3, 93.9 at 4
-// The norm and the backward pass use 0.42 and 0.43 of the issue slots: beside
-// HBM it is latency that is left, of each head's sums over its lanes, hidden by
-// the 16 warps of an SM that the registers (a norm's weights, angles and one
-// head's values) allow.
+// The norm and the backward pass use 0.42 of the issue slots: beside HBM it is
+// latency that is left, of each head's sums over its lanes, hidden by the 16
+// warps of an SM that the registers (a norm's weights, angles and one head's
+// values) allow.
 constexpr int HD_ROTARY_BLOCKS = 3, HD_NORM_BLOCKS = 2, HD_BWD_BLOCKS = 2;
 constexpr int HD_FWD_DEPTH = 3, HD_BWD_DEPTH = 2;
 // Partial dw rows of the backward pass: one per block, added up by
@@ -408,7 +408,9 @@ __device__ __forceinline__ void head_forward(HeadPairs& v, const HeadPairs& w, c
 // lane group without a token adds nothing).  A lane adds its share's terms one
 // after the other in fp32, 67 of them with 32 + 8 heads of 128 and 16384 tokens;
 // then lane groups, warps and blocks are added up.  The error grows with the
-// length of a share; fp64 sums would take 16 registers more.
+// length of a share; fp64 sums would take 16 registers more.  Against 64 bits dw is
+// off by 1.5e-7 of its size (fp32, 999 tokens) and 3.6e-7 (bf16 tensors, whose
+// cos and sin are the special-function unit's; 16384 tokens).
 template <class Angles>
 __device__ __forceinline__ void head_backward(HeadPairs& v, HeadPairs& g, const HeadPairs& w, HeadPairs& dw,
                                               const Angles& ang, const HeadParams& p, bool ok) {

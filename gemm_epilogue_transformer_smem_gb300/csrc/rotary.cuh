@@ -22,8 +22,8 @@ __device__ __forceinline__ int32_t phase_bits(int64_t position, uint64_t step) {
   return static_cast<int32_t>((static_cast<uint64_t>(position) * step) >> 32);
 }
 
-// cos and sin of a phase by the special-function unit: for bf16 results, which
-// keep 8 bits.  The unit is off by up to 2^-21.2 on [-pi, pi]; the phase, rounded
+// cos and sin of a phase by the special-function unit: for bf16 tensors, which
+// keep 8 bits, and what is summed from them.  The unit is off by up to 2^-21.2 on [-pi, pi]; the phase, rounded
 // to its top 23 bits and placed in the mantissa of a float in [2, 4) (an
 // int-to-float conversion would take the same unit as sin and cos), by 2 pi
 // 2^-24 = 2^-21.3, and its product with pi by 2^-23: 2^-20 together (2^-20.4 the
