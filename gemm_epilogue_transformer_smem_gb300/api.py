@@ -627,3 +627,208 @@ def qk_norm_rotary_backward(dyq, dyk, q, k, rope: Rotary, positions=None, *, q_w
     time (another stream's, another graph's) shares.  Asynchronous."""
     _head_call("gemm_epi_qk_norm_rotary_backward", q, k, rope, positions, dq, dk, stream, 0, eps, q_weight, k_weight,
                True, dyq, dyk, dwq, dwk, workspace)
+
+
+class Dropout:
+    """A dropout probability and the state its masks are drawn from: a seed and
+    a step in device memory, kept for every call.
+
+    p is rounded to a multiple of 2^-16; what stays is scaled by the inverse of
+    the share that stays, so that means are kept.  The mask of a call depends on
+    seed, step and the call's `site` (and the element's row and column), nothing
+    else: a backward pass with the same three drops what its forward pass
+    dropped.  advance() counts the step on, on the current stream; captured into
+    a graph, each replay draws masks of its own.
+    """
+
+    def __init__(self, p: float, seed: int = 0, step: int = 0, device="cuda"):
+        if not 0.0 <= p <= 1.0:
+            raise ValueError("p must be in [0, 1], got %r" % (p,))
+        if not 0 <= seed < 2 ** 64 or not 0 <= step < 2 ** 63:
+            raise ValueError("seed must be in [0, 2^64) and step in [0, 2^63), got %r and %r" % (seed, step))
+        self.p = float(p)
+        self.threshold = round(self.p * 65536)
+        # the seed's 64 bits in an int64 tensor, as Rotary.steps
+        self.state = torch.tensor([seed - 2 ** 64 if seed >= 2 ** 63 else seed, step], dtype=torch.int64).to(device)
+
+    @property
+    def state(self) -> torch.Tensor:
+        """The device's seed and step, as two int64; another tensor of that
+        type may be put in their place, or they may be written to."""
+        return self._state
+
+    @state.setter
+    def state(self, t: torch.Tensor) -> None:
+        # checked here, once, so that no call has to: the kernels read both
+        if t.dtype is not torch.int64 or t.shape != (2,) or not t.is_contiguous():
+            raise ValueError("state: expected 2 contiguous int64 values, got %s %s" % (t.dtype, tuple(t.shape)))
+        self._state = t
+
+    def advance(self, steps: int = 1) -> None:
+        """The next step's masks: adds to the step in device memory."""
+        self._state[1:].add_(steps)
+
+
+# Packed in one step, as _QK_ARGS.
+_DROPOUT_ARGS = struct.Struct("@qqiQIiQqQqQq")
+_LAYER_NORM_ARGS = struct.Struct("@qqifQIiQqQqQqQqQQQQ")
+_LAYER_NORM_BWD_ARGS = struct.Struct("@qqiQIiQqQqQqQqQqQQQQQQN")
+assert _DROPOUT_ARGS.size == ctypes.sizeof(N.gemm_epi_dropout_args)
+assert _LAYER_NORM_ARGS.size == ctypes.sizeof(N.gemm_epi_layer_norm_args)
+assert _LAYER_NORM_BWD_ARGS.size == ctypes.sizeof(N.gemm_epi_layer_norm_bwd_args)
+_NO_ROWS = (0, 0)
+_NO_MASK = (0, 0, 0)
+
+
+def _first_rows(name: str, t: torch.Tensor):
+    """(type code, rows, columns, (pointer, row stride)) of the tensor a call's
+    others are checked against."""
+    code = HEAD_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s: expected a bf16 or fp32 tensor, got %s" % (name, t.dtype))
+    shape = t.shape
+    if not shape:
+        raise ValueError("%s: expected (..., columns), got a scalar" % name)
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    return code, rows, shape[-1], _row_stride(name, t, shape)
+
+
+def _row_stride(name: str, t: torch.Tensor, shape):
+    """(pointer, stride between rows) of a (..., columns) tensor whose rows are
+    evenly spaced."""
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1 and t.numel():
+        raise ValueError("%s: the values of a row must be contiguous" % name)
+    if len(st) == 2:
+        return t.data_ptr(), st[0]
+    ld, spanned = shape[-1], None  # of the leading dimensions of more than one step, from the last
+    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n == 1:
+            continue
+        if spanned is None:
+            ld = s
+        elif s != spanned and t.numel():
+            raise ValueError("%s: its rows are not evenly spaced (strides %s)" % (name, st))
+        spanned = s * n
+    return t.data_ptr(), ld
+
+
+def _rows(name: str, t: torch.Tensor, first: torch.Tensor):
+    """(pointer, row stride) of a tensor of first's shape, type and device, checked."""
+    shape = t.shape
+    if shape != first.shape or t.dtype is not first.dtype:
+        raise ValueError("%s: %s %s does not match %s %s"
+                         % (name, t.dtype, tuple(shape), first.dtype, tuple(first.shape)))
+    if t.get_device() != first.get_device():
+        raise ValueError("%s is on %s, not with the other tensors" % (name, t.device))
+    return _row_stride(name, t, shape)
+
+
+def _values(name: str, t: torch.Tensor, n: int, index: int) -> int:
+    """Pointer of n contiguous fp32 values on device `index`, checked."""
+    if t.dtype is not torch.float32:
+        raise TypeError("%s: expected a f32 tensor, got %s" % (name, t.dtype))
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s: expected %d contiguous values, got %s" % (name, n, tuple(t.shape)))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, not with the other tensors" % (name, t.device))
+    return t.data_ptr()
+
+
+def _mask(rng: Optional[Dropout], site: int, index: int):
+    """(state, site, threshold) of a gemm_epi_mask."""
+    if rng is None or rng.threshold == 0:
+        return _NO_MASK
+    state = rng._state
+    if state.get_device() != index:
+        raise ValueError("the dropout state is on %s, not with the other tensors" % state.device)
+    if not 0 <= site < 2 ** 32:
+        raise ValueError("site must be in [0, 2^32), got %r" % (site,))
+    return state.data_ptr(), site, rng.threshold
+
+
+def _call_packed(entry: str, packed: bytes, first: torch.Tensor, stream) -> None:
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("expected CUDA tensors, got %s" % first.device)
+    fn = _head_entries.get(entry) or _head_entry(entry)
+    if index == _current_device():
+        status = fn(packed, _raw_stream(index) if stream is None else stream.cuda_stream)
+    else:
+        status = _call_on(first, stream, lambda s: fn(packed, s))
+    if status:
+        N.check(status)
+
+
+def dropout(x, rng: Dropout, *, out, residual=None, site: int = 0, stream=None) -> None:
+    """gemm_epi_dropout: x with its elements dropped by rng's mask of `site`, plus
+    the residual, into `out`.
+
+    x: (..., columns), bf16 or fp32, rows of contiguous values evenly spaced
+    (expanded rows among them); the others the same.  out may be x or residual.
+    The backward pass is the same call on out's gradient, without the residual,
+    whose own gradient is out's.  Asynchronous."""
+    code, rows, cols, tx = _first_rows("x", x)
+    tr = _NO_ROWS if residual is None else _rows("residual", residual, x)
+    _call_packed("gemm_epi_dropout", _DROPOUT_ARGS.pack(rows, cols, code, *_mask(rng, site, x.get_device()), *tx, *tr,
+                                                        *_rows("out", out, x)), x, stream)
+
+
+def layer_norm(x, *, weight=None, bias=None, eps: float = 1e-5, out, residual=None, dropout: Optional[Dropout] = None,
+               site: int = 0, sum_out=None, mean=None, rstd=None, stream=None) -> None:
+    """gemm_epi_layer_norm: h = x, dropped by `dropout`'s mask of `site`, plus the
+    residual; (h - mean(h)) / sqrt(var(h) + eps) * weight + bias into `out`, each
+    row over its columns, in one pass.
+
+    Tensors as for dropout(); weight and bias: fp32, one value per column (None:
+    1 and 0).  sum_out takes h, mean and rstd (fp32, one value per row) its
+    statistics: what layer_norm_backward reads.  out and sum_out may each be x
+    or residual.  Asynchronous."""
+    code, rows, cols, tx = _first_rows("x", x)
+    index = x.get_device()
+    if sum_out is not None and residual is None and dropout is None:
+        raise ValueError("sum_out without residual or dropout is x itself")
+    tr = _NO_ROWS if residual is None else _rows("residual", residual, x)
+    ts = _NO_ROWS if sum_out is None else _rows("sum_out", sum_out, x)
+    _call_packed("gemm_epi_layer_norm", _LAYER_NORM_ARGS.pack(
+        rows, cols, code, eps, *_mask(dropout, site, index), *tx, *tr, *_rows("out", out, x), *ts,
+        0 if weight is None else _values("weight", weight, cols, index),
+        0 if bias is None else _values("bias", bias, cols, index),
+        0 if mean is None else _values("mean", mean, rows, index),
+        0 if rstd is None else _values("rstd", rstd, rows, index)), x, stream)
+
+
+def layer_norm_workspace(cols: int) -> int:
+    """Bytes of workspace layer_norm_backward needs for dw or db."""
+    return int(N.load().gemm_epi_layer_norm_backward_workspace_size(cols))
+
+
+def layer_norm_backward(dy, x, mean, rstd, *, weight=None, dx=None, dw=None, db=None, add=None,
+                        dropout: Optional[Dropout] = None, site: int = 0, d_residual=None, workspace=None,
+                        stream=None) -> None:
+    """gemm_epi_layer_norm_backward: from the gradient dy of layer_norm's out, the
+    normalised sum x (its sum_out, or its x where nothing was added or dropped)
+    and the statistics it gave, the gradient g of that sum, plus `add`, which
+    reaches it past the norm: into d_residual as it is and into dx with the
+    forward pass's mask applied (`dropout` and `site` as there; None: dx is g).
+    dw and db (fp32, overwritten) take the weight's and bias's gradients, summed
+    over the rows.  Each of the four may be None; dx and d_residual may be the
+    memory of an input.  dw and db need a workspace of layer_norm_workspace(cols)
+    bytes that no call running at the same time (another stream's, another
+    graph's) shares.  Asynchronous."""
+    code, rows, cols, tdy = _first_rows("dy", dy)
+    index = dy.get_device()
+    ws = ws_bytes = 0
+    if workspace is not None:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace: expected a contiguous tensor with the others")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call_packed("gemm_epi_layer_norm_backward", _LAYER_NORM_BWD_ARGS.pack(
+        rows, cols, code, *_mask(dropout, site, index), *tdy, *_rows("x", x, dy),
+        *(_NO_ROWS if add is None else _rows("add", add, dy)), *(_NO_ROWS if dx is None else _rows("dx", dx, dy)),
+        *(_NO_ROWS if d_residual is None else _rows("d_residual", d_residual, dy)),
+        0 if weight is None else _values("weight", weight, cols, index), _values("mean", mean, rows, index),
+        _values("rstd", rstd, rows, index), 0 if dw is None else _values("dw", dw, cols, index),
+        0 if db is None else _values("db", db, cols, index), ws, ws_bytes), dy, stream)

@@ -163,6 +163,45 @@ class gemm_epi_qk_args(ctypes.Structure):
     ]
 
 
+class gemm_epi_mask(ctypes.Structure):
+    _fields_ = [("state", ctypes.c_void_p), ("site", ctypes.c_uint32), ("threshold", ctypes.c_int32)]
+
+
+class gemm_epi_dropout_args(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("type", ctypes.c_int32), ("mask", gemm_epi_mask),
+        ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+        ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64),
+    ]
+
+
+class gemm_epi_layer_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("type", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("mask", gemm_epi_mask),
+        ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+        ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64),
+        ("sum", ctypes.c_void_p), ("ld_sum", ctypes.c_int64),
+        ("w", ctypes.c_void_p), ("b", ctypes.c_void_p), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+    ]
+
+
+class gemm_epi_layer_norm_bwd_args(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("type", ctypes.c_int32), ("mask", gemm_epi_mask),
+        ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64),
+        ("add", ctypes.c_void_p), ("ld_add", ctypes.c_int64),
+        ("dx", ctypes.c_void_p), ("ld_dx", ctypes.c_int64),
+        ("d_residual", ctypes.c_void_p), ("ld_d_residual", ctypes.c_int64),
+        ("w", ctypes.c_void_p), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+        ("dw", ctypes.c_void_p), ("db", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 gemm_epi_handle = ctypes.c_void_p
 
 # (name, restype, argtypes): every entry point declared in include/gemm_epi.h.
@@ -182,6 +221,10 @@ SIGNATURES = [
     ("gemm_epi_qk_norm_rotary", ctypes.c_int, [ctypes.POINTER(gemm_epi_qk_args), ctypes.c_void_p]),
     ("gemm_epi_qk_norm_rotary_backward", ctypes.c_int, [ctypes.POINTER(gemm_epi_qk_args), ctypes.c_void_p]),
     ("gemm_epi_qk_norm_rotary_workspace_size", ctypes.c_size_t, [ctypes.c_int32]),
+    ("gemm_epi_dropout", ctypes.c_int, [ctypes.POINTER(gemm_epi_dropout_args), ctypes.c_void_p]),
+    ("gemm_epi_layer_norm", ctypes.c_int, [ctypes.POINTER(gemm_epi_layer_norm_args), ctypes.c_void_p]),
+    ("gemm_epi_layer_norm_backward", ctypes.c_int, [ctypes.POINTER(gemm_epi_layer_norm_bwd_args), ctypes.c_void_p]),
+    ("gemm_epi_layer_norm_backward_workspace_size", ctypes.c_size_t, [ctypes.c_int64]),
     ("gemm_epi_query_status", ctypes.c_int, [gemm_epi_handle, ctypes.c_void_p, ctypes.c_void_p]),
     ("gemm_epi_status_string", ctypes.c_char_p, [ctypes.c_int]),
     ("gemm_epi_last_error", ctypes.c_char_p, []),

@@ -127,7 +127,7 @@ typedef enum gemm_epi_type {
     GEMM_EPI_TYPE_BF16 = 0,
     GEMM_EPI_TYPE_E4M3 = 1,   /* OCP FP8 E4M3FN */
     GEMM_EPI_TYPE_E5M2 = 2,   /* OCP FP8 E5M2 */
-    GEMM_EPI_TYPE_F32 = 3     /* the head operators' tensors only (gemm_epi_qk_args) */
+    GEMM_EPI_TYPE_F32 = 3     /* the tensors of the operators on heads and on the residual stream only */
 } gemm_epi_type;
 
 typedef enum gemm_epi_b_layout {
@@ -492,6 +492,93 @@ GEMM_EPI_API gemm_epi_status gemm_epi_qk_norm_rotary_backward(const gemm_epi_qk_
 /* Bytes of workspace the backward pass needs for its weight gradients (0 for
  * a head_dim out of range). */
 GEMM_EPI_API size_t gemm_epi_qk_norm_rotary_workspace_size(int32_t head_dim);
+
+/*
+ * The residual stream between a block's GEMMs: dropout, and layer norm with the
+ * dropout and the residual add in front of it in the same pass.
+ *
+ * Dropout D of a matrix: element (row, col) has a number of 16 bits; below
+ * `threshold` the element becomes 0 (whatever it held, NaN too), else it is
+ * multiplied by 65536 / (65536 - threshold), in fp32.  The mask is never stored:
+ * the numbers are those of Philox 4x32-10 (Salmon et al., "Parallel random
+ * numbers: as easy as 1, 2, 3") with the seed as key (low 32 bits first) and the
+ * counter (col / 8, row, site, low 32 bits of step), whose eight 16-bit halves,
+ * the low half of each word first, go to columns 8 (col / 8) .. + 7.  So a
+ * backward pass draws the forward pass's mask by the same state and site, and a
+ * program with DROPOUT the same as gemm_epi_dropout on the stored matrix (its
+ * rows counted through the batch, b M + m; its columns those where the op acts).
+ * The state lies in device memory and is read when the kernel runs, so a
+ * captured graph draws new masks once something on the stream (the graph
+ * itself, say) has counted `step` on.
+ */
+typedef struct gemm_epi_mask {
+    const uint64_t *state;    /* device, 8-byte aligned: seed, step.  Unused with threshold 0 */
+    uint32_t site;            /* which of a step's masks: one for each place that drops */
+    int32_t threshold;        /* probability of being dropped, times 65536: 0 (no dropout) to 65536 */
+} gemm_epi_mask;
+
+/* y = D(x) (+ residual): M x N, row strides in elements.  Inputs may have any
+ * row stride >= 0 (0: one row for all), the output one >= N; x and residual may be
+ * y itself (same pointer and stride), otherwise nothing overlaps y.  A call moves
+ * 16 bytes per access where pointers and row strides are multiples of them
+ * (inputs and outputs each for themselves), single elements otherwise. */
+typedef struct gemm_epi_dropout_args {
+    int64_t M, N;             /* M < 2^31, 1 <= N <= 2^31 - 8; M 0 is allowed */
+    int32_t type;             /* BF16 or F32: x, residual and y */
+    gemm_epi_mask mask;
+    const void *x;        int64_t ld_x;
+    const void *residual; int64_t ld_residual;  /* or NULL */
+    void *y;              int64_t ld_y;
+} gemm_epi_dropout_args;
+
+/* h = D(x) + residual, mean and variance of h over its row (divided by N),
+ *   y = (h - mean) / sqrt(variance + eps) * w + b,
+ * h in fp32 throughout, rounded only where it is stored.  Strides, alignment and
+ * in-place use as in gemm_epi_dropout_args; `sum` is an output as well. */
+typedef struct gemm_epi_layer_norm_args {
+    int64_t M, N;
+    int32_t type;             /* BF16 or F32: x, residual, y and sum */
+    float eps;
+    gemm_epi_mask mask;       /* threshold 0: no dropout */
+    const void *x;        int64_t ld_x;
+    const void *residual; int64_t ld_residual;  /* or NULL */
+    void *y;              int64_t ld_y;
+    void *sum;            int64_t ld_sum;       /* h, or NULL */
+    const float *w, *b;       /* N values each, NULL: 1 and 0 */
+    float *mean, *rstd;       /* M values each, or NULL: mean and 1 / sqrt(variance + eps) */
+} gemm_epi_layer_norm_args;
+
+/* From the gradient dy of y, the stored sum x = h and its statistics: with
+ * n = (x - mean) rstd and a = dy w,
+ *   g = rstd (a - mean(a) - n mean(a n)) + add,
+ *   d_residual = g,  dx = D(g),  dw = sum of dy n over the rows,  db = sum of dy.
+ * `add` is the gradient that reaches h past the norm.  dx or d_residual may be an
+ * input itself (same pointer and stride). */
+typedef struct gemm_epi_layer_norm_bwd_args {
+    int64_t M, N;
+    int32_t type;             /* BF16 or F32: dy, x, add, dx and d_residual */
+    gemm_epi_mask mask;       /* as in the forward pass; threshold 0: dx = g */
+    const void *dy;  int64_t ld_dy;
+    const void *x;   int64_t ld_x;
+    const void *add; int64_t ld_add;                   /* or NULL */
+    void *dx;         int64_t ld_dx;                   /* each of the four outputs may be NULL */
+    void *d_residual; int64_t ld_d_residual;
+    const float *w;           /* N values, NULL: 1 */
+    const float *mean, *rstd; /* M values each, the forward pass's */
+    float *dw, *db;           /* N values each, overwritten */
+    void *workspace;          /* with dw or db: device, 16-byte aligned, not shared by calls that */
+    size_t workspace_bytes;   /* may run at once */
+} gemm_epi_layer_norm_bwd_args;
+
+/* Each enqueues its kernels on `stream`: asynchronous, capture-safe, checks
+ * sizes, pointers and alignment first, allocates nothing.  The same call with
+ * the same state gives the same bits every time. */
+GEMM_EPI_API gemm_epi_status gemm_epi_dropout(const gemm_epi_dropout_args *args, void *stream);
+GEMM_EPI_API gemm_epi_status gemm_epi_layer_norm(const gemm_epi_layer_norm_args *args, void *stream);
+GEMM_EPI_API gemm_epi_status gemm_epi_layer_norm_backward(const gemm_epi_layer_norm_bwd_args *args, void *stream);
+
+/* Bytes of workspace the backward pass needs for dw or db (0 for an N out of range). */
+GEMM_EPI_API size_t gemm_epi_layer_norm_backward_workspace_size(int64_t N);
 
 /* Synchronises `stream`, then reads the status words the last run on that
  * workspace left: GEMM_EPI_OK or GEMM_EPI_ERR_TIMEOUT (the last-error string
