@@ -8,7 +8,7 @@ colon):
   alpha, bias, row_scale, residual, gelu_tanh, relu, silu, pair_swiglu[:g], pair_mul[:g],
   gelu_tanh_grad, amax, store_bf16, store_e4m3, row_rms[:eps],
   row_rms_unrounded[:eps], col_sum, dswiglu[:g], col_scale, row_dot,
-  head_rms[:eps], rotary
+  head_rms[:eps], rotary, dropout
 """
 from __future__ import annotations
 
@@ -43,10 +43,11 @@ PROGRAM_OPS = {
     "col_sum": N.GEMM_EPI_OP_COL_SUM,
     "head_rms": N.GEMM_EPI_OP_HEAD_RMS,
     "rotary": N.GEMM_EPI_OP_ROTARY,
+    "dropout": N.GEMM_EPI_OP_DROPOUT,
 }
 
 
-def encode_program(program: Sequence[str]):
+def encode_program(program: Sequence[str], drop_threshold: int = 0):
     ops = (N.gemm_epi_op * max(1, len(program)))()
     for i, spec in enumerate(program):
         name, _, arg = spec.partition(":")
@@ -59,6 +60,8 @@ def encode_program(program: Sequence[str]):
         elif name.startswith("row_rms") or name == "head_rms":
             f0 = float(arg) if arg else 1e-6
             i0 = 1 if name == "row_rms_unrounded" else 0
+        elif name == "dropout":
+            i0 = drop_threshold
         ops[i] = N.gemm_epi_op(code, i0, f0)
     return ops
 
@@ -155,7 +158,10 @@ class Plan:
     Programs with head_rms or rotary (a q|k|v projection): columns
     [0, head_cols) are the heads of q and k, `rotary` holds the frequencies,
     head size and layout (head_dim alone is enough without the rotary op), and
-    run() takes the rows' positions."""
+    run() takes the rows' positions.
+
+    Programs with dropout: `dropout` holds the probability and the state, run()
+    takes the call's site; rows are counted through the batch."""
 
     def __init__(self, M: int, N_: int, K: int, program: Sequence[str], b_layout: str = "kn",
                  lda: Optional[int] = None, ldb: Optional[int] = None, ldc: Optional[int] = None,
@@ -164,13 +170,16 @@ class Plan:
                  batch_stride_b: Optional[int] = None, batch_stride_c: Optional[int] = None,
                  batch_stride_c8: Optional[int] = None, batch_stride_aux: Optional[int] = None,
                  a_type: str = "bf16", b_type: str = "bf16", rotary: Optional["Rotary"] = None,
-                 head_dim: Optional[int] = None, head_cols: int = 0):
+                 head_dim: Optional[int] = None, head_cols: int = 0, dropout: Optional["Dropout"] = None):
         self.lib = N.load()
         self.program = list(program)
         self.M, self.N, self.K = M, N_, K
         self.b_layout = b_layout
         n_out = out_cols(program, N_)
-        self._ops = encode_program(program)
+        if dropout is None and "dropout" in self.program:
+            raise ValueError("a program with the dropout op needs dropout=")
+        self.dropout = dropout if "dropout" in self.program else None
+        self._ops = encode_program(program, 0 if dropout is None else dropout.threshold)
         d = N.gemm_epi_desc()
         d.M, d.N, d.K = M, N_, K
         d.lda = K if lda is None else lda
@@ -220,7 +229,7 @@ class Plan:
     def args(self, A, B, *, alpha=1.0, fp8_scale=1.0, bias=None, row_scale=None, residual=None,
              preact=None, C=None, C8=None, amax=None, row_out=None, col_out=None, workspace=None,
              timeout_ms=0, debug_flags=0, B2=None, a_scale_inv=None, b_scale_inv=None,
-             col_scale=None, positions=None) -> N.gemm_epi_args:
+             col_scale=None, positions=None, site=0) -> N.gemm_epi_args:
         a = N.gemm_epi_args()
         a.alpha, a.fp8_scale = float(alpha), float(fp8_scale)
         for name, t in (("A", A), ("B", B), ("B2", B2), ("bias", bias), ("row_scale", row_scale),
@@ -257,6 +266,16 @@ class Plan:
                 a.positions, a.positions_64 = positions.data_ptr(), 1 if positions.dtype is torch.int64 else 0
         elif positions is not None:
             raise ValueError("positions: the plan has no rotary")
+        if self.dropout is not None:
+            index = self.dropout._state.get_device()
+            for name, t in (("A", A), ("the workspace", workspace)):
+                if t is not None and index != t.get_device():
+                    raise ValueError("the dropout state is on %s, %s on %s" % (self.dropout._state.device, name, t.device))
+            if not 0 <= site < 2 ** 32:
+                raise ValueError("site must be in [0, 2^32), got %r" % (site,))
+            a.dropout_state, a.dropout_site = self.dropout._state.data_ptr(), site
+        elif site:
+            raise ValueError("site: the plan has no dropout")
         return a
 
     def _operand_extents(self):

@@ -61,6 +61,7 @@
 #include <utility>
 
 #include "gemm_epi.h"
+#include "dropout.cuh"
 #include "ptx.cuh"
 #include "rotary.cuh"
 
@@ -202,6 +203,7 @@ struct KernelParams {
   const uint64_t* rot_steps;
   const void* positions;  // NULL: the row index
   int32_t positions_64;
+  Dropout drop;  // DROPOUT (programs with Prog::drops)
   EpiOpDev ops[GEMM_EPI_MAX_OPS];
 };
 
@@ -220,6 +222,7 @@ struct KernelParams {
 struct DynamicProgram {
   static constexpr bool is_static = false;
   static constexpr bool heads = false;
+  static constexpr bool drops = false;
 };
 
 // The interpreter for programs with HEAD_RMS or ROTARY: a kernel of its own,
@@ -227,6 +230,14 @@ struct DynamicProgram {
 struct DynamicHeadProgram {
   static constexpr bool is_static = false;
   static constexpr bool heads = true;
+  static constexpr bool drops = false;
+};
+
+// The interpreter for programs with DROPOUT, apart from the others likewise.
+struct DynamicDropProgram {
+  static constexpr bool is_static = false;
+  static constexpr bool heads = false;
+  static constexpr bool drops = true;
 };
 
 template <int... Ops>
@@ -268,6 +279,7 @@ struct StaticProgram {
     return -1;
   }
   static constexpr bool heads = has(GEMM_EPI_OP_HEAD_RMS) || has(GEMM_EPI_OP_ROTARY);
+  static constexpr bool drops = has(GEMM_EPI_OP_DROPOUT);
 };
 
 template <int Begin, class F, int... Is>
@@ -661,6 +673,20 @@ __device__ __forceinline__ void apply_pointwise(CodeT code, float (&v)[NV], cons
       break;
     default:
       break;
+  }
+}
+
+// DROPOUT on NV columns of a row from column col0, a multiple of 8: the mask
+// gemm_epi_dropout draws for that place of the stored matrix.
+template <int NV>
+__device__ __forceinline__ void drop_columns(const Dropout& d, const DropKey& key, uint32_t row, int col0, float (&v)[NV]) {
+  if (d.state == nullptr) return;  // nothing is dropped
+#pragma unroll
+  for (int g = 0; g < NV / 8; ++g) {
+    uint32_t w[4];
+    drop_words(key, row, static_cast<uint32_t>(col0 / 8 + g), w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[8 * g + j] = drop_keeps(w, j, d.above) ? v[8 * g + j] * d.scale : 0.0f;
   }
 }
 
@@ -1208,6 +1234,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int op_begin = Prog::heads ? max(head_rms_at, rotary_at) + 1
                                      : paired ? pair_at + 1 : expand ? expand_at + 1 : 0;
 
+    DropKey drop_state{};
+    if constexpr (Prog::drops) {
+      if (p.drop.state != nullptr) drop_state = drop_key(p.drop);
+    }
+
     float amax_f = 0.0f;  // max |y| so far; a NaN sticks (NaN wins, as in the integer maximum below)
     uint32_t gchunk = 0;                 // this warp's running chunk number
     bool ok = true;
@@ -1579,13 +1610,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               for (int j = 0; j < 16; ++j) dh[j] *= deq;
             }
           }
+          auto before = [&](auto code) {
+            if (Prog::drops && static_cast<int>(code) == GEMM_EPI_OP_DROPOUT)
+              drop_columns<16>(p.drop, drop_state, static_cast<uint32_t>(row_base + m), nacc0 + c * 16, dh);
+            else
+              apply_pointwise<16>(code, dh, p, nacc0 + c * 16, p.N, rs_m);
+          };
           if constexpr (kStatic) {
             static_for<0, (prog_expand_at<Prog>() < 0 ? 0 : prog_expand_at<Prog>())>([&](auto I) {
-              apply_pointwise<16>(std::integral_constant<int, Prog::code_of(decltype(I)::value)>{}, dh, p,
-                                  nacc0 + c * 16, p.N, rs_m);
+              before(std::integral_constant<int, Prog::code_of(decltype(I)::value)>{});
             });
           } else {
-            for (int i = 0; i < expand_at; ++i) apply_pointwise<16>(p.ops[i].code, dh, p, nacc0 + c * 16, p.N, rs_m);
+            for (int i = 0; i < expand_at; ++i) before(p.ops[i].code);
           }
         } else if constexpr (Prog::heads) {
           // What follows it up to ROTARY: the head's 1 / rms (1 where there is
@@ -1769,6 +1805,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             case GEMM_EPI_OP_ADD_RESIDUAL:
               for_pairs(v, [&](float2 y, int i) { return __fadd2_rn(y, make_float2(x[2 * i], x[2 * i + 1])); });
               packed = false;
+              break;
+            case GEMM_EPI_OP_DROPOUT:
+              if constexpr (Prog::drops) {
+                drop_columns<32>(p.drop, drop_state, static_cast<uint32_t>(row_base + m), col0, v);
+                packed = false;
+              }
               break;
             case GEMM_EPI_OP_MUL_GELU_TANH_GRAD:
               for_pairs(v, [&](float2 y, int i) {

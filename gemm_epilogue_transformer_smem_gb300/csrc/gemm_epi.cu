@@ -105,7 +105,7 @@ struct SpecTable {
 const SpecTable kSpecTables[] = {
     {ge::kSpecsForward, &ge::kNumSpecsForward}, {ge::kSpecsAux, &ge::kNumSpecsAux}, {ge::kSpecsFp8, &ge::kNumSpecsFp8},
     {ge::kSpecsCommon, &ge::kNumSpecsCommon}, {ge::kSpecsRotary, &ge::kNumSpecsRotary},
-    {ge::kSpecsHeadNorm, &ge::kNumSpecsHeadNorm}};
+    {ge::kSpecsHeadNorm, &ge::kNumSpecsHeadNorm}, {ge::kSpecsDropout, &ge::kNumSpecsDropout}};
 constexpr int kNumSpecTables = sizeof(kSpecTables) / sizeof(kSpecTables[0]);
 
 // The interpreting kernels (any program); static ones come from the tables.
@@ -140,6 +140,9 @@ gemm_epi_status device_state(DeviceState** out, int* dev_out) {
       for (int i = 0; i < 6 && e == cudaSuccess; ++i)
         e = cudaFuncSetAttribute(ge::kDynamicHeads[i / 3][i % 3], cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  i % 3 == 1 ? ge::Smem<2>::BYTES : ge::Smem<1>::BYTES);
+      for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+        e = cudaFuncSetAttribute(ge::kDynamicDrop[i / 2][i % 2], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 i % 2 == 1 ? ge::Smem<2>::BYTES : ge::Smem<1>::BYTES);
       for (int c = 0; c < 2 && e == cudaSuccess; ++c)
         e = cudaFuncSetAttribute(ge::kDynamicFp8[c], cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  c == 0 ? ge::Smem<1>::BYTES : ge::Smem<2>::BYTES);
@@ -300,6 +303,8 @@ struct gemm_epi_plan {
   int head_rms_at = -1, rotary_at = -1;
   float head_eps = 0.0f;
   bool heads() const { return head_rms_at >= 0 || rotary_at >= 0; }
+  bool drops = false;          // DROPOUT
+  int32_t drop_threshold = 0;  // 0: it changes nothing
   float rms_eps = 0.0f;
   int rms_unrounded = 0;
   int64_t num_m_tiles = 0, num_n_tiles = 0;
@@ -336,7 +341,7 @@ gemm_epi_status validate(gemm_epi_plan& P) {
   int seen[32] = {0};  // indexed by op code
   for (int i = 0; i < d.n_ops; ++i) {
     const gemm_epi_op& op = d.ops[i];
-    if (op.code < GEMM_EPI_OP_SCALE_ALPHA || op.code > GEMM_EPI_OP_ROTARY)
+    if (op.code < GEMM_EPI_OP_SCALE_ALPHA || op.code > GEMM_EPI_OP_DROPOUT)
       return fail(GEMM_EPI_ERR_INVALID_VALUE, "op %d: unknown code %d", i, op.code);
     if (is_output_op(op.code) && seen[op.code])
       return fail(GEMM_EPI_ERR_INVALID_VALUE, "op %d: output op %d appears twice", i, op.code);
@@ -353,7 +358,7 @@ gemm_epi_status validate(gemm_epi_plan& P) {
           return fail(GEMM_EPI_ERR_INVALID_VALUE, "DSWIGLU group %d needs N %% %d == 0", g, g);
         if (2 * d.N > 0x7FFFFFFF) return fail(GEMM_EPI_ERR_INVALID_VALUE, "DSWIGLU needs 2N < 2^31");
         for (int j = 0; j < i; ++j)
-          if (!is_pre_pair_op(d.ops[j].code))
+          if (!is_pre_pair_op(d.ops[j].code) && d.ops[j].code != GEMM_EPI_OP_DROPOUT)
             return fail(GEMM_EPI_ERR_UNSUPPORTED, "op %d (code %d) before DSWIGLU is not supported", j,
                         d.ops[j].code);
         for (int j = i + 1; j < d.n_ops; ++j)
@@ -406,6 +411,13 @@ gemm_epi_status validate(gemm_epi_plan& P) {
         if (norm) P.head_eps = op.f0;
         break;
       }
+      case GEMM_EPI_OP_DROPOUT:
+        if (P.drops) return fail(GEMM_EPI_ERR_INVALID_VALUE, "op %d: DROPOUT appears twice", i);
+        if (op.i0 < 0 || op.i0 > 65536)
+          return fail(GEMM_EPI_ERR_INVALID_VALUE, "the DROPOUT threshold must be in [0, 65536] (got %d)", op.i0);
+        P.drops = true;
+        P.drop_threshold = op.i0;
+        break;
       case GEMM_EPI_OP_ROW_RMS_RSQRT:
         if (!(op.f0 >= 0.0f) || !std::isfinite(op.f0))
           return fail(GEMM_EPI_ERR_INVALID_VALUE, "ROW_RMS_RSQRT eps must be finite and >= 0");
@@ -430,6 +442,7 @@ gemm_epi_status validate(gemm_epi_plan& P) {
       default: break;
     }
   }
+  if (P.drops && P.heads()) return fail(GEMM_EPI_ERR_UNSUPPORTED, "DROPOUT with HEAD_RMS or ROTARY");
   if (P.heads()) {
     if (P.pair_at >= 0 || P.expand_at >= 0 || P.uses_residual || P.uses_preact || P.dual)
       return fail(GEMM_EPI_ERR_UNSUPPORTED, "HEAD_RMS and ROTARY go with no pair op, DSWIGLU, GEMM_EPI_B_DUAL or "
@@ -509,6 +522,8 @@ gemm_epi_status validate(gemm_epi_plan& P) {
     if ((P.flags & ge::F_AUX) && bad_stride(d.batch_stride_aux, d.M * d.ld_aux, 8, false))
       return fail(GEMM_EPI_ERR_INVALID_VALUE, "batch_stride_aux must span M x ld_aux, a multiple of 8");
   }
+  if (P.drops && d.M * P.batch > (int64_t(1) << 32))
+    return fail(GEMM_EPI_ERR_INVALID_VALUE, "DROPOUT counts rows in 32 bits: M * batch is above 2^32");
   if (P.num_m_tiles * P.num_n_tiles * P.batch > LIM) return fail(GEMM_EPI_ERR_INVALID_VALUE, "too many tiles");
   // One row counter per 128-row block, counted in whole 256-row tiles so
   // both main-loop shapes fit.
@@ -619,6 +634,8 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
     L.kernel = L.split > 1 ? P.spec->kernel_split : L.cg == 2 ? P.spec->kernel_2sm : P.spec->kernel_1sm;
   else if (P.heads())
     L.kernel = ge::kDynamicHeads[P.in8 ? 1 : 0][L.split > 1 ? 2 : L.cg == 2 ? 1 : 0];
+  else if (P.drops)
+    L.kernel = ge::kDynamicDrop[P.in8 ? 1 : 0][L.cg == 2 ? 1 : 0];
   else if (P.in8)
     L.kernel = ge::kDynamicFp8[L.cg == 2 ? 1 : 0];
   else
@@ -707,6 +724,7 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
     k.positions = a.positions;
     k.positions_64 = a.positions_64 ? 1 : 0;
   }
+  if (P.drops) k.drop = ge::dropout_of(gemm_epi_mask{a.dropout_state, a.dropout_site, P.drop_threshold});
   for (size_t i = 0; i < P.ops.size(); ++i) {
     k.ops[i].code = P.ops[i].code;
     k.ops[i].i0 = P.ops[i].i0;
@@ -788,6 +806,11 @@ gemm_epi_status check_args(const gemm_epi_plan& P, const gemm_epi_args& a) {
     if (P.uses_row_scale && (s = need(a.row_scale, "row_scale"))) return s;
     if (P.uses_residual && (s = need(a.residual, "residual"))) return s;
     if (P.uses_preact && (s = need(a.preact, "preact"))) return s;
+    if (P.drop_threshold > 0) {
+      if (!a.dropout_state) return fail(GEMM_EPI_ERR_INVALID_VALUE, "dropout_state is NULL but the program uses it");
+      if (reinterpret_cast<uintptr_t>(a.dropout_state) & 7u)
+        return fail(GEMM_EPI_ERR_MISALIGNED, "dropout_state must be 8-byte aligned");
+    }
     if (P.rotary_at >= 0) {
       if (!a.rotary_steps) return fail(GEMM_EPI_ERR_INVALID_VALUE, "rotary_steps is NULL but the program uses it");
       if (!aligned16(a.rotary_steps) ||
@@ -917,6 +940,8 @@ gemm_epi_status gemm_epi_run_unfused(gemm_epi_handle h, const gemm_epi_args* arg
   if (h->heads())
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "the separate pass has no HEAD_RMS or ROTARY: run the GEMM and "
                                           "gemm_epi_qk_norm_rotary or gemm_epi_rotary");
+  if (h->drops)
+    return fail(GEMM_EPI_ERR_UNSUPPORTED, "the separate pass has no DROPOUT: run the GEMM and gemm_epi_dropout");
   if (h->expand_at >= 0 && h->expand_g > 4)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "the separate pass handles DSWIGLU groups up to 4");
   DeviceState* dev = nullptr;

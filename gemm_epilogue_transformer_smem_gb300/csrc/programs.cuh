@@ -72,6 +72,18 @@ using ProgRmsRotary = StaticProgram<GEMM_EPI_OP_MUL_ROW_SCALE, GEMM_EPI_OP_ROTAR
 using ProgRmsNormRotary = StaticProgram<GEMM_EPI_OP_MUL_ROW_SCALE, GEMM_EPI_OP_HEAD_RMS, GEMM_EPI_OP_MUL_COL_SCALE,
                                         GEMM_EPI_OP_ROTARY, GEMM_EPI_OP_STORE_BF16>;
 
+// Training with dropout: behind a projection in front of the residual add,
+// behind the activation of a feed-forward layer, and there on the way back.
+using ProgDropResidual = StaticProgram<GEMM_EPI_OP_DROPOUT, GEMM_EPI_OP_ADD_RESIDUAL, GEMM_EPI_OP_STORE_BF16>;
+using ProgBiasDropResidual = StaticProgram<GEMM_EPI_OP_ADD_BIAS_COL, GEMM_EPI_OP_DROPOUT, GEMM_EPI_OP_ADD_RESIDUAL,
+                                           GEMM_EPI_OP_STORE_BF16>;
+using ProgBiasGeluDrop = StaticProgram<GEMM_EPI_OP_ADD_BIAS_COL, GEMM_EPI_OP_ACT_GELU_TANH, GEMM_EPI_OP_DROPOUT,
+                                       GEMM_EPI_OP_STORE_BF16>;
+using ProgDropGeluGradColSum = StaticProgram<GEMM_EPI_OP_DROPOUT, GEMM_EPI_OP_MUL_GELU_TANH_GRAD,
+                                             GEMM_EPI_OP_STORE_BF16, GEMM_EPI_OP_COL_SUM>;
+using ProgSwiGLUDrop = StaticProgram<PAIR_G1, GEMM_EPI_OP_DROPOUT, GEMM_EPI_OP_STORE_BF16>;
+using ProgDropDSwiGLU = StaticProgram<GEMM_EPI_OP_DROPOUT, DSWIGLU_G1, GEMM_EPI_OP_STORE_BF16>;
+
 // One compiled program: its op list (code | pair group << 8), the operand
 // width it was compiled for, its kernels for the 1-SM and 2-SM main loops and
 // its separate-pass kernel for the unfused baseline (NULL if the pass does
@@ -126,6 +138,11 @@ extern const KernelSpec kSpecsRotary[];
 extern const int kNumSpecsRotary;
 extern const KernelSpec kSpecsHeadNorm[];
 extern const int kNumSpecsHeadNorm;
+extern const KernelSpec kSpecsDropout[];
+extern const int kNumSpecsDropout;
+// The interpreting kernels for programs with DROPOUT, for bf16 and 8-bit
+// operands (1-SM, 2-SM).
+extern const void* const kDynamicDrop[2][2];
 // The interpreting kernels for programs with HEAD_RMS or ROTARY, for bf16 and
 // 8-bit operands (1-SM, 2-SM, K split over a cluster).
 extern const void* const kDynamicHeads[2][3];

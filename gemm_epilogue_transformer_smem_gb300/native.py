@@ -66,6 +66,7 @@ GEMM_EPI_OP_MUL_COL_SCALE = 17
 GEMM_EPI_OP_ROW_DOT = 18
 GEMM_EPI_OP_HEAD_RMS = 19
 GEMM_EPI_OP_ROTARY = 20
+GEMM_EPI_OP_DROPOUT = 21
 
 GEMM_EPI_MAX_OPS = 16
 GEMM_EPI_NO_ALLOC_SCRATCH_BYTES = 65536
@@ -116,6 +117,7 @@ class gemm_epi_args(ctypes.Structure):
         ("col_scale", ctypes.c_void_p),
         ("rotary_steps", ctypes.c_void_p), ("positions", ctypes.c_void_p),
         ("positions_64", ctypes.c_int32), ("rotary_amplitude", ctypes.c_float),
+        ("dropout_state", ctypes.c_void_p), ("dropout_site", ctypes.c_uint32),
     ]
 
 

@@ -7,7 +7,7 @@
  * short epilogue program on it: scaling, bias, row scale, residual add,
  * activations, a pairwise SwiGLU on interleaved gate/up columns, the GELU-tanh
  * derivative, AMAX, row RMS statistics, column sums, the norm and rotary
- * positions of a projection's heads, and bf16 / FP8-e4m3
+ * positions of a projection's heads, dropout, and bf16 / FP8-e4m3
  * stores.  Only the program's outputs reach global memory.
  *
  * Where the operations come from (page title, section):
@@ -38,6 +38,10 @@
  *    long contexts (Peng et al., "YaRN": linear, base change, by parts); an RMS
  *    norm of every query and key head before them.  The pages have no
  *    counterpart: these complete the q|k|v projection whose GEMM they cover.
+ *  - dropout with masks drawn from a counter (Salmon et al., "Parallel random
+ *    numbers: as easy as 1, 2, 3") and layer norm (Ba, Kiros, Hinton) between
+ *    the GEMMs of a block.  The pages have no counterpart: these complete the
+ *    training step of the bias, GELU and residual programs.
  *  - create once (validate + plan), then execute with a pack of pointers and
  *    a caller-owned workspace: cuDNN Graph API tutorial, five-step build
  *    paragraph; launches are safe to capture in a CUDA graph (same page, CUDA
@@ -193,7 +197,7 @@ typedef enum gemm_epi_op_code {
                                            ROW_RMS_RSQRT (both write row_out).              */
     GEMM_EPI_OP_HEAD_RMS = 19,          /* columns n < desc.head_cols, in heads of desc.head_dim:
                                            y = y / sqrt(mean of y^2 over the head + f0), f0 = eps */
-    GEMM_EPI_OP_ROTARY = 20             /* the same columns: the first desc.rotary_dim values of
+    GEMM_EPI_OP_ROTARY = 20,            /* the same columns: the first desc.rotary_dim values of
                                            each head rotated in pairs by the row's position, as
                                            gemm_epi_rotary does (args.rotary_steps, positions,
                                            rotary_amplitude).  HEAD_RMS and ROTARY appear at most
@@ -205,6 +209,12 @@ typedef enum gemm_epi_op_code {
                                            for fp32 outputs (AMAX, COL_SUM).  Not with a pair op,
                                            DSWIGLU, GEMM_EPI_B_DUAL or ops reading residual or
                                            preact.                                               */
+    GEMM_EPI_OP_DROPOUT = 21            /* y = D(y): the dropout of gemm_epi_mask with threshold i0 at
+                                           row b M + m and column n, by args.dropout_state and
+                                           dropout_site; b M + m < 2^32.  At most once, on output
+                                           columns or before DSWIGLU (whose forward pass drops
+                                           behind PAIR_SWIGLU), not before a pair op and not with
+                                           HEAD_RMS or ROTARY.                                    */
 } gemm_epi_op_code;
 
 typedef struct gemm_epi_op {
@@ -277,6 +287,8 @@ typedef struct gemm_epi_args {
     const void *positions;    /* ROTARY: device int32 / int64, M values per batch; NULL: row m is at position m */
     int32_t positions_64;     /* 1: int64 positions */
     float rotary_amplitude;   /* ROTARY: factor of the rotated part, usually 1 */
+    const uint64_t *dropout_state; /* DROPOUT: device, 8-byte aligned: seed, step (gemm_epi_mask) */
+    uint32_t dropout_site;    /* DROPOUT: which of the step's masks */
 } gemm_epi_args;
 
 /* Test hook: the first CTA's producer skips the operand loads of the first
