@@ -160,7 +160,7 @@ class Plan:
     head size and layout (head_dim alone is enough without the rotary op), and
     run() takes the rows' positions.
 
-    Programs with dropout: `dropout` holds the probability and the state, run()
+    Programs with dropout: `dropout` holds the probability, seed and step, run()
     takes the call's site; rows are counted through the batch."""
 
     def __init__(self, M: int, N_: int, K: int, program: Sequence[str], b_layout: str = "kn",
@@ -267,13 +267,14 @@ class Plan:
         elif positions is not None:
             raise ValueError("positions: the plan has no rotary")
         if self.dropout is not None:
-            index = self.dropout._state.get_device()
+            step = self.dropout._step
+            index = step.get_device()
             for name, t in (("A", A), ("the workspace", workspace)):
                 if t is not None and index != t.get_device():
-                    raise ValueError("the dropout state is on %s, %s on %s" % (self.dropout._state.device, name, t.device))
+                    raise ValueError("the dropout step is on %s, %s on %s" % (step.device, name, t.device))
             if not 0 <= site < 2 ** 32:
                 raise ValueError("site must be in [0, 2^32), got %r" % (site,))
-            a.dropout_state, a.dropout_site = self.dropout._state.data_ptr(), site
+            a.dropout_step, a.dropout_seed, a.dropout_site = step.data_ptr(), self.dropout.seed, site
         elif site:
             raise ValueError("site: the plan has no dropout")
         return a
@@ -649,8 +650,8 @@ def qk_norm_rotary_backward(dyq, dyk, q, k, rope: Rotary, positions=None, *, q_w
 
 
 class Dropout:
-    """A dropout probability and the state its masks are drawn from: a seed and
-    a step in device memory, kept for every call.
+    """A dropout probability, the seed its masks are drawn from and the step,
+    which lies in device memory.
 
     p is rounded to a multiple of 2^-16; what stays is scaled by the inverse of
     the share that stays, so that means are kept.  The mask of a call depends on
@@ -667,36 +668,37 @@ class Dropout:
             raise ValueError("seed must be in [0, 2^64) and step in [0, 2^63), got %r and %r" % (seed, step))
         self.p = float(p)
         self.threshold = round(self.p * 65536)
-        # the seed's 64 bits in an int64 tensor, as Rotary.steps
-        self.state = torch.tensor([seed - 2 ** 64 if seed >= 2 ** 63 else seed, step], dtype=torch.int64).to(device)
+        self.seed = int(seed)
+        self.step = torch.tensor([step], dtype=torch.int64).to(device)
 
     @property
-    def state(self) -> torch.Tensor:
-        """The device's seed and step, as two int64; another tensor of that
-        type may be put in their place, or they may be written to."""
-        return self._state
+    def step(self) -> torch.Tensor:
+        """The device's step, one int64, of which the masks take the low 32 bits;
+        it may be written to, or another tensor put in its place (one that
+        several share, say)."""
+        return self._step
 
-    @state.setter
-    def state(self, t: torch.Tensor) -> None:
-        # checked here, once, so that no call has to: the kernels read both
-        if t.dtype is not torch.int64 or t.shape != (2,) or not t.is_contiguous():
-            raise ValueError("state: expected 2 contiguous int64 values, got %s %s" % (t.dtype, tuple(t.shape)))
-        self._state = t
+    @step.setter
+    def step(self, t: torch.Tensor) -> None:
+        # checked here, once, so that no call has to: the kernels read it
+        if t.dtype is not torch.int64 or t.shape != (1,):
+            raise ValueError("step: expected 1 int64 value, got %s %s" % (t.dtype, tuple(t.shape)))
+        self._step = t
 
     def advance(self, steps: int = 1) -> None:
         """The next step's masks: adds to the step in device memory."""
-        self._state[1:].add_(steps)
+        self._step.add_(steps)
 
 
 # Packed in one step, as _QK_ARGS.
-_DROPOUT_ARGS = struct.Struct("@qqiQIiQqQqQq")
-_LAYER_NORM_ARGS = struct.Struct("@qqifQIiQqQqQqQqQQQQ")
-_LAYER_NORM_BWD_ARGS = struct.Struct("@qqiQIiQqQqQqQqQqQQQQQQN")
+_DROPOUT_ARGS = struct.Struct("@qqiQQIiQqQqQq")
+_LAYER_NORM_ARGS = struct.Struct("@qqifQQIiQqQqQqQqQQQQ")
+_LAYER_NORM_BWD_ARGS = struct.Struct("@qqiQQIiQqQqQqQqQqQQQQQQN")
 assert _DROPOUT_ARGS.size == ctypes.sizeof(N.gemm_epi_dropout_args)
 assert _LAYER_NORM_ARGS.size == ctypes.sizeof(N.gemm_epi_layer_norm_args)
 assert _LAYER_NORM_BWD_ARGS.size == ctypes.sizeof(N.gemm_epi_layer_norm_bwd_args)
 _NO_ROWS = (0, 0)
-_NO_MASK = (0, 0, 0)
+_NO_MASK = (0, 0, 0, 0)
 
 
 def _first_rows(name: str, t: torch.Tensor):
@@ -757,15 +759,15 @@ def _values(name: str, t: torch.Tensor, n: int, index: int) -> int:
 
 
 def _mask(rng: Optional[Dropout], site: int, index: int):
-    """(state, site, threshold) of a gemm_epi_mask."""
+    """(step, seed, site, threshold) of a gemm_epi_mask."""
     if rng is None or rng.threshold == 0:
         return _NO_MASK
-    state = rng._state
-    if state.get_device() != index:
-        raise ValueError("the dropout state is on %s, not with the other tensors" % state.device)
+    step = rng._step
+    if step.get_device() != index:
+        raise ValueError("the dropout step is on %s, not with the other tensors" % step.device)
     if not 0 <= site < 2 ** 32:
         raise ValueError("site must be in [0, 2^32), got %r" % (site,))
-    return state.data_ptr(), site, rng.threshold
+    return step.data_ptr(), rng.seed, site, rng.threshold
 
 
 def _call_packed(entry: str, packed: bytes, first: torch.Tensor, stream) -> None:

@@ -679,15 +679,17 @@ __device__ __forceinline__ void apply_pointwise(CodeT code, float (&v)[NV], cons
 // DROPOUT on NV columns of a row from column col0, a multiple of 8: the mask
 // gemm_epi_dropout draws for that place of the stored matrix.
 template <int NV>
-__device__ __forceinline__ void drop_columns(const Dropout& d, const DropKey& key, uint32_t row, int col0, float (&v)[NV]) {
-  if (d.state == nullptr) return;  // nothing is dropped
+__device__ __forceinline__ void drop_columns(const Dropout& d, uint32_t step, uint32_t row, int col0, float (&v)[NV]) {
+  if (d.step == nullptr) return;  // nothing is dropped
+  constexpr int G = NV / 8;
+  uint32_t rows[G], groups[G], w[G][4];
 #pragma unroll
-  for (int g = 0; g < NV / 8; ++g) {
-    uint32_t w[4];
-    drop_words(key, row, static_cast<uint32_t>(col0 / 8 + g), w);
+  for (int g = 0; g < G; ++g) rows[g] = row, groups[g] = static_cast<uint32_t>(col0 / 8 + g);
+  drop_words(d, step, rows, groups, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[8 * g + j] = drop_keeps(w, j, d.above) ? v[8 * g + j] * d.scale : 0.0f;
-  }
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[8 * g + j] = drop_keeps(w[g], j, d.above) ? v[8 * g + j] * d.scale : 0.0f;
 }
 
 // out[j] = silu(a[gate(j)]) * a[up(j)] (SwiGLU) or a[gate(j)] * a[up(j)]
@@ -1234,9 +1236,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int op_begin = Prog::heads ? max(head_rms_at, rotary_at) + 1
                                      : paired ? pair_at + 1 : expand ? expand_at + 1 : 0;
 
-    DropKey drop_state{};
+    uint32_t dropout_step = 0;
     if constexpr (Prog::drops) {
-      if (p.drop.state != nullptr) drop_state = drop_key(p.drop);
+      if (p.drop.step != nullptr) dropout_step = drop_step(p.drop);
     }
 
     float amax_f = 0.0f;  // max |y| so far; a NaN sticks (NaN wins, as in the integer maximum below)
@@ -1612,7 +1614,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           auto before = [&](auto code) {
             if (Prog::drops && static_cast<int>(code) == GEMM_EPI_OP_DROPOUT)
-              drop_columns<16>(p.drop, drop_state, static_cast<uint32_t>(row_base + m), nacc0 + c * 16, dh);
+              drop_columns<16>(p.drop, dropout_step, static_cast<uint32_t>(row_base + m), nacc0 + c * 16, dh);
             else
               apply_pointwise<16>(code, dh, p, nacc0 + c * 16, p.N, rs_m);
           };
@@ -1808,7 +1810,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               break;
             case GEMM_EPI_OP_DROPOUT:
               if constexpr (Prog::drops) {
-                drop_columns<32>(p.drop, drop_state, static_cast<uint32_t>(row_base + m), col0, v);
+                drop_columns<32>(p.drop, dropout_step, static_cast<uint32_t>(row_base + m), col0, v);
                 packed = false;
               }
               break;

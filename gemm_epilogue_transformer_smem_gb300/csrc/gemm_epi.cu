@@ -724,7 +724,7 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
     k.positions = a.positions;
     k.positions_64 = a.positions_64 ? 1 : 0;
   }
-  if (P.drops) k.drop = ge::dropout_of(gemm_epi_mask{a.dropout_state, a.dropout_site, P.drop_threshold});
+  if (P.drops) k.drop = ge::dropout_of(gemm_epi_mask{a.dropout_step, a.dropout_seed, a.dropout_site, P.drop_threshold});
   for (size_t i = 0; i < P.ops.size(); ++i) {
     k.ops[i].code = P.ops[i].code;
     k.ops[i].i0 = P.ops[i].i0;
@@ -807,9 +807,9 @@ gemm_epi_status check_args(const gemm_epi_plan& P, const gemm_epi_args& a) {
     if (P.uses_residual && (s = need(a.residual, "residual"))) return s;
     if (P.uses_preact && (s = need(a.preact, "preact"))) return s;
     if (P.drop_threshold > 0) {
-      if (!a.dropout_state) return fail(GEMM_EPI_ERR_INVALID_VALUE, "dropout_state is NULL but the program uses it");
-      if (reinterpret_cast<uintptr_t>(a.dropout_state) & 7u)
-        return fail(GEMM_EPI_ERR_MISALIGNED, "dropout_state must be 8-byte aligned");
+      if (!a.dropout_step) return fail(GEMM_EPI_ERR_INVALID_VALUE, "dropout_step is NULL but the program uses it");
+      if (reinterpret_cast<uintptr_t>(a.dropout_step) & 7u)
+        return fail(GEMM_EPI_ERR_MISALIGNED, "dropout_step must be 8-byte aligned");
     }
     if (P.rotary_at >= 0) {
       if (!a.rotary_steps) return fail(GEMM_EPI_ERR_INVALID_VALUE, "rotary_steps is NULL but the program uses it");

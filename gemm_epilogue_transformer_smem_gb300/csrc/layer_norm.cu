@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "host.h"
 #include "layer_norm.cuh"
@@ -13,88 +14,157 @@ namespace {
 using ge_host::cuda_fail;
 using ge_host::fail;
 
-enum Pass { FORWARD = 0, BACKWARD = 1 };
-
 // ---------------------------------------------------------------- kernels
 
-// How a row's groups of 8 columns are dealt out.
-struct Shape {
-  int k;          // groups per thread
-  int log_lanes;  // teams within a warp: threads of a team
-  int threads;    // of a block
-  bool block;     // the team is the block
-  bool wide_row;  // too wide to hold: the re-reading kernels
+// The kernels of a pass, by what they are compiled for.
+struct Kernel {
+  void (*fn)(ge::NormParams);
+  int warp_bytes;  // dynamic shared memory of a warp
 };
 
-Shape shape_of(int pass, int groups) {
-  Shape s{1, 5, 32 * ge::LN_WARP_TEAMS, false, false};
+enum Form { NARROW, HELD, LONG };  // teams within a warp; rows held by warps; rows read again
+
+// How a row is dealt out and by what kernel.
+struct Shape {
+  Form form;
+  int k;          // HELD: pieces of 256 columns per warp
+  int warps;      // of a team
+  int teams;      // of a block
+  int log_lanes;  // NARROW: of a team
+  int rows;       // a team works on at once
+  bool staged;    // HELD: weights through shared memory
+  int index() const { return form == HELD ? k : form == NARROW ? 0 : 9; }
+};
+
+template <class T, bool DROP, bool ADD, int K, int R, bool WIDE>
+Kernel held_forward() {
+  return {ge::layer_norm_kernel<T, DROP, ADD, K, R, WIDE>, ge::RowRing<T, K, ADD ? 2 : 1, R>::WARP_BYTES};
+}
+
+template <class T, bool DROP, bool ADD>
+Kernel held_forward(const Shape& s, bool wide) {
+  if (!wide) return held_forward<T, DROP, ADD, 4, 1, false>();
+  constexpr int TWICE = sizeof(T) == 2 ? 2 : 1;  // as many bytes of rows for either type
+  if (s.k == 2) return s.rows == 1 ? held_forward<T, DROP, ADD, 2, 1, true>() : held_forward<T, DROP, ADD, 2, 2 * TWICE, true>();
+  return s.k == 3 ? held_forward<T, DROP, ADD, 3, TWICE, true>() : held_forward<T, DROP, ADD, 4, TWICE, true>();
+}
+
+template <class T, bool DROP, bool ADD, bool WIDE, int... Ks>
+Kernel held_backward(int k) {
+  Kernel r{nullptr, 0};
+  ((k == Ks ? void(r = {ge::layer_norm_backward_kernel<T, DROP, ADD, Ks, WIDE>,
+                        ge::RowRing<T, Ks, ADD ? 3 : 2, ge::LN_BACKWARD_DEPTH<T>>::WARP_BYTES})
+            : void()), ...);
+  return r;
+}
+
+// What the kernels of either pass are chosen by.
+struct Choice {
+  bool f32, drop, add, wide;
+  int index() const { return f32 | drop << 1 | add << 2 | wide << 3; }
+};
+
+struct Forward {
+  template <class T, bool DROP>
+  static Kernel of(const Shape& s, const Choice& c) {
+    if (s.form == NARROW)
+      return {c.wide ? ge::layer_norm_narrow_kernel<T, DROP, true> : ge::layer_norm_narrow_kernel<T, DROP, false>,
+              ge::NarrowRows<T, ge::LN_NARROW_ROWS<T>, 2>::WARP_BYTES};
+    if (s.form == LONG)
+      return {c.wide ? ge::layer_norm_long_kernel<T, DROP, true> : ge::layer_norm_long_kernel<T, DROP, false>, 0};
+    if (DROP || c.add) return held_forward<T, DROP, true>(s, c.wide);  // dropout alone adds zeros
+    return held_forward<T, false, false>(s, c.wide);
+  }
+};
+
+struct Backward {
+  template <class T, bool DROP>
+  static Kernel of(const Shape& s, const Choice& c) {
+    if (s.form == NARROW)
+      return {c.wide ? ge::layer_norm_backward_narrow_kernel<T, DROP, true> : ge::layer_norm_backward_narrow_kernel<T, DROP, false>,
+              ge::NarrowRows<T, ge::LN_NARROW_BACKWARD_ROWS<T>, 3>::WARP_BYTES};
+    if (s.form == LONG)
+      return {c.wide ? ge::layer_norm_backward_long_kernel<T, DROP, true> : ge::layer_norm_backward_long_kernel<T, DROP, false>, 0};
+    if (c.add) return c.wide ? held_backward<T, DROP, true, true, 1, 2, 3, 4>(s.k) : held_backward<T, DROP, true, false, 4>(s.k);
+    return c.wide ? held_backward<T, DROP, false, true, 1, 2, 3, 4>(s.k) : held_backward<T, DROP, false, false, 4>(s.k);
+  }
+};
+
+template <class Pass>
+Kernel kernel_of(const Shape& s, const Choice& c) {
+  if (c.f32) return c.drop ? Pass::template of<float, true>(s, c) : Pass::template of<float, false>(s, c);
+  return c.drop ? Pass::template of<uint16_t, true>(s, c) : Pass::template of<uint16_t, false>(s, c);
+}
+
+Shape shape_of(bool backward, int64_t rows, int64_t cols, bool f32, bool wide, int sms) {
+  const bool few = rows <= 2 * sms;
+  Shape s{NARROW, 0, 1, 1, 0, 1, false};
+  const int64_t groups = (cols + 7) / 8, pieces = (cols + ge::LN_PIECE - 1) / ge::LN_PIECE;
   if (groups <= 32) {
-    s.log_lanes = 0;
     while ((1 << s.log_lanes) < groups) ++s.log_lanes;
+    s.rows = backward ? (f32 ? ge::LN_NARROW_BACKWARD_ROWS<float> : ge::LN_NARROW_BACKWARD_ROWS<uint16_t>)
+                      : (f32 ? ge::LN_NARROW_ROWS<float> : ge::LN_NARROW_ROWS<uint16_t>);
+    s.teams = ge::LN_BLOCK_WARPS << (5 - s.log_lanes);
     return s;
   }
-  if (pass == FORWARD && groups <= 128) {
-    s.k = groups <= 64 ? 2 : 4;
+  if (pieces > 4 * ge::LN_MAX_WARPS) {
+    s.form = LONG;
+    s.warps = ge::LN_LONG_THREADS / 32;
     return s;
   }
-  s.block = true;
-  if (groups > ge::LN_MAX_GROUPS) {
-    s.wide_row = true;
-    s.threads = ge::LN_LONG_THREADS;
-    return s;
+  s.form = HELD;
+  auto take = [&](int k) {
+    const int warps = static_cast<int>((pieces + k - 1) / k);
+    if (warps > ge::LN_MAX_WARPS || (s.k && s.k * s.warps <= k * warps)) return;
+    s.k = k;
+    s.warps = warps;
+  };
+  if (!wide) {
+    take(4);
+  } else if (few) {
+    for (int k : {backward ? 1 : 2, backward ? 2 : 4, 4})
+      if (!s.k) take(k);
+  } else {
+    for (int k : {4, 3, 2}) take(k);
   }
-  s.k = pass == BACKWARD && groups <= 256 ? 1 : groups <= 1024 ? 2 : 4;
-  s.threads = 32 * ((groups + 32 * s.k - 1) / (32 * s.k));
+  if (!backward && wide && !(few && s.k == 2)) s.rows = (s.k == 2 ? 4 : 2) / (f32 ? 2 : 1);
+  // a block to every SM before a second team to a block
+  s.teams = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ge::LN_MAX_WARPS / s.warps, rows / (s.rows * sms))));
+  s.staged = wide && !few;  // pays where a team has several rows
   return s;
 }
 
-struct Kernel {
-  void (*fn)(ge::NormParams);
-  int ring_bytes;
-};
+int block_warps(const Shape& s) { return s.form == NARROW ? ge::LN_BLOCK_WARPS : s.warps * s.teams; }
 
-template <class T, bool DROP, int K, bool BLOCK>
-Kernel kernel_of(int pass, int threads) {
-  if (pass == FORWARD) return {ge::layer_norm_kernel<T, DROP, K, BLOCK>, ge::RowRing<T, K, 2>::bytes(threads)};
-  if constexpr (BLOCK || K == 1)
-    return {ge::layer_norm_backward_kernel<T, DROP, K, BLOCK>, ge::RowRing<T, K, 3>::bytes(threads)};
-  else
-    return {nullptr, 0};
+// The ring, and behind it the weights.
+size_t shared_bytes(bool backward, const Shape& s, const Kernel& k) {
+  return static_cast<size_t>(k.warp_bytes) * block_warps(s) +
+         (s.staged ? static_cast<size_t>(backward ? 1 : 2) * s.warps * s.k * ge::LN_PIECE * sizeof(float) : 0);
 }
 
-template <class T, bool DROP>
-Kernel kernel_of(int pass, const Shape& s) {
-  if (s.wide_row)
-    return {pass == FORWARD ? ge::layer_norm_long_kernel<T, DROP> : ge::layer_norm_backward_long_kernel<T, DROP>, 0};
-  if (s.block) {
-    if (s.k == 1 && pass == BACKWARD)
-      return {ge::layer_norm_backward_kernel<T, DROP, 1, true>, ge::RowRing<T, 1, 3>::bytes(s.threads)};
-    return s.k == 2 ? kernel_of<T, DROP, 2, true>(pass, s.threads) : kernel_of<T, DROP, 4, true>(pass, s.threads);
-  }
-  return s.k == 1   ? kernel_of<T, DROP, 1, false>(pass, s.threads)
-         : s.k == 2 ? kernel_of<T, DROP, 2, false>(pass, s.threads)
-                    : kernel_of<T, DROP, 4, false>(pass, s.threads);
-}
-
-Kernel kernel_of(int pass, const Shape& s, bool f32, bool drop) {
-  if (f32) return drop ? kernel_of<float, true>(pass, s) : kernel_of<float, false>(pass, s);
-  return drop ? kernel_of<uint16_t, true>(pass, s) : kernel_of<uint16_t, false>(pass, s);
+// Fewer teams where a block's rings need that; the weights only where there is
+// room beside them.
+void fit_shared(bool backward, Shape& s, const Kernel& k) {
+  if (shared_bytes(backward, s, k) > ge::LN_MAX_SHARED) s.staged = false;
+  while (s.teams > 1 && shared_bytes(backward, s, k) > ge::LN_MAX_SHARED) --s.teams;
 }
 
 // Blocks of a kernel resident on an SM of the current device, asked for once
-// for each kernel and block size (the shared memory goes with the size).
-gemm_epi_status resident_blocks(int dev, int pass, const Shape& s, bool f32, bool drop, const Kernel& k, int* blocks) {
-  static std::atomic<int> known[128][2][2][2][8][ge::LN_MAX_WARPS + 1];
-  const int form = s.wide_row ? 7 : (s.block ? 4 : 0) + (s.k == 4 ? 2 : s.k - 1);
-  std::atomic<int>& at = known[dev][pass][f32][drop][form][s.threads / 32];
+// for each kernel and team size (block size and shared memory go with them).
+gemm_epi_status resident_blocks(int dev, bool backward, const Shape& s, const Choice& c, const Kernel& k, int* blocks) {
+  static std::atomic<int> known[128][2][16][10][ge::LN_MAX_WARPS + 1][ge::LN_MAX_WARPS + 1][2];
+  std::atomic<int>& at = known[dev][backward][c.index()][s.index()][s.warps][block_warps(s) / s.warps][s.rows > 1];
   int n = at.load(std::memory_order_acquire);
   if (n == 0) {
     const void* fn = reinterpret_cast<const void*>(k.fn);
-    // the most that any block size needs, so that no other thread's call lowers it
-    const int most = k.ring_bytes / s.threads * (s.block ? 32 * ge::LN_MAX_WARPS : s.threads);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    // the most that a block may take, so that no other thread's call lowers it
+    cudaError_t e = cudaSuccess;
+    if (s.form != LONG)
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               s.form == HELD ? ge::LN_MAX_SHARED : static_cast<int>(shared_bytes(backward, s, k)));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, s.threads, static_cast<size_t>(k.ring_bytes));
+    const int warps = block_warps(s);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, 32 * warps, shared_bytes(backward, s, k));
     if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
     if (n < 1) return fail(GEMM_EPI_ERR_CUDA, "a layer norm kernel does not fit an SM");
     at.store(n, std::memory_order_release);
@@ -161,28 +231,34 @@ gemm_epi_status check_mask(const gemm_epi_mask& d, ge::Dropout* out) {
   if (d.threshold < 0 || d.threshold > 65536)
     return fail(GEMM_EPI_ERR_INVALID_VALUE, "the dropout threshold must be in [0, 65536] (got %d)", d.threshold);
   if (d.threshold == 0) return GEMM_EPI_OK;
-  if (!d.state) return fail(GEMM_EPI_ERR_INVALID_VALUE, "the dropout state is NULL");
-  if (!aligned(d.state, 8)) return fail(GEMM_EPI_ERR_MISALIGNED, "the dropout state must be 8-byte aligned");
+  if (!d.step) return fail(GEMM_EPI_ERR_INVALID_VALUE, "the dropout step is NULL");
+  if (!aligned(d.step, 8)) return fail(GEMM_EPI_ERR_MISALIGNED, "the dropout step must be 8-byte aligned");
   *out = ge::dropout_of(d);
   return GEMM_EPI_OK;
 }
 
 // ---------------------------------------------------------------- launches
 
-gemm_epi_status launch_norm(int pass, const ge::NormParams& p, bool f32, int64_t most_blocks, cudaStream_t st, int* grid) {
+template <class Pass>
+gemm_epi_status launch_norm(ge::NormParams& p, Choice c, int64_t most_blocks, cudaStream_t st, int* grid) {
+  constexpr bool backward = std::is_same<Pass, Backward>::value;
   int dev = 0, sms = 0, resident = 0;
   gemm_epi_status s = ge_host::device_sms(&dev, &sms);
   if (s) return s;
-  const Shape shape = shape_of(pass, p.groups);
-  const bool drop = p.drop.state != nullptr;
-  const Kernel k = kernel_of(pass, shape, f32, drop);
-  if ((s = resident_blocks(dev, pass, shape, f32, drop, k, &resident))) return s;
-  const int64_t rows = shape.block ? 1 : static_cast<int64_t>(ge::LN_WARP_TEAMS) << (5 - shape.log_lanes);  // of a block
+  c.drop = p.drop.step != nullptr;
+  c.add = backward ? p.add != nullptr : p.other != nullptr;
+  Shape shape = shape_of(backward, p.M, p.N, c.f32, c.wide, sms);
+  const Kernel k = kernel_of<Pass>(shape, c);
+  if (shape.form == HELD) fit_shared(backward, shape, k);
+  if ((s = resident_blocks(dev, backward, shape, c, k, &resident))) return s;
+  const int64_t rows = static_cast<int64_t>(shape.teams) * shape.rows;  // a block works on at once
   int64_t blocks = std::min<int64_t>((p.M + rows - 1) / rows, static_cast<int64_t>(sms) * resident);
   blocks = std::min(blocks, most_blocks);
-  ge::NormParams q = p;
-  q.log_lanes = shape.log_lanes;
-  k.fn<<<static_cast<unsigned>(blocks), static_cast<unsigned>(shape.threads), static_cast<size_t>(k.ring_bytes), st>>>(q);
+  p.warps = shape.warps;
+  p.log_lanes = shape.log_lanes;
+  p.staged = shape.staged;
+  const int warps = block_warps(shape);
+  k.fn<<<static_cast<unsigned>(blocks), static_cast<unsigned>(32 * warps), shared_bytes(backward, shape, k), st>>>(p);
   const cudaError_t e = cudaGetLastError();
   *grid = static_cast<int>(blocks);
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the layer norm kernel");
@@ -267,10 +343,9 @@ gemm_epi_status gemm_epi_layer_norm(const gemm_epi_layer_norm_args* a, void* str
   p.w = a->w, p.b = a->b;
   p.mean = a->mean, p.rstd = a->rstd;
   p.eps = a->eps;
-  p.wide_in = c.wide_in, p.wide_out = c.wide_out;
-  p.wide_w = aligned(a->w, 16) && aligned(a->b, 16);
+  const Choice choice{c.size == 4, false, false, c.wide_in && c.wide_out && aligned(a->w, 16) && aligned(a->b, 16)};
   int grid = 0;
-  return launch_norm(FORWARD, p, c.size == 4, LIM, static_cast<cudaStream_t>(stream), &grid);
+  return launch_norm<Forward>(p, choice, LIM, static_cast<cudaStream_t>(stream), &grid);
 }
 
 gemm_epi_status gemm_epi_layer_norm_backward(const gemm_epi_layer_norm_bwd_args* a, void* stream) {
@@ -324,10 +399,9 @@ gemm_epi_status gemm_epi_layer_norm_backward(const gemm_epi_layer_norm_bwd_args*
   p.w = a->w;
   p.mean = const_cast<float*>(a->mean), p.rstd = const_cast<float*>(a->rstd);
   p.partials = wants_dw ? static_cast<float*>(a->workspace) : nullptr;
-  p.wide_in = c.wide_in, p.wide_out = c.wide_out;
-  p.wide_w = aligned(a->w, 16);
+  const Choice choice{c.size == 4, false, false, c.wide_in && c.wide_out && aligned(a->w, 16)};
   int grid = 0;
-  if ((s = launch_norm(BACKWARD, p, c.size == 4, most_partials(c.N), st, &grid))) return s;
+  if ((s = launch_norm<Backward>(p, choice, most_partials(c.N), st, &grid))) return s;
   if (!wants_dw) return GEMM_EPI_OK;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);

@@ -117,7 +117,7 @@ class gemm_epi_args(ctypes.Structure):
         ("col_scale", ctypes.c_void_p),
         ("rotary_steps", ctypes.c_void_p), ("positions", ctypes.c_void_p),
         ("positions_64", ctypes.c_int32), ("rotary_amplitude", ctypes.c_float),
-        ("dropout_state", ctypes.c_void_p), ("dropout_site", ctypes.c_uint32),
+        ("dropout_step", ctypes.c_void_p), ("dropout_seed", ctypes.c_uint64), ("dropout_site", ctypes.c_uint32),
     ]
 
 
@@ -166,7 +166,8 @@ class gemm_epi_qk_args(ctypes.Structure):
 
 
 class gemm_epi_mask(ctypes.Structure):
-    _fields_ = [("state", ctypes.c_void_p), ("site", ctypes.c_uint32), ("threshold", ctypes.c_int32)]
+    _fields_ = [("step", ctypes.c_void_p), ("seed", ctypes.c_uint64), ("site", ctypes.c_uint32),
+                ("threshold", ctypes.c_int32)]
 
 
 class gemm_epi_dropout_args(ctypes.Structure):

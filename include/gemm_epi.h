@@ -210,8 +210,8 @@ typedef enum gemm_epi_op_code {
                                            DSWIGLU, GEMM_EPI_B_DUAL or ops reading residual or
                                            preact.                                               */
     GEMM_EPI_OP_DROPOUT = 21            /* y = D(y): the dropout of gemm_epi_mask with threshold i0 at
-                                           row b M + m and column n, by args.dropout_state and
-                                           dropout_site; b M + m < 2^32.  At most once, on output
+                                           row b M + m and column n, by args.dropout_step,
+                                           _seed and _site; b M + m < 2^32.  At most once, on output
                                            columns or before DSWIGLU (whose forward pass drops
                                            behind PAIR_SWIGLU), not before a pair op and not with
                                            HEAD_RMS or ROTARY.                                    */
@@ -287,8 +287,9 @@ typedef struct gemm_epi_args {
     const void *positions;    /* ROTARY: device int32 / int64, M values per batch; NULL: row m is at position m */
     int32_t positions_64;     /* 1: int64 positions */
     float rotary_amplitude;   /* ROTARY: factor of the rotated part, usually 1 */
-    const uint64_t *dropout_state; /* DROPOUT: device, 8-byte aligned: seed, step (gemm_epi_mask) */
-    uint32_t dropout_site;    /* DROPOUT: which of the step's masks */
+    const uint64_t *dropout_step;  /* DROPOUT: device, 8-byte aligned: step, seed and site of gemm_epi_mask */
+    uint64_t dropout_seed;
+    uint32_t dropout_site;
 } gemm_epi_args;
 
 /* Test hook: the first CTA's producer skips the operand loads of the first
@@ -516,15 +517,16 @@ GEMM_EPI_API size_t gemm_epi_qk_norm_rotary_workspace_size(int32_t head_dim);
  * numbers: as easy as 1, 2, 3") with the seed as key (low 32 bits first) and the
  * counter (col / 8, row, site, low 32 bits of step), whose eight 16-bit halves,
  * the low half of each word first, go to columns 8 (col / 8) .. + 7.  So a
- * backward pass draws the forward pass's mask by the same state and site, and a
+ * backward pass draws the forward pass's mask by the same seed, step and site, and a
  * program with DROPOUT the same as gemm_epi_dropout on the stored matrix (its
  * rows counted through the batch, b M + m; its columns those where the op acts).
- * The state lies in device memory and is read when the kernel runs, so a
- * captured graph draws new masks once something on the stream (the graph
- * itself, say) has counted `step` on.
+ * The step lies in device memory and is read when the kernel runs, so a captured
+ * graph draws new masks once something on the stream (the graph itself, say) has
+ * counted it on.
  */
 typedef struct gemm_epi_mask {
-    const uint64_t *state;    /* device, 8-byte aligned: seed, step.  Unused with threshold 0 */
+    const uint64_t *step;     /* device, 8-byte aligned; unused with threshold 0 */
+    uint64_t seed;
     uint32_t site;            /* which of a step's masks: one for each place that drops */
     int32_t threshold;        /* probability of being dropped, times 65536: 0 (no dropout) to 65536 */
 } gemm_epi_mask;
@@ -584,7 +586,7 @@ typedef struct gemm_epi_layer_norm_bwd_args {
 
 /* Each enqueues its kernels on `stream`: asynchronous, capture-safe, checks
  * sizes, pointers and alignment first, allocates nothing.  The same call with
- * the same state gives the same bits every time. */
+ * the same step gives the same bits every time. */
 GEMM_EPI_API gemm_epi_status gemm_epi_dropout(const gemm_epi_dropout_args *args, void *stream);
 GEMM_EPI_API gemm_epi_status gemm_epi_layer_norm(const gemm_epi_layer_norm_args *args, void *stream);
 GEMM_EPI_API gemm_epi_status gemm_epi_layer_norm_backward(const gemm_epi_layer_norm_bwd_args *args, void *stream);

@@ -52,8 +52,7 @@ class Mask:
         if rng is None or rng.threshold == 0:
             self.keep, self.scale = torch.ones(rows, cols, dtype=torch.bool), 1.0
             return
-        seed, step = (int(v) % 2 ** 64 for v in rng.state.tolist())
-        self.keep = kept(rows, cols, rng.threshold, seed, step, site, row0)
+        self.keep = kept(rows, cols, rng.threshold, rng.seed, int(rng.step), site, row0)
         self.scale = 65536.0 / (65536 - rng.threshold) if rng.threshold < 65536 else 0.0
 
     def __call__(self, x):

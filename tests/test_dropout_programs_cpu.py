@@ -78,7 +78,7 @@ def test_site_without_dropout(lib):
         plan(program=["store_bf16"]).args(None, None, site=1)
 
 
-def test_state_must_be_there_and_aligned(lib):
+def test_step_must_be_there_and_aligned(lib):
     if torch.cuda.is_available():
         pytest.skip("the pointers here are not device memory")
     buf = torch.zeros(65536, dtype=torch.uint8)
@@ -90,9 +90,9 @@ def test_state_must_be_there_and_aligned(lib):
     a.workspace, a.workspace_bytes = base + 16384, 32768
     run = lambda: lib.gemm_epi_run(p.handle, ctypes.byref(a), None)  # noqa: E731
     assert run() in (N.GEMM_EPI_ERR_CUDA, N.GEMM_EPI_ERR_ARCH)
-    a.dropout_state += 4
+    a.dropout_step += 4
     assert run() == N.GEMM_EPI_ERR_MISALIGNED
-    a.dropout_state = None
+    a.dropout_step = None
     assert run() == N.GEMM_EPI_ERR_INVALID_VALUE
     q = plan(0.0)
     assert lib.gemm_epi_run(q.handle, ctypes.byref(a), None) in (N.GEMM_EPI_ERR_CUDA, N.GEMM_EPI_ERR_ARCH)

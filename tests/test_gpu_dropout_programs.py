@@ -216,7 +216,7 @@ def test_without_a_workspace_of_the_callers(cuda_lib):
 
 
 def test_captured_and_replayed():
-    """Each replay draws the mask of its step: the state is read when the kernel runs."""
+    """Each replay draws the mask of its step: the step is read when the kernel runs."""
     p = Problem(("bias", "dropout", "store_bf16"), 200, 264, 64)
     plan = api.Plan(p.m, p.n, p.k, p.program, dropout=p.rng, **p.kw)
     o = api.allocate_outputs(plan, DEV)
@@ -227,7 +227,7 @@ def test_captured_and_replayed():
         call()
         want.append(o.C.clone())
         p.rng.advance()
-    p.rng.state[1] = 9
+    p.rng.step[0] = 9
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):

@@ -264,23 +264,23 @@ def test_captured_and_replayed():
     rows, cols = 70, 1032
     run, (x, *_), rng = all_outputs(rows, cols, BF, gen(6))
     bufs = [torch.empty_like(x) for _ in range(4)]
-    rng.state[1] = 5
+    rng.step[0] = 5
     want = []
     for _ in range(3):
         want.append([t.clone() for t in run(*bufs)])
         rng.advance()
     assert not torch.equal(want[0][1], want[1][1])
-    rng.state[1] = 5
+    rng.step[0] = 5
     graph = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(graph):
         got = run(*bufs)
         rng.advance()
-    assert int(rng.state[1]) == 5
+    assert int(rng.step) == 5
     for step in range(3):
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(got, want[step])), step
-    assert int(rng.state[1]) == 8
+    assert int(rng.step) == 8
 
 
 def test_first_call_inside_a_capture():

@@ -79,7 +79,7 @@ def dropout_args(**kw):
     a._keep = buf
     a.M, a.N, a.type = 4, 24, N.GEMM_EPI_TYPE_BF16
     a.x, a.ld_x, a.residual, a.ld_residual, a.y, a.ld_y = at, 24, at + 1024, 24, at + 2048, 24
-    a.mask.state, a.mask.threshold = at + 4096, 6554
+    a.mask.step, a.mask.threshold = at + 4096, 6554
     return fill(a, kw, at)
 
 
@@ -90,7 +90,7 @@ def norm_args(**kw):
     a.M, a.N, a.type, a.eps = 4, 24, N.GEMM_EPI_TYPE_BF16, 1e-5
     a.x, a.ld_x, a.residual, a.ld_residual, a.y, a.ld_y = at, 24, at + 1024, 24, at + 2048, 24
     a.sum, a.ld_sum, a.w, a.b, a.mean, a.rstd = at + 3072, 24, at + 5000, at + 5200, at + 5400, at + 5600
-    a.mask.state, a.mask.threshold = at + 4096, 6554
+    a.mask.step, a.mask.threshold = at + 4096, 6554
     return fill(a, kw, at)
 
 
@@ -103,7 +103,7 @@ def backward_args(**kw):
     a.dx, a.ld_dx, a.d_residual, a.ld_d_residual = at + 3072, 24, at + 6144, 24
     a.w, a.mean, a.rstd, a.dw, a.db = at + 5000, at + 5200, at + 5400, at + 5600, at + 5800
     a.workspace, a.workspace_bytes = at + 8192, N.load().gemm_epi_layer_norm_backward_workspace_size(24)
-    a.mask.state, a.mask.threshold = at + 4096, 6554
+    a.mask.step, a.mask.threshold = at + 4096, 6554
     return fill(a, kw, at)
 
 
@@ -112,7 +112,7 @@ def fill(a, kw, at):
         if isinstance(v, str):  # another tensor's address, or one shifted from the tensor's own
             v = getattr(a, name) + int(v) if v[0] in "+-" else getattr(a, v)
         target = a
-        if name in ("state", "site", "threshold"):
+        if name in ("step", "site", "threshold"):
             target = a.mask
         setattr(target, name, v)
     return a
@@ -123,8 +123,8 @@ ENTRIES = {"gemm_epi_dropout": dropout_args, "gemm_epi_layer_norm": norm_args,
 BOTH = [
     (dict(), TAKEN), (dict(M=0), TAKEN), (dict(M=-1), INVALID), (dict(M=2 ** 31), INVALID), (dict(N=0), INVALID),
     (dict(N=2 ** 31 - 7), INVALID), (dict(N=-5), INVALID), (dict(type=N.GEMM_EPI_TYPE_E4M3), UNSUPPORTED),
-    (dict(threshold=0, state=None), TAKEN), (dict(threshold=65536), TAKEN), (dict(threshold=65537), INVALID),
-    (dict(threshold=-1), INVALID), (dict(state=None), INVALID), (dict(x=None), INVALID), (dict(x="+1"), MISALIGNED),
+    (dict(threshold=0, step=None), TAKEN), (dict(threshold=65536), TAKEN), (dict(threshold=65537), INVALID),
+    (dict(threshold=-1), INVALID), (dict(step=None), INVALID), (dict(x=None), INVALID), (dict(x="+1"), MISALIGNED),
     (dict(x="+2"), TAKEN), (dict(ld_x=0), TAKEN), (dict(ld_x=1), TAKEN), (dict(ld_x=-24), INVALID),
     (dict(ld_x=2 ** 40 + 1), INVALID),
 ]
@@ -191,14 +191,14 @@ def test_dropout_object_refuses(kw):
 
 def test_dropout_object():
     d = api.Dropout(0.1, seed=2 ** 64 - 1, step=2 ** 40, device="cpu")
-    assert d.threshold == 6554 and d.state.tolist() == [-1, 2 ** 40]
+    assert d.threshold == 6554 and d.seed == 2 ** 64 - 1 and int(d.step) == 2 ** 40
     d.advance()
     d.advance(3)
-    assert d.state.tolist() == [-1, 2 ** 40 + 4]
-    d.state = torch.tensor([1, 2])
-    for bad in (torch.zeros(2), torch.zeros(3, dtype=torch.int64), torch.zeros(4, dtype=torch.int64)[::2]):
+    assert int(d.step) == 2 ** 40 + 4
+    d.step = torch.tensor([1])
+    for bad in (torch.zeros(1), torch.zeros(2, dtype=torch.int64), torch.zeros((), dtype=torch.int64)):
         with pytest.raises(ValueError):
-            d.state = bad
+            d.step = bad
     assert api.Dropout(1e-6, device="cpu").threshold == 0 and api.Dropout(1.0, device="cpu").threshold == 65536
 
 
