@@ -173,6 +173,27 @@ gemm_epi_status resident_blocks(int dev, bool backward, const Shape& s, const Ch
   return GEMM_EPI_OK;
 }
 
+struct DropoutKernel {
+  void (*fn)(ge::DropoutParams);
+  int span;  // columns of a warp's share of a row, or of a thread's
+  bool narrow;
+};
+
+template <class T>
+DropoutKernel dropout_kernel_of(int64_t cols) {
+  if (cols <= ge::LN_PIECE) return {ge::dropout_narrow_kernel<T>, 8, true};
+  // as many pieces to a warp as leave few of a row's last share's empty
+  constexpr int MOST = 4 / ge::Group<T>::PIECES;
+  const int64_t pieces = (cols + ge::LN_PIECE - 1) / ge::LN_PIECE;
+  if (MOST == 4 && ((pieces + 3) / 4 * 4 - pieces) * 8 <= pieces) return {ge::dropout_kernel<T, MOST>, MOST * ge::LN_PIECE, false};
+  if (((pieces + 1) / 2 * 2 - pieces) * 8 <= pieces) return {ge::dropout_kernel<T, 2>, 2 * ge::LN_PIECE, false};
+  return {ge::dropout_kernel<T, 1>, ge::LN_PIECE, false};
+}
+
+DropoutKernel dropout_kernel_of(int64_t cols, bool f32) {
+  return f32 ? dropout_kernel_of<float>(cols) : dropout_kernel_of<uint16_t>(cols);
+}
+
 // Rows of partial sums of dw and db: the most blocks a backward pass has.
 int most_partials(int64_t cols) { return cols <= 2048 ? 912 : 304; }
 
@@ -293,19 +314,20 @@ gemm_epi_status gemm_epi_dropout(const gemm_epi_dropout_args* a, void* stream) {
   int dev = 0, sms = 0;
   if ((s = ge_host::device_sms(&dev, &sms))) return s;
   if (c.M == 0) return GEMM_EPI_OK;
+  p.M = static_cast<int32_t>(c.M);
   p.N = static_cast<int32_t>(c.N);
-  p.groups = static_cast<int32_t>((c.N + 7) / 8);
-  p.total = c.M * p.groups;
   p.x = a->x, p.ld_x = a->ld_x;
   p.residual = a->residual, p.ld_residual = a->ld_residual;
   p.y = a->y, p.ld_y = a->ld_y;
   p.wide_in = c.wide_in, p.wide_out = c.wide_out;
-  const int64_t blocks = std::min<int64_t>((p.total + ge::DO_THREADS - 1) / ge::DO_THREADS,
-                                           static_cast<int64_t>(sms) * ge::DO_BLOCKS);
-  p.step_rows = blocks * ge::DO_THREADS / p.groups;
-  p.step_groups = static_cast<int32_t>(blocks * ge::DO_THREADS % p.groups);
-  const auto fn = c.size == 4 ? ge::dropout_kernel<float> : ge::dropout_kernel<uint16_t>;
-  fn<<<static_cast<unsigned>(blocks), ge::DO_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  const DropoutKernel k = dropout_kernel_of(c.N, c.size == 4);
+  p.spans = static_cast<int32_t>((c.N + k.span - 1) / k.span);
+  p.total = c.M * p.spans;
+  const int64_t each = k.narrow ? ge::DO_THREADS : ge::DO_THREADS / 32;  // spans of a block
+  const int64_t blocks = std::min<int64_t>((p.total + each - 1) / each, static_cast<int64_t>(sms) * ge::DO_BLOCKS);
+  p.step_rows = blocks * each / p.spans;
+  p.step_spans = static_cast<int32_t>(blocks * each % p.spans);
+  k.fn<<<static_cast<unsigned>(blocks), ge::DO_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the dropout kernel");
 }

@@ -105,6 +105,45 @@ struct Group<float> {
   static __device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
 };
 
+// The first `valid` values of 16 bytes' worth at p into q, which is zeros.
+// `wide`: p is on 16 bytes.
+template <class T>
+__device__ __forceinline__ void load_part(const T* p, int valid, bool wide, uint4& q) {
+  constexpr int EACH = 16 / sizeof(T);
+  if (wide && valid >= EACH) {
+    q = *reinterpret_cast<const uint4*>(p);
+  } else {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < EACH; ++j)
+      if (j < valid) {
+        if (sizeof(T) == 4)
+          w[j % 4] = *reinterpret_cast<const uint32_t*>(p + j);
+        else
+          w[j / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p + j)) << (j % 2 * 16);
+      }
+    q = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void store_part(T* p, int valid, bool wide, const uint4& q) {
+  constexpr int EACH = 16 / sizeof(T);
+  if (wide && valid >= EACH) {
+    *reinterpret_cast<uint4*>(p) = q;
+  } else {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < EACH; ++j)
+      if (j < valid) {
+        if (sizeof(T) == 4)
+          *reinterpret_cast<uint32_t*>(p + j) = w[j % 4];
+        else
+          *reinterpret_cast<uint16_t*>(p + j) = static_cast<uint16_t>(w[j / 2] >> (j % 2 * 16));
+      }
+  }
+}
+
 template <class T>
 __device__ __forceinline__ void load_group(const T* p, int valid, bool wide, float (&v)[8]) {
   Group<T> g;
@@ -159,26 +198,9 @@ struct Eight {
     g.unpack(f);
     from(f);
   }
-  template <class T>
-  __device__ __forceinline__ void load(const T* p, int valid, bool wide) {
-    Group<T> g;
-    g.load(p, valid, wide);
-    from(g);
-  }
   __device__ __forceinline__ void plus(const Eight& r) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = __fadd2_rn(v[i], r.v[i]);
-  }
-  template <class T>
-  __device__ __forceinline__ void store(T* p, int valid, bool wide) const {
-    float f[8];
-    to(f);
-    store_group(p, valid, wide, f);
-  }
-  __device__ __forceinline__ void weights(const float* w, int col, int valid, bool wide, float none) {
-    float f[8];
-    load_weights(w, col, valid, wide, none, f);
-    from(f);
   }
   // D(this) + r
   __device__ __forceinline__ void drop_onto(const Eight& r, const Dropout& d, const uint32_t (&w)[4]) {
@@ -202,7 +224,7 @@ struct Eight {
   __device__ __forceinline__ float2 sum() const {
     return __fadd2_rn(__fadd2_rn(v[0], v[1]), __fadd2_rn(v[2], v[3]));
   }
-  // Sum of (v - m)^2 over the first `valid`.
+  // Sum of (v - m)^2.
   __device__ __forceinline__ float2 squares(float m) const {
     const float2 minus = make_float2(-m, -m);
     float2 s = make_float2(0.0f, 0.0f);
@@ -211,14 +233,6 @@ struct Eight {
       const float2 c = __fadd2_rn(v[i], minus);
       s = __ffma2_rn(c, c, s);
     }
-    return s;
-  }
-  __device__ __forceinline__ float squares(float m, int valid) const {
-    float f[8], s = 0.0f;
-    to(f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < valid) s = fmaf(f[j] - m, f[j] - m, s);
     return s;
   }
   // (this - mean) rstd
@@ -234,71 +248,6 @@ __device__ __forceinline__ float2 fma2(const float2 a, float b, const float2 c) 
 }
 
 // ------------------------------------------------------------------ dropout
-
-constexpr int DO_THREADS = 256;
-constexpr int DO_BLOCKS = 3;  // resident per SM
-template <class T>
-constexpr int DO_UNROLL = 8 / sizeof(T);  // groups of a thread in flight
-
-struct DropoutParams {
-  int32_t N, groups;  // groups of 8 columns per row
-  int64_t total;      // rows * groups
-  int64_t step_rows;  // gridDim.x * DO_THREADS groups further on: rows and groups
-  int32_t step_groups;
-  const void* x;
-  int64_t ld_x;
-  const void* residual;  // or NULL
-  int64_t ld_residual;
-  void* y;
-  int64_t ld_y;
-  int32_t wide_in, wide_out;
-  Dropout drop;
-};
-
-template <class T>
-__global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_kernel(const __grid_constant__ DropoutParams p) {
-  constexpr int U = DO_UNROLL<T>;
-  int64_t i = static_cast<int64_t>(blockIdx.x) * DO_THREADS + threadIdx.x;
-  if (i >= p.total) return;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * DO_THREADS;
-  int64_t row = i / p.groups;
-  int32_t group = static_cast<int32_t>(i - row * p.groups);
-  const bool drops = p.drop.step != nullptr;
-  const uint32_t step = drops ? drop_step(p.drop) : 0;
-  while (i < p.total) {
-    uint32_t rows[U], groups[U];
-    Group<T> x[U], r[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      rows[u] = static_cast<uint32_t>(row), groups[u] = static_cast<uint32_t>(group);
-      x[u].clear();
-      r[u].clear();
-      if (i + u * stride < p.total) {
-        const int col = group * 8;
-        x[u].load(static_cast<const T*>(p.x) + row * p.ld_x + col, p.N - col, p.wide_in);
-        if (p.residual != nullptr)
-          r[u].load(static_cast<const T*>(p.residual) + row * p.ld_residual + col, p.N - col, p.wide_in);
-      }
-      row += p.step_rows, group += p.step_groups;
-      if (group >= p.groups) group -= p.groups, ++row;
-    }
-    uint32_t words[U][4];
-    if (drops) drop_words(p.drop, step, rows, groups, words);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      Eight v, add;
-      v.from(x[u]);
-      add.from(r[u]);
-      if (drops)
-        v.drop_onto(add, p.drop, words[u]);
-      else
-        v.plus(add);
-      const int col = static_cast<int>(groups[u]) * 8;
-      if (i + u * stride < p.total) v.store(static_cast<T*>(p.y) + rows[u] * p.ld_y + col, p.N - col, p.wide_out);
-    }
-    i += U * stride;
-  }
-}
 
 // ------------------------------------------------------------------ teams
 
@@ -354,96 +303,268 @@ __device__ __forceinline__ void team_sync(int team, int warps) {
   if (warps > 1) ptx::named_barrier_sync(team + 1, warps * 32);
 }
 
-// A thread's columns in its team's rows, and those it copies into the ring:
-// with fp32 two pieces of 16 bytes 128 columns apart, so that a warp's copy
-// takes whole sectors.
+// Where a thread's 8 K values of a row lie: in each of K pieces of 256 columns,
+// PARTS times 16 bytes, neighbouring threads' side by side, so that an access of
+// a warp takes whole sectors -- 8 neighbouring columns of bf16, twice 4 of fp32,
+// 128 columns apart.
 template <class T, int K>
 struct RowPlace {
-  static constexpr int EACH = 16 / sizeof(T);  // columns of 16 bytes
-  int col;   // of piece 0; piece k: LN_PIECE k further on
-  int left;  // columns from `col` to the row's end (<= 0: none)
-  int copy_col, copy_left;
+  static constexpr int PARTS = Group<T>::PIECES;
+  static constexpr int EACH = 8 / PARTS, APART = LN_PIECE / PARTS;
+  int col;    // of piece 0, part 0
+  int left;   // columns from `col` to the row's end (<= 0: none)
   bool full;  // all of the warp's columns are in the row
 
-  __device__ __forceinline__ RowPlace(const NormParams& p, int warp_in_team) {
-    const int begin = warp_in_team * K * LN_PIECE, lane = threadIdx.x & 31;
-    col = begin + lane * 8;
-    left = p.N - col;
-    copy_col = begin + lane * EACH;
-    copy_left = p.N - copy_col;
-    full = begin + K * LN_PIECE <= p.N;
+  __device__ __forceinline__ RowPlace(int N, int begin) {
+    col = begin + (threadIdx.x & 31) * EACH;
+    left = N - col;
+    full = begin + K * LN_PIECE <= N;
   }
-  __device__ __forceinline__ int valid(int k) const { return min(left - k * LN_PIECE, 8); }
-  // of the i-th 16 bytes that the thread copies of piece k
-  __device__ __forceinline__ int copied(int k, int i) const {
-    return min(copy_left - k * LN_PIECE - i * (LN_PIECE / 2), EACH);
+  // Columns of a part that are in the row (<= 0: none).
+  __device__ __forceinline__ int valid(int k, int i) const { return min(left - k * LN_PIECE - i * APART, EACH); }
+  // Piece k from a row at `col`, zeros behind its end.
+  __device__ __forceinline__ void load(const T* row, int k, bool wide, bool all, Group<T>& g) const {
+    g.clear();
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) load_part(row + k * LN_PIECE + i * APART, all ? EACH : valid(k, i), wide, g.q[i]);
+  }
+  __device__ __forceinline__ void store(T* row, int k, bool wide, bool all, const Eight& v) const {
+    Group<T> g;
+    float f[8];
+    v.to(f);
+    g.pack(f);
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) store_part(row + k * LN_PIECE + i * APART, all ? EACH : valid(k, i), wide, g.q[i]);
+  }
+  // fp32 vectors, `none` behind the row's end and without one.
+  __device__ __forceinline__ void weights(const float* w, int k, bool wide, float none, Eight& v) const {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+      const int at = col + k * LN_PIECE + i * APART, n = valid(k, i);
+      if (w != nullptr && wide && n >= EACH) {
+#pragma unroll
+        for (int j = 0; j < EACH; j += 4) {
+          const float4 q = __ldg(reinterpret_cast<const float4*>(w + at + j));
+          f[i * EACH + j] = q.x, f[i * EACH + j + 1] = q.y, f[i * EACH + j + 2] = q.z, f[i * EACH + j + 3] = q.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) f[i * EACH + j] = w != nullptr && j < n ? __ldg(w + at + j) : none;
+      }
+    }
+    v.from(f);
+  }
+  // f(value's place among the 8, its column) of piece k's columns in the row.
+  template <class F>
+  __device__ __forceinline__ void columns(int k, F&& f) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j % EACH < valid(k, j / EACH)) f(j, col + k * LN_PIECE + j / EACH * APART + j % EACH);
+  }
+  // Sum of (v - m)^2 over piece k's columns in the row.
+  __device__ __forceinline__ float squares(const Eight& v, float m, int k) const {
+    float f[8], s = 0.0f;
+    v.to(f);
+    columns(k, [&](int j, int) { s = fmaf(f[j] - m, f[j] - m, s); });
+    return s;
+  }
+  // The masks' words of B pieces from piece k0 on: words 0 and 1 of the first
+  // four values, 2 and 3 of the others.  fp32's two parts are of two groups,
+  // half of each: twice the work for an element, of twice the bytes.
+  template <int B>
+  __device__ __forceinline__ void words(const Dropout& d, uint32_t step, uint32_t row, int k0, uint32_t (&w)[B][4]) const {
+    uint32_t rows[B * PARTS], groups[B * PARTS], all[B * PARTS][4];
+#pragma unroll
+    for (int i = 0; i < B * PARTS; ++i) {
+      rows[i] = row;
+      groups[i] = static_cast<uint32_t>(col + k0 * LN_PIECE + i * APART) >> 3;
+    }
+    drop_words(d, step, rows, groups, all);
+    const bool second = PARTS == 2 && (col & 4);
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (PARTS == 1)
+          w[i][j] = all[i][j];
+        else
+          w[i][j] = second ? all[2 * i + j / 2][2 + j % 2] : all[2 * i + j / 2][j % 2];
+      }
   }
 };
 
-// Copies of a warp's values of the next rows on their way into its slots, 16
-// bytes of each lane side by side.  bf16: each thread copies what it reads.
-// fp32: 16 bytes j of a piece are part j % 2 of lane j / 2, so a __syncwarp()
-// lies between the copies' end and the reads, and the reads and the next copies.
+// Copies of a thread's values of the next rows on their way into slots that
+// only it reads.
 template <class T, int K, int TENSORS, int DEPTH>
 struct RowRing {
-  static constexpr int PARTS = Group<T>::PIECES;  // of 16 bytes
+  using Place = RowPlace<T, K>;
+  static constexpr int PARTS = Place::PARTS;
   static constexpr int WARP_BYTES = DEPTH * TENSORS * K * PARTS * 512;
-  const uint4* slots;  // this thread's first to read
-  uint4* to;           // and to fill
+  uint4* slots;  // this thread's first
   uint32_t at;
 
-  __device__ __forceinline__ RowRing(uint4* smem, int warp) {
-    const int lane = threadIdx.x & 31;
-    smem += warp * (WARP_BYTES / 16);
-    slots = smem + lane;
-    to = smem + (PARTS == 1 ? lane : (lane & 1) * 32 + (lane >> 1));
-    at = ptx::smem_addr(to);
-  }
-  static __device__ __forceinline__ constexpr int read_index(int d, int t, int k, int part) {
+  __device__ __forceinline__ RowRing(uint4* smem, int warp)
+      : slots(smem + warp * (WARP_BYTES / 16) + (threadIdx.x & 31)), at(ptx::smem_addr(slots)) {}
+  static __device__ __forceinline__ constexpr int index(int d, int t, int k, int part) {
     return (((d * TENSORS + t) * K + k) * PARTS + part) * 32;
   }
-  static __device__ __forceinline__ constexpr int fill_index(int d, int t, int k, int i) {
-    return ((d * TENSORS + t) * K + k) * PARTS * 32 + i * 16;
-  }
-  static __device__ __forceinline__ void sync() {
-    if (PARTS > 1) __syncwarp();
-  }
   // Zeros where no copy will land.
-  __device__ __forceinline__ void clear(const RowPlace<T, K>& place, int first_unused_tensor) const {
+  __device__ __forceinline__ void clear(const Place& place, int first_unused_tensor) const {
 #pragma unroll 1
     for (int d = 0; d < DEPTH; ++d)
       for (int t = 0; t < TENSORS; ++t)
         for (int k = 0; k < K; ++k)
           for (int i = 0; i < PARTS; ++i)
-            if (t >= first_unused_tensor || place.copied(k, i) <= 0) to[fill_index(d, t, k, i)] = make_uint4(0, 0, 0, 0);
+            if (t >= first_unused_tensor || place.valid(k, i) <= 0) slots[index(d, t, k, i)] = make_uint4(0, 0, 0, 0);
   }
   template <int... Is>
   static __device__ __forceinline__ void fetch_full(uint32_t to, const T* row, std::integer_sequence<int, Is...>) {
-    (ptx::cp_async16<fill_index(0, 0, Is / PARTS, Is % PARTS) * 16,
-                     (Is / PARTS * LN_PIECE + Is % PARTS * (LN_PIECE / 2)) * static_cast<int>(sizeof(T))>(to, row), ...);
+    (ptx::cp_async16<Is * 512, (Is / PARTS * LN_PIECE + Is % PARTS * Place::APART) * static_cast<int>(sizeof(T))>(to, row), ...);
   }
-  // `row`: at the first column that the thread copies.
-  __device__ __forceinline__ void fetch(int d, int t, const T* row, const RowPlace<T, K>& place) const {
-    const uint32_t first = at + static_cast<uint32_t>(fill_index(d, t, 0, 0)) * 16u;
+  // `row`: at the thread's first column.
+  __device__ __forceinline__ void fetch(int d, int t, const T* row, const Place& place) const {
+    const uint32_t to = at + static_cast<uint32_t>(index(d, t, 0, 0)) * 16u;
     if (place.full) {
-      fetch_full(first, row, std::make_integer_sequence<int, K * PARTS>{});
+      fetch_full(to, row, std::make_integer_sequence<int, K * PARTS>{});
     } else {
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < PARTS; ++i)
-          if (place.copied(k, i) > 0)
-            ptx::cp_async16(first + static_cast<uint32_t>(fill_index(0, 0, k, i)) * 16u,
-                            row + k * LN_PIECE + i * (LN_PIECE / 2), static_cast<uint32_t>(place.copied(k, i)) * sizeof(T));
+          if (place.valid(k, i) > 0)
+            ptx::cp_async16(to + static_cast<uint32_t>(index(0, 0, k, i)) * 16u, row + k * LN_PIECE + i * Place::APART,
+                            static_cast<uint32_t>(place.valid(k, i)) * sizeof(T));
     }
   }
   __device__ __forceinline__ void take(int d, int t, int k, Eight& v) const {
     Group<T> g;
 #pragma unroll
-    for (int i = 0; i < PARTS; ++i) g.q[i] = slots[read_index(d, t, k, i)];
+    for (int i = 0; i < PARTS; ++i) g.q[i] = slots[index(d, t, k, i)];
     v.from(g);
   }
 };
+
+// ------------------------------------------------------------------ dropout
+
+constexpr int DO_THREADS = 256;
+constexpr int DO_BLOCKS = 3;  // resident per SM
+
+struct DropoutParams {
+  int32_t M, N;
+  int32_t spans;      // of a warp's columns in a row; narrow rows: groups of 8 columns
+  int64_t total;      // rows * spans
+  int64_t step_rows;  // from one span of a warp (or group of a thread) to its next: rows and spans
+  int32_t step_spans;
+  const void* x;
+  int64_t ld_x;
+  const void* residual;  // or NULL
+  int64_t ld_residual;
+  void* y;
+  int64_t ld_y;
+  int32_t wide_in, wide_out;
+  Dropout drop;
+};
+
+__device__ __forceinline__ void drop_piece(const DropoutParams& p, const uint32_t (&words)[4], Eight& v, const Eight& add) {
+  if (p.drop.step != nullptr)
+    v.drop_onto(add, p.drop, words);
+  else
+    v.plus(add);
+}
+
+// A warp to K pieces of a row.
+template <class T, int K>
+__global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_kernel(const __grid_constant__ DropoutParams p) {
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (DO_THREADS / 32);
+  int64_t i = static_cast<int64_t>(blockIdx.x) * (DO_THREADS / 32) + (threadIdx.x >> 5);
+  int64_t row = i / p.spans;
+  int32_t span = static_cast<int32_t>(i - row * p.spans);
+  const uint32_t step = p.drop.step != nullptr ? drop_step(p.drop) : 0;
+  for (; i < p.total; i += warps) {
+    const RowPlace<T, K> place(p.N, span * K * LN_PIECE);
+    const T* x = static_cast<const T*>(p.x) + row * p.ld_x + place.col;
+    const T* residual = p.residual != nullptr ? static_cast<const T*>(p.residual) + row * p.ld_residual + place.col : nullptr;
+    T* y = static_cast<T*>(p.y) + row * p.ld_y + place.col;
+    Group<T> g[K], r[K];
+    uint32_t words[K][4];
+    auto load = [&](bool all, bool wide) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        place.load(x, k, wide, all, g[k]);
+        r[k].clear();
+        if (residual != nullptr) place.load(residual, k, wide, all, r[k]);
+      }
+    };
+    auto store = [&](bool all, bool wide) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        Eight v, add;
+        v.from(g[k]);
+        add.from(r[k]);
+        drop_piece(p, words[k], v, add);
+        place.store(y, k, wide, all, v);
+      }
+    };
+    if (place.full && p.wide_in)
+      load(true, true);
+    else
+      load(false, p.wide_in);
+    if (p.drop.step != nullptr) place.words(p.drop, step, static_cast<uint32_t>(row), 0, words);
+    if (place.full && p.wide_out)
+      store(true, true);
+    else
+      store(false, p.wide_out);
+    row += p.step_rows, span += p.step_spans;
+    if (span >= p.spans) span -= p.spans, ++row;
+  }
+}
+
+// Rows of up to 256 columns: a thread to 8 neighbouring columns, whatever row
+// they are in.
+template <class T>
+__global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_narrow_kernel(const __grid_constant__ DropoutParams p) {
+  const int64_t threads = static_cast<int64_t>(gridDim.x) * DO_THREADS;
+  int64_t i = static_cast<int64_t>(blockIdx.x) * DO_THREADS + threadIdx.x;
+  int64_t row = i / p.spans;
+  int32_t group = static_cast<int32_t>(i - row * p.spans);
+  const uint32_t step = p.drop.step != nullptr ? drop_step(p.drop) : 0;
+  constexpr int U = 4 / Group<T>::PIECES;  // of a thread in flight
+  while (i < p.total) {
+    uint32_t rows[U], groups[U], words[U][4];
+    Group<T> x[U], r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      rows[u] = static_cast<uint32_t>(row), groups[u] = static_cast<uint32_t>(group);
+      x[u].clear();
+      r[u].clear();
+      if (i + u * threads < p.total) {
+        const int col = group * 8;
+        x[u].load(static_cast<const T*>(p.x) + row * p.ld_x + col, p.N - col, p.wide_in);
+        if (p.residual != nullptr)
+          r[u].load(static_cast<const T*>(p.residual) + row * p.ld_residual + col, p.N - col, p.wide_in);
+      }
+      row += p.step_rows, group += p.step_spans;
+      if (group >= p.spans) group -= p.spans, ++row;
+    }
+    if (p.drop.step != nullptr) drop_words(p.drop, step, rows, groups, words);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      Eight v, add;
+      v.from(x[u]);
+      add.from(r[u]);
+      drop_piece(p, words[u], v, add);
+      float f[8];
+      v.to(f);
+      const int col = static_cast<int>(groups[u]) * 8;
+      if (i + u * threads < p.total)
+        store_group(static_cast<T*>(p.y) + rows[u] * p.ld_y + col, p.N - col, p.wide_out, f);
+    }
+    i += U * threads;
+  }
+}
+
+// ------------------------------------------------------------------ teams
 
 // A block's teams, and where its shared memory's parts begin: the ring, then
 // the norm's weights.
@@ -461,11 +582,12 @@ struct Teams {
 
 // Weights in shared memory, by all threads of the block: a row's cost is then
 // free of the L1 misses that its streams cause.  A piece's 256 lie as the first
-// halves of its lanes' groups and then the second ones, so that 16-byte reads
-// meet no bank twice.  A barrier has to follow.
+// four of its lanes' eight and then the others, so that 16-byte reads meet no
+// bank twice.  A barrier has to follow.
+template <class T>
 __device__ __forceinline__ void stage_weights(float* to, const float* w, int n, int width, float none) {
   for (int i = threadIdx.x; i < width; i += blockDim.x) {
-    const int col = (i & ~(LN_PIECE - 1)) + (i >> 2 & 31) * 8 + (i >> 7 & 1) * 4 + (i & 3);
+    const int col = sizeof(T) == 4 ? i : (i & ~(LN_PIECE - 1)) + (i >> 2 & 31) * 8 + (i >> 7 & 1) * 4 + (i & 3);
     to[i] = w != nullptr && col < n ? __ldg(w + col) : none;
   }
 }
@@ -476,15 +598,6 @@ __device__ __forceinline__ void staged_weights(const float* w, int k, Eight& v) 
   const float4 b = *reinterpret_cast<const float4*>(w + k * LN_PIECE + LN_PIECE / 2);
   v.v[0] = make_float2(a.x, a.y), v.v[1] = make_float2(a.z, a.w);
   v.v[2] = make_float2(b.x, b.y), v.v[3] = make_float2(b.z, b.w);
-}
-
-// The words of B of a thread's groups of a row, the first one at column `col`.
-template <int B>
-__device__ __forceinline__ void row_words(const Dropout& d, uint32_t step, uint32_t row, int col, uint32_t (&words)[B][4]) {
-  uint32_t rows[B], groups[B];
-#pragma unroll
-  for (int i = 0; i < B; ++i) rows[i] = row, groups[i] = static_cast<uint32_t>(col + i * LN_PIECE) >> 3;
-  drop_words(d, step, rows, groups, words);
 }
 
 // ------------------------------------------------------------------ forward
@@ -501,13 +614,13 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
   __shared__ float4 part[2][R][LN_MAX_WARPS];  // a warp's mean, sum of squares from it, count
   const Teams<K> teams(p);
   const int warp = teams.warp_in_team(p);
-  const RowPlace<T, K> place(p, warp);
+  const RowPlace<T, K> place(p.N, warp * K * LN_PIECE);
   const Ring ring(ln_smem, teams.warp);
   const uint32_t rows = static_cast<uint32_t>(p.M), stride = static_cast<uint32_t>(teams.stride) * R;
   // this thread's columns: of the rows to fetch next (WIDE) or to work on
-  const T* x = static_cast<const T*>(p.x) + teams.first * R * p.ld_x + (WIDE ? place.copy_col : place.col);
+  const T* x = static_cast<const T*>(p.x) + teams.first * R * p.ld_x + place.col;
   const T* residual = ADD && p.other != nullptr
-                          ? static_cast<const T*>(p.other) + teams.first * R * p.ld_other + (WIDE ? place.copy_col : place.col)
+                          ? static_cast<const T*>(p.other) + teams.first * R * p.ld_other + place.col
                           : nullptr;
   const int64_t step_x = stride * p.ld_x, step_residual = stride * p.ld_other;
   auto fetch = [&](uint32_t row) {
@@ -529,8 +642,8 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
   const float* weights = nullptr;  // this thread's, staged: w, then b `width` further on
   if (p.staged) {
     float* to = reinterpret_cast<float*>(ln_smem + (blockDim.x >> 5) * (Ring::WARP_BYTES / 16));
-    stage_weights(to, p.w, p.N, teams.width, 1.0f);
-    stage_weights(to + teams.width, p.b, p.N, teams.width, 0.0f);
+    stage_weights<T>(to, p.w, p.N, teams.width, 1.0f);
+    stage_weights<T>(to + teams.width, p.b, p.N, teams.width, 0.0f);
     weights = to + warp * K * LN_PIECE + (threadIdx.x & 31) * 4;
     __syncthreads();
   }
@@ -547,11 +660,8 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       uint32_t words[K][4];
-      if constexpr (DROP) row_words(p.drop, step, row + r, place.col, words);
-      if (WIDE && r == 0) {
-        ptx::cp_async_wait<0>();
-        Ring::sync();
-      }
+      if constexpr (DROP) place.words(p.drop, step, row + r, 0, words);
+      if (WIDE && r == 0) ptx::cp_async_wait<0>();
       float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -561,9 +671,13 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
           ring.take(r, 0, k, h[r][k]);
           if constexpr (ADD) ring.take(r, 1, k, add);
         } else {
-          const int valid = row + r < rows ? place.valid(k) : 0;
-          h[r][k].load(x + r * p.ld_x + k * LN_PIECE, valid, false);
-          if (ADD && residual != nullptr) add.load(residual + r * p.ld_other + k * LN_PIECE, valid, false);
+          Group<T> g;
+          place.load(x + r * p.ld_x, k, false, false, g);
+          h[r][k].from(g);
+          if (ADD && residual != nullptr) {
+            place.load(residual + r * p.ld_other, k, false, false, g);
+            add.from(g);
+          }
         }
         if constexpr (DROP)
           h[r][k].drop_onto(add, p.drop, words[k]);
@@ -575,10 +689,7 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
     }
     x += step_x;  // the slots' values are in registers
     if (ADD && residual != nullptr) residual += step_residual;
-    if constexpr (WIDE) {
-      Ring::sync();
-      fetch(row + stride);
-    }
+    if constexpr (WIDE) fetch(row + stride);
 
 #pragma unroll
     for (int r = 0; r < R; ++r) mean[r] = warp_sum(mean[r]) * inv_count;
@@ -592,7 +703,7 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
       } else {
         square[r] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) square[r] += h[r][k].squares(mean[r], place.valid(k));
+        for (int k = 0; k < K; ++k) square[r] += place.squares(h[r][k], mean[r], k);
       }
     }
 #pragma unroll
@@ -632,16 +743,16 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
         if (p.rstd != nullptr) p.rstd[row + r] = rstd[r];
       }
     }
-    auto finish = [&](int k, int valid, const Eight& w, const Eight& b) {
+    auto finish = [&](int k, bool all, const Eight& w, const Eight& b) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (row + r >= rows) break;
         Eight& v = h[r][k];
-        if (sum != nullptr) v.store(sum + r * p.ld_sum + k * LN_PIECE, valid, WIDE);
+        if (sum != nullptr) place.store(sum + r * p.ld_sum, k, WIDE, all, v);
         v.normalise(mean[r], rstd[r]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v.v[i] = __ffma2_rn(v.v[i], w.v[i], b.v[i]);
-        v.store(y + r * p.ld_y + k * LN_PIECE, valid, WIDE);
+        place.store(y + r * p.ld_y, k, WIDE, all, v);
       }
     };
     if (place.full && weights != nullptr) {
@@ -650,17 +761,16 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
         Eight w, b;
         staged_weights(weights, k, w);
         staged_weights(weights + teams.width, k, b);
-        finish(k, 8, w, b);
+        finish(k, true, w, b);
       }
     } else {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int valid = place.valid(k);
-        if (valid <= 0) continue;
+        if (place.valid(k, 0) <= 0) continue;
         Eight w, b;
-        w.weights(p.w, place.col + k * LN_PIECE, valid, WIDE, 1.0f);
-        b.weights(p.b, place.col + k * LN_PIECE, valid, WIDE, 0.0f);
-        finish(k, valid, w, b);
+        place.weights(p.w, k, WIDE, 1.0f, w);
+        place.weights(p.b, k, WIDE, 0.0f, b);
+        finish(k, false, w, b);
       }
     }
     y += step_y;
@@ -676,43 +786,41 @@ constexpr int LN_NARROW_ROWS = 8 / sizeof(T);
 template <class T>
 constexpr int LN_NARROW_BACKWARD_ROWS = 4 / sizeof(T);
 
-// A thread's place and its warp's ring, laid out and filled as RowRing.
+// A thread's place and its slots in the ring.  As RowPlace, with the team's
+// lanes in place of a warp's.
 template <class T, int R, int TENSORS>
 struct NarrowRows {
-  static constexpr int PARTS = Group<T>::PIECES, DEPTH = 2;
+  static constexpr int PARTS = Group<T>::PIECES, EACH = 8 / PARTS, DEPTH = 2;
   static constexpr int WARP_BYTES = DEPTH * TENSORS * R * PARTS * 512;
   int64_t row, stride;  // of R neighbouring ones
   int64_t leader;       // the warp's first: the same for all its lanes
-  int col, valid;
-  const uint4* slots;   // this thread's first to read
+  int col, apart, N;    // part i at col + i apart
+  uint4* slots;
 
   __device__ __forceinline__ NarrowRows(const NormParams& p, uint4* smem) {
     const int teams = 32 >> p.log_lanes, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     leader = (static_cast<int64_t>(blockIdx.x) * LN_BLOCK_WARPS + warp) * teams * R;
     row = leader + (lane >> p.log_lanes) * R;
     stride = static_cast<int64_t>(gridDim.x) * LN_BLOCK_WARPS * teams * R;
-    col = (lane & ((1 << p.log_lanes) - 1)) * 8;
-    valid = min(p.N - col, 8);
-    if (valid <= 0) col = valid = 0;
+    col = (lane & ((1 << p.log_lanes) - 1)) * EACH;
+    apart = EACH << p.log_lanes;
+    N = p.N;
     slots = smem + warp * (WARP_BYTES / 16) + lane;
   }
+  __device__ __forceinline__ int valid(int i) const { return max(min(N - col - i * apart, EACH), 0); }
   static __device__ __forceinline__ constexpr int index(int d, int t, int r, int part) {
     return (((d * TENSORS + t) * R + r) * PARTS + part) * 32;
   }
   // Rows `at` .. at + R - 1 of a tensor into set d, zeros behind its last row and
   // column.
-  __device__ __forceinline__ void fetch(const NormParams& p, int d, int t, const void* data, int64_t ld, int64_t at) const {
-    constexpr int EACH = 8 / PARTS;
-    const int lane = threadIdx.x & 31, lanes = 1 << p.log_lanes, in_team = lane & (lanes - 1);
+  __device__ __forceinline__ void fetch(int M, int d, int t, const void* data, int64_t ld, int64_t at) const {
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < PARTS; ++i) {
-        const int j = i * lanes + in_team;  // which 16 bytes of the row
-        const int n = at + r < p.M ? min(max(p.N - j * EACH, 0), EACH) : 0;
-        const T* src = static_cast<const T*>(data) + (n > 0 ? (at + r) * ld + j * EACH : 0);
-        const int to = PARTS == 1 ? index(d, t, r, 0) : index(d, t, r, j & 1) + (j >> 1) - in_team;
-        ptx::cp_async16(ptx::smem_addr(slots + to), src, static_cast<uint32_t>(n) * sizeof(T));
+        const int n = at + r < M ? valid(i) : 0;
+        const T* src = static_cast<const T*>(data) + (n > 0 ? (at + r) * ld + col + i * apart : 0);
+        ptx::cp_async16(ptx::smem_addr(slots + index(d, t, r, i)), src, static_cast<uint32_t>(n) * sizeof(T));
       }
   }
   __device__ __forceinline__ void take(int d, int t, int r, Eight& v) const {
@@ -721,15 +829,61 @@ struct NarrowRows {
     for (int i = 0; i < PARTS; ++i) g.q[i] = slots[index(d, t, r, i)];
     v.from(g);
   }
-  __device__ __forceinline__ void load(const NormParams& p, const void* data, int64_t ld, int64_t at, Eight& v) const {
-    v.load(static_cast<const T*>(data) + at * ld + col, at < p.M ? valid : 0, false);
-  }
-  // The words of the thread's group in its R rows.
-  __device__ __forceinline__ void words(const Dropout& d, uint32_t step, int64_t at, uint32_t (&w)[R][4]) const {
-    uint32_t rows[R], groups[R];
+  // The same of one row by single elements.
+  __device__ __forceinline__ void load(int M, const void* data, int64_t ld, int64_t at, Eight& v) const {
+    Group<T> g;
+    g.clear();
 #pragma unroll
-    for (int r = 0; r < R; ++r) rows[r] = static_cast<uint32_t>(at + r), groups[r] = static_cast<uint32_t>(col) >> 3;
-    drop_words(d, step, rows, groups, w);
+    for (int i = 0; i < PARTS; ++i)
+      if (at < M) load_part(static_cast<const T*>(data) + at * ld + col + i * apart, valid(i), false, g.q[i]);
+    v.from(g);
+  }
+  __device__ __forceinline__ void store(void* data, int64_t ld, int64_t at, bool wide, const Eight& v) const {
+    Group<T> g;
+    float f[8];
+    v.to(f);
+    g.pack(f);
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) store_part(static_cast<T*>(data) + at * ld + col + i * apart, valid(i), wide, g.q[i]);
+  }
+  // f(value's place among the 8, its column) of the columns in the row.
+  template <class F>
+  __device__ __forceinline__ void columns(F&& f) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j % EACH < valid(j / EACH)) f(j, col + j / EACH * apart + j % EACH);
+  }
+  __device__ __forceinline__ float squares(const Eight& v, float m) const {
+    float f[8], s = 0.0f;
+    v.to(f);
+    columns([&](int j, int) { s = fmaf(f[j] - m, f[j] - m, s); });
+    return s;
+  }
+  __device__ __forceinline__ void weights(const float* w, float none, Eight& v) const {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = none;
+    if (w != nullptr) columns([&](int j, int c) { f[j] = __ldg(w + c); });
+    v.from(f);
+  }
+  // The words of the thread's values in its R rows, as RowPlace::words.
+  __device__ __forceinline__ void words(const Dropout& d, uint32_t step, int64_t at, uint32_t (&w)[R][4]) const {
+    uint32_t rows[R * PARTS], groups[R * PARTS], all[R * PARTS][4];
+#pragma unroll
+    for (int i = 0; i < R * PARTS; ++i) {
+      rows[i] = static_cast<uint32_t>(at + i / PARTS);
+      groups[i] = static_cast<uint32_t>(col + i % PARTS * apart) >> 3;
+    }
+    drop_words(d, step, rows, groups, all);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (PARTS == 1)
+          w[r][j] = all[r][j];
+        else
+          w[r][j] = ((col + j / 2 * apart) & 4) ? all[2 * r + j / 2][2 + j % 2] : all[2 * r + j / 2][j % 2];
+      }
   }
 };
 
@@ -741,8 +895,8 @@ __global__ void __launch_bounds__(32 * LN_BLOCK_WARPS, 2) layer_norm_narrow_kern
   const Rows at(p, ln_smem);
   auto fetch = [&](int d, int64_t row) {
     if constexpr (WIDE) {
-      at.fetch(p, d, 0, p.x, p.ld_x, row);
-      if (p.other != nullptr) at.fetch(p, d, 1, p.other, p.ld_other, row);
+      at.fetch(p.M, d, 0, p.x, p.ld_x, row);
+      if (p.other != nullptr) at.fetch(p.M, d, 1, p.other, p.ld_other, row);
       ptx::cp_async_commit();
     }
   };
@@ -751,8 +905,8 @@ __global__ void __launch_bounds__(32 * LN_BLOCK_WARPS, 2) layer_norm_narrow_kern
   uint32_t step = 0;
   if constexpr (DROP) step = drop_step(p.drop);
   Eight w, b;
-  w.weights(p.w, at.col, at.valid, WIDE, 1.0f);
-  b.weights(p.b, at.col, at.valid, WIDE, 0.0f);
+  at.weights(p.w, 1.0f, w);
+  at.weights(p.b, 0.0f, b);
   int64_t row = at.row;
   int d = 0;
   for (int64_t leader = at.leader; leader < p.M; leader += at.stride, row += at.stride) {
@@ -760,10 +914,7 @@ __global__ void __launch_bounds__(32 * LN_BLOCK_WARPS, 2) layer_norm_narrow_kern
     float mean[R], square[R];
     uint32_t words[R][4];
     if constexpr (DROP) at.words(p.drop, step, row, words);
-    if constexpr (WIDE) {
-      ptx::cp_async_wait<1>();
-      __syncwarp();
-    }
+    if constexpr (WIDE) ptx::cp_async_wait<1>();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       Eight add;
@@ -772,8 +923,8 @@ __global__ void __launch_bounds__(32 * LN_BLOCK_WARPS, 2) layer_norm_narrow_kern
         at.take(d, 0, r, h[r]);
         if (p.other != nullptr) at.take(d, 1, r, add);
       } else {
-        at.load(p, p.x, p.ld_x, row + r, h[r]);
-        if (p.other != nullptr) at.load(p, p.other, p.ld_other, row + r, add);
+        at.load(p.M, p.x, p.ld_x, row + r, h[r]);
+        if (p.other != nullptr) at.load(p.M, p.other, p.ld_other, row + r, add);
       }
       if constexpr (DROP)
         h[r].drop_onto(add, p.drop, words[r]);
@@ -782,28 +933,27 @@ __global__ void __launch_bounds__(32 * LN_BLOCK_WARPS, 2) layer_norm_narrow_kern
       const float2 s = h[r].sum();
       mean[r] = s.x + s.y;
     }
-    __syncwarp();  // all lanes have read
     fetch(d, row + 2 * at.stride);
     d ^= 1;
 #pragma unroll
     for (int r = 0; r < R; ++r) mean[r] = team_sum(mean[r], p.log_lanes) * p.inv_n;
 #pragma unroll
-    for (int r = 0; r < R; ++r) square[r] = h[r].squares(mean[r], at.valid);
+    for (int r = 0; r < R; ++r) square[r] = at.squares(h[r], mean[r]);
 #pragma unroll
     for (int r = 0; r < R; ++r) square[r] = team_sum(square[r], p.log_lanes);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const float rstd = 1.0f / sqrtf(fmaf(square[r], p.inv_n, p.eps));
-      if (row + r >= p.M || at.valid == 0) continue;
+      if (row + r >= p.M) continue;
       if (at.col == 0) {
         if (p.mean != nullptr) p.mean[row + r] = mean[r];
         if (p.rstd != nullptr) p.rstd[row + r] = rstd;
       }
-      if (p.sum != nullptr) h[r].store(static_cast<T*>(p.sum) + (row + r) * p.ld_sum + at.col, at.valid, WIDE);
+      if (p.sum != nullptr) at.store(p.sum, p.ld_sum, row + r, WIDE, h[r]);
       h[r].normalise(mean[r], rstd);
 #pragma unroll
       for (int j = 0; j < 4; ++j) h[r].v[j] = __ffma2_rn(h[r].v[j], w.v[j], b.v[j]);
-      h[r].store(static_cast<T*>(p.y) + (row + r) * p.ld_y + at.col, at.valid, WIDE);
+      at.store(p.y, p.ld_y, row + r, WIDE, h[r]);
     }
   }
 }
@@ -845,13 +995,12 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
   __shared__ float2 part[2][LN_MAX_WARPS];  // a warp's sums of a and a n
   const Teams<K> teams(p);
   const int warp = teams.warp_in_team(p);
-  const RowPlace<T, K> place(p, warp);
-  const int col = WIDE ? place.copy_col : place.col;
+  const RowPlace<T, K> place(p.N, warp * K * LN_PIECE);
   const Ring ring(ln_smem, teams.warp);
   const uint32_t rows = static_cast<uint32_t>(p.M), stride = static_cast<uint32_t>(teams.stride);
   // Addresses are worked out where they are needed: kept, they would cost 20 of
   // the 128 registers, of which the sums of dw and db take 64 at K = 4.
-  auto at = [&](const void* data, int64_t ld, uint32_t row) { return static_cast<const T*>(data) + row * ld + col; };
+  auto at = [&](const void* data, int64_t ld, uint32_t row) { return static_cast<const T*>(data) + row * ld + place.col; };
   auto fetch = [&](int d, uint32_t row) {
     if (row < rows) {
       ring.fetch(d, 0, at(p.other, p.ld_other, row), place);
@@ -870,7 +1019,7 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
   const float* weights = nullptr;  // this thread's, staged
   if (p.staged) {
     float* to = reinterpret_cast<float*>(ln_smem + (blockDim.x >> 5) * (Ring::WARP_BYTES / 16));
-    stage_weights(to, p.w, p.N, teams.width, 1.0f);
+    stage_weights<T>(to, p.w, p.N, teams.width, 1.0f);
     weights = to + warp * K * LN_PIECE + (threadIdx.x & 31) * 4;
     __syncthreads();
   }
@@ -893,37 +1042,36 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
         ring.take(d, 0, k, g);
         ring.take(d, 1, k, n);
       } else {
-        g.load(at(p.other, p.ld_other, row) + k * LN_PIECE, place.valid(k), false);
-        n.load(at(p.x, p.ld_x, row) + k * LN_PIECE, place.valid(k), false);
+        Group<T> q;
+        place.load(at(p.other, p.ld_other, row), k, false, false, q);
+        g.from(q);
+        place.load(at(p.x, p.ld_x, row), k, false, false, q);
+        n.from(q);
       }
       n.normalise(mean, rstd);
     };
-    // f(k, valid columns, weights) of the thread's pieces that have any
+    // f(k, all of its columns are in the row, weights) of the pieces that have any
     auto pieces = [&](auto&& f) {
       if (place.full && weights != nullptr) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           Eight w;
           staged_weights(weights, k, w);
-          f(k, 8, w);
+          f(k, true, w);
         }
       } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          const int valid = place.valid(k);
-          if (valid <= 0) continue;
+          if (place.valid(k, 0) <= 0) continue;
           Eight w;
-          w.weights(p.w, place.col + k * LN_PIECE, valid, WIDE, 1.0f);
-          f(k, valid, w);
+          place.weights(p.w, k, WIDE, 1.0f, w);
+          f(k, false, w);
         }
       }
     };
-    if constexpr (WIDE) {
-      ptx::cp_async_wait<DEPTH - 1>();
-      Ring::sync();
-    }
+    if constexpr (WIDE) ptx::cp_async_wait<DEPTH - 1>();
     float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
-    pieces([&](int k, int, const Eight& w) {
+    pieces([&](int k, bool, const Eight& w) {
       Eight g, n;
       take(k, g, n);  // dy is zero behind the row's end
       add_group(g, n, w, dw[k], db[k], s1, s2);
@@ -947,9 +1095,9 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
       uint32_t words[BATCH][4];
       T* y = static_cast<T*>(p.y) + row * p.ld_y + place.col;
       T* sum = static_cast<T*>(p.sum) + row * p.ld_sum + place.col;
-      pieces([&](int k, int valid, const Eight& w) {
+      pieces([&](int k, bool all, const Eight& w) {
         if constexpr (DROP) {
-          if (k % BATCH == 0) row_words(p.drop, step, row, place.col + k * LN_PIECE, words);
+          if (k % BATCH == 0) place.words(p.drop, step, row, k, words);
         }
         Eight g, n, a;
         take(k, g, n);
@@ -958,16 +1106,19 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
           if constexpr (WIDE)
             ring.take(d, 2, k, a);
           else
-            a.load(at(p.add, p.ld_add, row) + k * LN_PIECE, valid, false);
+          {
+            Group<T> q;
+            place.load(at(p.add, p.ld_add, row), k, false, false, q);
+            a.from(q);
+          }
         }
         norm_gradient(g, n, w, a, rstd, m1, m2);
-        if (p.sum != nullptr) g.store(sum + k * LN_PIECE, valid, WIDE);
+        if (p.sum != nullptr) place.store(sum, k, WIDE, all, g);
         if constexpr (DROP) g.drop(p.drop, words[k % BATCH]);
-        if (p.y != nullptr) g.store(y + k * LN_PIECE, valid, WIDE);
+        if (p.y != nullptr) place.store(y, k, WIDE, all, g);
       });
     }
     if constexpr (WIDE) {
-      Ring::sync();
       fetch(d, row + DEPTH * stride);
       d = d + 1 == DEPTH ? 0 : d + 1;
     }
@@ -985,12 +1136,10 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
     float a[8], b[8];
     dw[k].to(a);
     db[k].to(b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < place.valid(k)) {
-        out[place.col + k * LN_PIECE + j] = a[j];
-        out[p.N + place.col + k * LN_PIECE + j] = b[j];
-      }
+    place.columns(k, [&](int j, int col) {
+      out[col] = a[j];
+      out[p.N + col] = b[j];
+    });
   }
   if (teams.count > 1) {
     __syncthreads();
@@ -1014,9 +1163,9 @@ __global__ void __launch_bounds__(32 * LN_BLOCK_WARPS, 2)
   float next_mean[R], next_rstd[R];
   auto fetch = [&](int d, int64_t row) {
     if constexpr (WIDE) {
-      at.fetch(p, d, 0, p.other, p.ld_other, row);
-      at.fetch(p, d, 1, p.x, p.ld_x, row);
-      if (p.add != nullptr) at.fetch(p, d, 2, p.add, p.ld_add, row);
+      at.fetch(p.M, d, 0, p.other, p.ld_other, row);
+      at.fetch(p.M, d, 1, p.x, p.ld_x, row);
+      if (p.add != nullptr) at.fetch(p.M, d, 2, p.add, p.ld_add, row);
       ptx::cp_async_commit();
     }
   };
@@ -1033,7 +1182,7 @@ __global__ void __launch_bounds__(32 * LN_BLOCK_WARPS, 2)
   uint32_t step = 0;
   if constexpr (DROP) step = drop_step(p.drop);
   Eight w, dw, db;
-  w.weights(p.w, at.col, at.valid, WIDE, 1.0f);
+  at.weights(p.w, 1.0f, w);
   dw.clear(), db.clear();
   int64_t row = at.row;
   int d = 0;
@@ -1042,18 +1191,15 @@ __global__ void __launch_bounds__(32 * LN_BLOCK_WARPS, 2)
     float m1[R], m2[R], rstd[R];
     uint32_t words[R][4];
     if constexpr (DROP) at.words(p.drop, step, row, words);
-    if constexpr (WIDE) {
-      ptx::cp_async_wait<1>();
-      __syncwarp();
-    }
+    if constexpr (WIDE) ptx::cp_async_wait<1>();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if constexpr (WIDE) {
         at.take(d, 0, r, g[r]);
         at.take(d, 1, r, n[r]);
       } else {
-        at.load(p, p.other, p.ld_other, row + r, g[r]);
-        at.load(p, p.x, p.ld_x, row + r, n[r]);
+        at.load(p.M, p.other, p.ld_other, row + r, g[r]);
+        at.load(p.M, p.x, p.ld_x, row + r, n[r]);
       }
       rstd[r] = next_rstd[r];
       n[r].normalise(next_mean[r], rstd[r]);
@@ -1076,15 +1222,14 @@ __global__ void __launch_bounds__(32 * LN_BLOCK_WARPS, 2)
         if constexpr (WIDE)
           at.take(d, 2, r, add);
         else
-          at.load(p, p.add, p.ld_add, row + r, add);
+          at.load(p.M, p.add, p.ld_add, row + r, add);
       }
-      if (row + r >= p.M || at.valid == 0) continue;
+      if (row + r >= p.M) continue;
       norm_gradient(g[r], n[r], w, add, rstd[r], m1[r], m2[r]);
-      if (p.sum != nullptr) g[r].store(static_cast<T*>(p.sum) + (row + r) * p.ld_sum + at.col, at.valid, WIDE);
+      if (p.sum != nullptr) at.store(p.sum, p.ld_sum, row + r, WIDE, g[r]);
       if constexpr (DROP) g[r].drop(p.drop, words[r]);
-      if (p.y != nullptr) g[r].store(static_cast<T*>(p.y) + (row + r) * p.ld_y + at.col, at.valid, WIDE);
+      if (p.y != nullptr) at.store(p.y, p.ld_y, row + r, WIDE, g[r]);
     }
-    __syncwarp();  // all lanes have read
     fetch(d, row + 2 * at.stride);
     d ^= 1;
   }
@@ -1095,16 +1240,16 @@ __global__ void __launch_bounds__(32 * LN_BLOCK_WARPS, 2)
   dw.to(a);
   db.to(b);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 8; ++j)
     for (int s = 1 << p.log_lanes; s < 32; s <<= 1) {
       a[j] += __shfl_xor_sync(0xffffffffu, a[j], s);
       b[j] += __shfl_xor_sync(0xffffffffu, b[j], s);
     }
-    if (lane >> p.log_lanes == 0 && j < at.valid) {
-      shared[warp][0][at.col + j] = a[j];
-      shared[warp][1][at.col + j] = b[j];
-    }
-  }
+  if (lane >> p.log_lanes == 0)
+    at.columns([&](int j, int col) {
+      shared[warp][0][col] = a[j];
+      shared[warp][1][col] = b[j];
+    });
   __syncthreads();
   float* out = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * p.N;
   for (int i = threadIdx.x; i < 2 * p.N; i += blockDim.x) {
@@ -1170,7 +1315,7 @@ __global__ void __launch_bounds__(LN_LONG_THREADS) layer_norm_long_kernel(const 
         load_group(static_cast<const T*>(p.other) + row * p.ld_other + g * 8, p.N - g * 8, WIDE, r);
       if constexpr (DROP) {
         uint32_t w[1][4];
-        row_words(p.drop, step, static_cast<uint32_t>(row), g * 8, w);
+        drop_words(p.drop, step, {static_cast<uint32_t>(row)}, {static_cast<uint32_t>(g)}, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[j] = drop_keeps(w[0], j, p.drop.above) ? fmaf(h[j], p.drop.scale, r[j]) : r[j];
       } else {
@@ -1188,11 +1333,12 @@ __global__ void __launch_bounds__(LN_LONG_THREADS) layer_norm_long_kernel(const 
     const float mean = block_sum(s, part) * p.inv_n;
     s = 0.0f;
     for (int g = threadIdx.x; g < p.groups; g += LN_LONG_THREADS) {
-      float f[8];
-      load(g, f);
-      Eight h;
-      h.from(f);
-      s += h.squares(mean, p.N - g * 8);
+      const int valid = p.N - g * 8;
+      float h[8];
+      load(g, h);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < valid) s = fmaf(h[j] - mean, h[j] - mean, s);
     }
     const float rstd = 1.0f / sqrtf(fmaf(block_sum(s, part), p.inv_n, p.eps));
     if (threadIdx.x == 0) {
@@ -1268,7 +1414,7 @@ __global__ void __launch_bounds__(LN_LONG_THREADS) layer_norm_backward_long_kern
       if (p.y != nullptr) {
         if constexpr (DROP) {
           uint32_t words[1][4];
-          row_words(p.drop, step, static_cast<uint32_t>(row), g * 8, words);
+          drop_words(p.drop, step, {static_cast<uint32_t>(row)}, {static_cast<uint32_t>(g)}, words);
 #pragma unroll
           for (int j = 0; j < 8; ++j) dy[j] = drop_keeps(words[0], j, p.drop.above) ? dy[j] * p.drop.scale : 0.0f;
         }
