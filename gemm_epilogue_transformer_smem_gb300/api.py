@@ -702,18 +702,21 @@ _NO_MASK = (0, 0, 0, 0)
 
 
 def _first_rows(name: str, t: torch.Tensor):
-    """(type code, rows, columns, (pointer, row stride)) of the tensor a call's
-    others are checked against."""
-    code = HEAD_TYPES.get(t.dtype)
+    """(shape, dtype, type code, rows, columns, device index, (pointer, row
+    stride)) of the tensor a call's others are checked against."""
+    shape, dtype = t.shape, t.dtype
+    code = HEAD_TYPES.get(dtype)
     if code is None:
-        raise TypeError("%s: expected a bf16 or fp32 tensor, got %s" % (name, t.dtype))
-    shape = t.shape
-    if not shape:
+        raise TypeError("%s: expected a bf16 or fp32 tensor, got %s" % (name, dtype))
+    if len(shape) == 2:
+        rows, cols = shape
+    elif shape:
+        rows, cols = 1, shape[-1]
+        for n in shape[:-1]:
+            rows *= n
+    else:
         raise ValueError("%s: expected (..., columns), got a scalar" % name)
-    rows = 1
-    for n in shape[:-1]:
-        rows *= n
-    return code, rows, shape[-1], _row_stride(name, t, shape)
+    return shape, dtype, code, rows, cols, t.get_device(), _row_stride(name, t, shape)
 
 
 def _row_stride(name: str, t: torch.Tensor, shape):
@@ -736,19 +739,22 @@ def _row_stride(name: str, t: torch.Tensor, shape):
     return t.data_ptr(), ld
 
 
-def _rows(name: str, t: torch.Tensor, first: torch.Tensor):
-    """(pointer, row stride) of a tensor of first's shape, type and device, checked."""
-    shape = t.shape
-    if shape != first.shape or t.dtype is not first.dtype:
-        raise ValueError("%s: %s %s does not match %s %s"
-                         % (name, t.dtype, tuple(shape), first.dtype, tuple(first.shape)))
-    if t.get_device() != first.get_device():
+def _rows(name: str, t: Optional[torch.Tensor], shape, dtype, index: int):
+    """(pointer, row stride) of a tensor of the first one's shape, type and
+    device, checked; (0, 0) for None."""
+    if t is None:
+        return _NO_ROWS
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError("%s: %s %s does not match %s %s" % (name, t.dtype, tuple(t.shape), dtype, tuple(shape)))
+    if t.get_device() != index:
         raise ValueError("%s is on %s, not with the other tensors" % (name, t.device))
     return _row_stride(name, t, shape)
 
 
-def _values(name: str, t: torch.Tensor, n: int, index: int) -> int:
-    """Pointer of n contiguous fp32 values on device `index`, checked."""
+def _values(name: str, t: Optional[torch.Tensor], n: int, index: int) -> int:
+    """Pointer of n contiguous fp32 values on device `index`, checked; 0 for None."""
+    if t is None:
+        return 0
     if t.dtype is not torch.float32:
         raise TypeError("%s: expected a f32 tensor, got %s" % (name, t.dtype))
     if t.numel() != n or not t.is_contiguous():
@@ -770,8 +776,7 @@ def _mask(rng: Optional[Dropout], site: int, index: int):
     return step.data_ptr(), rng.seed, site, rng.threshold
 
 
-def _call_packed(entry: str, packed: bytes, first: torch.Tensor, stream) -> None:
-    index = first.get_device()
+def _call_packed(entry: str, packed: bytes, first: torch.Tensor, index: int, stream) -> None:
     if index < 0:
         raise ValueError("expected CUDA tensors, got %s" % first.device)
     fn = _head_entries.get(entry) or _head_entry(entry)
@@ -791,10 +796,10 @@ def dropout(x, rng: Dropout, *, out, residual=None, site: int = 0, stream=None) 
     (expanded rows among them); the others the same.  out may be x or residual.
     The backward pass is the same call on out's gradient, without the residual,
     whose own gradient is out's.  Asynchronous."""
-    code, rows, cols, tx = _first_rows("x", x)
-    tr = _NO_ROWS if residual is None else _rows("residual", residual, x)
-    _call_packed("gemm_epi_dropout", _DROPOUT_ARGS.pack(rows, cols, code, *_mask(rng, site, x.get_device()), *tx, *tr,
-                                                        *_rows("out", out, x)), x, stream)
+    shape, dtype, code, rows, cols, index, tx = _first_rows("x", x)
+    _call_packed("gemm_epi_dropout", _DROPOUT_ARGS.pack(
+        rows, cols, code, *_mask(rng, site, index), *tx, *_rows("residual", residual, shape, dtype, index),
+        *_rows("out", out, shape, dtype, index)), x, index, stream)
 
 
 def layer_norm(x, *, weight=None, bias=None, eps: float = 1e-5, out, residual=None, dropout: Optional[Dropout] = None,
@@ -807,18 +812,14 @@ def layer_norm(x, *, weight=None, bias=None, eps: float = 1e-5, out, residual=No
     1 and 0).  sum_out takes h, mean and rstd (fp32, one value per row) its
     statistics: what layer_norm_backward reads.  out and sum_out may each be x
     or residual.  Asynchronous."""
-    code, rows, cols, tx = _first_rows("x", x)
-    index = x.get_device()
     if sum_out is not None and residual is None and dropout is None:
         raise ValueError("sum_out without residual or dropout is x itself")
-    tr = _NO_ROWS if residual is None else _rows("residual", residual, x)
-    ts = _NO_ROWS if sum_out is None else _rows("sum_out", sum_out, x)
+    shape, dtype, code, rows, cols, index, tx = _first_rows("x", x)
     _call_packed("gemm_epi_layer_norm", _LAYER_NORM_ARGS.pack(
-        rows, cols, code, eps, *_mask(dropout, site, index), *tx, *tr, *_rows("out", out, x), *ts,
-        0 if weight is None else _values("weight", weight, cols, index),
-        0 if bias is None else _values("bias", bias, cols, index),
-        0 if mean is None else _values("mean", mean, rows, index),
-        0 if rstd is None else _values("rstd", rstd, rows, index)), x, stream)
+        rows, cols, code, eps, *_mask(dropout, site, index), *tx, *_rows("residual", residual, shape, dtype, index),
+        *_rows("out", out, shape, dtype, index), *_rows("sum_out", sum_out, shape, dtype, index),
+        _values("weight", weight, cols, index), _values("bias", bias, cols, index), _values("mean", mean, rows, index),
+        _values("rstd", rstd, rows, index)), x, index, stream)
 
 
 def layer_norm_workspace(cols: int) -> int:
@@ -839,17 +840,17 @@ def layer_norm_backward(dy, x, mean, rstd, *, weight=None, dx=None, dw=None, db=
     memory of an input.  dw and db need a workspace of layer_norm_workspace(cols)
     bytes that no call running at the same time (another stream's, another
     graph's) shares.  Asynchronous."""
-    code, rows, cols, tdy = _first_rows("dy", dy)
-    index = dy.get_device()
+    shape, dtype, code, rows, cols, index, tdy = _first_rows("dy", dy)
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd, which the forward pass gave, are needed")
     ws = ws_bytes = 0
     if workspace is not None:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace: expected a contiguous tensor with the others")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _call_packed("gemm_epi_layer_norm_backward", _LAYER_NORM_BWD_ARGS.pack(
-        rows, cols, code, *_mask(dropout, site, index), *tdy, *_rows("x", x, dy),
-        *(_NO_ROWS if add is None else _rows("add", add, dy)), *(_NO_ROWS if dx is None else _rows("dx", dx, dy)),
-        *(_NO_ROWS if d_residual is None else _rows("d_residual", d_residual, dy)),
-        0 if weight is None else _values("weight", weight, cols, index), _values("mean", mean, rows, index),
-        _values("rstd", rstd, rows, index), 0 if dw is None else _values("dw", dw, cols, index),
-        0 if db is None else _values("db", db, cols, index), ws, ws_bytes), dy, stream)
+        rows, cols, code, *_mask(dropout, site, index), *tdy, *_rows("x", x, shape, dtype, index),
+        *_rows("add", add, shape, dtype, index), *_rows("dx", dx, shape, dtype, index),
+        *_rows("d_residual", d_residual, shape, dtype, index), _values("weight", weight, cols, index),
+        _values("mean", mean, rows, index), _values("rstd", rstd, rows, index), _values("dw", dw, cols, index),
+        _values("db", db, cols, index), ws, ws_bytes), dy, index, stream)

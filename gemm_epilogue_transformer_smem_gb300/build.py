@@ -21,7 +21,7 @@ LIB = os.path.join(OUT_DIR, "libgemm_epi.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 UNITS = ["gemm_epi.cu", "spec_forward.cu", "spec_aux.cu", "spec_fp8.cu", "spec_common.cu", "spec_heads.cu",
          "spec_rotary.cu", "spec_head_norm.cu", "spec_dropout.cu", "spec_dropout_any.cu",
-         "heads.cu", "layer_norm.cu"]
+         "heads.cu", "layer_norm.cu", "layer_norm_forward.cu", "layer_norm_backward.cu"]
 
 
 def sources(csrc=CSRC):

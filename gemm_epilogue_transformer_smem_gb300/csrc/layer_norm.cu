@@ -4,97 +4,23 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
-#include <type_traits>
 
 #include "host.h"
 #include "layer_norm.cuh"
+#include "layer_norm_kernels.h"
 
 namespace {
 
 using ge_host::cuda_fail;
 using ge_host::fail;
+using ge_norm::Choice;
+using ge_norm::HELD;
+using ge_norm::Kernel;
+using ge_norm::LONG;
+using ge_norm::NARROW;
+using ge_norm::Shape;
 
 // ---------------------------------------------------------------- kernels
-
-// The kernels of a pass, by what they are compiled for.
-struct Kernel {
-  void (*fn)(ge::NormParams);
-  int warp_bytes;  // dynamic shared memory of a warp
-};
-
-enum Form { NARROW, HELD, LONG };  // teams within a warp; rows held by warps; rows read again
-
-// How a row is dealt out and by what kernel.
-struct Shape {
-  Form form;
-  int k;          // HELD: pieces of 256 columns per warp
-  int warps;      // of a team
-  int teams;      // of a block
-  int log_lanes;  // NARROW: of a team
-  int rows;       // a team works on at once
-  bool staged;    // HELD: weights through shared memory
-  int index() const { return form == HELD ? k : form == NARROW ? 0 : 9; }
-};
-
-template <class T, bool DROP, bool ADD, int K, int R, bool WIDE>
-Kernel held_forward() {
-  return {ge::layer_norm_kernel<T, DROP, ADD, K, R, WIDE>, ge::RowRing<T, K, ADD ? 2 : 1, R>::WARP_BYTES};
-}
-
-template <class T, bool DROP, bool ADD>
-Kernel held_forward(const Shape& s, bool wide) {
-  if (!wide) return held_forward<T, DROP, ADD, 4, 1, false>();
-  constexpr int TWICE = sizeof(T) == 2 ? 2 : 1;  // as many bytes of rows for either type
-  if (s.k == 2) return s.rows == 1 ? held_forward<T, DROP, ADD, 2, 1, true>() : held_forward<T, DROP, ADD, 2, 2 * TWICE, true>();
-  return s.k == 3 ? held_forward<T, DROP, ADD, 3, TWICE, true>() : held_forward<T, DROP, ADD, 4, TWICE, true>();
-}
-
-template <class T, bool DROP, bool ADD, bool WIDE, int... Ks>
-Kernel held_backward(int k) {
-  Kernel r{nullptr, 0};
-  ((k == Ks ? void(r = {ge::layer_norm_backward_kernel<T, DROP, ADD, Ks, WIDE>,
-                        ge::RowRing<T, Ks, ADD ? 3 : 2, ge::LN_BACKWARD_DEPTH<T>>::WARP_BYTES})
-            : void()), ...);
-  return r;
-}
-
-// What the kernels of either pass are chosen by.
-struct Choice {
-  bool f32, drop, add, wide;
-  int index() const { return f32 | drop << 1 | add << 2 | wide << 3; }
-};
-
-struct Forward {
-  template <class T, bool DROP>
-  static Kernel of(const Shape& s, const Choice& c) {
-    if (s.form == NARROW)
-      return {c.wide ? ge::layer_norm_narrow_kernel<T, DROP, true> : ge::layer_norm_narrow_kernel<T, DROP, false>,
-              ge::NarrowRows<T, ge::LN_NARROW_ROWS<T>, 2>::WARP_BYTES};
-    if (s.form == LONG)
-      return {c.wide ? ge::layer_norm_long_kernel<T, DROP, true> : ge::layer_norm_long_kernel<T, DROP, false>, 0};
-    if (DROP || c.add) return held_forward<T, DROP, true>(s, c.wide);  // dropout alone adds zeros
-    return held_forward<T, false, false>(s, c.wide);
-  }
-};
-
-struct Backward {
-  template <class T, bool DROP>
-  static Kernel of(const Shape& s, const Choice& c) {
-    if (s.form == NARROW)
-      return {c.wide ? ge::layer_norm_backward_narrow_kernel<T, DROP, true> : ge::layer_norm_backward_narrow_kernel<T, DROP, false>,
-              ge::NarrowRows<T, ge::LN_NARROW_BACKWARD_ROWS<T>, 3>::WARP_BYTES};
-    if (s.form == LONG)
-      return {c.wide ? ge::layer_norm_backward_long_kernel<T, DROP, true> : ge::layer_norm_backward_long_kernel<T, DROP, false>, 0};
-    if (c.add) return c.wide ? held_backward<T, DROP, true, true, 1, 2, 3, 4>(s.k) : held_backward<T, DROP, true, false, 4>(s.k);
-    return c.wide ? held_backward<T, DROP, false, true, 1, 2, 3, 4>(s.k) : held_backward<T, DROP, false, false, 4>(s.k);
-  }
-};
-
-template <class Pass>
-Kernel kernel_of(const Shape& s, const Choice& c) {
-  if (c.f32) return c.drop ? Pass::template of<float, true>(s, c) : Pass::template of<float, false>(s, c);
-  return c.drop ? Pass::template of<uint16_t, true>(s, c) : Pass::template of<uint16_t, false>(s, c);
-}
 
 Shape shape_of(bool backward, int64_t rows, int64_t cols, bool f32, bool wide, int sms) {
   const bool few = rows <= 2 * sms;
@@ -260,16 +186,20 @@ gemm_epi_status check_mask(const gemm_epi_mask& d, ge::Dropout* out) {
 
 // ---------------------------------------------------------------- launches
 
-template <class Pass>
-gemm_epi_status launch_norm(ge::NormParams& p, Choice c, int64_t most_blocks, cudaStream_t st, int* grid) {
-  constexpr bool backward = std::is_same<Pass, Backward>::value;
+// What the sum of the blocks' partial sums has to know.
+struct Launched {
+  int blocks, width;
+  bool staged;
+};
+
+gemm_epi_status launch_norm(bool backward, ge::NormParams& p, Choice c, int64_t most_blocks, cudaStream_t st, Launched* launched) {
   int dev = 0, sms = 0, resident = 0;
   gemm_epi_status s = ge_host::device_sms(&dev, &sms);
   if (s) return s;
   c.drop = p.drop.step != nullptr;
   c.add = backward ? p.add != nullptr : p.other != nullptr;
   Shape shape = shape_of(backward, p.M, p.N, c.f32, c.wide, sms);
-  const Kernel k = kernel_of<Pass>(shape, c);
+  const Kernel k = backward ? ge_norm::backward_kernel(shape, c) : ge_norm::forward_kernel(shape, c);
   if (shape.form == HELD) fit_shared(backward, shape, k);
   if ((s = resident_blocks(dev, backward, shape, c, k, &resident))) return s;
   const int64_t rows = static_cast<int64_t>(shape.teams) * shape.rows;  // a block works on at once
@@ -281,7 +211,8 @@ gemm_epi_status launch_norm(ge::NormParams& p, Choice c, int64_t most_blocks, cu
   const int warps = block_warps(shape);
   k.fn<<<static_cast<unsigned>(blocks), static_cast<unsigned>(32 * warps), shared_bytes(backward, shape, k), st>>>(p);
   const cudaError_t e = cudaGetLastError();
-  *grid = static_cast<int>(blocks);
+  *launched = {static_cast<int>(blocks), shape.form == HELD ? shape.warps * shape.k * ge::LN_PIECE : static_cast<int>(ge::partial_width(p.N)),
+               shape.form == HELD && !c.f32};
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the layer norm kernel");
 }
 
@@ -366,8 +297,8 @@ gemm_epi_status gemm_epi_layer_norm(const gemm_epi_layer_norm_args* a, void* str
   p.mean = a->mean, p.rstd = a->rstd;
   p.eps = a->eps;
   const Choice choice{c.size == 4, false, false, c.wide_in && c.wide_out && aligned(a->w, 16) && aligned(a->b, 16)};
-  int grid = 0;
-  return launch_norm<Forward>(p, choice, LIM, static_cast<cudaStream_t>(stream), &grid);
+  Launched launched;
+  return launch_norm(false, p, choice, LIM, static_cast<cudaStream_t>(stream), &launched);
 }
 
 gemm_epi_status gemm_epi_layer_norm_backward(const gemm_epi_layer_norm_bwd_args* a, void* stream) {
@@ -422,12 +353,12 @@ gemm_epi_status gemm_epi_layer_norm_backward(const gemm_epi_layer_norm_bwd_args*
   p.mean = const_cast<float*>(a->mean), p.rstd = const_cast<float*>(a->rstd);
   p.partials = wants_dw ? static_cast<float*>(a->workspace) : nullptr;
   const Choice choice{c.size == 4, false, false, c.wide_in && c.wide_out && aligned(a->w, 16)};
-  int grid = 0;
-  if ((s = launch_norm<Backward>(p, choice, most_partials(c.N), st, &grid))) return s;
+  Launched launched;
+  if ((s = launch_norm(true, p, choice, most_partials(c.N), st, &launched))) return s;
   if (!wants_dw) return GEMM_EPI_OK;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(static_cast<unsigned>((c.N + 31) / 32), 2);
+  cfg.gridDim = dim3(static_cast<unsigned>((launched.width + 127) / 128), 2);
   cfg.blockDim = dim3(32, 32);
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -436,14 +367,15 @@ gemm_epi_status gemm_epi_layer_norm_backward(const gemm_epi_layer_norm_bwd_args*
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, ge::layer_norm_weight_grad_kernel, static_cast<const float*>(p.partials), grid, p.N, a->dw,
-                         a->db);
+  e = cudaLaunchKernelEx(&cfg, ge_norm::weight_grad_kernel, static_cast<const float*>(p.partials), launched.blocks,
+                         launched.width, static_cast<int>(launched.staged), p.N, a->dw, a->db);
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the weight gradient kernel");
 }
 
 size_t gemm_epi_layer_norm_backward_workspace_size(int64_t N) {
   if (N < 1 || N > LIM - 7) return 0;
-  return static_cast<size_t>(most_partials(N)) * 2 * static_cast<size_t>(N) * sizeof(float);
+  // HELD: up to three pieces more than the row has
+  return static_cast<size_t>(most_partials(N)) * 2 * static_cast<size_t>(ge::partial_width(N) + 3 * ge::LN_PIECE) * sizeof(float);
 }
 
 }  // extern "C"
