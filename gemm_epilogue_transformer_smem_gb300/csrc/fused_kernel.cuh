@@ -204,6 +204,7 @@ struct KernelParams {
   const void* positions;  // NULL: the row index
   int32_t positions_64;
   Dropout drop;  // DROPOUT (programs with Prog::drops)
+  int32_t masks_ahead;  // 1: a tile's masks are drawn while its main loop runs
   EpiOpDev ops[GEMM_EPI_MAX_OPS];
 };
 
@@ -319,6 +320,15 @@ __host__ __device__ constexpr int prog_index_of(int code) {
 template <class Prog>
 __host__ __device__ constexpr bool prog_stages_columns() {
   if constexpr (Prog::is_static) return Prog::heads && !Prog::has(GEMM_EPI_OP_STORE_E4M3); else return Prog::heads;
+}
+// Compiled programs with dropout do so with the bias of output columns.
+template <class Prog>
+__host__ __device__ constexpr bool prog_stages_bias() {
+  if constexpr (Prog::is_static)
+    return Prog::drops && Prog::has(GEMM_EPI_OP_ADD_BIAS_COL) && !Prog::has(GEMM_EPI_OP_STORE_E4M3) &&
+           Prog::pair_at() < 0 && Prog::expand_at() < 0;
+  else
+    return false;
 }
 // First op applied to output columns: after the pair, expanding or head ops.
 template <class Prog>
@@ -676,20 +686,23 @@ __device__ __forceinline__ void apply_pointwise(CodeT code, float (&v)[NV], cons
   }
 }
 
-// DROPOUT on NV columns of a row from column col0, a multiple of 8: the mask
-// gemm_epi_dropout draws for that place of the stored matrix.
-template <int NV>
-__device__ __forceinline__ void drop_columns(const Dropout& d, uint32_t step, uint32_t row, int col0, float (&v)[NV]) {
-  if (d.step == nullptr) return;  // nothing is dropped
-  constexpr int G = NV / 8;
-  uint32_t rows[G], groups[G], w[G][4];
+// DROPOUT: which of 32 columns of a row stay, from column col0, a multiple of 32:
+// the mask gemm_epi_dropout draws for that place of the stored matrix.
+__device__ __forceinline__ uint32_t drop_bits(const Dropout& d, uint32_t step, uint32_t row, int col0) {
+  uint32_t rows[4], groups[4], w[4][4], bits = 0;
 #pragma unroll
-  for (int g = 0; g < G; ++g) rows[g] = row, groups[g] = static_cast<uint32_t>(col0 / 8 + g);
+  for (int g = 0; g < 4; ++g) rows[g] = row, groups[g] = static_cast<uint32_t>(col0 / 8 + g);
   drop_words(d, step, rows, groups, w);
 #pragma unroll
-  for (int g = 0; g < G; ++g)
+  for (int j = 0; j < 32; ++j) bits |= drop_keeps(w[j / 8], j % 8, d.above) ? 1u << j : 0u;
+  return bits;
+}
+
+// The first NV of these columns, dropped.
+template <int NV>
+__device__ __forceinline__ void drop_columns(uint32_t bits, float scale, float (&v)[NV]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[8 * g + j] = drop_keeps(w[g], j, d.above) ? v[8 * g + j] * d.scale : 0.0f;
+  for (int j = 0; j < NV; ++j) v[j] = bits >> j & 1u ? v[j] * scale : 0.0f;
 }
 
 // out[j] = silu(a[gate(j)]) * a[up(j)] (SwiGLU) or a[gate(j)] * a[up(j)]
@@ -1330,6 +1343,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
 
+      // A column vector of the tile's 256 accumulator columns, `none` past its end.
+      auto stage = [&](const float* src, float none, float* dst) {
+        const int col = nacc0 + lane * 8;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = none;
+        if (col + 8 <= p.N) {
+          const float4 a = __ldg(reinterpret_cast<const float4*>(src + col));
+          const float4 b = __ldg(reinterpret_cast<const float4*>(src + col) + 1);
+          v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (col + j < p.N) v[j] = __ldg(src + col + j);
+        }
+        float4* d = reinterpret_cast<float4*>(dst + lane * 8);
+        d[0] = make_float4(v[0], v[1], v[2], v[3]);
+        d[1] = make_float4(v[4], v[5], v[6], v[7]);
+      };
+
       // With heads, while the main loop runs: the row's position, the angles of
       // the first chunks, and the tile's column vectors, which programs without
       // an e4m3 store read from the warp's staging buffers for it; a first read
@@ -1343,24 +1376,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           position = p.positions_64 ? __ldg(static_cast<const long long*>(p.positions) + row_base + m)
                                     : __ldg(static_cast<const int*>(p.positions) + row_base + m);
         if constexpr (kStaged) {
-          auto stage = [&](const float* src, float none, float* dst) {
-            const int col = nacc0 + lane * 8;
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = none;
-            if (col + 8 <= p.N) {
-              const float4 a = __ldg(reinterpret_cast<const float4*>(src + col));
-              const float4 b = __ldg(reinterpret_cast<const float4*>(src + col) + 1);
-              v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (col + j < p.N) v[j] = __ldg(src + col + j);
-            }
-            float4* d = reinterpret_cast<float4*>(dst + lane * 8);
-            d[0] = make_float4(v[0], v[1], v[2], v[3]);
-            d[1] = make_float4(v[4], v[5], v[6], v[7]);
-          };
           if (staged) {
             __syncwarp();  // the previous tile's reads
             if (p.uses_col_scale) stage(p.col_scale, 1.0f, staged_cols);
@@ -1378,6 +1393,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
       }
+
+      // With dropout, while the main loop runs: the bias likewise, and with
+      // masks_ahead the row's mask, a bit for each column where it is dropped
+      // (accumulator columns in front of DSWIGLU), into a column of shared memory
+      // of the thread's own.  Programs with an e4m3 store, whose buffers these
+      // are, draw it between chunks.
+      uint32_t* masks = reinterpret_cast<uint32_t*>(staged_cols + BLOCK_N) + lane;
+      if constexpr (Prog::drops) {
+        if constexpr (prog_stages_bias<Prog>()) {
+          __syncwarp();  // the previous tile's reads
+          stage(p.bias, 0.0f, staged_cols);
+          __syncwarp();
+        }
+        if (p.masks_ahead) {
+          const int first = expand ? nacc0 : n0, words = paired ? BLOCK_N / 64 : BLOCK_N / 32;
+#pragma unroll 1
+          for (int i = 0; i < words; ++i)
+            masks[i * 32] = drop_bits(p.drop, dropout_step, static_cast<uint32_t>(row_base + m), first + i * 32);
+        }
+      }
+      // of the i-th 32 columns
+      auto mask_of = [&](int i) {
+        if (p.masks_ahead) return masks[i * 32];
+        return drop_bits(p.drop, dropout_step, static_cast<uint32_t>(row_base + m), (expand ? nacc0 : n0) + i * 32);
+      };
 
       // All lanes wait; the outcome is made warp-uniform so that no lane
       // leaves while the others enter a warp-synchronous step.
@@ -1613,10 +1653,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
           auto before = [&](auto code) {
-            if (Prog::drops && static_cast<int>(code) == GEMM_EPI_OP_DROPOUT)
-              drop_columns<16>(p.drop, dropout_step, static_cast<uint32_t>(row_base + m), nacc0 + c * 16, dh);
-            else
+            if (Prog::drops && static_cast<int>(code) == GEMM_EPI_OP_DROPOUT) {
+              if (p.drop.step != nullptr) drop_columns(mask_of(c / 2) >> (c % 2 * 16), p.drop.scale, dh);
+            } else {
               apply_pointwise<16>(code, dh, p, nacc0 + c * 16, p.N, rs_m);
+            }
           };
           if constexpr (kStatic) {
             static_for<0, (prog_expand_at<Prog>() < 0 ? 0 : prog_expand_at<Prog>())>([&](auto I) {
@@ -1808,9 +1849,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               for_pairs(v, [&](float2 y, int i) { return __fadd2_rn(y, make_float2(x[2 * i], x[2 * i + 1])); });
               packed = false;
               break;
+            case GEMM_EPI_OP_ADD_BIAS_COL:
+              if constexpr (prog_stages_bias<Prog>()) {
+                const float4* b4 = reinterpret_cast<const float4*>(staged_cols) + c * 8;
+                for_pairs(v, [&](float2 y, int i) {
+                  const float4 b = b4[i / 2];
+                  return __fadd2_rn(y, (i & 1) ? make_float2(b.z, b.w) : make_float2(b.x, b.y));
+                });
+              } else {
+                apply_pointwise<32>(code, v, p, col0, p.n_out, rs_m);
+              }
+              packed = false;
+              break;
             case GEMM_EPI_OP_DROPOUT:
               if constexpr (Prog::drops) {
-                drop_columns<32>(p.drop, dropout_step, static_cast<uint32_t>(row_base + m), col0, v);
+                if (p.drop.step != nullptr) drop_columns(mask_of(c), p.drop.scale, v);
                 packed = false;
               }
               break;

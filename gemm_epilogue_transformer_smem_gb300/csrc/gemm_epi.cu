@@ -739,6 +739,16 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
     L.grid = 2 * static_cast<int>(std::min<int64_t>(k.num_tiles, dev.pair_clusters));
   else
     L.grid = static_cast<int>(std::min<int64_t>(k.num_tiles, dev.sms));
+  // Drawn ahead, masks cost a few instructions more but no time where the
+  // epilogue waits for the main loop: 1003 x 4112 x 2056, one tile to a CTA pair,
+  // bias + GELU + dropout 28.8 us drawn between chunks, 26.9 ahead; dropout +
+  // DSWIGLU 38.0 and 34.1, 8192 x 4096 x 1024 143.7 and 124.4.  Programs that read
+  // a residual or pre-activation for every chunk hide that read's latency behind
+  // the drawing once the epilogue is the longer part: dropout + residual 8192 x
+  // 4096 x 1024 79.0 and 88.2, x 4096 158.0 and 158.6, 1003 x 4112 x 2056 29.1 and 26.9.
+  const int64_t at_once = L.cg == 2 ? dev.pair_clusters : dev.sms;
+  k.masks_ahead = k.drop.step != nullptr && !(P.flags & ge::F_E8) &&
+                  (!(P.flags & ge::F_AUX) || P.expand_at >= 0 || k.num_tiles <= at_once);
 
   if (d.K > 0) {
     const CUtensorMapDataType op_dt = P.in8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
