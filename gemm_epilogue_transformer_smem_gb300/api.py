@@ -716,7 +716,8 @@ def _first_rows(name: str, t: torch.Tensor):
             rows *= n
     else:
         raise ValueError("%s: expected (..., columns), got a scalar" % name)
-    return shape, dtype, code, rows, cols, t.get_device(), _row_stride(name, t, shape)
+    at = (t.data_ptr(), cols) if t.is_contiguous() else _row_stride(name, t, shape)
+    return shape, dtype, code, rows, cols, t.get_device(), at
 
 
 def _row_stride(name: str, t: torch.Tensor, shape):
@@ -748,6 +749,8 @@ def _rows(name: str, t: Optional[torch.Tensor], shape, dtype, index: int):
         raise ValueError("%s: %s %s does not match %s %s" % (name, t.dtype, tuple(t.shape), dtype, tuple(shape)))
     if t.get_device() != index:
         raise ValueError("%s is on %s, not with the other tensors" % (name, t.device))
+    if t.is_contiguous():  # a third of the time that strides take
+        return t.data_ptr(), shape[-1]
     return _row_stride(name, t, shape)
 
 

@@ -22,41 +22,93 @@ using ge_norm::Shape;
 
 // ---------------------------------------------------------------- kernels
 
-Shape shape_of(bool backward, int64_t rows, int64_t cols, bool f32, bool wide, int sms) {
+// How many pieces of 256 columns a warp holds, how many rows a team works on at
+// once, how many teams share a block and whether they share the weights: from
+// timing them all at 512 to 14336 columns (one GB300, 537 MB forward, 671 MB
+// backward with dropout; the times beside the rules are of those).  Few rows:
+// not more than two to an SM, whose latency counts, so many warps to a row and
+// nothing staged.
+Shape forward_shape(int64_t rows, int64_t pieces, const Choice& c, int sms) {
   const bool few = rows <= 2 * sms;
-  Shape s{NARROW, 0, 1, 1, 0, 1, false};
+  bool staged = c.drop;
+  Shape s{HELD, 4, 1, 1, 0, 1, false};
+  auto take = [&](int k, int r) {
+    s.k = k, s.rows = r;
+    s.warps = static_cast<int>((pieces + k - 1) / k);
+  };
+  auto warps = [&](int n) { s.teams = std::max(1, n / s.warps); };
+  if (!c.wide) {
+    take(4, 1);
+  } else if (few && pieces <= 2 * ge::LN_MAX_WARPS) {
+    take(2, 1);
+  } else if (c.f32) {
+    // 8192 x 4096: 2 pieces, 2 rows 90.8 us with dropout, 4 and 1 94.9
+    pieces <= 2 * ge::LN_MAX_WARPS ? take(2, 2) : take(4, 1);
+    if (c.drop || !c.add) warps(16);
+  } else if (!c.drop && !c.add) {
+    // one stream in: 4096 columns with 2 pieces, 1 row over 75 us, 4 and 2 47.8 (57.1
+    // not staged); 512: 46.0 with 2 and 1, over 53 with 4 and 2
+    pieces <= 2 ? take(2, 1) : take(4, 2);
+    warps(16);
+    staged = true;
+  } else if (pieces <= (c.drop ? 8 : 16)) {
+    // 2048 columns: 2 pieces, 1 row 85.3 us (89.4 with dropout), 4 and 2 92.2 (93.5);
+    // 4096: 88.7 (96.3) and 91.5 (91.5)
+    take(2, 1);
+    warps(c.drop || s.warps <= 4 ? 16 : 8);
+  } else {
+    // 8192: one team to a block 89.4 us (95.6 with dropout), two that share the
+    // weights 100 (94.2)
+    take(4, 2);
+    if (c.drop) warps(16);
+  }
+  // For few rounds staging the weights costs more than their misses in L1 (1777 x
+  // 1024 5.9 us staged, 4.9 not).
+  s.staged = c.wide && !c.f32 && staged && rows > 16 * sms;
+  return s;
+}
+
+Shape backward_shape(int64_t rows, int64_t pieces, const Choice& c, int sms) {
+  const bool few = rows <= 2 * sms;
+  Shape s{HELD, 4, 1, 1, 0, 1, false};
+  auto take = [&](int k) {
+    s.k = k;
+    s.warps = static_cast<int>((pieces + k - 1) / k);
+  };
+  if (!c.wide) {
+    take(4);
+  } else if (few) {
+    take(pieces <= ge::LN_MAX_WARPS ? 1 : pieces <= 2 * ge::LN_MAX_WARPS ? 2 : 4);
+    return s;
+  } else if (c.f32) {
+    // 67108 x 1000: 1 piece 94.2 us, 4 109.9; 8192 x 4096: 2 pieces 95.6 us, 4 100.0
+    take(pieces <= 4 ? 1 : pieces <= 2 * ge::LN_MAX_WARPS ? 2 : 4);
+  } else {
+    // 1024 columns: 2 pieces 88.1 us (109.6 with dropout), 4 91.5 (123.9);
+    // 4096: 101.7 (130.0) and 91.5 (115.7)
+    take(pieces <= 8 ? 2 : 4);
+  }
+  // 4096 columns with dropout: one team to a block 115.7 us, four 126.5; without 94.2
+  // and 91.5
+  s.teams = c.drop && pieces > 8 ? 1 : ge::LN_MAX_WARPS / s.warps;
+  s.staged = c.wide;  // 4096: 91.5 us, 113.3 from L1
+  return s;
+}
+
+Shape shape_of(bool backward, int64_t rows, int64_t cols, const Choice& c, int sms) {
   const int64_t groups = (cols + 7) / 8, pieces = (cols + ge::LN_PIECE - 1) / ge::LN_PIECE;
   if (groups <= 32) {
+    Shape s{NARROW, 0, 1, 1, 0, 1, false};
     while ((1 << s.log_lanes) < groups) ++s.log_lanes;
-    s.rows = backward ? (f32 ? ge::LN_NARROW_BACKWARD_ROWS<float> : ge::LN_NARROW_BACKWARD_ROWS<uint16_t>)
-                      : (f32 ? ge::LN_NARROW_ROWS<float> : ge::LN_NARROW_ROWS<uint16_t>);
+    s.rows = backward ? (c.f32 ? ge::LN_NARROW_BACKWARD_ROWS<float> : ge::LN_NARROW_BACKWARD_ROWS<uint16_t>)
+                      : (c.f32 ? ge::LN_NARROW_ROWS<float> : ge::LN_NARROW_ROWS<uint16_t>);
     s.teams = ge::LN_BLOCK_WARPS << (5 - s.log_lanes);
     return s;
   }
-  if (pieces > 4 * ge::LN_MAX_WARPS) {
-    s.form = LONG;
-    s.warps = ge::LN_LONG_THREADS / 32;
-    return s;
-  }
-  s.form = HELD;
-  auto take = [&](int k) {
-    const int warps = static_cast<int>((pieces + k - 1) / k);
-    if (warps > ge::LN_MAX_WARPS || (s.k && s.k * s.warps <= k * warps)) return;
-    s.k = k;
-    s.warps = warps;
-  };
-  if (!wide) {
-    take(4);
-  } else if (few) {
-    for (int k : {backward ? 1 : 2, backward ? 2 : 4, 4})
-      if (!s.k) take(k);
-  } else {
-    for (int k : {4, 3, 2}) take(k);
-  }
-  if (!backward && wide && !(few && s.k == 2)) s.rows = (s.k == 2 ? 4 : 2) / (f32 ? 2 : 1);
+  if (pieces > 4 * ge::LN_MAX_WARPS) return Shape{LONG, 0, ge::LN_LONG_THREADS / 32, 1, 0, 1, false};
+  Shape s = backward ? backward_shape(rows, pieces, c, sms) : forward_shape(rows, pieces, c, sms);
   // a block to every SM before a second team to a block
-  s.teams = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(ge::LN_MAX_WARPS / s.warps, rows / (s.rows * sms))));
-  s.staged = wide && !few;  // pays where a team has several rows
+  s.teams = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s.teams, rows / (s.rows * sms))));
   return s;
 }
 
@@ -198,7 +250,7 @@ gemm_epi_status launch_norm(bool backward, ge::NormParams& p, Choice c, int64_t 
   if (s) return s;
   c.drop = p.drop.step != nullptr;
   c.add = backward ? p.add != nullptr : p.other != nullptr;
-  Shape shape = shape_of(backward, p.M, p.N, c.f32, c.wide, sms);
+  Shape shape = shape_of(backward, p.M, p.N, c, sms);
   const Kernel k = backward ? ge_norm::backward_kernel(shape, c) : ge_norm::forward_kernel(shape, c);
   if (shape.form == HELD) fit_shared(backward, shape, k);
   if ((s = resident_blocks(dev, backward, shape, c, k, &resident))) return s;

@@ -23,8 +23,8 @@ Kernel of(const Shape& s, const Choice& c) {
             ge::NarrowRows<T, ge::LN_NARROW_BACKWARD_ROWS<T>, 3>::WARP_BYTES};
   if (s.form == LONG)
     return {c.wide ? ge::layer_norm_backward_long_kernel<T, DROP, true> : ge::layer_norm_backward_long_kernel<T, DROP, false>, 0};
-  if (c.add) return c.wide ? held_backward<T, DROP, true, true, 1, 2, 3, 4>(s.k) : held_backward<T, DROP, true, false, 4>(s.k);
-  return c.wide ? held_backward<T, DROP, false, true, 1, 2, 3, 4>(s.k) : held_backward<T, DROP, false, false, 4>(s.k);
+  if (c.add) return c.wide ? held_backward<T, DROP, true, true, 1, 2, 4>(s.k) : held_backward<T, DROP, true, false, 4>(s.k);
+  return c.wide ? held_backward<T, DROP, false, true, 1, 2, 4>(s.k) : held_backward<T, DROP, false, false, 4>(s.k);
 }
 
 }  // namespace

@@ -14,9 +14,11 @@ Kernel held_forward() {
 template <class T, bool DROP, bool ADD>
 Kernel held_forward(const Shape& s, bool wide) {
   if (!wide) return held_forward<T, DROP, ADD, 4, 1, false>();
-  constexpr int TWICE = sizeof(T) == 2 ? 2 : 1;  // as many bytes of rows for either type
-  if (s.k == 2) return s.rows == 1 ? held_forward<T, DROP, ADD, 2, 1, true>() : held_forward<T, DROP, ADD, 2, 2 * TWICE, true>();
-  return s.k == 3 ? held_forward<T, DROP, ADD, 3, TWICE, true>() : held_forward<T, DROP, ADD, 4, TWICE, true>();
+  if (s.k == 2 && s.rows == 1) return held_forward<T, DROP, ADD, 2, 1, true>();
+  if constexpr (sizeof(T) == 2)
+    return held_forward<T, DROP, ADD, 4, 2, true>();
+  else
+    return s.k == 2 ? held_forward<T, DROP, ADD, 2, 2, true>() : held_forward<T, DROP, ADD, 4, 1, true>();
 }
 
 template <class T, bool DROP>
