@@ -62,9 +62,10 @@ Shape forward_shape(int64_t rows, int64_t pieces, const Choice& c, int sms) {
     take(4, 2);
     if (c.drop) warps(16);
   }
+  if (!c.wide) warps(16);
   // For few rounds staging the weights costs more than their misses in L1 (1777 x
   // 1024 5.9 us staged, 4.9 not).
-  s.staged = c.wide && !c.f32 && staged && rows > 16 * sms;
+  s.staged = c.wide ? !c.f32 && staged && rows > 16 * sms : !few;
   return s;
 }
 
@@ -76,7 +77,9 @@ Shape backward_shape(int64_t rows, int64_t pieces, const Choice& c, int sms) {
     s.warps = static_cast<int>((pieces + k - 1) / k);
   };
   if (!c.wide) {
-    take(4);
+    // by words 4 pieces spill 124 to 192 bytes of registers
+    take(pieces <= 2 * ge::LN_MAX_WARPS ? 2 : 4);
+    if (few) return s;
   } else if (few) {
     take(pieces <= ge::LN_MAX_WARPS ? 1 : pieces <= 2 * ge::LN_MAX_WARPS ? 2 : 4);
     return s;
@@ -90,8 +93,8 @@ Shape backward_shape(int64_t rows, int64_t pieces, const Choice& c, int sms) {
   }
   // 4096 columns with dropout: one team to a block 115.7 us, four 126.5; without 94.2
   // and 91.5
-  s.teams = c.drop && pieces > 8 ? 1 : ge::LN_MAX_WARPS / s.warps;
-  s.staged = c.wide;  // 4096: 91.5 us, 113.3 from L1
+  s.teams = c.wide && c.drop && pieces > 8 ? 1 : ge::LN_MAX_WARPS / s.warps;
+  s.staged = true;  // 4096: 91.5 us, 113.3 from L1
   return s;
 }
 
@@ -155,21 +158,25 @@ struct DropoutKernel {
   void (*fn)(ge::DropoutParams);
   int span;  // columns of a warp's share of a row, or of a thread's
   bool narrow;
+  int bytes;  // dynamic shared memory
 };
 
-template <class T>
-DropoutKernel dropout_kernel_of(int64_t cols) {
-  if (cols <= ge::LN_PIECE) return {ge::dropout_narrow_kernel<T>, 8, true};
-  // as many pieces to a warp as leave few of a row's last share's empty
-  constexpr int MOST = 4 / ge::Group<T>::PIECES;
-  const int64_t pieces = (cols + ge::LN_PIECE - 1) / ge::LN_PIECE;
-  if (MOST == 4 && ((pieces + 3) / 4 * 4 - pieces) * 8 <= pieces) return {ge::dropout_kernel<T, MOST>, MOST * ge::LN_PIECE, false};
-  if (((pieces + 1) / 2 * 2 - pieces) * 8 <= pieces) return {ge::dropout_kernel<T, 2>, 2 * ge::LN_PIECE, false};
-  return {ge::dropout_kernel<T, 1>, ge::LN_PIECE, false};
+template <class T, int K>
+DropoutKernel dropout_kernel_of(bool wide) {
+  if (wide) return {ge::dropout_kernel<T, K, true>, K * ge::LN_PIECE, false, 0};
+  return {ge::dropout_kernel<T, K, false>, K * ge::LN_PIECE, false,
+          ge::DO_THREADS / 32 * (ge::WordRing<T, K, 2, 1>::WARP_BYTES + 1024)};
 }
 
-DropoutKernel dropout_kernel_of(int64_t cols, bool f32) {
-  return f32 ? dropout_kernel_of<float>(cols) : dropout_kernel_of<uint16_t>(cols);
+template <class T>
+DropoutKernel dropout_kernel_of(int64_t cols, bool wide) {
+  if (cols <= ge::LN_PIECE) return {ge::dropout_narrow_kernel<T>, 8, true, 0};
+  // as many pieces to a warp as leave few of a row's last share's empty
+  const int64_t pieces = (cols + ge::LN_PIECE - 1) / ge::LN_PIECE;
+  auto few_empty = [&](int64_t k) { return ((pieces + k - 1) / k * k - pieces) * 8 <= pieces; };
+  if constexpr (sizeof(T) == 2)
+    if (few_empty(4)) return dropout_kernel_of<T, 4>(wide);
+  return few_empty(2) ? dropout_kernel_of<T, 2>(wide) : dropout_kernel_of<T, 1>(wide);
 }
 
 // Rows of partial sums of dw and db: the most blocks a backward pass has.
@@ -303,14 +310,15 @@ gemm_epi_status gemm_epi_dropout(const gemm_epi_dropout_args* a, void* stream) {
   p.residual = a->residual, p.ld_residual = a->ld_residual;
   p.y = a->y, p.ld_y = a->ld_y;
   p.wide_in = c.wide_in, p.wide_out = c.wide_out;
-  const DropoutKernel k = dropout_kernel_of(c.N, c.size == 4);
+  const bool wide = c.wide_in && c.wide_out;
+  const DropoutKernel k = c.size == 4 ? dropout_kernel_of<float>(c.N, wide) : dropout_kernel_of<uint16_t>(c.N, wide);
   p.spans = static_cast<int32_t>((c.N + k.span - 1) / k.span);
   p.total = c.M * p.spans;
   const int64_t each = k.narrow ? ge::DO_THREADS : ge::DO_THREADS / 32;  // spans of a block
   const int64_t blocks = std::min<int64_t>((p.total + each - 1) / each, static_cast<int64_t>(sms) * ge::DO_BLOCKS);
   p.step_rows = blocks * each / p.spans;
   p.step_spans = static_cast<int32_t>(blocks * each % p.spans);
-  k.fn<<<static_cast<unsigned>(blocks), ge::DO_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  k.fn<<<static_cast<unsigned>(blocks), ge::DO_THREADS, static_cast<size_t>(k.bytes), static_cast<cudaStream_t>(stream)>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? GEMM_EPI_OK : cuda_fail(e, "launch of the dropout kernel");
 }
@@ -348,7 +356,8 @@ gemm_epi_status gemm_epi_layer_norm(const gemm_epi_layer_norm_args* a, void* str
   p.w = a->w, p.b = a->b;
   p.mean = a->mean, p.rstd = a->rstd;
   p.eps = a->eps;
-  const Choice choice{c.size == 4, false, false, c.wide_in && c.wide_out && aligned(a->w, 16) && aligned(a->b, 16)};
+  p.wide_w = aligned(a->w, 16) && aligned(a->b, 16);
+  const Choice choice{c.size == 4, false, false, c.wide_in && c.wide_out && p.wide_w};
   Launched launched;
   return launch_norm(false, p, choice, LIM, static_cast<cudaStream_t>(stream), &launched);
 }
@@ -404,7 +413,8 @@ gemm_epi_status gemm_epi_layer_norm_backward(const gemm_epi_layer_norm_bwd_args*
   p.w = a->w;
   p.mean = const_cast<float*>(a->mean), p.rstd = const_cast<float*>(a->rstd);
   p.partials = wants_dw ? static_cast<float*>(a->workspace) : nullptr;
-  const Choice choice{c.size == 4, false, false, c.wide_in && c.wide_out && aligned(a->w, 16)};
+  p.wide_w = aligned(a->w, 16);
+  const Choice choice{c.size == 4, false, false, c.wide_in && c.wide_out && p.wide_w};
   Launched launched;
   if ((s = launch_norm(true, p, choice, most_partials(c.N), st, &launched))) return s;
   if (!wants_dw) return GEMM_EPI_OK;

@@ -23,6 +23,7 @@
 
 #include <stdint.h>
 
+#include <type_traits>
 #include <utility>
 
 #include "dropout.cuh"
@@ -267,6 +268,7 @@ struct NormParams {
   int32_t M, N, groups;
   int32_t warps;      // of a team
   int32_t staged;     // the norm's weights go through shared memory
+  int32_t wide_w;     // else: 16-byte accesses serve them
   int32_t log_lanes;  // teams within a warp: 2^log_lanes threads each
   const void* x;      // backward: h, the forward pass's normalised sum
   int64_t ld_x;
@@ -449,6 +451,97 @@ struct RowRing {
   }
 };
 
+// The same for rows that start anywhere: a warp copies its columns word by word
+// as they lie in memory, so a lane reads what others copied, and with bf16 rows
+// that start between two words every lane's values lie half a word off.  A
+// __syncwarp() lies between the copies' end and the reads, and the reads and the
+// next copies.  (By single elements straight to registers, 16384 x 4095 bf16 with
+// dropout and residual took 435 us.)
+template <class T, int K, int TENSORS, int DEPTH>
+struct WordRing {
+  using Place = RowPlace<T, K>;
+  static constexpr int SEGMENT = K * Place::PARTS * 512 + 128;  // of a row's columns, half a word off or not
+  static constexpr int WARP_BYTES = DEPTH * TENSORS * SEGMENT;
+  uint8_t* slots;  // the warp's
+  uint32_t at;
+
+  __device__ __forceinline__ WordRing(uint4* smem, int warp)
+      : slots(reinterpret_cast<uint8_t*>(smem) + warp * WARP_BYTES), at(ptx::smem_addr(slots)) {}
+  // Bytes that `row` lies behind a word's start: 2 or 0.
+  static __device__ __forceinline__ uint32_t shift(const T* row) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 3u;
+  }
+  // `row`: at the warp's first column, `count` of which are in the row.
+  __device__ __forceinline__ void fetch(int d, int t, const T* row, int count) const {
+    if (count <= 0) return;
+    const uint32_t off = shift(row), bytes = static_cast<uint32_t>(count) * sizeof(T) + off;
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(row) - off;
+    const int segment = (d * TENSORS + t) * SEGMENT;
+#pragma unroll 4
+    for (uint32_t i = (threadIdx.x & 31) * 4; i < bytes; i += 128) {
+      if (i == 0 && off != 0)  // nothing in front of the row is read
+        *reinterpret_cast<uint16_t*>(slots + segment + 2) = *reinterpret_cast<const uint16_t*>(row);
+      else
+        ptx::cp_async4(at + segment + i, src + i, min(bytes - i, 4u));
+    }
+  }
+  // Zeros behind the row's end.
+  __device__ __forceinline__ void take(int d, int t, int k, const T* row, const Place& place, Eight& v) const {
+    Group<T> g;
+    const uint8_t* from = slots + (d * TENSORS + t) * SEGMENT + (k * LN_PIECE + (threadIdx.x & 31) * Place::EACH) * sizeof(T);
+#pragma unroll
+    for (int i = 0; i < Place::PARTS; ++i)
+      g.q[i] = *reinterpret_cast<const uint4*>(from + i * Place::APART * sizeof(T));
+    if (shift(row) != 0) {
+      const uint32_t next = *reinterpret_cast<const uint32_t*>(from + 16);
+      uint4& q = g.q[0];
+      q = make_uint4(__funnelshift_r(q.x, q.y, 16), __funnelshift_r(q.y, q.z, 16), __funnelshift_r(q.z, q.w, 16),
+                     __funnelshift_r(q.w, next, 16));
+    }
+    float f[8];
+    g.unpack(f);
+    if (!place.full) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = j % Place::EACH < place.valid(k, j / Place::EACH) ? f[j] : 0.0f;
+    }
+    v.from(f);
+  }
+};
+
+// Piece k of a warp's columns to a row that starts anywhere, through 1 KB of
+// shared memory of the warp's own: words, side by side.  `row`: at the warp's
+// first column, `count` of which are in the row.
+template <class T>
+__device__ __forceinline__ void store_words(uint4* smem, T* row, int count, int k, const Eight& v) {
+  Group<T> g;
+  float f[8];
+  v.to(f);
+  g.pack(f);
+  const int lane = threadIdx.x & 31, left = min(count - k * LN_PIECE, LN_PIECE);
+#pragma unroll
+  for (int i = 0; i < Group<T>::PIECES; ++i) smem[i * 32 + lane] = g.q[i];
+  __syncwarp();
+  T* to = row + k * LN_PIECE;
+  const T* from = reinterpret_cast<const T*>(smem);
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (lane + 32 * j < left) to[lane + 32 * j] = from[lane + 32 * j];
+  } else {
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1) & 1;  // an element in front of the first word
+    if (odd && lane == 0 && left > 0) to[0] = from[0];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = odd + 2 * (lane + 32 * j);
+      if (e + 1 < left)
+        *reinterpret_cast<uint32_t*>(to + e) = static_cast<uint32_t>(from[e]) | static_cast<uint32_t>(from[e + 1]) << 16;
+      else if (e < left)
+        to[e] = from[e];
+    }
+  }
+  __syncwarp();
+}
+
 // ------------------------------------------------------------------ dropout
 
 constexpr int DO_THREADS = 256;
@@ -470,55 +563,75 @@ struct DropoutParams {
   Dropout drop;
 };
 
-__device__ __forceinline__ void drop_piece(const DropoutParams& p, const uint32_t (&words)[4], Eight& v, const Eight& add) {
-  if (p.drop.step != nullptr)
-    v.drop_onto(add, p.drop, words);
-  else
-    v.plus(add);
-}
-
-// A warp to K pieces of a row.
-template <class T, int K>
+// A warp to K pieces of a row.  WIDE as in the norm's kernels.
+template <class T, int K, bool WIDE>
 __global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_kernel(const __grid_constant__ DropoutParams p) {
+  using Words = WordRing<T, K, 2, 1>;
+  extern __shared__ __align__(128) uint4 ln_smem[];  // by words: rings, then what is stored through
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (DO_THREADS / 32);
   int64_t i = static_cast<int64_t>(blockIdx.x) * (DO_THREADS / 32) + (threadIdx.x >> 5);
   int64_t row = i / p.spans;
   int32_t span = static_cast<int32_t>(i - row * p.spans);
   const uint32_t step = p.drop.step != nullptr ? drop_step(p.drop) : 0;
   for (; i < p.total; i += warps) {
-    const RowPlace<T, K> place(p.N, span * K * LN_PIECE);
-    const T* x = static_cast<const T*>(p.x) + row * p.ld_x + place.col;
-    const T* residual = p.residual != nullptr ? static_cast<const T*>(p.residual) + row * p.ld_residual + place.col : nullptr;
-    T* y = static_cast<T*>(p.y) + row * p.ld_y + place.col;
-    Group<T> g[K], r[K];
+    const int begin = span * K * LN_PIECE;
+    const RowPlace<T, K> place(p.N, begin);
     uint32_t words[K][4];
-    auto load = [&](bool all, bool wide) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        place.load(x, k, wide, all, g[k]);
-        r[k].clear();
-        if (residual != nullptr) place.load(residual, k, wide, all, r[k]);
-      }
+    auto finish = [&](int k, Eight& v, const Eight& add) {
+      if (p.drop.step != nullptr)
+        v.drop_onto(add, p.drop, words[k]);
+      else
+        v.plus(add);
     };
-    auto store = [&](bool all, bool wide) {
+    if constexpr (WIDE) {
+      const T* x = static_cast<const T*>(p.x) + row * p.ld_x + place.col;
+      const T* residual = p.residual != nullptr ? static_cast<const T*>(p.residual) + row * p.ld_residual + place.col : nullptr;
+      T* y = static_cast<T*>(p.y) + row * p.ld_y + place.col;
+      Group<T> g[K], r[K];
+      auto load = [&](bool all) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          place.load(x, k, true, all, g[k]);
+          r[k].clear();
+          if (residual != nullptr) place.load(residual, k, true, all, r[k]);
+        }
+      };
+      auto store = [&](bool all) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          Eight v, add;
+          v.from(g[k]);
+          add.from(r[k]);
+          finish(k, v, add);
+          place.store(y, k, true, all, v);
+        }
+      };
+      place.full ? load(true) : load(false);
+      if (p.drop.step != nullptr) place.words(p.drop, step, static_cast<uint32_t>(row), 0, words);
+      place.full ? store(true) : store(false);
+    } else {
+      const int warp = threadIdx.x >> 5, count = min(p.N - begin, K * LN_PIECE);
+      const Words ring(ln_smem, warp);
+      uint4* staging = ln_smem + DO_THREADS / 32 * (Words::WARP_BYTES / 16) + warp * 64;
+      const T* x = static_cast<const T*>(p.x) + row * p.ld_x + begin;
+      const T* residual = p.residual != nullptr ? static_cast<const T*>(p.residual) + row * p.ld_residual + begin : nullptr;
+      __syncwarp();  // the previous share's reads
+      ring.fetch(0, 0, x, count);
+      if (residual != nullptr) ring.fetch(0, 1, residual, count);
+      ptx::cp_async_commit();
+      if (p.drop.step != nullptr) place.words(p.drop, step, static_cast<uint32_t>(row), 0, words);
+      ptx::cp_async_wait<0>();
+      __syncwarp();
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         Eight v, add;
-        v.from(g[k]);
-        add.from(r[k]);
-        drop_piece(p, words[k], v, add);
-        place.store(y, k, wide, all, v);
+        add.clear();
+        ring.take(0, 0, k, x, place, v);
+        if (residual != nullptr) ring.take(0, 1, k, residual, place, add);
+        finish(k, v, add);
+        store_words<T>(staging, static_cast<T*>(p.y) + row * p.ld_y + begin, count, k, v);
       }
-    };
-    if (place.full && p.wide_in)
-      load(true, true);
-    else
-      load(false, p.wide_in);
-    if (p.drop.step != nullptr) place.words(p.drop, step, static_cast<uint32_t>(row), 0, words);
-    if (place.full && p.wide_out)
-      store(true, true);
-    else
-      store(false, p.wide_out);
+    }
     row += p.step_rows, span += p.step_spans;
     if (span >= p.spans) span -= p.spans, ++row;
   }
@@ -557,7 +670,10 @@ __global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_narrow_kernel(c
       Eight v, add;
       v.from(x[u]);
       add.from(r[u]);
-      drop_piece(p, words[u], v, add);
+      if (p.drop.step != nullptr)
+        v.drop_onto(add, p.drop, words[u]);
+      else
+        v.plus(add);
       float f[8];
       v.to(f);
       const int col = static_cast<int>(groups[u]) * 8;
@@ -570,8 +686,12 @@ __global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_narrow_kernel(c
 
 // ------------------------------------------------------------------ teams
 
-// A block's teams, and where its shared memory's parts begin: the ring, then
-// the norm's weights.
+// Shared memory of a warp: its ring, and what it stores words through.
+template <class Ring, bool WIDE>
+constexpr int HELD_WARP_BYTES = Ring::WARP_BYTES + (WIDE ? 0 : 1024);
+
+// A block's teams.  Its shared memory: the warps' rings, by words what they store
+// through, the norm's weights.
 template <int K>
 struct Teams {
   int warp, team, count;  // of the thread; of the block
@@ -609,47 +729,54 @@ __device__ __forceinline__ void staged_weights(const float* w, int k, Eight& v) 
 // A team works on R neighbouring rows at once: they share the weights' reads,
 // and their sums' shuffles and the barrier overlap.  WIDE: every tensor takes
 // 16-byte accesses, and its rows come through the ring (with a depth of 1: rows
-// are in registers while the next ones are on their way); else single elements,
-// straight to registers.
+// are in registers while the next ones are on their way); else they come and go
+// by words.
 template <class T, bool DROP, bool ADD, int K, int R, bool WIDE>
 __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __grid_constant__ NormParams p) {
-  using Ring = RowRing<T, K, ADD ? 2 : 1, R>;
+  using Ring = std::conditional_t<WIDE, RowRing<T, K, ADD ? 2 : 1, R>, WordRing<T, K, ADD ? 2 : 1, R>>;
   extern __shared__ __align__(128) uint4 ln_smem[];
   __shared__ float4 part[2][R][LN_MAX_WARPS + 3];  // a warp's mean, sum of squares from it, count
   const Teams<K> teams(p);
   const int warp = teams.warp_in_team(p);
   const RowPlace<T, K> place(p.N, warp * K * LN_PIECE);
   const Ring ring(ln_smem, teams.warp);
+  uint4* staging = ln_smem + (blockDim.x >> 5) * (Ring::WARP_BYTES / 16) + teams.warp * 64;  // by words: the warp's 1 KB
   const uint32_t rows = static_cast<uint32_t>(p.M), stride = static_cast<uint32_t>(teams.stride) * R;
   const bool residual = ADD && p.other != nullptr;
   // worked out where they are needed: kept, they would cost registers
-  auto at = [&](const void* data, int64_t ld, uint32_t row) { return static_cast<const T*>(data) + row * ld + place.col; };
+  const int begin = WIDE ? place.col : warp * K * LN_PIECE;
+  const int count = min(max(p.N - warp * K * LN_PIECE, 0), K * LN_PIECE);  // of the warp's values
+  auto at = [&](const void* data, int64_t ld, uint32_t row) { return static_cast<const T*>(data) + row * ld + begin; };
   auto fetch = [&](uint32_t row) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
       if (row + r < rows) {
-        ring.fetch(r, 0, at(p.x, p.ld_x, row + r), place);
-        if (residual) ring.fetch(r, 1, at(p.other, p.ld_other, row + r), place);
+        if constexpr (WIDE) {
+          ring.fetch(r, 0, at(p.x, p.ld_x, row + r), place);
+          if (residual) ring.fetch(r, 1, at(p.other, p.ld_other, row + r), place);
+        } else {
+          ring.fetch(r, 0, at(p.x, p.ld_x, row + r), count);
+          if (residual) ring.fetch(r, 1, at(p.other, p.ld_other, row + r), count);
+        }
       }
     ptx::cp_async_commit();
   };
   const uint32_t first_row = static_cast<uint32_t>(teams.first) * R;
   if constexpr (WIDE) {
     if (!place.full || (ADD && !residual)) ring.clear(place, residual ? 2 : 1);
-    fetch(first_row);
   }
+  fetch(first_row);
   uint32_t step = 0;
   if constexpr (DROP) step = drop_step(p.drop);
   const float* weights = nullptr;  // this thread's, staged: w, then b `width` further on
   if (p.staged) {
-    float* to = reinterpret_cast<float*>(ln_smem + (blockDim.x >> 5) * (Ring::WARP_BYTES / 16));
+    float* to = reinterpret_cast<float*>(ln_smem + (blockDim.x >> 5) * (HELD_WARP_BYTES<Ring, WIDE> / 16));
     stage_weights<T>(to, p.w, p.N, teams.width, 1.0f);
     stage_weights<T>(to + teams.width, p.b, p.N, teams.width, 0.0f);
     weights = to + warp * K * LN_PIECE + (threadIdx.x & 31) * 4;
     __syncthreads();
   }
 
-  const int count = min(max(p.N - warp * K * LN_PIECE, 0), K * LN_PIECE);  // of the warp's values
   const float inv_count = 1.0f / static_cast<float>(max(count, 1));
   int parity = 0;
   for (uint32_t row = first_row; row < rows; row += stride) {
@@ -659,7 +786,10 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
     for (int r = 0; r < R; ++r) {
       uint32_t words[K][4];
       if constexpr (DROP) place.words(p.drop, step, row + r, 0, words);
-      if (WIDE && r == 0) ptx::cp_async_wait<0>();
+      if (r == 0) {
+        ptx::cp_async_wait<0>();
+        if constexpr (!WIDE) __syncwarp();
+      }
       float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -669,13 +799,8 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
           ring.take(r, 0, k, h[r][k]);
           if constexpr (ADD) ring.take(r, 1, k, add);
         } else {
-          Group<T> g;
-          place.load(at(p.x, p.ld_x, row + r), k, false, false, g);
-          h[r][k].from(g);
-          if (residual) {
-            place.load(at(p.other, p.ld_other, row + r), k, false, false, g);
-            add.from(g);
-          }
+          ring.take(r, 0, k, at(p.x, p.ld_x, row + r), place, h[r][k]);
+          if (residual) ring.take(r, 1, k, at(p.other, p.ld_other, row + r), place, add);
         }
         if constexpr (DROP)
           h[r][k].drop_onto(add, p.drop, words[k]);
@@ -685,7 +810,8 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
       }
       mean[r] = s2.x + s2.y;
     }
-    if constexpr (WIDE) fetch(row + stride);  // the slots' values are in registers
+    if constexpr (!WIDE) __syncwarp();
+    fetch(row + stride);  // the slots' values are in registers
 
 #pragma unroll
     for (int r = 0; r < R; ++r) mean[r] = warp_sum(mean[r]) * inv_count;
@@ -742,18 +868,24 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
         if (p.rstd != nullptr) p.rstd[row + r] = rstd[r];
       }
     }
-    T* y = static_cast<T*>(p.y) + row * p.ld_y + place.col;
-    T* sum = static_cast<T*>(p.sum) + row * p.ld_sum + place.col;
+    T* y = static_cast<T*>(p.y) + row * p.ld_y + begin;
+    T* sum = static_cast<T*>(p.sum) + row * p.ld_sum + begin;
+    auto store = [&](T* to, int k, bool all, const Eight& v) {
+      if constexpr (WIDE)
+        place.store(to, k, true, all, v);
+      else
+        store_words<T>(staging, to, count, k, v);
+    };
     auto finish = [&](int k, bool all, const Eight& w, const Eight& b) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (row + r >= rows) break;
         Eight& v = h[r][k];
-        if (p.sum != nullptr) place.store(sum + r * p.ld_sum, k, WIDE, all, v);
+        if (p.sum != nullptr) store(sum + r * p.ld_sum, k, all, v);
         v.normalise(mean[r], rstd[r]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v.v[i] = __ffma2_rn(v.v[i], w.v[i], b.v[i]);
-        place.store(y + r * p.ld_y, k, WIDE, all, v);
+        store(y + r * p.ld_y, k, all, v);
       }
     };
     if (place.full && weights != nullptr) {
@@ -767,10 +899,15 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
     } else {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (place.valid(k, 0) <= 0) continue;
+        if (WIDE ? place.valid(k, 0) <= 0 : count <= k * LN_PIECE) continue;  // by words: the warp as one
         Eight w, b;
-        place.weights(p.w, k, WIDE, 1.0f, w);
-        place.weights(p.b, k, WIDE, 0.0f, b);
+        if (!WIDE && weights != nullptr) {
+          staged_weights(weights, k, w);
+          staged_weights(weights + teams.width, k, b);
+        } else {
+          place.weights(p.w, k, WIDE || p.wide_w, 1.0f, w);
+          place.weights(p.b, k, WIDE || p.wide_w, 0.0f, b);
+        }
         finish(k, false, w, b);
       }
     }
@@ -1025,8 +1162,8 @@ __global__ void __launch_bounds__(LN_LONG_THREADS) layer_norm_long_kernel(const 
       float h[8], w[8], b[8];
       load(g, h);
       if (p.sum != nullptr) store_group(static_cast<T*>(p.sum) + row * p.ld_sum + g * 8, valid, WIDE, h);
-      load_weights(p.w, g * 8, valid, WIDE, 1.0f, w);
-      load_weights(p.b, g * 8, valid, WIDE, 0.0f, b);
+      load_weights(p.w, g * 8, valid, p.wide_w, 1.0f, w);
+      load_weights(p.b, g * 8, valid, p.wide_w, 0.0f, b);
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = fmaf((h[j] - mean) * rstd, w[j], b[j]);
       store_group(static_cast<T*>(p.y) + row * p.ld_y + g * 8, valid, WIDE, w);

@@ -7,13 +7,19 @@ namespace ge_norm {
 
 namespace {
 
-template <class T, bool DROP, bool ADD, bool WIDE, int... Ks>
-Kernel held_backward(int k) {
-  Kernel r{nullptr, 0};
-  ((k == Ks ? void(r = {ge::layer_norm_backward_kernel<T, DROP, ADD, Ks, WIDE>,
-                        ge::RowRing<T, Ks, ADD ? 3 : 2, ge::LN_BACKWARD_DEPTH<T>>::WARP_BYTES})
-            : void()), ...);
-  return r;
+template <class T, bool DROP, bool ADD, int K, bool WIDE>
+Kernel held_backward() {
+  constexpr int TENSORS = ADD ? 3 : 2, DEPTH = ge::LN_BACKWARD_DEPTH<T>;
+  using Ring = std::conditional_t<WIDE, ge::RowRing<T, K, TENSORS, DEPTH>, ge::WordRing<T, K, TENSORS, DEPTH>>;
+  return {ge::layer_norm_backward_kernel<T, DROP, ADD, K, WIDE>, ge::HELD_WARP_BYTES<Ring, WIDE>};
+}
+
+template <class T, bool DROP, bool ADD>
+Kernel held_backward(int k, bool wide) {
+  if (!wide) return k == 2 ? held_backward<T, DROP, ADD, 2, false>() : held_backward<T, DROP, ADD, 4, false>();
+  return k == 1   ? held_backward<T, DROP, ADD, 1, true>()
+         : k == 2 ? held_backward<T, DROP, ADD, 2, true>()
+                  : held_backward<T, DROP, ADD, 4, true>();
 }
 
 template <class T, bool DROP>
@@ -23,8 +29,7 @@ Kernel of(const Shape& s, const Choice& c) {
             ge::NarrowRows<T, ge::LN_NARROW_BACKWARD_ROWS<T>, 3>::WARP_BYTES};
   if (s.form == LONG)
     return {c.wide ? ge::layer_norm_backward_long_kernel<T, DROP, true> : ge::layer_norm_backward_long_kernel<T, DROP, false>, 0};
-  if (c.add) return c.wide ? held_backward<T, DROP, true, true, 1, 2, 4>(s.k) : held_backward<T, DROP, true, false, 4>(s.k);
-  return c.wide ? held_backward<T, DROP, false, true, 1, 2, 4>(s.k) : held_backward<T, DROP, false, false, 4>(s.k);
+  return c.add ? held_backward<T, DROP, true>(s.k, c.wide) : held_backward<T, DROP, false>(s.k, c.wide);
 }
 
 }  // namespace

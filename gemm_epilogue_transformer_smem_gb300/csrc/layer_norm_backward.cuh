@@ -35,7 +35,7 @@ template <class T, bool DROP, bool ADD, int K, bool WIDE>
 __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(const __grid_constant__ NormParams p) {
   ptx::launch_dependents();  // the sum of the partial sums, once there is room for it
   constexpr int DEPTH = LN_BACKWARD_DEPTH<T>;
-  using Ring = RowRing<T, K, ADD ? 3 : 2, DEPTH>;
+  using Ring = std::conditional_t<WIDE, RowRing<T, K, ADD ? 3 : 2, DEPTH>, WordRing<T, K, ADD ? 3 : 2, DEPTH>>;
   constexpr int BATCH = K % 2 == 0 ? 2 : K;
   extern __shared__ __align__(128) uint4 ln_smem[];
   __shared__ __align__(16) float2 part[2][LN_MAX_WARPS + 3];  // a warp's sums of a and a n
@@ -43,28 +43,37 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
   const int warp = teams.warp_in_team(p);
   const RowPlace<T, K> place(p.N, warp * K * LN_PIECE);
   const Ring ring(ln_smem, teams.warp);
+  uint4* staging = ln_smem + (blockDim.x >> 5) * (Ring::WARP_BYTES / 16) + teams.warp * 64;  // by words: the warp's 1 KB
+  const int begin = WIDE ? place.col : warp * K * LN_PIECE;
+  const int count = min(max(p.N - warp * K * LN_PIECE, 0), K * LN_PIECE);  // of the warp's columns in the row
   const uint32_t rows = static_cast<uint32_t>(p.M), stride = static_cast<uint32_t>(teams.stride);
   // Addresses are worked out where they are needed: kept, they would cost 20 of
   // the 128 registers, of which the sums of dw and db take 64 at K = 4.
-  auto at = [&](const void* data, int64_t ld, uint32_t row) { return static_cast<const T*>(data) + row * ld + place.col; };
+  auto at = [&](const void* data, int64_t ld, uint32_t row) { return static_cast<const T*>(data) + row * ld + begin; };
   auto fetch = [&](int d, uint32_t row) {
     if (row < rows) {
-      ring.fetch(d, 0, at(p.other, p.ld_other, row), place);
-      ring.fetch(d, 1, at(p.x, p.ld_x, row), place);
-      if constexpr (ADD) ring.fetch(d, 2, at(p.add, p.ld_add, row), place);
+      if constexpr (WIDE) {
+        ring.fetch(d, 0, at(p.other, p.ld_other, row), place);
+        ring.fetch(d, 1, at(p.x, p.ld_x, row), place);
+        if constexpr (ADD) ring.fetch(d, 2, at(p.add, p.ld_add, row), place);
+      } else {
+        ring.fetch(d, 0, at(p.other, p.ld_other, row), count);
+        ring.fetch(d, 1, at(p.x, p.ld_x, row), count);
+        if constexpr (ADD) ring.fetch(d, 2, at(p.add, p.ld_add, row), count);
+      }
     }
     ptx::cp_async_commit();
   };
   if constexpr (WIDE) {
     if (!place.full) ring.clear(place, 3);
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) fetch(d, static_cast<uint32_t>(teams.first) + d * stride);
   }
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) fetch(d, static_cast<uint32_t>(teams.first) + d * stride);
   uint32_t step = 0;
   if constexpr (DROP) step = drop_step(p.drop);
   const float* weights = nullptr;  // this thread's, staged
   if (p.staged) {
-    float* to = reinterpret_cast<float*>(ln_smem + (blockDim.x >> 5) * (Ring::WARP_BYTES / 16));
+    float* to = reinterpret_cast<float*>(ln_smem + (blockDim.x >> 5) * (HELD_WARP_BYTES<Ring, WIDE> / 16));
     stage_weights<T>(to, p.w, p.N, teams.width, 1.0f);
     weights = to + warp * K * LN_PIECE + (threadIdx.x & 31) * 4;
     __syncthreads();
@@ -88,11 +97,8 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
         ring.take(d, 0, k, g);
         ring.take(d, 1, k, n);
       } else {
-        Group<T> q;
-        place.load(at(p.other, p.ld_other, row), k, false, false, q);
-        g.from(q);
-        place.load(at(p.x, p.ld_x, row), k, false, false, q);
-        n.from(q);
+        ring.take(d, 0, k, at(p.other, p.ld_other, row), place, g);
+        ring.take(d, 1, k, at(p.x, p.ld_x, row), place, n);
       }
       n.normalise(mean, rstd);
     };
@@ -108,14 +114,18 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
       } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (place.valid(k, 0) <= 0) continue;
+          if (WIDE ? place.valid(k, 0) <= 0 : count <= k * LN_PIECE) continue;  // by words: the warp as one
           Eight w;
-          place.weights(p.w, k, WIDE, 1.0f, w);
+          if (!WIDE && weights != nullptr)
+            staged_weights(weights, k, w);
+          else
+            place.weights(p.w, k, WIDE || p.wide_w, 1.0f, w);
           f(k, false, w);
         }
       }
     };
-    if constexpr (WIDE) ptx::cp_async_wait<DEPTH - 1>();
+    ptx::cp_async_wait<DEPTH - 1>();
+    if constexpr (!WIDE) __syncwarp();
     float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
     pieces([&](int k, bool, const Eight& w) {
       Eight g, n;
@@ -142,8 +152,14 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
       m1 *= p.inv_n;
       m2 *= p.inv_n;
       uint32_t words[BATCH][4];
-      T* y = static_cast<T*>(p.y) + row * p.ld_y + place.col;
-      T* sum = static_cast<T*>(p.sum) + row * p.ld_sum + place.col;
+      T* y = static_cast<T*>(p.y) + row * p.ld_y + begin;
+      T* sum = static_cast<T*>(p.sum) + row * p.ld_sum + begin;
+      auto store = [&](T* to, int k, bool all, const Eight& v) {
+        if constexpr (WIDE)
+          place.store(to, k, true, all, v);
+        else
+          store_words<T>(staging, to, count, k, v);
+      };
       pieces([&](int k, bool all, const Eight& w) {
         if constexpr (DROP) {
           if (k % BATCH == 0) place.words(p.drop, step, row, k, words);
@@ -155,25 +171,20 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
           if constexpr (WIDE)
             ring.take(d, 2, k, a);
           else
-          {
-            Group<T> q;
-            place.load(at(p.add, p.ld_add, row), k, false, false, q);
-            a.from(q);
-          }
+            ring.take(d, 2, k, at(p.add, p.ld_add, row), place, a);
         }
         norm_gradient(g, n, w, a, rstd, m1, m2);
-        if (p.sum != nullptr) place.store(sum, k, WIDE, all, g);
+        if (p.sum != nullptr) store(sum, k, all, g);
         if constexpr (DROP) g.drop(p.drop, words[k % BATCH]);
-        if (p.y != nullptr) place.store(y, k, WIDE, all, g);
+        if (p.y != nullptr) store(y, k, all, g);
       });
     }
-    if constexpr (WIDE) {
-      fetch(d, row + DEPTH * stride);
-      d = d + 1 == DEPTH ? 0 : d + 1;
-    }
+    if constexpr (!WIDE) __syncwarp();
+    fetch(d, row + DEPTH * stride);
+    d = d + 1 == DEPTH ? 0 : d + 1;
   }
   if (p.partials == nullptr) return;
-  if constexpr (WIDE) ptx::cp_async_wait<0>();
+  ptx::cp_async_wait<0>();
   // In the order of the staged weights, [2][width] of each block: 16 bytes of
   // each lane side by side.
   const int mine = warp * K * LN_PIECE + (threadIdx.x & 31) * 4;
@@ -375,7 +386,7 @@ __global__ void __launch_bounds__(LN_LONG_THREADS) layer_norm_backward_long_kern
       const int valid = p.N - g * 8;
       float dy[8], n[8], w[8];
       load(g, dy, n);
-      load_weights(p.w, g * 8, valid, WIDE, 1.0f, w);
+      load_weights(p.w, g * 8, valid, p.wide_w, 1.0f, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float a = dy[j] * w[j];
@@ -397,7 +408,7 @@ __global__ void __launch_bounds__(LN_LONG_THREADS) layer_norm_backward_long_kern
       const int valid = p.N - g * 8;
       float dy[8], n[8], w[8];
       load(g, dy, n);
-      load_weights(p.w, g * 8, valid, WIDE, 1.0f, w);
+      load_weights(p.w, g * 8, valid, p.wide_w, 1.0f, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) dy[j] = rstd * (fmaf(dy[j], w[j], -s1) - n[j] * s2);
       if (p.add != nullptr) {

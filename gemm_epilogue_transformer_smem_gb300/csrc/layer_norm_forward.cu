@@ -8,7 +8,8 @@ namespace {
 
 template <class T, bool DROP, bool ADD, int K, int R, bool WIDE>
 Kernel held_forward() {
-  return {ge::layer_norm_kernel<T, DROP, ADD, K, R, WIDE>, ge::RowRing<T, K, ADD ? 2 : 1, R>::WARP_BYTES};
+  using Ring = std::conditional_t<WIDE, ge::RowRing<T, K, ADD ? 2 : 1, R>, ge::WordRing<T, K, ADD ? 2 : 1, R>>;
+  return {ge::layer_norm_kernel<T, DROP, ADD, K, R, WIDE>, ge::HELD_WARP_BYTES<Ring, WIDE>};
 }
 
 template <class T, bool DROP, bool ADD>

@@ -32,7 +32,7 @@ def placed(t, order):
         return t
     if order == "same":
         return t[:1].expand(rows, cols)
-    width, at = ((cols + 7) // 8 * 8 + 16, 8) if order == "view" else (cols + 4 + cols % 2, 1)
+    width, at = ((cols + 7) // 8 * 8 + 16, 8) if order == "view" else ((cols + 4) | 1, 1)
     buf = torch.full((rows, width), float("nan"), dtype=t.dtype, device=DEV)
     buf[:, at:at + cols] = t
     return buf[:, at:at + cols]
@@ -48,7 +48,7 @@ class Framed:
     """An output inside a larger buffer of sevens: what lies around it stays."""
 
     def __init__(self, rows, cols, dtype, odd):
-        self.at, width = (3, cols + 10 + cols % 2) if odd else (8, (cols + 7) // 8 * 8 + 16)
+        self.at, width = (3, (cols + 10) | 1) if odd else (8, (cols + 7) // 8 * 8 + 16)
         self.buf = torch.full((rows + 2, width), 7.0, dtype=dtype, device=DEV)
         self.t = self.buf[1:1 + rows, self.at:self.at + cols]
 
@@ -223,6 +223,26 @@ def test_far_from_zero(cols):
     want = R.norm(h, torch.zeros_like(h), None, None, 1e-5)
     for t, name in ((out, "y"), (mean, "mean"), (rstd, "rstd")):
         R.close(t, *want[name], F32, name)
+
+
+@pytest.mark.parametrize("cols", [40, 1000, 4096, 16400])
+def test_weights_that_start_anywhere(cols):
+    """Weights one value past an aligned address."""
+    g, rows = gen(cols), 700
+    x, dy = values(g, rows, cols, BF), values(g, rows, cols, BF)
+    w, b = (torch.cat([v[:1], v])[1:] for v in (vector(g, cols, 1.0), vector(g, cols)))
+    assert w.data_ptr() % 16 and b.data_ptr() % 16
+    ws = torch.empty(api.layer_norm_workspace(cols), dtype=torch.uint8, device=DEV)
+    out, dx, dw, db = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w), torch.empty_like(w)
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    api.layer_norm(x, weight=w, bias=b, out=out, mean=mean, rstd=rstd)
+    api.layer_norm_backward(dy, x, mean, rstd, weight=w, dx=dx, dw=dw, db=db, workspace=ws)
+    mask = R.Mask(None, rows, cols)
+    R.close(out, *R.norm(R.wide(x), torch.zeros(rows, cols).double(), w, b, 1e-5)["y"], BF, "y")
+    want = R.norm_backward(dy, x, mean, rstd, w, None, mask)
+    R.close(dx, *want["dx"], BF, "dx")
+    R.close(dw, *want["dw"], F32, "dw")
+    R.close(db, *want["db"], F32, "db")
 
 
 def all_outputs(rows, cols, dtype, g):
