@@ -740,11 +740,9 @@ def _row_stride(name: str, t: torch.Tensor, shape):
     return t.data_ptr(), ld
 
 
-def _rows(name: str, t: Optional[torch.Tensor], shape, dtype, index: int):
+def _rows(name: str, t: torch.Tensor, shape, dtype, index: int):
     """(pointer, row stride) of a tensor of the first one's shape, type and
-    device, checked; (0, 0) for None."""
-    if t is None:
-        return _NO_ROWS
+    device, checked."""
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError("%s: %s %s does not match %s %s" % (name, t.dtype, tuple(t.shape), dtype, tuple(shape)))
     if t.get_device() != index:
@@ -754,10 +752,8 @@ def _rows(name: str, t: Optional[torch.Tensor], shape, dtype, index: int):
     return _row_stride(name, t, shape)
 
 
-def _values(name: str, t: Optional[torch.Tensor], n: int, index: int) -> int:
-    """Pointer of n contiguous fp32 values on device `index`, checked; 0 for None."""
-    if t is None:
-        return 0
+def _values(name: str, t: torch.Tensor, n: int, index: int) -> int:
+    """Pointer of n contiguous fp32 values on device `index`, checked."""
     if t.dtype is not torch.float32:
         raise TypeError("%s: expected a f32 tensor, got %s" % (name, t.dtype))
     if t.numel() != n or not t.is_contiguous():
@@ -767,9 +763,9 @@ def _values(name: str, t: Optional[torch.Tensor], n: int, index: int) -> int:
     return t.data_ptr()
 
 
-def _mask(rng: Optional[Dropout], site: int, index: int):
+def _mask(rng: Dropout, site: int, index: int):
     """(step, seed, site, threshold) of a gemm_epi_mask."""
-    if rng is None or rng.threshold == 0:
+    if rng.threshold == 0:
         return _NO_MASK
     step = rng._step
     if step.get_device() != index:
@@ -801,7 +797,8 @@ def dropout(x, rng: Dropout, *, out, residual=None, site: int = 0, stream=None) 
     whose own gradient is out's.  Asynchronous."""
     shape, dtype, code, rows, cols, index, tx = _first_rows("x", x)
     _call_packed("gemm_epi_dropout", _DROPOUT_ARGS.pack(
-        rows, cols, code, *_mask(rng, site, index), *tx, *_rows("residual", residual, shape, dtype, index),
+        rows, cols, code, *_mask(rng, site, index), *tx,
+        *(_NO_ROWS if residual is None else _rows("residual", residual, shape, dtype, index)),
         *_rows("out", out, shape, dtype, index)), x, index, stream)
 
 
@@ -819,10 +816,14 @@ def layer_norm(x, *, weight=None, bias=None, eps: float = 1e-5, out, residual=No
         raise ValueError("sum_out without residual or dropout is x itself")
     shape, dtype, code, rows, cols, index, tx = _first_rows("x", x)
     _call_packed("gemm_epi_layer_norm", _LAYER_NORM_ARGS.pack(
-        rows, cols, code, eps, *_mask(dropout, site, index), *tx, *_rows("residual", residual, shape, dtype, index),
-        *_rows("out", out, shape, dtype, index), *_rows("sum_out", sum_out, shape, dtype, index),
-        _values("weight", weight, cols, index), _values("bias", bias, cols, index), _values("mean", mean, rows, index),
-        _values("rstd", rstd, rows, index)), x, index, stream)
+        rows, cols, code, eps, *(_NO_MASK if dropout is None else _mask(dropout, site, index)), *tx,
+        *(_NO_ROWS if residual is None else _rows("residual", residual, shape, dtype, index)),
+        *_rows("out", out, shape, dtype, index),
+        *(_NO_ROWS if sum_out is None else _rows("sum_out", sum_out, shape, dtype, index)),
+        0 if weight is None else _values("weight", weight, cols, index),
+        0 if bias is None else _values("bias", bias, cols, index),
+        0 if mean is None else _values("mean", mean, rows, index),
+        0 if rstd is None else _values("rstd", rstd, rows, index)), x, index, stream)
 
 
 def layer_norm_workspace(cols: int) -> int:
@@ -852,8 +853,10 @@ def layer_norm_backward(dy, x, mean, rstd, *, weight=None, dx=None, dw=None, db=
             raise ValueError("workspace: expected a contiguous tensor with the others")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _call_packed("gemm_epi_layer_norm_backward", _LAYER_NORM_BWD_ARGS.pack(
-        rows, cols, code, *_mask(dropout, site, index), *tdy, *_rows("x", x, shape, dtype, index),
-        *_rows("add", add, shape, dtype, index), *_rows("dx", dx, shape, dtype, index),
-        *_rows("d_residual", d_residual, shape, dtype, index), _values("weight", weight, cols, index),
-        _values("mean", mean, rows, index), _values("rstd", rstd, rows, index), _values("dw", dw, cols, index),
-        _values("db", db, cols, index), ws, ws_bytes), dy, index, stream)
+        rows, cols, code, *(_NO_MASK if dropout is None else _mask(dropout, site, index)), *tdy,
+        *_rows("x", x, shape, dtype, index), *(_NO_ROWS if add is None else _rows("add", add, shape, dtype, index)),
+        *(_NO_ROWS if dx is None else _rows("dx", dx, shape, dtype, index)),
+        *(_NO_ROWS if d_residual is None else _rows("d_residual", d_residual, shape, dtype, index)),
+        0 if weight is None else _values("weight", weight, cols, index), _values("mean", mean, rows, index),
+        _values("rstd", rstd, rows, index), 0 if dw is None else _values("dw", dw, cols, index),
+        0 if db is None else _values("db", db, cols, index), ws, ws_bytes), dy, index, stream)

@@ -108,7 +108,11 @@ Shape shape_of(bool backward, int64_t rows, int64_t cols, const Choice& c, int s
     s.teams = ge::LN_BLOCK_WARPS << (5 - s.log_lanes);
     return s;
   }
-  if (pieces > 4 * ge::LN_MAX_WARPS) return Shape{LONG, 0, ge::LN_LONG_THREADS / 32, 1, 0, 1, false};
+  if (pieces > 4 * ge::LN_MAX_WARPS) {
+    Shape s{LONG, 0, ge::LN_LONG_THREADS / 32, 1, 0, 1, false};
+    if (backward) s.rows = static_cast<int>(std::min<int64_t>(ge::LN_LONG_ROWS, std::max<int64_t>(1, rows / (2 * sms))));
+    return s;
+  }
   Shape s = backward ? backward_shape(rows, pieces, c, sms) : forward_shape(rows, pieces, c, sms);
   // a block to every SM before a second team to a block
   s.teams = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s.teams, rows / (s.rows * sms))));
@@ -130,26 +134,33 @@ void fit_shared(bool backward, Shape& s, const Kernel& k) {
   while (s.teams > 1 && shared_bytes(backward, s, k) > ge::LN_MAX_SHARED) --s.teams;
 }
 
-// Blocks of a kernel resident on an SM of the current device, asked for once
-// for each kernel and team size (block size and shared memory go with them).
-gemm_epi_status resident_blocks(int dev, bool backward, const Shape& s, const Choice& c, const Kernel& k, int* blocks) {
-  static std::atomic<int> known[128][2][16][10][ge::LN_MAX_WARPS + 1][ge::LN_MAX_WARPS + 1][2];
-  std::atomic<int>& at = known[dev][backward][c.index()][s.index()][s.warps][block_warps(s) / s.warps][s.rows > 1];
-  int n = at.load(std::memory_order_acquire);
-  if (n == 0) {
-    const void* fn = reinterpret_cast<const void*>(k.fn);
-    // the most that a block may take, so that no other thread's call lowers it
-    cudaError_t e = cudaSuccess;
-    if (s.form != LONG)
-      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               s.form == HELD ? ge::LN_MAX_SHARED : static_cast<int>(shared_bytes(backward, s, k)));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-    const int warps = block_warps(s);
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, 32 * warps, shared_bytes(backward, s, k));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
-    if (n < 1) return fail(GEMM_EPI_ERR_CUDA, "a layer norm kernel does not fit an SM");
-    at.store(n, std::memory_order_release);
+// Blocks of a kernel resident on an SM of the current device: asked for once and
+// kept by what the answer depends on, one word to an entry, so that an entry is
+// read and written whole.
+gemm_epi_status resident_blocks(int dev, bool backward, const Shape& s, const Choice& c, const Kernel& k, size_t bytes,
+                                int* blocks) {
+  constexpr size_t ENTRIES = 1024;
+  static std::atomic<uint64_t> known[ENTRIES];
+  uint64_t key = static_cast<uint64_t>(dev) << 1 | static_cast<uint64_t>(backward);
+  for (const int part : {c.index(), s.index(), s.warps, block_warps(s), s.rows, static_cast<int>(bytes / 1024)})
+    key = key << 8 | static_cast<uint64_t>(part);
+  key = key << 1 | 1;  // an empty entry is zero
+  std::atomic<uint64_t>& at = known[(key * 0x9E3779B97F4A7C15u >> 32) % ENTRIES];
+  const uint64_t entry = at.load(std::memory_order_acquire);
+  if (entry >> 7 == key) {
+    *blocks = static_cast<int>(entry & 127);
+    return GEMM_EPI_OK;
   }
+  const void* fn = reinterpret_cast<const void*>(k.fn);
+  // the most that a block may take, so that no other thread's call lowers it
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       s.form == HELD ? ge::LN_MAX_SHARED : static_cast<int>(bytes));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  int n = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, 32 * block_warps(s), bytes);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+  if (n < 1) return fail(GEMM_EPI_ERR_CUDA, "a layer norm kernel does not fit an SM");
+  at.store(key << 7 | static_cast<uint64_t>(n), std::memory_order_release);
   *blocks = n;
   return GEMM_EPI_OK;
 }
@@ -179,12 +190,13 @@ DropoutKernel dropout_kernel_of(int64_t cols, bool wide) {
   return few_empty(2) ? dropout_kernel_of<T, 2>(wide) : dropout_kernel_of<T, 1>(wide);
 }
 
-// Rows of partial sums of dw and db: the most blocks a backward pass has.
-int most_partials(int64_t cols) { return cols <= 2048 ? 912 : 304; }
+// Partial sums of dw and db: the most blocks a backward pass has, two to an SM.
+constexpr int MOST_PARTIALS = 304;
 
 // ---------------------------------------------------------------- checks
 
 constexpr int64_t LIM = 0x7FFFFFFF;
+constexpr int64_t MOST_COLUMNS = LIM - 4095;  // a column past the end of the last pieces is still an int
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
@@ -202,7 +214,7 @@ struct Checked {
 
   gemm_epi_status sizes(int64_t rows, int64_t cols, int32_t type) {
     if (rows < 0 || rows > LIM) return fail(GEMM_EPI_ERR_INVALID_VALUE, "M must be in [0, 2^31)");
-    if (cols < 1 || cols > LIM - 7) return fail(GEMM_EPI_ERR_INVALID_VALUE, "N must be in [1, 2^31 - 8]");
+    if (cols < 1 || cols > MOST_COLUMNS) return fail(GEMM_EPI_ERR_INVALID_VALUE, "N must be in [1, 2^31 - 4096]");
     if (type != GEMM_EPI_TYPE_BF16 && type != GEMM_EPI_TYPE_F32)
       return fail(GEMM_EPI_ERR_UNSUPPORTED, "the tensors must be BF16 or F32 (type %d)", type);
     M = rows, N = cols;
@@ -260,15 +272,16 @@ gemm_epi_status launch_norm(bool backward, ge::NormParams& p, Choice c, int64_t 
   Shape shape = shape_of(backward, p.M, p.N, c, sms);
   const Kernel k = backward ? ge_norm::backward_kernel(shape, c) : ge_norm::forward_kernel(shape, c);
   if (shape.form == HELD) fit_shared(backward, shape, k);
-  if ((s = resident_blocks(dev, backward, shape, c, k, &resident))) return s;
+  const size_t bytes = (shared_bytes(backward, shape, k) + 1023) / 1024 * 1024;
+  if ((s = resident_blocks(dev, backward, shape, c, k, bytes, &resident))) return s;
   const int64_t rows = static_cast<int64_t>(shape.teams) * shape.rows;  // a block works on at once
   int64_t blocks = std::min<int64_t>((p.M + rows - 1) / rows, static_cast<int64_t>(sms) * resident);
   blocks = std::min(blocks, most_blocks);
   p.warps = shape.warps;
   p.log_lanes = shape.log_lanes;
   p.staged = shape.staged;
-  const int warps = block_warps(shape);
-  k.fn<<<static_cast<unsigned>(blocks), static_cast<unsigned>(32 * warps), shared_bytes(backward, shape, k), st>>>(p);
+  p.rows = shape.rows;
+  k.fn<<<static_cast<unsigned>(blocks), static_cast<unsigned>(32 * block_warps(shape)), bytes, st>>>(p);
   const cudaError_t e = cudaGetLastError();
   *launched = {static_cast<int>(blocks), shape.form == HELD ? shape.warps * shape.k * ge::LN_PIECE : static_cast<int>(ge::partial_width(p.N)),
                shape.form == HELD && !c.f32};
@@ -416,7 +429,7 @@ gemm_epi_status gemm_epi_layer_norm_backward(const gemm_epi_layer_norm_bwd_args*
   p.wide_w = aligned(a->w, 16);
   const Choice choice{c.size == 4, false, false, c.wide_in && c.wide_out && p.wide_w};
   Launched launched;
-  if ((s = launch_norm(true, p, choice, most_partials(c.N), st, &launched))) return s;
+  if ((s = launch_norm(true, p, choice, MOST_PARTIALS, st, &launched))) return s;
   if (!wants_dw) return GEMM_EPI_OK;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
@@ -435,9 +448,10 @@ gemm_epi_status gemm_epi_layer_norm_backward(const gemm_epi_layer_norm_bwd_args*
 }
 
 size_t gemm_epi_layer_norm_backward_workspace_size(int64_t N) {
-  if (N < 1 || N > LIM - 7) return 0;
-  // HELD: up to three pieces more than the row has
-  return static_cast<size_t>(most_partials(N)) * 2 * static_cast<size_t>(ge::partial_width(N) + 3 * ge::LN_PIECE) * sizeof(float);
+  if (N < 1 || N > MOST_COLUMNS) return 0;
+  // rows held by warps: up to three pieces more than the row has
+  const int64_t width = ge::partial_width(N) + (N <= ge::LN_PIECE ? 0 : 3 * ge::LN_PIECE);
+  return static_cast<size_t>(MOST_PARTIALS) * 2 * static_cast<size_t>(width) * sizeof(float);
 }
 
 }  // extern "C"

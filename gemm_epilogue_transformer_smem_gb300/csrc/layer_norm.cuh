@@ -1,5 +1,5 @@
 // layer_norm.cuh -- dropout, and layer norm with the dropout and the residual
-// add in front of it in the same pass, and that pass's backward.
+// add in front of it in the same pass (its backward: layer_norm_backward.cuh).
 //
 // For a row x of N values (D: dropout, w and b the norm's weight and bias):
 //   dropout    y  = D(x) + residual
@@ -8,17 +8,31 @@
 //   backward   n  = (h - mean) r,  a = dy w
 //              g  = r (a - mean(a) - n mean(a n)) + add     (the gradient of h)
 //              d_residual = g,  dx = D(g),  dw = sum of dy n,  db = sum of dy
-// Everything is fp32 between one load and one store of each value.  The
-// variance is that of the differences from a mean taken first, never a
+// Everything is fp32 between one load and one store of each value, the sums of
+// dw and db too: each thread's over its rows, then the blocks' in a fixed order.
+// The variance is that of the differences from a mean taken first, never a
 // difference of squares.
 //
 // All of it is memory-bound, so a row is read once: a team of threads -- part of
-// a warp, a warp, or a block, as the width asks for -- holds a row in registers
-// while its sums are taken, each thread K groups of 8 neighbouring columns
-// (16-byte accesses, neighbouring threads neighbouring groups).  The teams stay
-// for all rows, so that the next rows are on their way while one is worked on:
-// per-thread asynchronous copies bring them into shared-memory slots that only
-// that thread reads, without a barrier and without registers.
+// a warp, a warp, or up to 16 of them, as the width asks for -- holds a row in
+// registers while its sums are taken.  The teams stay for all rows, so that the
+// next rows are on their way while one is worked on: per-thread asynchronous
+// copies bring them into shared-memory slots that only that thread reads,
+// without a barrier and without registers.
+//
+// One GB300, of the measured copy bandwidth (6792 GB/s), what is left beside the
+// copies: the chain from a row's sums to its stores, which 16 warps of an SM
+// hide, and with dropout 8 integer instructions an element for the mask.
+//   norm, dropout and residual, 16384 x 4096 bf16 (537 MB)   92.7 us  0.85
+//   the same without dropout                                 88.6 us  0.89
+//   norm alone, 16384 x 4096 (268 MB)                        48.0 us  0.82
+//   backward with dropout and `add`, 16384 x 4096 (671 MB)  116.5 us  0.85
+//   the same of 65536 x 1024                                111.4 us  0.89
+//   backward with `add`, 2048 x 14336 (235 MB)               53.3 us  0.65: 14 warps
+//     to a row leave room for one row on an SM, whose phases nothing overlaps
+//   dropout, 8192 x 14336 (470 MB)                           78.5 us  0.88
+//   rows that start anywhere, 16384 x 4095 (537 MB)         200   us  0.39: words
+//     of 4 bytes in place of 16
 #pragma once
 
 #include <stdint.h>
@@ -54,22 +68,6 @@ struct Group<uint16_t> {
                       ptx::pack_bf16x2(v[6], v[7]));
   }
   __device__ __forceinline__ void clear() { q[0] = make_uint4(0, 0, 0, 0); }
-  // The first `valid` (up to 8) values at p, zeros behind them.  `wide`: p is on 16 bytes.
-  __device__ __forceinline__ void load(const uint16_t* p, int valid, bool wide) {
-    if (wide && valid >= 8) {
-      q[0] = *reinterpret_cast<const uint4*>(p);
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
-        w[h] = (2 * h < valid ? static_cast<uint32_t>(p[2 * h]) : 0u) |
-               (2 * h + 1 < valid ? static_cast<uint32_t>(p[2 * h + 1]) << 16 : 0u);
-      q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-  static __device__ __forceinline__ void store_one(uint16_t* p, float v) {
-    *p = static_cast<uint16_t>(ptx::pack_bf16x2(v, 0.0f) & 0xFFFFu);
-  }
 };
 
 template <>
@@ -92,18 +90,6 @@ struct Group<float> {
                         __float_as_uint(v[4 * i + 3]));
   }
   __device__ __forceinline__ void clear() { q[0] = q[1] = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void load(const float* p, int valid, bool wide) {
-    if (wide && valid >= 8) {
-      q[0] = reinterpret_cast<const uint4*>(p)[0];
-      q[1] = reinterpret_cast<const uint4*>(p)[1];
-    } else {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < valid ? p[j] : 0.0f;
-      pack(v);
-    }
-  }
-  static __device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
 };
 
 // The first `valid` values of 16 bytes' worth at p into q, which is zeros.
@@ -145,25 +131,29 @@ __device__ __forceinline__ void store_part(T* p, int valid, bool wide, const uin
   }
 }
 
+// Eight neighbouring values likewise.
+template <class T>
+__device__ __forceinline__ void load_group(const T* p, int valid, bool wide, Group<T>& g) {
+  constexpr int EACH = 16 / sizeof(T);
+  g.clear();
+#pragma unroll
+  for (int i = 0; i < Group<T>::PIECES; ++i) load_part(p + i * EACH, valid - i * EACH, wide, g.q[i]);
+}
+
 template <class T>
 __device__ __forceinline__ void load_group(const T* p, int valid, bool wide, float (&v)[8]) {
   Group<T> g;
-  g.load(p, valid, wide);
+  load_group(p, valid, wide, g);
   g.unpack(v);
 }
 
 template <class T>
 __device__ __forceinline__ void store_group(T* p, int valid, bool wide, const float (&v)[8]) {
-  if (wide && valid >= 8) {
-    Group<T> g;
-    g.pack(v);
+  constexpr int EACH = 16 / sizeof(T);
+  Group<T> g;
+  g.pack(v);
 #pragma unroll
-    for (int i = 0; i < Group<T>::PIECES; ++i) reinterpret_cast<uint4*>(p)[i] = g.q[i];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < valid) Group<T>::store_one(p + j, v[j]);
-  }
+  for (int i = 0; i < Group<T>::PIECES; ++i) store_part(p + i * EACH, valid - i * EACH, wide, g.q[i]);
 }
 
 // Weights of a group's columns, `none` without any.
@@ -244,13 +234,7 @@ struct Eight {
   }
 };
 
-__device__ __forceinline__ float2 fma2(const float2 a, float b, const float2 c) {
-  return __ffma2_rn(a, make_float2(b, b), c);
-}
-
-// ------------------------------------------------------------------ dropout
-
-// ------------------------------------------------------------------ teams
+// ------------------------------------------------------------------ rows
 
 // A team of W warps holds a row: warp i the columns from i K 256 on, lane l in
 // each of its K pieces of 256 columns the 8 from 8 l.  The offsets between
@@ -268,6 +252,7 @@ struct NormParams {
   int32_t M, N, groups;
   int32_t warps;      // of a team
   int32_t staged;     // the norm's weights go through shared memory
+  int32_t rows;       // rows too wide to hold, backward: at a time
   int32_t wide_w;     // else: 16-byte accesses serve them
   int32_t log_lanes;  // teams within a warp: 2^log_lanes threads each
   const void* x;      // backward: h, the forward pass's normalised sum
@@ -327,19 +312,19 @@ struct RowPlace {
   }
   // Columns of a part that are in the row (<= 0: none).
   __device__ __forceinline__ int valid(int k, int i) const { return min(left - k * LN_PIECE - i * APART, EACH); }
-  // Piece k from a row at `col`, zeros behind its end.
-  __device__ __forceinline__ void load(const T* row, int k, bool wide, bool all, Group<T>& g) const {
+  // Piece k from a row at `col`, zeros behind its end; all: none is there.
+  __device__ __forceinline__ void load(const T* row, int k, bool all, Group<T>& g) const {
     g.clear();
 #pragma unroll
-    for (int i = 0; i < PARTS; ++i) load_part(row + k * LN_PIECE + i * APART, all ? EACH : valid(k, i), wide, g.q[i]);
+    for (int i = 0; i < PARTS; ++i) load_part(row + k * LN_PIECE + i * APART, all ? EACH : valid(k, i), true, g.q[i]);
   }
-  __device__ __forceinline__ void store(T* row, int k, bool wide, bool all, const Eight& v) const {
+  __device__ __forceinline__ void store(T* row, int k, bool all, const Eight& v) const {
     Group<T> g;
     float f[8];
     v.to(f);
     g.pack(f);
 #pragma unroll
-    for (int i = 0; i < PARTS; ++i) store_part(row + k * LN_PIECE + i * APART, all ? EACH : valid(k, i), wide, g.q[i]);
+    for (int i = 0; i < PARTS; ++i) store_part(row + k * LN_PIECE + i * APART, all ? EACH : valid(k, i), true, g.q[i]);
   }
   // fp32 vectors, `none` behind the row's end and without one.
   __device__ __forceinline__ void weights(const float* w, int k, bool wide, float none, Eight& v) const {
@@ -591,9 +576,9 @@ __global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_kernel(const __
       auto load = [&](bool all) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          place.load(x, k, true, all, g[k]);
+          place.load(x, k, all, g[k]);
           r[k].clear();
-          if (residual != nullptr) place.load(residual, k, true, all, r[k]);
+          if (residual != nullptr) place.load(residual, k, all, r[k]);
         }
       };
       auto store = [&](bool all) {
@@ -603,7 +588,7 @@ __global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_kernel(const __
           v.from(g[k]);
           add.from(r[k]);
           finish(k, v, add);
-          place.store(y, k, true, all, v);
+          place.store(y, k, all, v);
         }
       };
       place.full ? load(true) : load(false);
@@ -657,9 +642,9 @@ __global__ void __launch_bounds__(DO_THREADS, DO_BLOCKS) dropout_narrow_kernel(c
       r[u].clear();
       if (i + u * threads < p.total) {
         const int col = group * 8;
-        x[u].load(static_cast<const T*>(p.x) + row * p.ld_x + col, p.N - col, p.wide_in);
+        load_group(static_cast<const T*>(p.x) + row * p.ld_x + col, p.N - col, p.wide_in, x[u]);
         if (p.residual != nullptr)
-          r[u].load(static_cast<const T*>(p.residual) + row * p.ld_residual + col, p.N - col, p.wide_in);
+          load_group(static_cast<const T*>(p.residual) + row * p.ld_residual + col, p.N - col, p.wide_in, r[u]);
       }
       row += p.step_rows, group += p.step_spans;
       if (group >= p.spans) group -= p.spans, ++row;
@@ -872,7 +857,7 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
     T* sum = static_cast<T*>(p.sum) + row * p.ld_sum + begin;
     auto store = [&](T* to, int k, bool all, const Eight& v) {
       if constexpr (WIDE)
-        place.store(to, k, true, all, v);
+        place.store(to, k, all, v);
       else
         store_words<T>(staging, to, count, k, v);
     };
@@ -1096,9 +1081,11 @@ __global__ void __launch_bounds__(32 * LN_BLOCK_WARPS, 2) layer_norm_narrow_kern
 
 // ------------------------------------------------------------------ rows too wide to hold
 
-// A block to a row, which it reads three times (forward) or twice (backward):
-// the second time from L2.
+// A block to a row, which it reads three times forward and twice backward, from
+// L2 after the first.  (Forward, h kept in shared memory for the second and third
+// time leaves one block to two to an SM: 4096 x 16392 bf16 212 us, 195 read again.)
 constexpr int LN_LONG_THREADS = 512;
+constexpr int LN_LONG_ROWS = 4;  // of a block at a time, backward
 
 // Sum over the block, in every thread.
 __device__ __forceinline__ float block_sum(float v, float (&part)[LN_LONG_THREADS / 32]) {
@@ -1118,7 +1105,7 @@ __global__ void __launch_bounds__(LN_LONG_THREADS) layer_norm_long_kernel(const 
   uint32_t step = 0;
   if constexpr (DROP) step = drop_step(p.drop);
   for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
-    auto load = [&](int g, float (&h)[8]) {
+    auto read = [&](int g, float (&h)[8]) {
       load_group(static_cast<const T*>(p.x) + row * p.ld_x + g * 8, p.N - g * 8, WIDE, h);
       float r[8];
 #pragma unroll
@@ -1138,7 +1125,7 @@ __global__ void __launch_bounds__(LN_LONG_THREADS) layer_norm_long_kernel(const 
     float s = 0.0f;
     for (int g = threadIdx.x; g < p.groups; g += LN_LONG_THREADS) {
       float h[8];
-      load(g, h);  // zeros behind the row's end
+      read(g, h);  // zeros behind the row's end
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += h[j];
     }
@@ -1147,7 +1134,7 @@ __global__ void __launch_bounds__(LN_LONG_THREADS) layer_norm_long_kernel(const 
     for (int g = threadIdx.x; g < p.groups; g += LN_LONG_THREADS) {
       const int valid = p.N - g * 8;
       float h[8];
-      load(g, h);
+      read(g, h);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j < valid) s = fmaf(h[j] - mean, h[j] - mean, s);
@@ -1160,7 +1147,7 @@ __global__ void __launch_bounds__(LN_LONG_THREADS) layer_norm_long_kernel(const 
     for (int g = threadIdx.x; g < p.groups; g += LN_LONG_THREADS) {
       const int valid = p.N - g * 8;
       float h[8], w[8], b[8];
-      load(g, h);
+      read(g, h);
       if (p.sum != nullptr) store_group(static_cast<T*>(p.sum) + row * p.ld_sum + g * 8, valid, WIDE, h);
       load_weights(p.w, g * 8, valid, p.wide_w, 1.0f, w);
       load_weights(p.b, g * 8, valid, p.wide_w, 0.0f, b);

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
       T* sum = static_cast<T*>(p.sum) + row * p.ld_sum + begin;
       auto store = [&](T* to, int k, bool all, const Eight& v) {
         if constexpr (WIDE)
-          place.store(to, k, true, all, v);
+          place.store(to, k, all, v);
         else
           store_words<T>(staging, to, count, k, v);
       };
@@ -363,70 +363,98 @@ __global__ void __launch_bounds__(1024) layer_norm_weight_grad_kernel(const floa
 
 // ------------------------------------------------------------------ rows too wide to hold
 
-// The sums over rows are kept in the block's partials themselves, each column
-// by the thread that works on it in every row.
+// A block takes up to four rows at a time: first the two sums of each, then,
+// column by column, the gradients of all four, read again from L2 (304 blocks'
+// four rows of 16392 bf16 columns are 80 of its 126 MB).  The sums over rows are
+// kept in the block's partials themselves, each column by the thread that works
+// on it every time.
 template <class T, bool DROP, bool WIDE>
 __global__ void __launch_bounds__(LN_LONG_THREADS) layer_norm_backward_long_kernel(const __grid_constant__ NormParams p) {
   ptx::launch_dependents();
+  constexpr int R = LN_LONG_ROWS;
   __shared__ float part[LN_LONG_THREADS / 32];
+  __shared__ float stats[R][4];  // mean, rstd and the two means
   uint32_t step = 0;
   if constexpr (DROP) step = drop_step(p.drop);
   const int64_t width = partial_width(p.N);
   float* sums = p.partials == nullptr ? nullptr : p.partials + static_cast<int64_t>(blockIdx.x) * 2 * width;
-  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
-    const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
-    auto load = [&](int g, float (&dy)[8], float (&n)[8]) {
-      load_group(static_cast<const T*>(p.other) + row * p.ld_other + g * 8, p.N - g * 8, WIDE, dy);
-      load_group(static_cast<const T*>(p.x) + row * p.ld_x + g * 8, p.N - g * 8, WIDE, n);
+  const bool wants_g = p.y != nullptr || p.sum != nullptr;
+  auto load = [&](int64_t row, int g, float mean, float rstd, float (&dy)[8], float (&n)[8]) {
+    load_group(static_cast<const T*>(p.other) + row * p.ld_other + g * 8, p.N - g * 8, WIDE, dy);
+    load_group(static_cast<const T*>(p.x) + row * p.ld_x + g * 8, p.N - g * 8, WIDE, n);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) n[j] = (n[j] - mean) * rstd;
-    };
-    float s1 = 0.0f, s2 = 0.0f;
+    for (int j = 0; j < 8; ++j) n[j] = (n[j] - mean) * rstd;
+  };
+  bool first = true;
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows; row0 < p.M; row0 += static_cast<int64_t>(gridDim.x) * p.rows) {
+    const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows), p.M - row0));
+    for (int r = 0; r < rows; ++r) {
+      const float mean = __ldg(p.mean + row0 + r), rstd = __ldg(p.rstd + row0 + r);
+      float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll 2
+      for (int g = threadIdx.x; wants_g && g < p.groups; g += LN_LONG_THREADS) {
+        float dy[8], n[8], w[8];
+        load(row0 + r, g, mean, rstd, dy, n);  // dy is zero behind the row's end
+        load_weights(p.w, g * 8, p.N - g * 8, p.wide_w, 1.0f, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float a = dy[j] * w[j];
+          s1 += a;
+          s2 = fmaf(a, n[j], s2);
+        }
+      }
+      s1 = block_sum(s1, part) * p.inv_n;
+      s2 = block_sum(s2, part) * p.inv_n;
+      if (threadIdx.x == 0) stats[r][0] = mean, stats[r][1] = rstd, stats[r][2] = s1, stats[r][3] = s2;
+    }
+    __syncthreads();
     for (int g = threadIdx.x; g < p.groups; g += LN_LONG_THREADS) {
       const int valid = p.N - g * 8;
-      float dy[8], n[8], w[8];
-      load(g, dy, n);
+      float w[8], dw[8], db[8];
       load_weights(p.w, g * 8, valid, p.wide_w, 1.0f, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = dy[j] * w[j];
-        s1 += a;
-        s2 = fmaf(a, n[j], s2);
-        if (sums != nullptr && j < valid) {
-          const int c = g * 8 + j;
-          const bool first = row == blockIdx.x;
-          float& db = sums[width + c];
-          sums[c] = first ? dy[j] * n[j] : fmaf(dy[j], n[j], sums[c]);
-          db = first ? dy[j] : db + dy[j];
+      for (int j = 0; j < 8; ++j) dw[j] = db[j] = 0.0f;
+      for (int r = 0; r < rows; ++r) {
+        const int64_t row = row0 + r;
+        const float rstd = stats[r][1], m1 = stats[r][2], m2 = stats[r][3];
+        float dy[8], n[8];
+        load(row, g, stats[r][0], rstd, dy, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          dw[j] = fmaf(dy[j], n[j], dw[j]);
+          db[j] += dy[j];
+          dy[j] = rstd * (fmaf(dy[j], w[j], -m1) - n[j] * m2);
+        }
+        if (p.add != nullptr && wants_g) {
+          load_group(static_cast<const T*>(p.add) + row * p.ld_add + g * 8, valid, WIDE, n);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dy[j] += n[j];
+        }
+        if (p.sum != nullptr) store_group(static_cast<T*>(p.sum) + row * p.ld_sum + g * 8, valid, WIDE, dy);
+        if (p.y != nullptr) {
+          if constexpr (DROP) {
+            uint32_t words[1][4];
+            drop_words(p.drop, step, {static_cast<uint32_t>(row)}, {static_cast<uint32_t>(g)}, words);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dy[j] = drop_keeps(words[0], j, p.drop.above) ? dy[j] * p.drop.scale : 0.0f;
+          }
+          store_group(static_cast<T*>(p.y) + row * p.ld_y + g * 8, valid, WIDE, dy);
+        }
+      }
+      if (sums != nullptr) {
+        float* at[2] = {sums + g * 8, sums + width + g * 8};  // whole groups: the width is in pieces
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float4* q = reinterpret_cast<float4*>(at[i / 2]) + i % 2;
+          const float* v = (i < 2 ? dw : db) + i % 2 * 4;
+          float4 t = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *q;
+          t.x += v[0], t.y += v[1], t.z += v[2], t.w += v[3];
+          *q = t;
         }
       }
     }
-    if (p.y == nullptr && p.sum == nullptr) continue;
-    s1 = block_sum(s1, part) * p.inv_n;
-    s2 = block_sum(s2, part) * p.inv_n;
-    for (int g = threadIdx.x; g < p.groups; g += LN_LONG_THREADS) {
-      const int valid = p.N - g * 8;
-      float dy[8], n[8], w[8];
-      load(g, dy, n);
-      load_weights(p.w, g * 8, valid, p.wide_w, 1.0f, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) dy[j] = rstd * (fmaf(dy[j], w[j], -s1) - n[j] * s2);
-      if (p.add != nullptr) {
-        load_group(static_cast<const T*>(p.add) + row * p.ld_add + g * 8, valid, WIDE, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dy[j] += w[j];
-      }
-      if (p.sum != nullptr) store_group(static_cast<T*>(p.sum) + row * p.ld_sum + g * 8, valid, WIDE, dy);
-      if (p.y != nullptr) {
-        if constexpr (DROP) {
-          uint32_t words[1][4];
-          drop_words(p.drop, step, {static_cast<uint32_t>(row)}, {static_cast<uint32_t>(g)}, words);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) dy[j] = drop_keeps(words[0], j, p.drop.above) ? dy[j] * p.drop.scale : 0.0f;
-        }
-        store_group(static_cast<T*>(p.y) + row * p.ld_y + g * 8, valid, WIDE, dy);
-      }
-    }
+    first = false;
+    __syncthreads();  // the statistics are read
   }
 }
 

@@ -537,7 +537,7 @@ typedef struct gemm_epi_mask {
  * 16 bytes per access where pointers and row strides are multiples of them
  * (inputs and outputs each for themselves), single elements otherwise. */
 typedef struct gemm_epi_dropout_args {
-    int64_t M, N;             /* M < 2^31, 1 <= N <= 2^31 - 8; M 0 is allowed */
+    int64_t M, N;             /* M < 2^31, 1 <= N <= 2^31 - 4096; M 0 is allowed */
     int32_t type;             /* BF16 or F32: x, residual and y */
     gemm_epi_mask mask;
     const void *x;        int64_t ld_x;

@@ -122,7 +122,7 @@ ENTRIES = {"gemm_epi_dropout": dropout_args, "gemm_epi_layer_norm": norm_args,
            "gemm_epi_layer_norm_backward": backward_args}
 BOTH = [
     (dict(), TAKEN), (dict(M=0), TAKEN), (dict(M=-1), INVALID), (dict(M=2 ** 31), INVALID), (dict(N=0), INVALID),
-    (dict(N=2 ** 31 - 7), INVALID), (dict(N=-5), INVALID), (dict(type=N.GEMM_EPI_TYPE_E4M3), UNSUPPORTED),
+    (dict(N=2 ** 31 - 4095), INVALID), (dict(N=-5), INVALID), (dict(type=N.GEMM_EPI_TYPE_E4M3), UNSUPPORTED),
     (dict(threshold=0, step=None), TAKEN), (dict(threshold=65536), TAKEN), (dict(threshold=65537), INVALID),
     (dict(threshold=-1), INVALID), (dict(step=None), INVALID), (dict(x=None), INVALID), (dict(x="+1"), MISALIGNED),
     (dict(x="+2"), TAKEN), (dict(ld_x=0), TAKEN), (dict(ld_x=1), TAKEN), (dict(ld_x=-24), INVALID),
@@ -167,9 +167,9 @@ def test_null_arguments(lib, entry):
 
 def test_workspace_size(lib):
     size = lib.gemm_epi_layer_norm_backward_workspace_size
-    assert size(0) == size(-1) == size(2 ** 31 - 7) == 0
-    assert size(1) % 8 == 0 and 0 < size(1) < size(24) < size(2048)
-    assert 1 <= size(2 ** 31 - 8) / (304 * 2 * (2 ** 31 - 8) * 4) < 1.001  # no overflow
+    assert size(0) == size(-1) == size(2 ** 31 - 4095) == 0
+    assert size(1) % 16 == 0 and 0 < size(1) <= size(24) < size(257) < size(2048)
+    assert 1 <= size(2 ** 31 - 4096) / (304 * 2 * (2 ** 31 - 4096) * 4) < 1.001  # no overflow
 
 
 # ---------------------------------------------------------------- the binding
