@@ -81,10 +81,12 @@ def forms(cases):
     return out
 
 
+# The widest rows a team holds, by words: the most shared memory a block takes.
+CASES = forms(SIZES) + [(40, 16383, dtype, "odd", True, 0.1) for dtype in (BF, F32)]
 IDS = lambda c: "%dx%d-%s-%s-%s-p%g" % (c[0], c[1], str(c[2])[6:], c[3], "res" if c[4] else "x", c[5])  # noqa: E731
 
 
-@pytest.mark.parametrize("case", forms(SIZES), ids=IDS)
+@pytest.mark.parametrize("case", CASES, ids=IDS)
 def test_layer_norm(case):
     rows, cols, dtype, order, has_residual, p = case
     g = gen(rows * 31 + cols)
@@ -111,7 +113,7 @@ def test_layer_norm(case):
     assert float(mean[rows]) == 7.0 and float(rstd[rows]) == 7.0
 
 
-@pytest.mark.parametrize("case", forms(SIZES), ids=IDS)
+@pytest.mark.parametrize("case", CASES, ids=IDS)
 def test_layer_norm_backward(case):
     rows, cols, dtype, order, has_add, p = case
     g = gen(rows * 37 + cols)
@@ -135,7 +137,7 @@ def test_layer_norm_backward(case):
     dx.kept(), dr.kept()
 
 
-@pytest.mark.parametrize("case", forms(SIZES), ids=IDS)
+@pytest.mark.parametrize("case", CASES, ids=IDS)
 def test_dropout(case):
     rows, cols, dtype, order, has_residual, p = case
     g = gen(rows * 41 + cols)
@@ -262,7 +264,9 @@ def all_outputs(rows, cols, dtype, g):
     return run, (x, residual, dy, add), rng
 
 
-@pytest.mark.parametrize("rows,cols,dtype", [(300, 200, BF), (2500, 4096, BF), (50, 1000, F32), (20, 16392, BF)])
+@pytest.mark.parametrize("rows,cols,dtype", [(300, 200, BF), (2500, 4096, BF), (50, 1000, F32), (20, 16392, BF),
+                                             (3001, 17, F32), (300, 253, BF), (400, 1001, F32), (700, 4095, BF),
+                                             (9, 16383, F32), (20, 16389, BF)])
 def test_same_bits_every_time_in_place_and_on_a_stream(rows, cols, dtype):
     run, (x, residual, dy, add), _ = all_outputs(rows, cols, dtype, gen(5))
     fresh = lambda: [torch.empty_like(x) for _ in range(4)]  # noqa: E731
@@ -277,6 +281,20 @@ def test_same_bits_every_time_in_place_and_on_a_stream(rows, cols, dtype):
     # y over x, the sum over the residual, dx over dy, the residual's gradient over `add`
     placed_ = run(x, residual, dy, add)
     assert all(torch.equal(a, b) for a, b in zip(first, placed_))
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(64, 200, BF), (900, 4096, BF), (333, 1001, F32), (7, 16392, F32)])
+def test_two_at_once(rows, cols, dtype):
+    """Forward and backward passes on two streams, each with a workspace of its own, and a third on the caller's."""
+    runs = [all_outputs(rows, cols, dtype, gen(seed)) for seed in (21, 22, 23)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(), None]
+    fresh = lambda x: [torch.empty_like(x) for _ in range(4)]  # noqa: E731
+    want = [run(*fresh(x)) for run, (x, *_), _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [run(*fresh(x), stream=s) for (run, (x, *_), _), s in zip(runs, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for w, g in zip(want, got) for a, b in zip(w, g))
 
 
 def test_captured_and_replayed():

@@ -89,7 +89,7 @@ def norm_args(**kw):
     a._keep = buf
     a.M, a.N, a.type, a.eps = 4, 24, N.GEMM_EPI_TYPE_BF16, 1e-5
     a.x, a.ld_x, a.residual, a.ld_residual, a.y, a.ld_y = at, 24, at + 1024, 24, at + 2048, 24
-    a.sum, a.ld_sum, a.w, a.b, a.mean, a.rstd = at + 3072, 24, at + 5000, at + 5200, at + 5400, at + 5600
+    a.sum, a.ld_sum, a.w, a.b, a.mean, a.rstd = at + 3008, 24, at + 5000, at + 5200, at + 5400, at + 5600
     a.mask.step, a.mask.threshold = at + 4096, 6554
     return fill(a, kw, at)
 
@@ -100,7 +100,7 @@ def backward_args(**kw):
     a._keep = buf
     a.M, a.N, a.type = 4, 24, N.GEMM_EPI_TYPE_BF16
     a.dy, a.ld_dy, a.x, a.ld_x, a.add, a.ld_add = at, 24, at + 1024, 24, at + 2048, 24
-    a.dx, a.ld_dx, a.d_residual, a.ld_d_residual = at + 3072, 24, at + 6144, 24
+    a.dx, a.ld_dx, a.d_residual, a.ld_d_residual = at + 3008, 24, at + 6144, 24
     a.w, a.mean, a.rstd, a.dw, a.db = at + 5000, at + 5200, at + 5400, at + 5600, at + 5800
     a.workspace, a.workspace_bytes = at + 8192, N.load().gemm_epi_layer_norm_backward_workspace_size(24)
     a.mask.step, a.mask.threshold = at + 4096, 6554
