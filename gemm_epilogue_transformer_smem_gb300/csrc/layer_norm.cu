@@ -25,10 +25,10 @@ using ge_norm::Shape;
 // How many pieces of 256 columns a warp holds, how many rows a team works on at
 // once, how many teams share a block and whether they share the weights: from
 // timing them all at 512 to 14336 columns (one GB300, 537 MB forward, 671 MB
-// backward with dropout; the times beside the rules are of those).  Few rows:
-// not more than two to an SM, whose latency counts, so many warps to a row and
-// nothing staged.
-Shape forward_shape(int64_t rows, int64_t pieces, const Choice& c, int sms) {
+// backward with dropout, unless others are named; the times beside the rules are
+// of those).  Few rows: not more than two to an SM, whose latency counts, so many
+// warps to a row and nothing staged.
+Shape forward_shape(int64_t rows, int64_t cols, int64_t pieces, const Choice& c, int sms) {
   const bool few = rows <= 2 * sms;
   bool staged = c.drop;
   Shape s{HELD, 4, 1, 1, 0, 1, false};
@@ -37,23 +37,30 @@ Shape forward_shape(int64_t rows, int64_t pieces, const Choice& c, int sms) {
     s.warps = static_cast<int>((pieces + k - 1) / k);
   };
   auto warps = [&](int n) { s.teams = std::max(1, n / s.warps); };
+  // bf16 with a second stream: two pieces and one row make for more teams, but the
+  // last warp of a row that ends inside its columns has no staged weights there.
+  // With dropout 1024 columns 79.9 us for 84.5 with 4 and 2 (268 MB), 1000 102 for
+  // 94.4, 1800 110 for 93.8, 1280, which fills 5 of 8 pieces, 105 for 109.8; without
+  // 4096 88.7 for 91.5, 4000 92.0 for 86.6, 768 95.4 for 98.2, 600 112 for 101.
+  const bool even = cols % (2 * ge::LN_PIECE) == 0;
+  const bool two = c.drop ? pieces <= 8 && (even || pieces <= 2 || pieces == 5 || pieces == 6)
+                          : pieces <= 16 && (even || (pieces <= 8 && pieces != 3));
   if (!c.wide) {
     take(4, 1);
   } else if (few && pieces <= 2 * ge::LN_MAX_WARPS) {
     take(2, 1);
   } else if (c.f32) {
-    // 8192 x 4096: 2 pieces, 2 rows 90.8 us with dropout, 4 and 1 94.9
-    pieces <= 2 * ge::LN_MAX_WARPS ? take(2, 2) : take(4, 1);
-    if (c.drop || !c.add) warps(16);
+    // 8192 x 4096: 2 pieces, 2 rows 90.8 us with dropout, 4 and 1 94.9; 13421 x 5000
+    // 98.9 and 87.9
+    pieces <= 16 ? take(2, 2) : take(4, 1);
+    if (pieces <= 16 && (c.drop || !c.add)) warps(16);
   } else if (!c.drop && !c.add) {
     // one stream in: 4096 columns with 2 pieces, 1 row over 75 us, 4 and 2 47.8 (57.1
     // not staged); 512: 46.0 with 2 and 1, over 53 with 4 and 2
     pieces <= 2 ? take(2, 1) : take(4, 2);
     warps(16);
     staged = true;
-  } else if (pieces <= (c.drop ? 8 : 16)) {
-    // 2048 columns: 2 pieces, 1 row 85.3 us (89.4 with dropout), 4 and 2 92.2 (93.5);
-    // 4096: 88.7 (96.3) and 91.5 (91.5)
+  } else if (two) {
     take(2, 1);
     warps(c.drop || s.warps <= 4 ? 16 : 8);
   } else {
@@ -61,6 +68,7 @@ Shape forward_shape(int64_t rows, int64_t pieces, const Choice& c, int sms) {
     // weights 100 (94.2)
     take(4, 2);
     if (c.drop) warps(16);
+    else if (s.warps <= 2) warps(8);
   }
   if (!c.wide) warps(16);
   // For few rounds staging the weights costs more than their misses in L1 (1777 x
@@ -84,16 +92,19 @@ Shape backward_shape(int64_t rows, int64_t pieces, const Choice& c, int sms) {
     take(pieces <= ge::LN_MAX_WARPS ? 1 : pieces <= 2 * ge::LN_MAX_WARPS ? 2 : 4);
     return s;
   } else if (c.f32) {
-    // 67108 x 1000: 1 piece 94.2 us, 4 109.9; 8192 x 4096: 2 pieces 95.6 us, 4 100.0
-    take(pieces <= 4 ? 1 : pieces <= 2 * ge::LN_MAX_WARPS ? 2 : 4);
+    // of 235 MB: 1280 columns 1 piece 46.0 us (55.1 with dropout), 2 52.3 (62.9);
+    // 4096: 2 pieces 51.0 (61.2), 4 53.1 (63.6); 6000: 65.9 (82.0) and 53.6 (76.0)
+    take(pieces <= 5 ? 1 : pieces <= 16 ? 2 : 4);
   } else {
-    // 1024 columns: 2 pieces 88.1 us (109.6 with dropout), 4 91.5 (123.9);
-    // 4096: 101.7 (130.0) and 91.5 (115.7)
-    take(pieces <= 8 ? 2 : 4);
+    // 768 columns of 268 MB: 2 pieces 57.2 us (63.9 with dropout), all 3 in a warp 47.2
+    // (59.2); 1024: 2 pieces 90.3 (110.4), 4 93.4 (127.8); 4096: 99.5 (120.6) and 89.3
+    // (113.5)
+    take(pieces == 3 || pieces > 8 ? 4 : 2);
   }
-  // 4096 columns with dropout: one team to a block 115.7 us, four 126.5; without 94.2
-  // and 91.5
-  s.teams = c.wide && c.drop && pieces > 8 ? 1 : ge::LN_MAX_WARPS / s.warps;
+  // 3000 columns: one team of 3 warps to a block 126 us (158 with dropout, and only two
+  // blocks to an SM have room for their sums), five 103 (123); 4096: three of 4 warps 89.3
+  // (113.5), four 94.1 (126.8)
+  s.teams = c.wide && !c.f32 && s.warps == 4 && s.k == 4 ? 3 : ge::LN_MAX_WARPS / s.warps;
   s.staged = true;  // 4096: 91.5 us, 113.3 from L1
   return s;
 }
@@ -113,7 +124,7 @@ Shape shape_of(bool backward, int64_t rows, int64_t cols, const Choice& c, int s
     if (backward) s.rows = static_cast<int>(std::min<int64_t>(ge::LN_LONG_ROWS, std::max<int64_t>(1, rows / (2 * sms))));
     return s;
   }
-  Shape s = backward ? backward_shape(rows, pieces, c, sms) : forward_shape(rows, pieces, c, sms);
+  Shape s = backward ? backward_shape(rows, pieces, c, sms) : forward_shape(rows, cols, pieces, c, sms);
   // a block to every SM before a second team to a block
   s.teams = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s.teams, rows / (s.rows * sms))));
   return s;

@@ -215,13 +215,13 @@ struct Eight {
   __device__ __forceinline__ float2 sum() const {
     return __fadd2_rn(__fadd2_rn(v[0], v[1]), __fadd2_rn(v[2], v[3]));
   }
-  // Sum of (v - m)^2.
-  __device__ __forceinline__ float2 squares(float m) const {
-    const float2 minus = make_float2(-m, -m);
+  // Sum of (v - m)^2, m0 of the first four and m1 of the others.
+  __device__ __forceinline__ float2 squares(float m0, float m1) const {
     float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 c = __fadd2_rn(v[i], minus);
+      const float minus = -(i < 2 ? m0 : m1);
+      const float2 c = __fadd2_rn(v[i], make_float2(minus, minus));
       s = __ffma2_rn(c, c, s);
     }
     return s;
@@ -241,6 +241,7 @@ struct Eight {
 // pieces are constants, and what a row costs a thread beside its values (its
 // sums' shuffles, the barrier, the addresses) is spread over 8 K of them.
 constexpr int LN_PIECE = 256;
+enum { LN_ANY, LN_WHOLE, LN_ALL };
 constexpr int LN_MAX_WARPS = 16;
 constexpr int LN_BLOCK_WARPS = 8;  // of blocks that hold several teams
 constexpr int LN_MAX_SHARED = 224 * 1024;  // of the 227 KB of a block, beside what is not dynamic
@@ -303,12 +304,14 @@ struct RowPlace {
   static constexpr int EACH = 8 / PARTS, APART = LN_PIECE / PARTS;
   int col;    // of piece 0, part 0
   int left;   // columns from `col` to the row's end (<= 0: none)
-  bool full;  // all of the warp's columns are in the row
+  bool full;   // all of the warp's columns are in the row
+  bool whole;  // each of a thread's 16 bytes is in the row or is not
 
   __device__ __forceinline__ RowPlace(int N, int begin) {
     col = begin + (threadIdx.x & 31) * EACH;
     left = N - col;
     full = begin + K * LN_PIECE <= N;
+    whole = N % EACH == 0;
   }
   // Columns of a part that are in the row (<= 0: none).
   __device__ __forceinline__ int valid(int k, int i) const { return min(left - k * LN_PIECE - i * APART, EACH); }
@@ -325,6 +328,34 @@ struct RowPlace {
     g.pack(f);
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) store_part(row + k * LN_PIECE + i * APART, all ? EACH : valid(k, i), true, g.q[i]);
+  }
+  // The same of a row whose 16 bytes are there whole or not at all, without a branch.
+  __device__ __forceinline__ void store_whole(T* row, int k, const Eight& v) const {
+    Group<T> g;
+    float f[8];
+    v.to(f);
+    g.pack(f);
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i)
+      if (valid(k, i) > 0) *reinterpret_cast<uint4*>(row + k * LN_PIECE + i * APART) = g.q[i];
+  }
+  // fp32 vectors on 16 bytes likewise; behind the row's end any of its values.
+  __device__ __forceinline__ void weights_whole(const float* w, int k, float none, Eight& v) const {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = none;
+    if (w != nullptr) {
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i) {
+        const float* from = w + (valid(k, i) > 0 ? col + k * LN_PIECE + i * APART : 0);
+#pragma unroll
+        for (int j = 0; j < EACH; j += 4) {
+          const float4 q = __ldg(reinterpret_cast<const float4*>(from + j));
+          f[i * EACH + j] = q.x, f[i * EACH + j + 1] = q.y, f[i * EACH + j + 2] = q.z, f[i * EACH + j + 3] = q.w;
+        }
+      }
+    }
+    v.from(f);
   }
   // fp32 vectors, `none` behind the row's end and without one.
   __device__ __forceinline__ void weights(const float* w, int k, bool wide, float none, Eight& v) const {
@@ -352,7 +383,10 @@ struct RowPlace {
     for (int j = 0; j < 8; ++j)
       if (j % EACH < valid(k, j / EACH)) f(j, col + k * LN_PIECE + j / EACH * APART + j % EACH);
   }
-  // Sum of (v - m)^2 over piece k's columns in the row.
+  // Sum of (v - m)^2 over piece k's columns in the row, behind whose end v is 0.
+  __device__ __forceinline__ float2 squares_whole(const Eight& v, float m, int k) const {
+    return v.squares(valid(k, 0) > 0 ? m : 0.0f, valid(k, PARTS - 1) > 0 ? m : 0.0f);
+  }
   __device__ __forceinline__ float squares(const Eight& v, float m, int k) const {
     float f[8], s = 0.0f;
     v.to(f);
@@ -456,19 +490,39 @@ struct WordRing {
   static __device__ __forceinline__ uint32_t shift(const T* row) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 3u;
   }
+  // The I-th words of a warp's lanes: 1 to ...
+  template <int... Is>
+  static __device__ __forceinline__ void fetch_full(uint32_t to, const uint8_t* from, std::integer_sequence<int, Is...>) {
+    (ptx::cp_async4<(Is + 1) * 128, (Is + 1) * 128>(to, from), ...);
+  }
   // `row`: at the warp's first column, `count` of which are in the row.
   __device__ __forceinline__ void fetch(int d, int t, const T* row, int count) const {
     if (count <= 0) return;
     const uint32_t off = shift(row), bytes = static_cast<uint32_t>(count) * sizeof(T) + off;
     const uint8_t* src = reinterpret_cast<const uint8_t*>(row) - off;
     const int segment = (d * TENSORS + t) * SEGMENT;
-#pragma unroll 4
-    for (uint32_t i = (threadIdx.x & 31) * 4; i < bytes; i += 128) {
-      if (i == 0 && off != 0)  // nothing in front of the row is read
-        *reinterpret_cast<uint16_t*>(slots + segment + 2) = *reinterpret_cast<const uint16_t*>(row);
-      else
-        ptx::cp_async4(at + segment + i, src + i, min(bytes - i, 4u));
+    if (count == K * LN_PIECE) {  // an instruction to a word: 16384 x 4095 backward X us, Y with the loop alone
+      constexpr int FULL = K * LN_PIECE * static_cast<int>(sizeof(T)) / 128;
+      const uint32_t lane = threadIdx.x & 31;
+      if (off != 0 && lane == 0) {  // the first and the last half words
+        uint16_t* to = reinterpret_cast<uint16_t*>(slots + segment);
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(row);
+        to[1] = from[0];
+        to[K * LN_PIECE] = from[K * LN_PIECE - 1];
+      } else {
+        ptx::cp_async4<0, 0>(at + segment + lane * 4, src + lane * 4);
+      }
+      fetch_full(at + segment + lane * 4, src + lane * 4, std::make_integer_sequence<int, FULL - 1>{});
+      return;
     }
+    uint32_t i = (threadIdx.x & 31) * 4;
+    if (i == 0 && off != 0) {  // nothing in front of the row is read
+      *reinterpret_cast<uint16_t*>(slots + segment + 2) = *reinterpret_cast<const uint16_t*>(row);
+      i += 128;
+    }
+#pragma unroll 4
+    for (; i + 4 <= bytes; i += 128) ptx::cp_async4<0, 0>(at + segment + i, src + i);
+    if (i < bytes) ptx::cp_async4(at + segment + i, src + i, bytes - i);
   }
   // Zeros behind the row's end.
   __device__ __forceinline__ void take(int d, int t, int k, const T* row, const Place& place, Eight& v) const {
@@ -508,7 +562,27 @@ __device__ __forceinline__ void store_words(uint4* smem, T* row, int count, int 
   __syncwarp();
   T* to = row + k * LN_PIECE;
   const T* from = reinterpret_cast<const T*>(smem);
-  if constexpr (sizeof(T) == 4) {
+  if (left == LN_PIECE) {
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(smem) + lane;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) reinterpret_cast<uint32_t*>(to)[lane + 32 * j] = words[32 * j];
+    } else if ((reinterpret_cast<uintptr_t>(to) & 2) == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(to)[lane + 32 * j] = words[32 * j];
+    } else {  // an element in front of the first word, one behind the last
+      if (lane == 0) to[0] = from[0];
+      uint32_t* at = reinterpret_cast<uint32_t*>(to + 1) + lane;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = __funnelshift_r(words[32 * j], words[32 * j + 1], 16);
+        if (j == 3 && lane == 31)
+          *reinterpret_cast<uint16_t*>(at + 32 * j) = static_cast<uint16_t>(w);
+        else
+          at[32 * j] = w;
+      }
+    }
+  } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (lane + 32 * j < left) to[lane + 32 * j] = from[lane + 32 * j];
@@ -728,6 +802,7 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
   uint4* staging = ln_smem + (blockDim.x >> 5) * (Ring::WARP_BYTES / 16) + teams.warp * 64;  // by words: the warp's 1 KB
   const uint32_t rows = static_cast<uint32_t>(p.M), stride = static_cast<uint32_t>(teams.stride) * R;
   const bool residual = ADD && p.other != nullptr;
+  constexpr bool BY_16 = K * R > 2;
   // worked out where they are needed: kept, they would cost registers
   const int begin = WIDE ? place.col : warp * K * LN_PIECE;
   const int count = min(max(p.N - warp * K * LN_PIECE, 0), K * LN_PIECE);  // of the warp's values
@@ -802,10 +877,11 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
     for (int r = 0; r < R; ++r) mean[r] = warp_sum(mean[r]) * inv_count;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (place.full) {
+      if (place.full || (WIDE && BY_16 && place.whole)) {
         float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int k = 0; k < K; ++k) s2 = __fadd2_rn(s2, h[r][k].squares(mean[r]));
+        for (int k = 0; k < K; ++k)
+          s2 = __fadd2_rn(s2, WIDE && BY_16 ? place.squares_whole(h[r][k], mean[r], k) : h[r][k].squares(mean[r], mean[r]));
         square[r] = s2.x + s2.y;
       } else {
         square[r] = 0.0f;
@@ -855,32 +931,39 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
     }
     T* y = static_cast<T*>(p.y) + row * p.ld_y + begin;
     T* sum = static_cast<T*>(p.sum) + row * p.ld_sum + begin;
-    auto store = [&](T* to, int k, bool all, const Eight& v) {
-      if constexpr (WIDE)
-        place.store(to, k, all, v);
-      else
+    // PART: which of the warp's columns are in the row -- all, 16 bytes whole or not
+    // at all, any.
+    auto store = [&](T* to, int k, auto part, const Eight& v) {
+      if constexpr (!WIDE)
         store_words<T>(staging, to, count, k, v);
+      else if constexpr (part == LN_WHOLE)
+        place.store_whole(to, k, v);
+      else
+        place.store(to, k, part == LN_ALL, v);
     };
-    auto finish = [&](int k, bool all, const Eight& w, const Eight& b) {
+    auto finish = [&](int k, auto part, const Eight& w, const Eight& b) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (row + r >= rows) break;
         Eight& v = h[r][k];
-        if (p.sum != nullptr) store(sum + r * p.ld_sum, k, all, v);
+        if (p.sum != nullptr) store(sum + r * p.ld_sum, k, part, v);
         v.normalise(mean[r], rstd[r]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v.v[i] = __ffma2_rn(v.v[i], w.v[i], b.v[i]);
-        store(y + r * p.ld_y, k, all, v);
+        store(y + r * p.ld_y, k, part, v);
       }
     };
-    if (place.full && weights != nullptr) {
+    auto staged = [&](auto part) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         Eight w, b;
         staged_weights(weights, k, w);
         staged_weights(weights + teams.width, k, b);
-        finish(k, true, w, b);
+        finish(k, part, w, b);
       }
+    };
+    if (WIDE && (place.full || (BY_16 && place.whole)) && weights != nullptr) {
+      staged(std::integral_constant<int, BY_16 ? LN_WHOLE : LN_ALL>{});
     } else {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -893,7 +976,7 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
           place.weights(p.w, k, WIDE || p.wide_w, 1.0f, w);
           place.weights(p.b, k, WIDE || p.wide_w, 0.0f, b);
         }
-        finish(k, false, w, b);
+        finish(k, std::integral_constant<int, LN_ANY>{}, w, b);
       }
     }
   }

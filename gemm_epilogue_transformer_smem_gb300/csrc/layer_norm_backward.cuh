@@ -102,32 +102,35 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
       }
       n.normalise(mean, rstd);
     };
-    // f(k, all of its columns are in the row, weights) of the pieces that have any
+    // f(k, which of its columns are in the row, weights) of the pieces
     auto pieces = [&](auto&& f) {
-      if (place.full && weights != nullptr) {
+      auto staged = [&](auto part) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           Eight w;
           staged_weights(weights, k, w);
-          f(k, true, w);
+          f(k, part, w);
         }
+      };
+      if (WIDE && (place.full || place.whole) && weights != nullptr) {
+        staged(std::integral_constant<int, LN_WHOLE>{});
       } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           if (WIDE ? place.valid(k, 0) <= 0 : count <= k * LN_PIECE) continue;  // by words: the warp as one
           Eight w;
-          if (!WIDE && weights != nullptr)
+          if (weights != nullptr)
             staged_weights(weights, k, w);
           else
             place.weights(p.w, k, WIDE || p.wide_w, 1.0f, w);
-          f(k, false, w);
+          f(k, std::integral_constant<int, LN_ANY>{}, w);
         }
       }
     };
     ptx::cp_async_wait<DEPTH - 1>();
     if constexpr (!WIDE) __syncwarp();
     float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
-    pieces([&](int k, bool, const Eight& w) {
+    pieces([&](int k, auto, const Eight& w) {
       Eight g, n;
       take(k, g, n);  // dy is zero behind the row's end
       add_group(g, n, w, dw[k], db[k], s1, s2);
@@ -154,13 +157,15 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
       uint32_t words[BATCH][4];
       T* y = static_cast<T*>(p.y) + row * p.ld_y + begin;
       T* sum = static_cast<T*>(p.sum) + row * p.ld_sum + begin;
-      auto store = [&](T* to, int k, bool all, const Eight& v) {
-        if constexpr (WIDE)
-          place.store(to, k, all, v);
-        else
+      auto store = [&](T* to, int k, auto part, const Eight& v) {
+        if constexpr (!WIDE)
           store_words<T>(staging, to, count, k, v);
+        else if constexpr (part == LN_WHOLE)
+          place.store_whole(to, k, v);
+        else
+          place.store(to, k, part == LN_ALL, v);
       };
-      pieces([&](int k, bool all, const Eight& w) {
+      pieces([&](int k, auto part, const Eight& w) {
         if constexpr (DROP) {
           if (k % BATCH == 0) place.words(p.drop, step, row, k, words);
         }
@@ -174,9 +179,9 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_backward_kernel(
             ring.take(d, 2, k, at(p.add, p.ld_add, row), place, a);
         }
         norm_gradient(g, n, w, a, rstd, m1, m2);
-        if (p.sum != nullptr) store(sum, k, all, g);
+        if (p.sum != nullptr) store(sum, k, part, g);
         if constexpr (DROP) g.drop(p.drop, words[k % BATCH]);
-        if (p.y != nullptr) store(y, k, all, g);
+        if (p.y != nullptr) store(y, k, part, g);
       });
     }
     if constexpr (!WIDE) __syncwarp();
