@@ -45,8 +45,11 @@ Shape forward_shape(int64_t rows, int64_t cols, int64_t pieces, const Choice& c,
   const bool even = cols % (2 * ge::LN_PIECE) == 0;
   const bool two = c.drop ? pieces <= 8 && (even || pieces <= 2 || pieces == 5 || pieces == 6)
                           : pieces <= 16 && (even || (pieces <= 8 && pieces != 3));
-  if (!c.wide) {
+  if (!c.wide && (!few || pieces > 2 * ge::LN_MAX_WARPS)) {
+    // by words 8 warps to a block: 16384 x 4095 149 us with dropout (fp32 240), 16 151
+    // (261); 1777 x 1003 fp32 4 warps 5.6, 16 8.6
     take(4, 1);
+    warps(rows > 16 * sms ? 8 : 4);
   } else if (few && pieces <= 2 * ge::LN_MAX_WARPS) {
     take(2, 1);
   } else if (c.f32) {
@@ -70,10 +73,9 @@ Shape forward_shape(int64_t rows, int64_t cols, int64_t pieces, const Choice& c,
     if (c.drop) warps(16);
     else if (s.warps <= 2) warps(8);
   }
-  if (!c.wide) warps(16);
   // For few rounds staging the weights costs more than their misses in L1 (1777 x
   // 1024 5.9 us staged, 4.9 not).
-  s.staged = c.wide ? !c.f32 && staged && rows > 16 * sms : !few;
+  s.staged = rows > 16 * sms && (!c.wide || (!c.f32 && staged));
   return s;
 }
 
@@ -85,8 +87,9 @@ Shape backward_shape(int64_t rows, int64_t pieces, const Choice& c, int sms) {
     s.warps = static_cast<int>((pieces + k - 1) / k);
   };
   if (!c.wide) {
-    // by words 4 pieces spill 124 to 192 bytes of registers
-    take(pieces <= 2 * ge::LN_MAX_WARPS ? 2 : 4);
+    // by words, with dropout, 4 pieces spill 60 to 148 bytes of registers: 12000 x 4095
+    // 203 us with 2, 259 with 4; without 141 and 117
+    take(pieces > 2 * ge::LN_MAX_WARPS || (!c.drop && pieces > 2 && rows > 16 * sms) ? 4 : 2);
     if (few) return s;
   } else if (few) {
     take(pieces <= ge::LN_MAX_WARPS ? 1 : pieces <= 2 * ge::LN_MAX_WARPS ? 2 : 4);

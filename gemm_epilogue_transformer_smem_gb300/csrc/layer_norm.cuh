@@ -23,16 +23,17 @@
 // One GB300, of the measured copy bandwidth (6792 GB/s), what is left beside the
 // copies: the chain from a row's sums to its stores, which 16 warps of an SM
 // hide, and with dropout 8 integer instructions an element for the mask.
-//   norm, dropout and residual, 16384 x 4096 bf16 (537 MB)   92.7 us  0.85
+//   norm, dropout and residual, 16384 x 4096 bf16 (537 MB)   92.4 us  0.86
 //   the same without dropout                                 88.6 us  0.89
-//   norm alone, 16384 x 4096 (268 MB)                        48.0 us  0.82
-//   backward with dropout and `add`, 16384 x 4096 (671 MB)  116.5 us  0.85
-//   the same of 65536 x 1024                                111.4 us  0.89
-//   backward with `add`, 2048 x 14336 (235 MB)               53.3 us  0.65: 14 warps
-//     to a row leave room for one row on an SM, whose phases nothing overlaps
+//   norm alone, 16384 x 4096 (268 MB)                        47.5 us  0.83
+//   backward with dropout and `add`, 16384 x 4096 (671 MB)  114.5 us  0.86
+//   the same of 65536 x 1024                                112.4 us  0.88
+//   backward with `add`, 2048 x 14336 (235 MB)               53.6 us  0.65: 14 warps
+//     to a row leave room for one row on an SM, whose phases nothing overlaps (a
+//     row shared by a cluster of two blocks, so that two rows fit: 61)
 //   dropout, 8192 x 14336 (470 MB)                           78.5 us  0.88
-//   rows that start anywhere, 16384 x 4095 (537 MB)         200   us  0.39: words
-//     of 4 bytes in place of 16
+//   rows that start anywhere, 16384 x 4095 (537 MB)         151   us  0.52: words
+//     of 4 bytes in place of 16; backward (671 MB) 271 us, 0.36
 #pragma once
 
 #include <stdint.h>
@@ -241,6 +242,8 @@ struct Eight {
 // pieces are constants, and what a row costs a thread beside its values (its
 // sums' shuffles, the barrier, the addresses) is spread over 8 K of them.
 constexpr int LN_PIECE = 256;
+// Which columns of a piece are in the row: any, each 16 bytes' worth whole or not
+// at all, all.
 enum { LN_ANY, LN_WHOLE, LN_ALL };
 constexpr int LN_MAX_WARPS = 16;
 constexpr int LN_BLOCK_WARPS = 8;  // of blocks that hold several teams
@@ -338,24 +341,6 @@ struct RowPlace {
 #pragma unroll
     for (int i = 0; i < PARTS; ++i)
       if (valid(k, i) > 0) *reinterpret_cast<uint4*>(row + k * LN_PIECE + i * APART) = g.q[i];
-  }
-  // fp32 vectors on 16 bytes likewise; behind the row's end any of its values.
-  __device__ __forceinline__ void weights_whole(const float* w, int k, float none, Eight& v) const {
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = none;
-    if (w != nullptr) {
-#pragma unroll
-      for (int i = 0; i < PARTS; ++i) {
-        const float* from = w + (valid(k, i) > 0 ? col + k * LN_PIECE + i * APART : 0);
-#pragma unroll
-        for (int j = 0; j < EACH; j += 4) {
-          const float4 q = __ldg(reinterpret_cast<const float4*>(from + j));
-          f[i * EACH + j] = q.x, f[i * EACH + j + 1] = q.y, f[i * EACH + j + 2] = q.z, f[i * EACH + j + 3] = q.w;
-        }
-      }
-    }
-    v.from(f);
   }
   // fp32 vectors, `none` behind the row's end and without one.
   __device__ __forceinline__ void weights(const float* w, int k, bool wide, float none, Eight& v) const {
@@ -490,7 +475,7 @@ struct WordRing {
   static __device__ __forceinline__ uint32_t shift(const T* row) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 3u;
   }
-  // The I-th words of a warp's lanes: 1 to ...
+  // A warp's words but the first of each lane.
   template <int... Is>
   static __device__ __forceinline__ void fetch_full(uint32_t to, const uint8_t* from, std::integer_sequence<int, Is...>) {
     (ptx::cp_async4<(Is + 1) * 128, (Is + 1) * 128>(to, from), ...);
@@ -501,7 +486,7 @@ struct WordRing {
     const uint32_t off = shift(row), bytes = static_cast<uint32_t>(count) * sizeof(T) + off;
     const uint8_t* src = reinterpret_cast<const uint8_t*>(row) - off;
     const int segment = (d * TENSORS + t) * SEGMENT;
-    if (count == K * LN_PIECE) {  // an instruction to a word: 16384 x 4095 backward X us, Y with the loop alone
+    if (count == K * LN_PIECE) {  // an instruction to a word: 16384 x 4095 plain 94.5 us, 115 with the loop alone
       constexpr int FULL = K * LN_PIECE * static_cast<int>(sizeof(T)) / 128;
       const uint32_t lane = threadIdx.x & 31;
       if (off != 0 && lane == 0) {  // the first and the last half words
@@ -802,6 +787,9 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
   uint4* staging = ln_smem + (blockDim.x >> 5) * (Ring::WARP_BYTES / 16) + teams.warp * 64;  // by words: the warp's 1 KB
   const uint32_t rows = static_cast<uint32_t>(p.M), stride = static_cast<uint32_t>(teams.stride) * R;
   const bool residual = ADD && p.other != nullptr;
+  // A row that ends inside the warp's columns, on 16 bytes, costs next to nothing more
+  // (4000 columns plain 43 us, 58 else); the small kernels have no registers for it:
+  // 64 are two blocks to an SM.
   constexpr bool BY_16 = K * R > 2;
   // worked out where they are needed: kept, they would cost registers
   const int begin = WIDE ? place.col : warp * K * LN_PIECE;
@@ -931,8 +919,6 @@ __global__ void __launch_bounds__(32 * LN_MAX_WARPS) layer_norm_kernel(const __g
     }
     T* y = static_cast<T*>(p.y) + row * p.ld_y + begin;
     T* sum = static_cast<T*>(p.sum) + row * p.ld_sum + begin;
-    // PART: which of the warp's columns are in the row -- all, 16 bytes whole or not
-    // at all, any.
     auto store = [&](T* to, int k, auto part, const Eight& v) {
       if constexpr (!WIDE)
         store_words<T>(staging, to, count, k, v);

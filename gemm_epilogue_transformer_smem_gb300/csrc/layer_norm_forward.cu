@@ -14,7 +14,7 @@ Kernel held_forward() {
 
 template <class T, bool DROP, bool ADD>
 Kernel held_forward(const Shape& s, bool wide) {
-  if (!wide) return held_forward<T, DROP, ADD, 4, 1, false>();
+  if (!wide) return s.k == 2 ? held_forward<T, DROP, ADD, 2, 1, false>() : held_forward<T, DROP, ADD, 4, 1, false>();
   if (s.k == 2 && s.rows == 1) return held_forward<T, DROP, ADD, 2, 1, true>();
   if constexpr (sizeof(T) == 2)
     return held_forward<T, DROP, ADD, 4, 2, true>();
