@@ -28,9 +28,10 @@
 //   norm alone, 16384 x 4096 (268 MB)                        47.5 us  0.83
 //   backward with dropout and `add`, 16384 x 4096 (671 MB)  114.5 us  0.86
 //   the same of 65536 x 1024                                112.4 us  0.88
-//   backward with `add`, 2048 x 14336 (235 MB)               53.6 us  0.65: 14 warps
-//     to a row leave room for one row on an SM, whose phases nothing overlaps (a
-//     row shared by a cluster of two blocks, so that two rows fit: 61)
+//   backward with `add`, 2048 x 14336 (235 MB)               53.6 us  0.65 (16384
+//     rows 290 us, 0.95): 13.5 rows to an SM, so that the way in of the first, the
+//     14th round and the sum of the partial sums (5.5 us) weigh.  A row shared by a
+//     cluster of two blocks, with two rows on an SM: 61
 //   dropout, 8192 x 14336 (470 MB)                           78.5 us  0.88
 //   rows that start anywhere, 16384 x 4095 (537 MB)         151   us  0.52: words
 //     of 4 bytes in place of 16; backward (671 MB) 271 us, 0.36
