@@ -1397,8 +1397,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // With dropout, while the main loop runs: the bias likewise, and with
       // masks_ahead the row's mask, a bit for each column where it is dropped
       // (accumulator columns in front of DSWIGLU), into a column of shared memory
-      // of the thread's own.  Programs with an e4m3 store, whose buffers these
-      // are, draw it between chunks.
+      // of the thread's own: eight words, which the 512 output columns of a tile
+      // behind DSWIGLU would overrun.  Programs that drop there, and those with an
+      // e4m3 store, whose buffers these are, draw it between chunks.
       uint32_t* masks = reinterpret_cast<uint32_t*>(staged_cols + BLOCK_N) + lane;
       if constexpr (Prog::drops) {
         if constexpr (prog_stages_bias<Prog>()) {
@@ -1413,10 +1414,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             masks[i * 32] = drop_bits(p.drop, dropout_step, static_cast<uint32_t>(row_base + m), first + i * 32);
         }
       }
-      // of the i-th 32 columns
-      auto mask_of = [&](int i) {
+      // of the i-th 32 columns from `first` on, the tile's first where it is dropped
+      auto mask_of = [&](int i, int first) {
         if (p.masks_ahead) return masks[i * 32];
-        return drop_bits(p.drop, dropout_step, static_cast<uint32_t>(row_base + m), (expand ? nacc0 : n0) + i * 32);
+        return drop_bits(p.drop, dropout_step, static_cast<uint32_t>(row_base + m), first + i * 32);
       };
 
       // All lanes wait; the outcome is made warp-uniform so that no lane
@@ -1654,7 +1655,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           auto before = [&](auto code) {
             if (Prog::drops && static_cast<int>(code) == GEMM_EPI_OP_DROPOUT) {
-              if (p.drop.step != nullptr) drop_columns(mask_of(c / 2) >> (c % 2 * 16), p.drop.scale, dh);
+              if (p.drop.step != nullptr) drop_columns(mask_of(c / 2, nacc0) >> (c % 2 * 16), p.drop.scale, dh);
             } else {
               apply_pointwise<16>(code, dh, p, nacc0 + c * 16, p.N, rs_m);
             }
@@ -1863,7 +1864,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               break;
             case GEMM_EPI_OP_DROPOUT:
               if constexpr (Prog::drops) {
-                if (p.drop.step != nullptr) drop_columns(mask_of(c), p.drop.scale, v);
+                if (p.drop.step != nullptr) drop_columns(mask_of(c, n0), p.drop.scale, v);
                 packed = false;
               }
               break;

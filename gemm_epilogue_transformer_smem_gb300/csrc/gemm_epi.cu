@@ -303,7 +303,8 @@ struct gemm_epi_plan {
   int head_rms_at = -1, rotary_at = -1;
   float head_eps = 0.0f;
   bool heads() const { return head_rms_at >= 0 || rotary_at >= 0; }
-  bool drops = false;          // DROPOUT
+  int drop_at = -1;            // DROPOUT
+  bool drops() const { return drop_at >= 0; }
   int32_t drop_threshold = 0;  // 0: it changes nothing
   float rms_eps = 0.0f;
   int rms_unrounded = 0;
@@ -412,10 +413,10 @@ gemm_epi_status validate(gemm_epi_plan& P) {
         break;
       }
       case GEMM_EPI_OP_DROPOUT:
-        if (P.drops) return fail(GEMM_EPI_ERR_INVALID_VALUE, "op %d: DROPOUT appears twice", i);
+        if (P.drops()) return fail(GEMM_EPI_ERR_INVALID_VALUE, "op %d: DROPOUT appears twice", i);
         if (op.i0 < 0 || op.i0 > 65536)
           return fail(GEMM_EPI_ERR_INVALID_VALUE, "the DROPOUT threshold must be in [0, 65536] (got %d)", op.i0);
-        P.drops = true;
+        P.drop_at = i;
         P.drop_threshold = op.i0;
         break;
       case GEMM_EPI_OP_ROW_RMS_RSQRT:
@@ -442,7 +443,7 @@ gemm_epi_status validate(gemm_epi_plan& P) {
       default: break;
     }
   }
-  if (P.drops && P.heads()) return fail(GEMM_EPI_ERR_UNSUPPORTED, "DROPOUT with HEAD_RMS or ROTARY");
+  if (P.drops() && P.heads()) return fail(GEMM_EPI_ERR_UNSUPPORTED, "DROPOUT with HEAD_RMS or ROTARY");
   if (P.heads()) {
     if (P.pair_at >= 0 || P.expand_at >= 0 || P.uses_residual || P.uses_preact || P.dual)
       return fail(GEMM_EPI_ERR_UNSUPPORTED, "HEAD_RMS and ROTARY go with no pair op, DSWIGLU, GEMM_EPI_B_DUAL or "
@@ -522,7 +523,7 @@ gemm_epi_status validate(gemm_epi_plan& P) {
     if ((P.flags & ge::F_AUX) && bad_stride(d.batch_stride_aux, d.M * d.ld_aux, 8, false))
       return fail(GEMM_EPI_ERR_INVALID_VALUE, "batch_stride_aux must span M x ld_aux, a multiple of 8");
   }
-  if (P.drops && d.M * P.batch > (int64_t(1) << 32))
+  if (P.drops() && d.M * P.batch > (int64_t(1) << 32))
     return fail(GEMM_EPI_ERR_INVALID_VALUE, "DROPOUT counts rows in 32 bits: M * batch is above 2^32");
   if (P.num_m_tiles * P.num_n_tiles * P.batch > LIM) return fail(GEMM_EPI_ERR_INVALID_VALUE, "too many tiles");
   // One row counter per 128-row block, counted in whole 256-row tiles so
@@ -634,7 +635,7 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
     L.kernel = L.split > 1 ? P.spec->kernel_split : L.cg == 2 ? P.spec->kernel_2sm : P.spec->kernel_1sm;
   else if (P.heads())
     L.kernel = ge::kDynamicHeads[P.in8 ? 1 : 0][L.split > 1 ? 2 : L.cg == 2 ? 1 : 0];
-  else if (P.drops)
+  else if (P.drops())
     L.kernel = ge::kDynamicDrop[P.in8 ? 1 : 0][L.cg == 2 ? 1 : 0];
   else if (P.in8)
     L.kernel = ge::kDynamicFp8[L.cg == 2 ? 1 : 0];
@@ -724,7 +725,7 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
     k.positions = a.positions;
     k.positions_64 = a.positions_64 ? 1 : 0;
   }
-  if (P.drops) k.drop = ge::dropout_of(gemm_epi_mask{a.dropout_step, a.dropout_seed, a.dropout_site, P.drop_threshold});
+  if (P.drops()) k.drop = ge::dropout_of(gemm_epi_mask{a.dropout_step, a.dropout_seed, a.dropout_site, P.drop_threshold});
   for (size_t i = 0; i < P.ops.size(); ++i) {
     k.ops[i].code = P.ops[i].code;
     k.ops[i].i0 = P.ops[i].i0;
@@ -747,7 +748,9 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
   // the drawing once the epilogue is the longer part: dropout + residual 8192 x
   // 4096 x 1024 79.0 and 88.2, x 4096 158.0 and 158.6, 1003 x 4112 x 2056 29.1 and 26.9.
   const int64_t at_once = L.cg == 2 ? dev.pair_clusters : dev.sms;
-  k.masks_ahead = k.drop.step != nullptr && !(P.flags & ge::F_E8) &&
+  // Behind DSWIGLU a tile has more columns than there is room for masks.
+  const bool fits = !(P.flags & ge::F_E8) && !(P.expand_at >= 0 && P.drop_at > P.expand_at);
+  k.masks_ahead = k.drop.step != nullptr && fits &&
                   (!(P.flags & ge::F_AUX) || P.expand_at >= 0 || k.num_tiles <= at_once);
 
   if (d.K > 0) {
@@ -950,7 +953,7 @@ gemm_epi_status gemm_epi_run_unfused(gemm_epi_handle h, const gemm_epi_args* arg
   if (h->heads())
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "the separate pass has no HEAD_RMS or ROTARY: run the GEMM and "
                                           "gemm_epi_qk_norm_rotary or gemm_epi_rotary");
-  if (h->drops)
+  if (h->drops())
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "the separate pass has no DROPOUT: run the GEMM and gemm_epi_dropout");
   if (h->expand_at >= 0 && h->expand_g > 4)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "the separate pass handles DSWIGLU groups up to 4");
