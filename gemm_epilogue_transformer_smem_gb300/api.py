@@ -61,6 +61,8 @@ def encode_program(program: Sequence[str], drop_threshold: int = 0):
             f0 = float(arg) if arg else 1e-6
             i0 = 1 if name == "row_rms_unrounded" else 0
         elif name == "dropout":
+            if arg:
+                raise ValueError("the dropout op takes its probability from dropout=, not %r" % spec)
             i0 = drop_threshold
         ops[i] = N.gemm_epi_op(code, i0, f0)
     return ops
