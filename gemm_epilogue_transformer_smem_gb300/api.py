@@ -655,11 +655,11 @@ class Dropout:
     """A dropout probability, the seed its masks are drawn from and the step,
     which lies in device memory.
 
-    p is rounded to a multiple of 2^-16; what stays is scaled by the inverse of
-    the share that stays, so that means are kept.  The mask of a call depends on
-    seed, step and the call's `site` (and the element's row and column), nothing
-    else: a backward pass with the same three drops what its forward pass
-    dropped.  advance() counts the step on, on the current stream; captured into
+    p is rounded to a multiple of 2^-16 and cannot be changed later: plans made
+    with the object hold it.  What stays is scaled by the inverse of the share
+    that stays, so that means are kept.  The mask of a call depends on p, seed,
+    step and the call's `site` (and the element's row and column), nothing else: a
+    backward pass with the same ones drops what its forward pass dropped.  advance() counts the step on, on the current stream; captured into
     a graph, each replay draws masks of its own.
     """
 
@@ -668,10 +668,19 @@ class Dropout:
             raise ValueError("p must be in [0, 1], got %r" % (p,))
         if not 0 <= seed < 2 ** 64 or not 0 <= step < 2 ** 63:
             raise ValueError("seed must be in [0, 2^64) and step in [0, 2^63), got %r and %r" % (seed, step))
-        self.p = float(p)
-        self.threshold = round(self.p * 65536)
+        self._p = float(p)
+        self._threshold = round(self._p * 65536)
         self.seed = int(seed)
         self.step = torch.tensor([step], dtype=torch.int64).to(device)
+
+    @property
+    def p(self) -> float:
+        return self._p
+
+    @property
+    def threshold(self) -> int:
+        """Of the 65536 values an element's number has, those that drop it."""
+        return self._threshold
 
     @property
     def step(self) -> torch.Tensor:
@@ -767,14 +776,15 @@ def _values(name: str, t: torch.Tensor, n: int, index: int) -> int:
 
 def _mask(rng: Dropout, site: int, index: int):
     """(step, seed, site, threshold) of a gemm_epi_mask."""
-    if rng.threshold == 0:
+    threshold = rng._threshold
+    if threshold == 0:
         return _NO_MASK
     step = rng._step
     if step.get_device() != index:
         raise ValueError("the dropout step is on %s, not with the other tensors" % step.device)
     if not 0 <= site < 2 ** 32:
         raise ValueError("site must be in [0, 2^32), got %r" % (site,))
-    return step.data_ptr(), rng.seed, site, rng.threshold
+    return step.data_ptr(), rng.seed, site, threshold
 
 
 def _call_packed(entry: str, packed: bytes, first: torch.Tensor, index: int, stream) -> None:

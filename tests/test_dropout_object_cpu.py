@@ -16,3 +16,13 @@ def test_the_op_takes_no_number(spec, dropout):
     rng = None if dropout is None else api.Dropout(dropout, device="cpu")
     with pytest.raises(ValueError):
         api.Plan(64, 64, 64, [spec, "store_bf16"], b_layout="nk", dropout=rng)
+
+
+@pytest.mark.parametrize("name,value", [("p", 0.0), ("threshold", 0)])
+def test_the_probability_stays(name, value):
+    """Plans hold it: one that changed later would give masks of two probabilities for one step."""
+    rng = api.Dropout(0.5, device="cpu")
+    with pytest.raises(AttributeError):
+        setattr(rng, name, value)
+    assert rng.p == 0.5 and rng.threshold == 32768
+    assert api._mask(rng, 3, -1) == (rng.step.data_ptr(), 0, 3, 32768)
