@@ -659,8 +659,9 @@ class Dropout:
     with the object hold it.  What stays is scaled by the inverse of the share
     that stays, so that means are kept.  The mask of a call depends on p, seed,
     step and the call's `site` (and the element's row and column), nothing else: a
-    backward pass with the same ones drops what its forward pass dropped.  advance() counts the step on, on the current stream; captured into
-    a graph, each replay draws masks of its own.
+    backward pass with the same ones drops what its forward pass dropped.
+    advance() counts the step on, on the current stream; captured into a graph,
+    each replay draws masks of its own.
     """
 
     def __init__(self, p: float, seed: int = 0, step: int = 0, device="cuda"):
