@@ -39,11 +39,18 @@ Shape forward_shape(int64_t rows, int64_t cols, int64_t pieces, const Choice& c,
   auto warps = [&](int n) { s.teams = std::max(1, n / s.warps); };
   // bf16 with a second stream: two pieces and one row make for more teams, but the
   // last warp of a row that ends inside its columns has no staged weights there.
-  // With dropout 1024 columns 79.9 us for 84.5 with 4 and 2 (268 MB), 1000 102 for
-  // 94.4, 1800 110 for 93.8, 1280, which fills 5 of 8 pieces, 105 for 109.8; without
-  // 4096 88.7 for 91.5, 4000 92.0 for 86.6, 768 95.4 for 98.2, 600 112 for 101.
+  // With dropout they are taken where every warp is full, or where of four to a warp
+  // two or more would be empty, at up to ten pieces (537 MB, two against four): 3 of
+  // them 113 us and 91.4, 4 (800 columns) 116 and 95.0, 1024 columns 90.0 and 99.1,
+  // 5 (1280) 105.5 and 116, 6 (1400) 103 and 117, 7 (1792) 99.5 and 94.3, 8 (1904)
+  // 102 and 95.4, 9 (2304) 99.0 and 107, 10 (2560) 89.6 and 101, 11 (2816) 103 and
+  // 94.3, 12 (3000) 104 and 96.2, 13 (3328) 103 and 98.4, 14 (3400) 104 and 108, 15
+  // (3840) 103 and 93.3, 16 (4096) 95.0 and 90.7.  Without it: 3 (640) 105 and 98.3,
+  // one warp in place of two, 4 (896) 90.0 and 101, 6 (1480) 92.2 and 103, 8 (1992)
+  // 93.5 and 97.9, 9 (2304) 93.6 and 90.3, 11 (2816) 92.4 and 89.5, 16 (4000) 91.0 and
+  // 88.0, 4096 columns 87.3 and 93.4.
   const bool even = cols % (2 * ge::LN_PIECE) == 0;
-  const bool two = c.drop ? pieces <= 8 && (even || pieces <= 2 || pieces == 5 || pieces == 6)
+  const bool two = c.drop ? pieces <= 10 && (even || pieces % 4 == 1 || pieces % 4 == 2)
                           : pieces <= 16 && (even || (pieces <= 8 && pieces != 3));
   if (!c.wide && (!few || pieces > 2 * ge::LN_MAX_WARPS)) {
     // by words 8 warps to a block: 16384 x 4095 149 us with dropout (fp32 240), 16 151
@@ -79,7 +86,7 @@ Shape forward_shape(int64_t rows, int64_t cols, int64_t pieces, const Choice& c,
   return s;
 }
 
-Shape backward_shape(int64_t rows, int64_t pieces, const Choice& c, int sms) {
+Shape backward_shape(int64_t rows, int64_t cols, int64_t pieces, const Choice& c, int sms) {
   const bool few = rows <= 2 * sms;
   Shape s{HELD, 4, 1, 1, 0, 1, false};
   auto take = [&](int k) {
@@ -105,9 +112,21 @@ Shape backward_shape(int64_t rows, int64_t pieces, const Choice& c, int sms) {
     take(pieces == 3 || pieces > 8 ? 4 : 2);
   }
   // 3000 columns: one team of 3 warps to a block 126 us (158 with dropout, and only two
-  // blocks to an SM have room for their sums), five 103 (123); 4096: three of 4 warps 89.3
-  // (113.5), four 94.1 (126.8)
-  s.teams = c.wide && !c.f32 && s.warps == 4 && s.k == 4 ? 3 : ge::LN_MAX_WARPS / s.warps;
+  // blocks to an SM have room for their sums), five 103 (123)
+  s.teams = ge::LN_MAX_WARPS / s.warps;
+  // A team fewer where `add` is the third stream, more than 176 KB would be on their
+  // way to a block (two rows of each team) and 12 warps stay: over many rows of whole
+  // 64 bytes the copies then get in each other's way.  Three teams of 4 warps against
+  // four, with dropout and without, at 4096 columns 112.2 and 123.8 us, 87.3 and 91.0
+  // (67 M elements); 3968 112.8 and 122.7, 87.7 and 90.4; 3776 116.6 and 119.9, 88.8
+  // and 89.2.  With less on the way they lose: 3712 118.8 and 117.7, 3456 125.3 and
+  // 110.9, 4096 without `add` 100.5 and 92.5.  So do they in rows off 64 bytes (4088
+  // 128.4 and 122.3) and in few of them (2929 of 4096 30.2 and 29.0, 7500 of 4000 59.1
+  // and 57.2).  Four teams of 3 against five: 3040 111.4 and 122.5, 87.5 and 93.4.
+  const int64_t on_the_way = int64_t{2 * 3} * s.teams * cols * static_cast<int64_t>(sizeof(uint16_t));
+  if (c.wide && !c.f32 && c.add && on_the_way > 176 * 1024 && cols % 32 == 0 && rows > 64 * sms &&
+      (s.teams - 1) * s.warps >= 12)
+    --s.teams;
   s.staged = true;  // 4096: 91.5 us, 113.3 from L1
   return s;
 }
@@ -127,7 +146,7 @@ Shape shape_of(bool backward, int64_t rows, int64_t cols, const Choice& c, int s
     if (backward) s.rows = static_cast<int>(std::min<int64_t>(ge::LN_LONG_ROWS, std::max<int64_t>(1, rows / (2 * sms))));
     return s;
   }
-  Shape s = backward ? backward_shape(rows, pieces, c, sms) : forward_shape(rows, cols, pieces, c, sms);
+  Shape s = backward ? backward_shape(rows, cols, pieces, c, sms) : forward_shape(rows, cols, pieces, c, sms);
   // a block to every SM before a second team to a block
   s.teams = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(s.teams, rows / (s.rows * sms))));
   return s;

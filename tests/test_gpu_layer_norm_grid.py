@@ -36,6 +36,9 @@ MANY = [(ROWS, cols, dtype, order, residual, p)
 MANY += [(ROWS, cols, dtype, "odd", residual, p) for cols in (600, 1003, 4096) for dtype in (BF, F32)
          for residual, p in ((True, 0.1), (False, 0.0), (True, 0.0))]
 MANY += [(20001, cols, dtype, "packed", True, p) for cols in (16, 64, 200) for dtype in (BF, F32) for p in (0.0, 0.1)]
+MANY += [(ROWS, cols, BF, "packed", residual, 0.1) for cols in (2304, 2560, 2816) for residual in (False, True)]
+# more than 64 rows to an SM: a team fewer to a block where `add` is read too
+MANY += [(9800, cols, BF, "packed", True, p) for cols in (3040, 4088, 4096) for p in (0.0, 0.1)]
 MANY += [(700, cols, BF, "packed", True, 0.1) for cols in (8192, 14336, 16392)]
 CASES = SMALL + MANY
 IDS = lambda c: "%dx%d-%s-%s-%s-p%g" % (c[0], c[1], str(c[2])[6:], c[3], "res" if c[4] else "x", c[5])  # noqa: E731
