@@ -748,7 +748,8 @@ gemm_epi_status prepare(const gemm_epi_plan& P, const gemm_epi_args& a, const De
   // the drawing once the epilogue is the longer part: dropout + residual 8192 x
   // 4096 x 1024 79.0 and 88.2, x 4096 158.0 and 158.6, 1003 x 4112 x 2056 29.1 and 26.9.
   const int64_t at_once = L.cg == 2 ? dev.pair_clusters : dev.sms;
-  // Behind DSWIGLU a tile has more columns than there is room for masks.
+  // Behind DSWIGLU a tile has more columns than there is room for masks (8192 x 4096
+  // x 1024 in the interpreter 224 us, 109 without the op).
   const bool fits = !(P.flags & ge::F_E8) && !(P.expand_at >= 0 && P.drop_at > P.expand_at);
   k.masks_ahead = k.drop.step != nullptr && fits &&
                   (!(P.flags & ge::F_AUX) || P.expand_at >= 0 || k.num_tiles <= at_once);

@@ -10,8 +10,9 @@
 //              d_residual = g,  dx = D(g),  dw = sum of dy n,  db = sum of dy
 // Everything is fp32 between one load and one store of each value, the sums of
 // dw and db too: each thread's over its rows, then the blocks' in a fixed order.
-// The variance is that of the differences from a mean taken first, never a
-// difference of squares.
+// The variance is that of the differences from a mean taken first, never of the
+// squares and the mean; several warps take theirs from means of their own, which
+// are joined by the means' differences.
 //
 // All of it is memory-bound, so a row is read once: a team of threads -- part of
 // a warp, a warp, or up to 16 of them, as the width asks for -- holds a row in
@@ -26,7 +27,7 @@
 //   norm, dropout and residual, 16384 x 4096 bf16 (537 MB)   92.4 us  0.86
 //   the same without dropout                                 88.6 us  0.89
 //   norm alone, 16384 x 4096 (268 MB)                        47.5 us  0.83
-//   backward with dropout and `add`, 16384 x 4096 (671 MB)  114.5 us  0.86
+//   backward with dropout and `add`, 16384 x 4096 (671 MB)  112.7 us  0.88
 //   the same of 65536 x 1024                                112.4 us  0.88
 //   backward with `add`, 2048 x 14336 (235 MB)               53.6 us  0.65 (16384
 //     rows 290 us, 0.95): 13.5 rows to an SM, so that the way in of the first, the
@@ -34,7 +35,10 @@
 //     cluster of two blocks, with two rows on an SM: 61
 //   dropout, 8192 x 14336 (470 MB)                           78.5 us  0.88
 //   rows that start anywhere, 16384 x 4095 (537 MB)         151   us  0.52: words
-//     of 4 bytes in place of 16; backward (671 MB) 271 us, 0.36
+//     of 4 bytes in place of 16; backward (671 MB) 265 us, 0.37; up to 256 columns
+//     by single elements, 65536 x 253 (133 MB) 73 us, 0.27, backward 96, 0.25; more
+//     than 16384 likewise, 4096 x 16389 443 us, 0.18, backward 416, 0.24
+//   weights off 16 bytes take aligned rows with them: 16384 x 4096 129 us, backward 210
 #pragma once
 
 #include <stdint.h>

@@ -534,8 +534,10 @@ typedef struct gemm_epi_mask {
 /* y = D(x) (+ residual): M x N, row strides in elements.  Inputs may have any
  * row stride >= 0 (0: one row for all), the output one >= N; x and residual may be
  * y itself (same pointer and stride), otherwise nothing overlaps y.  A call moves
- * 16 bytes per access where pointers and row strides are multiples of them
- * (inputs and outputs each for themselves), single elements otherwise. */
+ * 16 bytes per access where all its tensors' pointers and row strides are
+ * multiples of them; one that is not takes the others with it.  Rows of more than
+ * 256 columns then go by 4-byte words, narrower ones by single elements (here
+ * inputs and output each for themselves). */
 typedef struct gemm_epi_dropout_args {
     int64_t M, N;             /* M < 2^31, 1 <= N <= 2^31 - 4096; M 0 is allowed */
     int32_t type;             /* BF16 or F32: x, residual and y */
@@ -547,8 +549,12 @@ typedef struct gemm_epi_dropout_args {
 
 /* h = D(x) + residual, mean and variance of h over its row (divided by N),
  *   y = (h - mean) / sqrt(variance + eps) * w + b,
- * h in fp32 throughout, rounded only where it is stored.  Strides, alignment and
- * in-place use as in gemm_epi_dropout_args; `sum` is an output as well. */
+ * h and the sums over it in fp32 throughout, rounded only where they are stored.
+ * Strides, alignment and in-place use as in gemm_epi_dropout_args, w and b among
+ * the pointers that decide the access; `sum` is an output as well.  Rows off 16
+ * bytes go by words up to 16384 columns, above them by single elements.  A row of
+ * more than 16384 columns is summed in 512 strands: its mean and variance are good
+ * to some N / 512 of fp32's roundings. */
 typedef struct gemm_epi_layer_norm_args {
     int64_t M, N;
     int32_t type;             /* BF16 or F32: x, residual, y and sum */
@@ -567,7 +573,7 @@ typedef struct gemm_epi_layer_norm_args {
  *   g = rstd (a - mean(a) - n mean(a n)) + add,
  *   d_residual = g,  dx = D(g),  dw = sum of dy n over the rows,  db = sum of dy.
  * `add` is the gradient that reaches h past the norm.  dx or d_residual may be an
- * input itself (same pointer and stride). */
+ * input itself (same pointer and stride).  Accesses as in gemm_epi_layer_norm_args. */
 typedef struct gemm_epi_layer_norm_bwd_args {
     int64_t M, N;
     int32_t type;             /* BF16 or F32: dy, x, add, dx and d_residual */
